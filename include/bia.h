@@ -421,6 +421,137 @@ BIA_API int bia_append_paged_kv(const bia_attn_desc *desc, const void *k_new, co
                         const int32_t *kv_last_page_len_host, int32_t batch, int32_t *status,
                         void *stream);
 
+/*
+ * The 8-bit paged cache: keys and values in half the bytes of the bf16 cache.
+ *   k_cache, v_cache  [num_pages, page_size, num_kv_heads, head_dim] e4m3 codes
+ *   k_scale, v_scale  [num_pages, page_size, num_kv_heads] e8m0 scales: one
+ *                     power of two, 2^(byte - 127), per (key, kv head) row
+ *   row value d = code_d * scale
+ * The append below writes a row with e = the smallest integer >= -120 for
+ * which the row's largest finite magnitude is at most 448 * 2^e, codes
+ * rounded to nearest even, and the byte e + 127; a non-finite element is
+ * stored as NaN (and the 8-bit decode hands a NaN on to the outputs that it
+ * reaches).  A row's codes and scale depend on that row alone, so what the
+ * cache holds, and every result from it, is free of batch, page and chunk.
+ * With those scales every value is exact in bf16: reading back rounds nothing
+ * (an element above 248 * 2^120, 3.29e38, is stored as 2^128, which reads back
+ * as an infinity).
+ * head_dim, page sizes and head counts are those of the bf16 calls.
+ */
+
+/*
+ * bia_append_paged_kv for the 8-bit cache: new token t of request b is
+ * quantised into position kv_len(b) - n_new(b) + (t - append_indptr[b]).
+ *   k_new, v_new: bf16 rows of num_kv_heads * head_dim elements, 16-byte
+ *                 aligned; k_stride / v_stride elements from one token to the
+ *                 next (a multiple of 8, at least the row; 0: dense), so that
+ *                 both may lie inside a fused projection's rows
+ * Everything else, the status word included, as for bia_append_paged_kv.
+ * append_indptr[batch] * num_kv_heads must stay below 2^30 (else
+ * BIA_ERR_UNSUPPORTED).
+ */
+BIA_API int bia_append_paged_kv_fp8(const bia_attn_desc *desc, const void *k_new,
+                            const void *v_new, int64_t k_stride, int64_t v_stride, void *k_cache,
+                            void *v_cache, void *k_scale, void *v_scale, int64_t num_pages,
+                            const int32_t *append_indptr, const int32_t *kv_indptr,
+                            const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                            const int32_t *append_indptr_host, const int32_t *kv_indptr_host,
+                            const int32_t *kv_last_page_len_host, int32_t batch, int32_t *status,
+                            void *stream);
+
+/*
+ * Reads rows of the 8-bit cache back as bf16, packed one request after the
+ * other: the FIRST n(b) = out_indptr[b+1] - out_indptr[b] <= kv_len(b) keys of
+ * request b become rows out_indptr[b] .. of
+ *   k_out, v_out: [out_indptr[batch], num_kv_heads, head_dim] bf16, 16-byte
+ *                 aligned, dense
+ * which is what bia_prefill_ragged attends over when a chunk follows a cached
+ * prefix (append the chunk, read everything back: each chunk then sees the
+ * same keys, wherever its boundary lies).  A page index outside
+ * [0, num_pages) reads as zeros and sets bit 0 of *status (NULL, or a device
+ * int32 the call zeroes first).  out_indptr[batch] * num_kv_heads must stay
+ * below 2^30.
+ */
+BIA_API int bia_gather_paged_kv_fp8(const bia_attn_desc *desc, const void *k_cache,
+                            const void *v_cache, const void *k_scale, const void *v_scale,
+                            int64_t num_pages, const int32_t *out_indptr,
+                            const int32_t *kv_indptr, const int32_t *kv_indices,
+                            const int32_t *kv_last_page_len, const int32_t *out_indptr_host,
+                            const int32_t *kv_indptr_host, const int32_t *kv_last_page_len_host,
+                            int32_t batch, void *k_out, void *v_out, int32_t *status,
+                            void *stream);
+
+/*
+ * bia_decode_paged over the 8-bit cache: q, out and lse, the page table, the
+ * fixed split-KV tiles (0 = BIA_DECODE_SPLIT) and their ascending merge, the
+ * ownership and the errors are the same.  The workspace is
+ * bia_decode_fp8_workspace_size's.
+ */
+BIA_API int bia_decode_paged_fp8(const bia_attn_desc *desc, const void *q, const void *k_cache,
+                         const void *v_cache, const void *k_scale, const void *v_scale,
+                         int64_t num_pages, const int32_t *kv_indptr, const int32_t *kv_indices,
+                         const int32_t *kv_last_page_len, const int32_t *kv_indptr_host,
+                         const int32_t *kv_last_page_len_host, int32_t batch, int32_t split_size,
+                         void *workspace, size_t workspace_bytes, void *out, float *lse,
+                         void *stream);
+
+/* Workspace bytes bia_decode_paged_fp8 needs for this call (0 on invalid input). */
+BIA_API size_t bia_decode_fp8_workspace_size(const bia_attn_desc *desc,
+                                     const int32_t *kv_indptr_host,
+                                     const int32_t *kv_last_page_len_host, int32_t batch,
+                                     int32_t split_size);
+
+/* bia_decode_paged_fp8 sized from `bounds`, as bia_decode_paged_bounded is:
+ * one captured graph replays while the device arrays change, with the bits of
+ * the exact call. */
+BIA_API int bia_decode_paged_fp8_bounded(const bia_attn_desc *desc, const bia_bounds *bounds,
+                                 const void *q, const void *k_cache, const void *v_cache,
+                                 const void *k_scale, const void *v_scale, int64_t num_pages,
+                                 const int32_t *kv_indptr, const int32_t *kv_indices,
+                                 const int32_t *kv_last_page_len, int32_t batch,
+                                 int32_t split_size, void *workspace, size_t workspace_bytes,
+                                 void *out, float *lse, void *stream);
+
+/* Workspace bytes of every bounded 8-bit decode of `batch` requests within
+ * `bounds` (0 on invalid input). */
+BIA_API size_t bia_decode_fp8_bounded_workspace_size(const bia_attn_desc *desc,
+                                             const bia_bounds *bounds, int32_t batch,
+                                             int32_t split_size);
+
+/*
+ * Attention of packed sequences over contiguous keys and values: the prompt
+ * (or chunk over a prefix read back from the 8-bit cache) of a server whose
+ * cache holds no bf16 pages to prefill from.
+ *   q     [total_q, num_qo_heads, head_dim] bf16, out the same (dense)
+ *   k, v  [total_kv, num_kv_heads, head_dim] bf16
+ *   q_stride, k_stride, v_stride: elements from one token to the next (a
+ *         multiple of 8, at least the token's row; 0: dense): q, k and v may
+ *         be the parts of one fused projection
+ *   qo_indptr, kv_indptr: int32 [batch+1], both starting at 0: request b owns
+ *         q tokens qo_indptr[b] .. and keys kv_indptr[b] ..
+ * Request b's q tokens are the last q_len of its kv_len keys (the rule of
+ * bia_prefill_paged); causal calls need q_len <= kv_len, and without causal a
+ * request without keys gives out 0 and lse -inf.  page_size of desc is not
+ * used.  Tiles, split_size (0 = BIA_PREFILL_SPLIT), merge, workspace,
+ * ownership and errors as for bia_prefill_paged; a row's bits depend only on
+ * its own request up to its position, under any chunking, on the q-tile grid
+ * or off it.  What lies past a request's last key never reaches its rows; a
+ * non-finite key or value of the request itself may reach every row of the
+ * 128-row q tiles that see its 128-key block.
+ */
+BIA_API int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k,
+                       const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                       const int32_t *qo_indptr, const int32_t *kv_indptr,
+                       const int32_t *qo_indptr_host, const int32_t *kv_indptr_host,
+                       int32_t batch, int32_t causal, int32_t split_size, void *workspace,
+                       size_t workspace_bytes, void *out, float *lse, void *stream);
+
+/* Workspace bytes bia_prefill_ragged needs for this call (0 on invalid input). */
+BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
+                                         const int32_t *qo_indptr_host,
+                                         const int32_t *kv_indptr_host, int32_t batch,
+                                         int32_t causal, int32_t split_size);
+
 /* Tokens per q tile for GQA group size G = num_qo_heads / num_kv_heads:
  * 128 / G, the chunk grid on which chunked prefill is guaranteed to be
  * bit-identical ("sglang PR #43612", Summary).  0 if G does not divide 128. */

@@ -41,7 +41,10 @@ EXPORTS = ("bia_prefill_paged", "bia_prefill_workspace_size", "bia_decode_paged"
            "bia_mla_decode_workspace_size", "bia_mla_prefill_paged",
            "bia_mla_prefill_workspace_size", "bia_prefill_paged_bounded",
            "bia_prefill_bounded_workspace_size", "bia_decode_paged_bounded",
-           "bia_decode_bounded_workspace_size")
+           "bia_decode_bounded_workspace_size", "bia_append_paged_kv_fp8",
+           "bia_gather_paged_kv_fp8", "bia_decode_paged_fp8", "bia_decode_fp8_workspace_size",
+           "bia_decode_paged_fp8_bounded", "bia_decode_fp8_bounded_workspace_size",
+           "bia_prefill_ragged", "bia_prefill_ragged_workspace_size")
 
 
 class BiaError(RuntimeError):
@@ -141,6 +144,27 @@ def load(path: str = LIB_PATH):
     lib.bia_decode_paged_bounded.restype = ctypes.c_int
     lib.bia_decode_bounded_workspace_size.argtypes = [dp, bp, i32, i32]
     lib.bia_decode_bounded_workspace_size.restype = sz
+    lib.bia_append_paged_kv_fp8.argtypes = [dp, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp,
+                                            vp, vp, vp, vp, i32, vp, vp]
+    lib.bia_append_paged_kv_fp8.restype = ctypes.c_int
+    lib.bia_gather_paged_kv_fp8.argtypes = [dp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp,
+                                            i32, vp, vp, vp, vp]
+    lib.bia_gather_paged_kv_fp8.restype = ctypes.c_int
+    lib.bia_decode_paged_fp8.argtypes = [dp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i32,
+                                         i32, vp, sz, vp, vp, vp]
+    lib.bia_decode_paged_fp8.restype = ctypes.c_int
+    lib.bia_decode_fp8_workspace_size.argtypes = [dp, vp, vp, i32, i32]
+    lib.bia_decode_fp8_workspace_size.restype = sz
+    lib.bia_decode_paged_fp8_bounded.argtypes = [dp, bp, vp, vp, vp, vp, vp, i64, vp, vp, vp, i32,
+                                                 i32, vp, sz, vp, vp, vp]
+    lib.bia_decode_paged_fp8_bounded.restype = ctypes.c_int
+    lib.bia_decode_fp8_bounded_workspace_size.argtypes = [dp, bp, i32, i32]
+    lib.bia_decode_fp8_bounded_workspace_size.restype = sz
+    lib.bia_prefill_ragged.argtypes = [dp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, i32,
+                                       i32, vp, sz, vp, vp, vp]
+    lib.bia_prefill_ragged.restype = ctypes.c_int
+    lib.bia_prefill_ragged_workspace_size.argtypes = [dp, vp, vp, i32, i32, i32]
+    lib.bia_prefill_ragged_workspace_size.restype = sz
     _lib = lib
     return lib
 
@@ -152,6 +176,7 @@ def _ptr(t):
 
 
 BF16, F32, I32, I64, U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu  # the 8-bit cache's codes and scales
 
 
 # The library sees only the addresses of the device tensors: a host tensor, a
@@ -562,3 +587,227 @@ def bia_mla_prefill_paged(desc, q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, k
         _stream(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_mla_prefill_paged")
+
+
+# ---------------------------------------------------------------- 8-bit cache
+
+
+def _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale):
+    _check_caches(k_cache, v_cache)
+    want = (k_cache.shape[0], desc.page_size, desc.num_kv_heads, desc.head_dim)
+    if tuple(k_cache.shape) != want:
+        raise ValueError(f"the caches must be {want} (num_pages, page_size, num_kv_heads, "
+                         f"head_dim) for this descriptor, got {tuple(k_cache.shape)}")
+    if tuple(k_scale.shape) != want[:3] or tuple(v_scale.shape) != want[:3]:
+        raise ValueError(f"k_scale and v_scale must be {want[:3]}, got {tuple(k_scale.shape)} and "
+                         f"{tuple(v_scale.shape)}")
+
+
+def _check_lengths(batch, **arrays):
+    """Every index array holds the entries the call reads: batch + 1 of an
+    indptr, batch of a last page length."""
+    for name, t in arrays.items():
+        want = batch + ("indptr" in name)
+        if t.numel() != want:
+            raise ValueError(f"{name} must hold {want} entries for {batch} requests, got "
+                             f"{t.numel()}")
+
+
+def _check_packed(name, t, heads, head_dim):
+    """(name, tensor) and token stride of packed bf16 rows [tokens, heads,
+    head_dim]: a token's heads and columns dense, any multiple of 8 elements
+    from one token to the next."""
+    if t is None:
+        raise TypeError(f"{name} is required")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != BF16:
+        raise TypeError(f"{name} must be {BF16}, got {t.dtype}")
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+        raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}], got {tuple(t.shape)}")
+    row = heads * head_dim
+    if t.shape[0] == 0:
+        return (name, t), row
+    if (head_dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name} must hold each token's heads one after the other, got strides "
+                         f"{t.stride()}")
+    step = t.stride(0) if t.shape[0] > 1 else row
+    if step < row or step % 8 != 0:
+        raise ValueError(f"{name} must step a multiple of 8 elements, at least {row}, from token "
+                         f"to token, got {step}")
+    return (name, t), step
+
+
+def bia_append_paged_kv_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_scale, append_indptr,
+                            kv_indptr, kv_indices, kv_last_page_len, append_indptr_host,
+                            kv_indptr_host, kv_last_page_len_host, status=None, stream=None):
+    """bia_append_paged_kv into the 8-bit cache: codes torch.float8_e4m3fn
+    [num_pages, page_size, Hkv, D], scales torch.float8_e8m0fnu [num_pages,
+    page_size, Hkv] (include/bia.h states the format).  k_new and v_new
+    [total_new, Hkv, D] may be slices of a fused projection's rows."""
+    ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                      ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                      ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                      ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                      ("status", status, I32, True))
+    _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
+    k_given, k_step = _check_packed("k_new", k_new, desc.num_kv_heads, desc.head_dim)
+    v_given, v_step = _check_packed("v_new", v_new, desc.num_kv_heads, desc.head_dim)
+    ap, kvp, last = (_host_i32(append_indptr_host), _host_i32(kv_indptr_host),
+                     _host_i32(kv_last_page_len_host))
+    _check_lengths(len(ap) - 1, append_indptr=append_indptr, kv_indptr=kv_indptr,
+                   kv_last_page_len=kv_last_page_len, kv_indptr_host=kvp,
+                   kv_last_page_len_host=last)
+    if k_new.shape[0] != int(ap[-1]) or v_new.shape[0] != int(ap[-1]):
+        raise ValueError(f"k_new and v_new must hold append_indptr[batch] = {int(ap[-1])} tokens, "
+                         f"got {k_new.shape[0]} and {v_new.shape[0]}")
+    if kv_indices.numel() < int(kvp[-1]):
+        raise ValueError(f"kv_indices holds {kv_indices.numel()} pages, kv_indptr ends at "
+                         f"{int(kvp[-1])}")
+    _check_cuda(ts + [k_given, v_given], stream)
+    rc = load().bia_append_paged_kv_fp8(
+        ctypes.byref(desc), _ptr(k_new), _ptr(v_new), k_step, v_step, _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(append_indptr),
+        _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(ap), _ptr(kvp),
+        _ptr(last), len(ap) - 1, _ptr(status), _stream(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_append_paged_kv_fp8")
+
+
+def bia_gather_paged_kv_fp8(desc, k_cache, v_cache, k_scale, v_scale, k_out, v_out, out_indptr,
+                            kv_indptr, kv_indices, kv_last_page_len, out_indptr_host,
+                            kv_indptr_host, kv_last_page_len_host, status=None, stream=None):
+    """Reads the first out_indptr[b+1] - out_indptr[b] keys of each request
+    back from the 8-bit cache into k_out / v_out [out_indptr[batch], Hkv, D]
+    bf16, packed (include/bia.h states the rule)."""
+    ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                      ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                      ("k_out", k_out, BF16), ("v_out", v_out, BF16),
+                      ("out_indptr", out_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                      ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                      ("status", status, I32, True))
+    _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
+    op, kvp, last = (_host_i32(out_indptr_host), _host_i32(kv_indptr_host),
+                     _host_i32(kv_last_page_len_host))
+    _check_lengths(len(op) - 1, out_indptr=out_indptr, kv_indptr=kv_indptr,
+                   kv_last_page_len=kv_last_page_len, kv_indptr_host=kvp,
+                   kv_last_page_len_host=last)
+    want = (int(op[-1]), desc.num_kv_heads, desc.head_dim)
+    if tuple(k_out.shape) != want or tuple(v_out.shape) != want:
+        raise ValueError(f"k_out and v_out must be {want}, got {tuple(k_out.shape)} and "
+                         f"{tuple(v_out.shape)}")
+    if kv_indices.numel() < int(kvp[-1]):
+        raise ValueError(f"kv_indices holds {kv_indices.numel()} pages, kv_indptr ends at "
+                         f"{int(kvp[-1])}")
+    _check_cuda(ts, stream)
+    rc = load().bia_gather_paged_kv_fp8(
+        ctypes.byref(desc), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        k_cache.shape[0], _ptr(out_indptr), _ptr(kv_indptr), _ptr(kv_indices),
+        _ptr(kv_last_page_len), _ptr(op), _ptr(kvp), _ptr(last), len(op) - 1, _ptr(k_out),
+        _ptr(v_out), _ptr(status), _stream(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_gather_paged_kv_fp8")
+
+
+def bia_decode_fp8_workspace_size(desc, kv_indptr_host, kv_last_page_len_host,
+                                  split_size=0) -> int:
+    kvp, last = _host_i32(kv_indptr_host), _host_i32(kv_last_page_len_host)
+    return int(load().bia_decode_fp8_workspace_size(ctypes.byref(desc), _ptr(kvp), _ptr(last),
+                                                    len(kvp) - 1, int(split_size)))
+
+
+def _decode_fp8_tensors(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                        kv_last_page_len, workspace, out, lse, stream):
+    ts = _check_types(("q", q, BF16), ("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                      ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                      ("kv_indptr", kv_indptr, I32), ("kv_indices", kv_indices, I32),
+                      ("kv_last_page_len", kv_last_page_len, I32), ("workspace", workspace, None),
+                      ("out", out, BF16), ("lse", lse, F32, True))
+    _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
+    batch = kv_indptr.numel() - 1
+    if tuple(q.shape) != (batch, desc.num_qo_heads, desc.head_dim):
+        raise ValueError(f"q must be {(batch, desc.num_qo_heads, desc.head_dim)}, got "
+                         f"{tuple(q.shape)}")
+    _check_rows(q, out, lse)
+    _check_lengths(batch, kv_last_page_len=kv_last_page_len)
+    _check_cuda(ts, stream)
+
+
+def bia_decode_paged_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                         kv_last_page_len, kv_indptr_host, kv_last_page_len_host, workspace, out,
+                         lse=None, split_size=0, stream=None):
+    """bia_decode_paged over the 8-bit cache (include/bia.h states the format)."""
+    _decode_fp8_tensors(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                        kv_last_page_len, workspace, out, lse, stream)
+    kvp, last = _host_i32(kv_indptr_host), _host_i32(kv_last_page_len_host)
+    _check_lengths(q.shape[0], kv_indptr_host=kvp, kv_last_page_len_host=last)
+    if kv_indices.numel() < int(kvp[-1]):
+        raise ValueError(f"kv_indices holds {kv_indices.numel()} pages, kv_indptr ends at "
+                         f"{int(kvp[-1])}")
+    rc = load().bia_decode_paged_fp8(
+        ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        k_cache.shape[0], _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(kvp),
+        _ptr(last), len(kvp) - 1, int(split_size), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _stream(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_decode_paged_fp8")
+
+
+def bia_decode_fp8_bounded_workspace_size(desc, bounds, batch, split_size=0) -> int:
+    return int(load().bia_decode_fp8_bounded_workspace_size(
+        ctypes.byref(desc), ctypes.byref(bounds), int(batch), int(split_size)))
+
+
+def bia_decode_paged_fp8_bounded(desc, bounds, q, k_cache, v_cache, k_scale, v_scale, kv_indptr,
+                                 kv_indices, kv_last_page_len, workspace, out, lse=None,
+                                 split_size=0, stream=None):
+    """bia_decode_paged_fp8 sized from `bounds` (max_kv_len): the index arrays
+    are read on the device only, so a captured decode replays step after step."""
+    _decode_fp8_tensors(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                        kv_last_page_len, workspace, out, lse, stream)
+    rc = load().bia_decode_paged_fp8_bounded(
+        ctypes.byref(desc), ctypes.byref(bounds), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(kv_indptr), _ptr(kv_indices),
+        _ptr(kv_last_page_len), q.shape[0], int(split_size), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _stream(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_decode_paged_fp8_bounded")
+
+
+# ---------------------------------------------------------------- packed prompts
+
+
+def bia_prefill_ragged_workspace_size(desc, qo_indptr_host, kv_indptr_host, causal=True,
+                                      split_size=0) -> int:
+    qo, kvp = _host_i32(qo_indptr_host), _host_i32(kv_indptr_host)
+    return int(load().bia_prefill_ragged_workspace_size(ctypes.byref(desc), _ptr(qo), _ptr(kvp),
+                                                        len(qo) - 1, int(bool(causal)),
+                                                        int(split_size)))
+
+
+def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_indptr_host,
+                       workspace, out, lse=None, causal=True, split_size=0, stream=None):
+    """Attention of packed sequences: q [total_q, Hq, D] over k, v [total_kv,
+    Hkv, D], each dense or a slice of a fused projection's rows
+    (include/bia.h states the rule)."""
+    ts = _check_types(("qo_indptr", qo_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                      ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+    q_given, q_step = _check_packed("q", q, desc.num_qo_heads, desc.head_dim)
+    k_given, k_step = _check_packed("k", k, desc.num_kv_heads, desc.head_dim)
+    v_given, v_step = _check_packed("v", v, desc.num_kv_heads, desc.head_dim)
+    _check_rows(q, out, lse)
+    qo, kvp = _host_i32(qo_indptr_host), _host_i32(kv_indptr_host)
+    _check_lengths(len(qo) - 1, qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indptr_host=kvp)
+    if q.shape[0] != int(qo[-1]):
+        raise ValueError(f"q must hold qo_indptr[batch] = {int(qo[-1])} tokens, got {q.shape[0]}")
+    if k.shape[0] != int(kvp[-1]) or v.shape[0] != int(kvp[-1]):
+        raise ValueError(f"k and v must hold kv_indptr[batch] = {int(kvp[-1])} tokens, got "
+                         f"{k.shape[0]} and {v.shape[0]}")
+    _check_cuda(ts + [q_given, k_given, v_given], stream)
+    rc = load().bia_prefill_ragged(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), q_step, k_step, v_step, _ptr(qo_indptr),
+        _ptr(kv_indptr), _ptr(qo), _ptr(kvp), len(qo) - 1, int(bool(causal)), int(split_size),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
+        _stream(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_prefill_ragged")

@@ -141,10 +141,11 @@ int check_desc(const bia_attn_desc *d) {
 // Validates the host mirrors and computes the same plan sizes the device
 // planner will produce.  qo == nullptr: decode (one query per request).
 // stream: single-token tail tiles become streamed units (prefill).
+// last == nullptr with page_size 1: packed keys (every "page" is one key).
 int host_plan(const bia_attn_desc *d, const int32_t *qo, const int32_t *kvp,
               const int32_t *last, int32_t batch, int32_t causal, int32_t split, int tile_tokens,
               int tiles_per_unit, int ctas, int stream, HostPlan *hp) {
-  if (batch <= 0 || !kvp || !last) return BIA_ERR_INVALID_ARG;
+  if (batch <= 0 || !kvp || (!last && d->page_size != 1)) return BIA_ERR_INVALID_ARG;
   if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
   if (qo && qo[0] != 0) return BIA_ERR_INVALID_ARG;
   if (kvp[0] < 0) return BIA_ERR_INVALID_ARG;
@@ -153,8 +154,9 @@ int host_plan(const bia_attn_desc *d, const int32_t *qo, const int32_t *kvp,
     const int64_t q_len = qo ? static_cast<int64_t>(qo[b + 1]) - qo[b] : 1;
     const int64_t pages = static_cast<int64_t>(kvp[b + 1]) - kvp[b];
     if (q_len < 0 || pages < 0) return BIA_ERR_INVALID_ARG;
-    if (pages > 0 && (last[b] < 1 || last[b] > d->page_size)) return BIA_ERR_INVALID_ARG;
-    const int64_t kv_len = pages > 0 ? (pages - 1) * d->page_size + last[b] : 0;
+    const int32_t last_len = last ? last[b] : 1;
+    if (pages > 0 && (last_len < 1 || last_len > d->page_size)) return BIA_ERR_INVALID_ARG;
+    const int64_t kv_len = pages > 0 ? (pages - 1) * d->page_size + last_len : 0;
     if (kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
     if (causal && q_len > kv_len) return BIA_ERR_INVALID_ARG;
     if (!qo && kv_len == 0) return BIA_ERR_INVALID_ARG;
@@ -256,6 +258,44 @@ int encode_q_map(CUtensorMap *map, const void *base, int64_t total_q, int Hq, in
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(T)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return static_cast<int>(enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
+}
+
+// Packed rows [tokens][heads][head_dim] bf16 with `stride` elements between
+// tokens, as a 3-D map whose boxes are 64 columns x box_heads heads x
+// box_tokens tokens (128-byte swizzle); tokens past the end and columns past
+// head_dim read as zeros.
+int encode_packed_map(CUtensorMap *map, const void *base, int64_t tokens, int heads, int head_dim,
+                      int64_t stride, int box_heads, int box_tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return -1;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                                 static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return static_cast<int>(enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
+}
+
+// The same rows as a 2-D map (a row is a token, all its heads side by side)
+// in boxes of 64 columns x 1 row, for row gathers.
+int encode_packed_rows_map(CUtensorMap *map, const void *base, int64_t tokens, int heads,
+                           int head_dim, int64_t stride) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return -1;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(heads) * head_dim,
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[2] = {64, 1};
+  const cuuint32_t estr[2] = {1, 1};
+  return static_cast<int>(enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
                               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
@@ -785,6 +825,477 @@ int decode_on_scratch(const bia_attn_desc *desc, const void *q, const void *k_ca
 }
 
 } // namespace bia
+
+// ---------------------------------------------------------------- 8-bit cache
+
+extern "C" {
+
+namespace {
+
+// The checks append and gather share: n(b) = rows[b+1] - rows[b] rows of
+// request b among its kv_len(b) keys.
+int check_cache_fp8(const bia_attn_desc *desc, const void *k_rows, const void *v_rows,
+                    const void *k_cache, const void *v_cache, const void *k_scale,
+                    const void *v_scale, int64_t num_pages, const int32_t *row_indptr,
+                    const int32_t *kv_indptr, const int32_t *kv_indices,
+                    const int32_t *kv_last_page_len, const int32_t *rows_host,
+                    const int32_t *kvp_host, const int32_t *last_host, int32_t batch,
+                    const int32_t *status) {
+  int rc = check_desc(desc);
+  if (rc != BIA_OK) return rc;
+  if (batch <= 0 || !rows_host || !kvp_host || !last_host) return BIA_ERR_INVALID_ARG;
+  if (rows_host[0] != 0 || kvp_host[0] < 0) return BIA_ERR_INVALID_ARG;
+  for (int b = 0; b < batch; ++b) {
+    const int64_t n = static_cast<int64_t>(rows_host[b + 1]) - rows_host[b];
+    const int64_t pages = static_cast<int64_t>(kvp_host[b + 1]) - kvp_host[b];
+    if (n < 0 || pages < 0) return BIA_ERR_INVALID_ARG;
+    const int32_t last = last_host[b];
+    if (pages > 0 && (last < 1 || last > desc->page_size)) return BIA_ERR_INVALID_ARG;
+    const int64_t kv_len = pages > 0 ? (pages - 1) * desc->page_size + last : 0;
+    if (kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
+    if (n > kv_len) return BIA_ERR_INVALID_ARG;
+  }
+  const int64_t total = rows_host[batch];
+  if (misaligned(status, 4)) return BIA_ERR_INVALID_ARG;
+  if (total > 0) {
+    if (!k_rows || !v_rows || !k_cache || !v_cache || !k_scale || !v_scale || !row_indptr ||
+        !kv_indptr || !kv_indices || !kv_last_page_len || num_pages <= 0)
+      return BIA_ERR_INVALID_ARG;
+    if (misaligned(k_rows, 16) || misaligned(v_rows, 16) || misaligned(k_cache, 16) ||
+        misaligned(v_cache, 16) || misaligned(row_indptr, 4) || misaligned(kv_indptr, 4) ||
+        misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
+      return BIA_ERR_INVALID_ARG;
+    // one group of lanes per (token, head) row of K and of V
+    if (total * desc->num_kv_heads * 2 > INT32_MAX) return BIA_ERR_UNSUPPORTED;
+  }
+  if (total == 0) return status ? check_resident({{"status", status}}) : BIA_OK;
+  return check_resident({{"status", status},
+                         {"k rows", k_rows},
+                         {"v rows", v_rows},
+                         {"k_cache", k_cache},
+                         {"v_cache", v_cache},
+                         {"k_scale", k_scale},
+                         {"v_scale", v_scale},
+                         {"row indptr", row_indptr},
+                         {"kv_indptr", kv_indptr},
+                         {"kv_indices", kv_indices},
+                         {"kv_last_page_len", kv_last_page_len}});
+}
+
+int run_cache_fp8(bool append, const bia::CacheFp8Args &a, cudaStream_t st) {
+  if (a.status) {
+    const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), st);
+    if (e != cudaSuccess) return cuda_fail("status reset", e);
+  }
+  if (a.total == 0) return BIA_OK;
+  const cudaError_t e = bia::launch_cache_fp8(a, append, st);
+  if (e != cudaSuccess) return cuda_fail(append ? "append kernel launch" : "gather kernel launch", e);
+  __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  return BIA_OK;
+}
+
+bia::CacheFp8Args cache_fp8_args(const bia_attn_desc *desc, void *k_cache, void *v_cache,
+                                 void *k_scale, void *v_scale, int64_t num_pages,
+                                 const int32_t *row_indptr, const int32_t *kv_indptr,
+                                 const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                                 int64_t total, int32_t batch, int32_t *status) {
+  bia::CacheFp8Args a{};
+  a.k_codes = static_cast<uint8_t *>(k_cache);
+  a.v_codes = static_cast<uint8_t *>(v_cache);
+  a.k_scale = static_cast<uint8_t *>(k_scale);
+  a.v_scale = static_cast<uint8_t *>(v_scale);
+  a.row_indptr = row_indptr;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.kv_last_page_len = kv_last_page_len;
+  a.num_pages = num_pages;
+  a.total = total;
+  a.batch = batch;
+  a.Hkv = desc->num_kv_heads;
+  a.D = desc->head_dim;
+  a.page_size = desc->page_size;
+  a.status = status;
+  return a;
+}
+
+// A token stride (elements) of packed rows of `row` elements: 0 selects dense.
+int token_stride(int64_t given, int64_t row, int64_t *stride) {
+  *stride = given == 0 ? row : given;
+  if (*stride < row || *stride > (int64_t{1} << 38)) return BIA_ERR_INVALID_ARG;
+  return *stride % 8 == 0 ? BIA_OK : BIA_ERR_INVALID_ARG; // 16-byte rows
+}
+
+int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const void *q,
+                   const void *k_cache, const void *v_cache, const void *k_scale,
+                   const void *v_scale, int64_t num_pages, const int32_t *kv_indptr,
+                   const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                   const int32_t *kvp_host, const int32_t *last_host, int32_t batch,
+                   int32_t split, void *workspace, size_t workspace_bytes, void *out, float *lse,
+                   void *stream) {
+  int rc = check_desc(desc);
+  if (rc != BIA_OK) return rc;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !kv_indptr || !kv_indices ||
+      !kv_last_page_len || !out || !workspace || num_pages <= 0)
+    return BIA_ERR_INVALID_ARG;
+  if (misaligned(workspace, 256) || misaligned(q, 16) || misaligned(k_cache, 16) ||
+      misaligned(v_cache, 16) || misaligned(out, 16) || misaligned(lse, 4) ||
+      misaligned(kv_indptr, 4) || misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
+    return BIA_ERR_INVALID_ARG;
+  if (split == 0) split = BIA_DECODE_SPLIT;
+  HostPlan hp;
+  rc = bounds ? bounded_plan(bounds, batch, 1, split, 1, 1, 1, 0, true, &hp)
+              : host_plan(desc, nullptr, kvp_host, last_host, batch, 1, split, 1, 1, 1, 0, &hp);
+  if (rc != BIA_OK) return rc;
+  if (hp.n_units * desc->num_kv_heads > INT32_MAX) return BIA_ERR_UNSUPPORTED;
+  const WsLayout w = bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows,
+                                      desc->num_qo_heads, desc->head_dim);
+  if (workspace_bytes < w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
+  rc = check_resident({{"q", q},
+                       {"k_cache", k_cache},
+                       {"v_cache", v_cache},
+                       {"k_scale", k_scale},
+                       {"v_scale", v_scale},
+                       {"out", out},
+                       {"lse", lse},
+                       {"kv_indptr", kv_indptr},
+                       {"kv_indices", kv_indices},
+                       {"kv_last_page_len", kv_last_page_len},
+                       {"workspace", workspace}});
+  if (rc != BIA_OK) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  PlanArgs pa{};
+  pa.kv_indptr = kv_indptr;
+  pa.kv_last_page_len = kv_last_page_len;
+  pa.batch = batch;
+  pa.page_size = desc->page_size;
+  pa.tile_tokens = pa.tiles_per_unit = pa.ctas = pa.causal = 1;
+  pa.split = split;
+  pa.bounded = bounds ? 1 : 0;
+  if (bounds) {
+    pa.max_q_len = 1;
+    pa.max_kv_len = bounds->max_kv_len;
+    pa.max_total_q = hp.total_q;
+  }
+  pa.n_groups_expected = hp.n_groups;
+  pa.n_units_expected = hp.n_units;
+  pa.part_rows_expected = hp.part_rows;
+  pa.out = static_cast<uint16_t *>(out);
+  pa.out_elems = hp.total_q * desc->num_qo_heads * desc->head_dim;
+  pa.lse = lse;
+  pa.lse_elems = hp.total_q * desc->num_qo_heads;
+  pa.status = reinterpret_cast<int32_t *>(ws + w.status);
+  pa.reqs = reinterpret_cast<bia::ReqInfo *>(ws + w.reqs);
+  pa.group_off = reinterpret_cast<int32_t *>(ws + w.group_off);
+  pa.group_cnt = reinterpret_cast<int32_t *>(ws + w.group_cnt);
+  pa.units = reinterpret_cast<bia::Unit *>(ws + w.units);
+  pa.sunits = reinterpret_cast<bia::Unit *>(ws + w.sunits);
+  cudaError_t e = bia::launch_plan(pa, st);
+  if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
+  __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+
+  bia::DecodeFp8Args f{};
+  AttnArgs &a = f.a;
+  a.q = static_cast<const uint16_t *>(q);
+  a.kv_indices = kv_indices;
+  a.num_pages = num_pages;
+  a.Hq = desc->num_qo_heads;
+  a.Hkv = desc->num_kv_heads;
+  a.D = desc->head_dim;
+  a.G = desc->num_qo_heads / desc->num_kv_heads;
+  a.page_shift = log2i(desc->page_size);
+  a.causal = 1;
+  a.split = split;
+  a.tile_tokens = 1;
+  a.scale_log2 = effective_scale(desc);
+  a.batch = batch;
+  a.n_units = hp.n_units;
+  a.reqs = pa.reqs;
+  a.units = pa.units;
+  a.part_o = reinterpret_cast<float *>(ws + w.part_o);
+  a.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
+  a.total_rows = hp.total_q;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.status = pa.status;
+  f.k_codes = static_cast<const uint8_t *>(k_cache);
+  f.v_codes = static_cast<const uint8_t *>(v_cache);
+  f.k_scale = static_cast<const uint8_t *>(k_scale);
+  f.v_scale = static_cast<const uint8_t *>(v_scale);
+  const bool profile = g_attn_begin != nullptr && g_attn_end != nullptr;
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_begin, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  e = bia::launch_decode_fp8(f, st);
+  if (e != cudaSuccess) return cuda_fail("8-bit decode kernel launch", e);
+  __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_end, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  if (hp.part_rows > 0) {
+    e = bia::launch_merge_partials(a, st);
+    if (e != cudaSuccess) return cuda_fail("merge kernel launch", e);
+    __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  }
+  return BIA_OK;
+}
+
+size_t decode_fp8_workspace(const bia_attn_desc *desc, const bia_bounds *bounds,
+                            const int32_t *kvp_host, const int32_t *last_host, int32_t batch,
+                            int32_t split) {
+  if (check_desc(desc) != BIA_OK) return 0;
+  if (split == 0) split = BIA_DECODE_SPLIT;
+  HostPlan hp;
+  const int rc =
+      bounds ? bounded_plan(bounds, batch, 1, split, 1, 1, 1, 0, true, &hp)
+             : host_plan(desc, nullptr, kvp_host, last_host, batch, 1, split, 1, 1, 1, 0, &hp);
+  if (rc != BIA_OK) return 0;
+  return bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows, desc->num_qo_heads,
+                          desc->head_dim)
+      .total;
+}
+
+// Packed keys: the descriptor with its page size (not used) replaced by 1.
+int ragged_plan(const bia_attn_desc *desc, const int32_t *qo_host, const int32_t *kv_host,
+                int32_t batch, int32_t causal, int32_t split, bia_attn_desc *d, HostPlan *hp) {
+  if (!desc || !qo_host || !kv_host) return BIA_ERR_INVALID_ARG;
+  *d = *desc;
+  d->page_size = 1;
+  const int rc = check_desc(d);
+  if (rc != BIA_OK) return rc;
+  if (kv_host[0] != 0) return BIA_ERR_INVALID_ARG;
+  return host_plan(d, qo_host, kv_host, nullptr, batch, causal, split,
+                   bia::kTileRows / (d->num_qo_heads / d->num_kv_heads),
+                   bia::ragged_tiles_per_unit(d->head_dim), bia::ragged_ctas(d->head_dim), 0, hp);
+}
+} // namespace
+
+int bia_append_paged_kv_fp8(const bia_attn_desc *desc, const void *k_new, const void *v_new,
+                            int64_t k_stride, int64_t v_stride, void *k_cache, void *v_cache,
+                            void *k_scale, void *v_scale, int64_t num_pages,
+                            const int32_t *append_indptr, const int32_t *kv_indptr,
+                            const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                            const int32_t *append_indptr_host, const int32_t *kv_indptr_host,
+                            const int32_t *kv_last_page_len_host, int32_t batch, int32_t *status,
+                            void *stream) {
+  int rc = check_cache_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_scale, num_pages,
+                           append_indptr, kv_indptr, kv_indices, kv_last_page_len,
+                           append_indptr_host, kv_indptr_host, kv_last_page_len_host, batch,
+                           status);
+  if (rc != BIA_OK) return rc;
+  bia::CacheFp8Args a = cache_fp8_args(desc, k_cache, v_cache, k_scale, v_scale, num_pages,
+                                       append_indptr, kv_indptr, kv_indices, kv_last_page_len,
+                                       append_indptr_host[batch], batch, status);
+  a.k_rows = k_new;
+  a.v_rows = v_new;
+  const int64_t row = static_cast<int64_t>(a.Hkv) * a.D;
+  rc = token_stride(k_stride, row, &a.k_stride);
+  if (rc == BIA_OK) rc = token_stride(v_stride, row, &a.v_stride);
+  if (rc != BIA_OK) return rc;
+  return run_cache_fp8(true, a, static_cast<cudaStream_t>(stream));
+}
+
+int bia_gather_paged_kv_fp8(const bia_attn_desc *desc, const void *k_cache, const void *v_cache,
+                            const void *k_scale, const void *v_scale, int64_t num_pages,
+                            const int32_t *out_indptr, const int32_t *kv_indptr,
+                            const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                            const int32_t *out_indptr_host, const int32_t *kv_indptr_host,
+                            const int32_t *kv_last_page_len_host, int32_t batch, void *k_out,
+                            void *v_out, int32_t *status, void *stream) {
+  const int rc = check_cache_fp8(desc, k_out, v_out, k_cache, v_cache, k_scale, v_scale,
+                                 num_pages, out_indptr, kv_indptr, kv_indices, kv_last_page_len,
+                                 out_indptr_host, kv_indptr_host, kv_last_page_len_host, batch,
+                                 status);
+  if (rc != BIA_OK) return rc;
+  bia::CacheFp8Args a =
+      cache_fp8_args(desc, const_cast<void *>(k_cache), const_cast<void *>(v_cache),
+                     const_cast<void *>(k_scale), const_cast<void *>(v_scale), num_pages,
+                     out_indptr, kv_indptr, kv_indices, kv_last_page_len, out_indptr_host[batch],
+                     batch, status);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  return run_cache_fp8(false, a, static_cast<cudaStream_t>(stream));
+}
+
+int bia_decode_paged_fp8(const bia_attn_desc *desc, const void *q, const void *k_cache,
+                         const void *v_cache, const void *k_scale, const void *v_scale,
+                         int64_t num_pages, const int32_t *kv_indptr, const int32_t *kv_indices,
+                         const int32_t *kv_last_page_len, const int32_t *kv_indptr_host,
+                         const int32_t *kv_last_page_len_host, int32_t batch, int32_t split_size,
+                         void *workspace, size_t workspace_bytes, void *out, float *lse,
+                         void *stream) {
+  return run_decode_fp8(desc, nullptr, q, k_cache, v_cache, k_scale, v_scale, num_pages,
+                        kv_indptr, kv_indices, kv_last_page_len, kv_indptr_host,
+                        kv_last_page_len_host, batch, split_size, workspace, workspace_bytes,
+                        out, lse, stream);
+}
+
+size_t bia_decode_fp8_workspace_size(const bia_attn_desc *desc, const int32_t *kv_indptr_host,
+                                     const int32_t *kv_last_page_len_host, int32_t batch,
+                                     int32_t split_size) {
+  return decode_fp8_workspace(desc, nullptr, kv_indptr_host, kv_last_page_len_host, batch,
+                              split_size);
+}
+
+int bia_decode_paged_fp8_bounded(const bia_attn_desc *desc, const bia_bounds *bounds,
+                                 const void *q, const void *k_cache, const void *v_cache,
+                                 const void *k_scale, const void *v_scale, int64_t num_pages,
+                                 const int32_t *kv_indptr, const int32_t *kv_indices,
+                                 const int32_t *kv_last_page_len, int32_t batch,
+                                 int32_t split_size, void *workspace, size_t workspace_bytes,
+                                 void *out, float *lse, void *stream) {
+  if (!bounds) return BIA_ERR_INVALID_ARG;
+  return run_decode_fp8(desc, bounds, q, k_cache, v_cache, k_scale, v_scale, num_pages, kv_indptr,
+                        kv_indices, kv_last_page_len, nullptr, nullptr, batch, split_size,
+                        workspace, workspace_bytes, out, lse, stream);
+}
+
+size_t bia_decode_fp8_bounded_workspace_size(const bia_attn_desc *desc, const bia_bounds *bounds,
+                                             int32_t batch, int32_t split_size) {
+  if (!bounds) return 0;
+  return decode_fp8_workspace(desc, bounds, nullptr, nullptr, batch, split_size);
+}
+
+int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, const void *v,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                       const int32_t *qo_indptr, const int32_t *kv_indptr,
+                       const int32_t *qo_indptr_host, const int32_t *kv_indptr_host,
+                       int32_t batch, int32_t causal, int32_t split_size, void *workspace,
+                       size_t workspace_bytes, void *out, float *lse, void *stream) {
+  causal = causal ? 1 : 0;
+  if (split_size == 0) split_size = BIA_PREFILL_SPLIT;
+  if (!q || !qo_indptr || !kv_indptr || !out || !workspace) return BIA_ERR_INVALID_ARG;
+  if (misaligned(workspace, 256) || misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) ||
+      misaligned(out, 16) || misaligned(lse, 4) || misaligned(qo_indptr, 4) ||
+      misaligned(kv_indptr, 4))
+    return BIA_ERR_INVALID_ARG;
+  bia_attn_desc d;
+  HostPlan hp;
+  int rc = ragged_plan(desc, qo_indptr_host, kv_indptr_host, batch, causal, split_size, &d, &hp);
+  if (rc != BIA_OK) return rc;
+  const int D = d.head_dim, Hq = d.num_qo_heads, Hkv = d.num_kv_heads, G = Hq / Hkv;
+  rc = token_stride(q_stride, static_cast<int64_t>(Hq) * D, &q_stride);
+  if (rc == BIA_OK) rc = token_stride(k_stride, static_cast<int64_t>(Hkv) * D, &k_stride);
+  if (rc == BIA_OK) rc = token_stride(v_stride, static_cast<int64_t>(Hkv) * D, &v_stride);
+  if (rc != BIA_OK) return rc;
+  const WsLayout w =
+      bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows, Hq, D);
+  if (workspace_bytes < w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
+  if (hp.total_q == 0) return BIA_OK;
+  const int64_t total_kv = kv_indptr_host[batch];
+  if (total_kv > 0 && (!k || !v)) return BIA_ERR_INVALID_ARG;
+  rc = check_resident({{"q", q},
+                       {"k", k},
+                       {"v", v},
+                       {"out", out},
+                       {"lse", lse},
+                       {"qo_indptr", qo_indptr},
+                       {"kv_indptr", kv_indptr},
+                       {"workspace", workspace}});
+  if (rc != BIA_OK) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  PlanArgs pa{};
+  pa.qo_indptr = qo_indptr;
+  pa.kv_indptr = kv_indptr;
+  pa.batch = batch;
+  pa.page_size = 1;
+  pa.tile_tokens = bia::kTileRows / G;
+  pa.tiles_per_unit = bia::ragged_tiles_per_unit(D);
+  pa.ctas = bia::ragged_ctas(D);
+  pa.causal = causal;
+  pa.split = split_size;
+  pa.n_groups_expected = hp.n_groups;
+  pa.n_units_expected = hp.n_units;
+  pa.part_rows_expected = hp.part_rows;
+  pa.out = static_cast<uint16_t *>(out);
+  pa.out_elems = hp.total_q * Hq * D;
+  pa.lse = lse;
+  pa.lse_elems = hp.total_q * Hq;
+  pa.status = reinterpret_cast<int32_t *>(ws + w.status);
+  pa.reqs = reinterpret_cast<bia::ReqInfo *>(ws + w.reqs);
+  pa.group_off = reinterpret_cast<int32_t *>(ws + w.group_off);
+  pa.group_cnt = reinterpret_cast<int32_t *>(ws + w.group_cnt);
+  pa.units = reinterpret_cast<bia::Unit *>(ws + w.units);
+  pa.sunits = reinterpret_cast<bia::Unit *>(ws + w.sunits);
+  cudaError_t e = bia::launch_plan(pa, st);
+  if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
+  __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+
+  AttnArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.qo_indptr = qo_indptr;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.G = G;
+  a.causal = causal;
+  a.split = split_size;
+  a.tile_tokens = pa.tile_tokens;
+  a.scale_log2 = effective_scale(&d);
+  a.batch = batch;
+  a.n_units = hp.n_units;
+  a.reqs = pa.reqs;
+  a.units = pa.units;
+  a.part_o = reinterpret_cast<float *>(ws + w.part_o);
+  a.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
+  a.total_rows = hp.total_q;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.status = pa.status;
+  a.kv_rows = static_cast<int32_t>(total_kv);
+  int ce = encode_packed_map(&a.tm_q, q, hp.total_q, Hq, D, q_stride, G, pa.tile_tokens);
+  if (total_kv > 0) { // without keys no unit reads a block
+    if (D == 256) {
+      if (ce == 0) ce = encode_packed_rows_map(&a.tm_k, k, total_kv, Hkv, D, k_stride);
+      if (ce == 0) ce = encode_packed_rows_map(&a.tm_v, v, total_kv, Hkv, D, v_stride);
+      if (ce == 0) ce = encode_packed_map(&a.tm_k3, k, total_kv, Hkv, D, k_stride, 1, 16);
+      if (ce == 0) ce = encode_packed_map(&a.tm_v3, v, total_kv, Hkv, D, v_stride, 1, 16);
+    } else {
+      if (ce == 0) ce = encode_packed_map(&a.tm_k, k, total_kv, Hkv, D, k_stride, 1, bia::kKvBlock);
+      if (ce == 0) ce = encode_packed_map(&a.tm_v, v, total_kv, Hkv, D, v_stride, 1, bia::kKvBlock);
+    }
+  }
+  if (ce != 0) return fail(BIA_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable", ce);
+  const bool profile = g_attn_begin != nullptr && g_attn_end != nullptr;
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_begin, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  e = D == 256 ? bia::launch_prefill_ragged_wide(a, st) : bia::launch_prefill_ragged(a, st);
+  if (e != cudaSuccess) return cuda_fail("packed prefill kernel launch", e);
+  if (hp.n_units > 0) __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_end, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  if (hp.part_rows > 0) {
+    e = bia::launch_merge_partials(a, st);
+    if (e != cudaSuccess) return cuda_fail("merge kernel launch", e);
+    __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  }
+  return BIA_OK;
+}
+
+size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc, const int32_t *qo_indptr_host,
+                                         const int32_t *kv_indptr_host, int32_t batch,
+                                         int32_t causal, int32_t split_size) {
+  if (split_size == 0) split_size = BIA_PREFILL_SPLIT;
+  bia_attn_desc d;
+  HostPlan hp;
+  if (ragged_plan(desc, qo_indptr_host, kv_indptr_host, batch, causal ? 1 : 0, split_size, &d,
+                  &hp) != BIA_OK)
+    return 0;
+  return bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows, d.num_qo_heads,
+                          d.head_dim)
+      .total;
+}
+
+} // extern "C"
 
 extern "C" {
 

@@ -173,7 +173,7 @@ inline WsLayout make_layout(int batch, int64_t n_groups, int64_t n_units, int64_
 struct PlanArgs {
   const int32_t *qo_indptr;  // NULL for decode (one token per request)
   const int32_t *kv_indptr;
-  const int32_t *kv_last_page_len;
+  const int32_t *kv_last_page_len; // NULL: every page is full (packed keys, page_size 1)
   int32_t batch, page_size, tile_tokens, tiles_per_unit, ctas, causal, split;
   int32_t stream; // 1: single-token tail tiles become streamed units (prefill)
   // 0: the launch was sized from the host mirrors and the device plan must
@@ -247,6 +247,28 @@ struct AppendArgs {
   int32_t *status; // may be NULL
 };
 
+// Rows of the 8-bit paged cache (fp8.cuh): token t of request b is row
+// t - row_indptr[b] of its last (append) or first (gather) rows.
+struct CacheFp8Args {
+  const void *k_rows, *v_rows;  // append: bf16 [total, Hkv, D], token strides below
+  int64_t k_stride, v_stride;   // elements between tokens of k_rows / v_rows
+  void *k_out, *v_out;          // gather: bf16 [total, Hkv, D], dense
+  uint8_t *k_codes, *v_codes;   // e4m3 [num_pages, page_size, Hkv, D]
+  uint8_t *k_scale, *v_scale;   // e8m0 [num_pages, page_size, Hkv]
+  const int32_t *row_indptr, *kv_indptr, *kv_indices, *kv_last_page_len;
+  int64_t num_pages, total;
+  int32_t batch, Hkv, D, page_size;
+  int32_t *status; // may be NULL
+};
+
+// Decode over the 8-bit paged cache: the geometry of the bf16 decode (the
+// cache pointers of `a` unused) and the codes and scales.
+struct DecodeFp8Args {
+  AttnArgs a;
+  const uint8_t *k_codes, *v_codes; // e4m3 [num_pages, page_size, Hkv, D]
+  const uint8_t *k_scale, *v_scale; // e8m0 [num_pages, page_size, Hkv]
+};
+
 // The decode of bia_decode_paged split in two for the static-scratch entry
 // point: decode_check runs every host-side check of the call and reports the
 // workspace bytes it needs (*need), enqueuing nothing; decode_on_scratch runs
@@ -283,6 +305,15 @@ bool decode_tc_supported(const AttnArgs &a);
 cudaError_t launch_decode_tc(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s); // head_dim 256
+cudaError_t launch_cache_fp8(const CacheFp8Args &a, bool append, cudaStream_t s);
+cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s);
+// Packed keys and values: head_dim 64, 96 and 128; 256
+cudaError_t launch_prefill_ragged(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s);
+inline int ragged_tiles_per_unit(int head_dim) {
+  return head_dim == 256 ? 1 : kPrefillTilesPerUnit;
+}
+inline int ragged_ctas(int head_dim) { return head_dim == 256 ? kPrefillClusterCtas : 1; }
 cudaError_t launch_mla_decode(const AttnArgs &a, cudaStream_t s);
 // q heads per CTA of the MLA kernel: 32 when the head count is a multiple of
 // 32, else 16 (the q tensor map's boxes are this many rows high)

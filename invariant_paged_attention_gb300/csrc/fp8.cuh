@@ -1,0 +1,56 @@
+// The number formats of the 8-bit paged cache: e4m3 codes and one e8m0
+// (power-of-two) scale per (key, kv head) row.
+//
+//   e = the smallest integer >= kMinRowExp with amax(row) <= 448 * 2^e
+//   code_d = e4m3(x_d * 2^-e)  (nearest even)      scale byte = e + 127
+//   value_d = code_d * 2^e
+//
+// A power of two costs a floating code no accuracy (scaling by it is exact),
+// takes one byte a row, and makes the value exact in bf16: a code has 4
+// significant bits, and with e >= -120 its last place (2^(e-9)) is at least
+// bf16's smallest subnormal.  A row's codes and scale depend on that row
+// alone, so what a cache holds never depends on batch, page or chunk.
+#pragma once
+
+#include <cstdint>
+
+namespace bia {
+
+constexpr int kMinRowExp = -120;
+constexpr uint32_t kBf16Inf = 0x7f80u; // |x| bits of an infinity; above it NaN
+
+// Row exponent from the largest finite magnitude (>= 0): 448 = 1.75 * 2^8.
+__device__ __forceinline__ int row_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int ex = static_cast<int>(b >> 23) - 127; // subnormals and zero: below the clamp
+  const int e = (b & 0x7fffffu) <= 0x600000u ? ex - 8 : ex - 7;
+  return max(e, kMinRowExp);
+}
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float exp2_int(int e) {
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+// Value of an e8m0 byte: 2^(b - 127); 255 is NaN, 0 the subnormal 2^-127.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  const uint32_t bits = b == 0 ? 0x00400000u : b == 255u ? 0x7fc00000u : b << 23;
+  return __uint_as_float(bits);
+}
+// Two fp32 -> two e4m3 codes (nearest even, saturating; NaN stays NaN), first
+// argument in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 codes -> two fp32, exactly.
+__device__ __forceinline__ void e4m3x2_values(uint32_t codes, float &lo, float &hi) {
+  asm("{\n\t.reg .b32 h;\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %2;\n\t"
+      "mov.b32 {a, b}, h;\n\t"
+      "cvt.f32.f16 %0, a;\n\t"
+      "cvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "h"(static_cast<uint16_t>(codes)));
+}
+
+} // namespace bia

@@ -18,6 +18,7 @@
 // TMEM), 5 TMA producer.  Like prefill.cu, four CTAs form a cluster over
 // consecutive q tiles of one request, kv head and split, each gathering a
 // quarter of every K/V block's rows (gather4) multicast into all four rings.
+// RAGGED: the keys are packed rows (prefill_ragged.cu) instead of pages.
 #include "bia_internal.h"
 #include "ptx.cuh"
 #include "softmax_rows.cuh"
@@ -50,7 +51,7 @@ struct SmemW {
   static_assert(kAlloc <= 232448, "shared memory per block");
 };
 
-template <bool MASK>
+template <bool MASK, bool RAGGED>
 __global__ void __launch_bounds__(kThreadsW, 1)
     prefill_wide_kernel(const __grid_constant__ AttnArgs a) {
   using L = SmemW;
@@ -143,11 +144,12 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     const bool issues = hh < kD / 64;
     const int32_t row0 = (kKB / kCtasW) * static_cast<int32_t>(rank) + 4 * rg;
     const uint32_t dst_off = static_cast<uint32_t>(hh * kAtomKV + (row0 / 4) * 512);
+    const int32_t x0 = RAGGED ? kvh * kD : 0; // column of the head in a gathered row
     auto fetch = [&](int j, int32_t (&pg)[4]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int32_t key = key_begin + j * kKB + row0 + i;
-        pg[i] = (j < n_blocks && key < r.kv_len)
+        pg[i] = (!RAGGED && j < n_blocks && key < r.kv_len)
                     ? __ldg(a.kv_indices + r.page_base + (key >> a.page_shift)) : -1;
       }
     };
@@ -161,7 +163,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         const int32_t key = key_begin + j * kKB + row0 + i;
         rows[i] = a.kv_rows; // outside the map: zeros
         if (key < r.kv_len) {
-          if (pg[i] < 0 || pg[i] >= a.num_pages)
+          if (RAGGED) // packed keys: a row is a token, the head a column offset
+            rows[i] = r.page_base + key;
+          else if (pg[i] < 0 || pg[i] >= a.num_pages)
             atomicOr(a.status, kStatusBadPage);
           else
             rows[i] = ((pg[i] << a.page_shift) + (key & page_mask)) * a.Hkv + kvh;
@@ -174,9 +178,10 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       // bounds this kernel); otherwise the rows are gathered one by one.
       const int32_t kb = key_begin + j * kKB + (kKB / kCtasW) * static_cast<int32_t>(rank);
       const int32_t pg0 = __shfl_sync(0xffffffffu, pg[0], 0); // lane 0 holds key kb's page
-      const bool tiled = a.page_shift >= 4 && kb + kKB / kCtasW <= r.kv_len && pg0 >= 0 &&
-                         pg0 < a.num_pages;
-      const int32_t slot0 = (pg0 << a.page_shift) + (kb & page_mask);
+      // (packed keys: consecutive rows, tiled unless they pass the last key)
+      const bool tiled = kb + kKB / kCtasW <= r.kv_len &&
+                         (RAGGED || (a.page_shift >= 4 && pg0 >= 0 && pg0 < a.num_pages));
+      const int32_t slot0 = RAGGED ? r.page_base + kb : (pg0 << a.page_shift) + (kb & page_mask);
       const uint32_t tile_off = static_cast<uint32_t>(lane * kAtomKV + (kb - key_begin - j * kKB) * 128);
       fetch(j + 1, pg);
       bool ok = j < 2 || mbar_wait(bar(L::kKEmpty + st), ((j >> 1) - 1) & 1, a.status);
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           tma_load_3d_mc(sK(st) + tile_off, &a.tm_k3, 64 * lane, kvh, slot0, bar(L::kKFull + st),
                          kMaskW);
       } else if (issues) {
-        tma_gather4_mc(sK(st) + dst_off, &a.tm_k, 64 * hh, rows[0], rows[1], rows[2], rows[3],
+        tma_gather4_mc(sK(st) + dst_off, &a.tm_k, x0 + 64 * hh, rows[0], rows[1], rows[2], rows[3],
                        bar(L::kKFull + st), kMaskW);
       }
       ok = j < 2 || mbar_wait(bar(L::kVEmpty + st), ((j >> 1) - 1) & 1, a.status);
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           tma_load_3d_mc(sV(st) + tile_off, &a.tm_v3, 64 * lane, kvh, slot0, bar(L::kVFull + st),
                          kMaskW);
       } else if (issues) {
-        tma_gather4_mc(sV(st) + dst_off, &a.tm_v, 64 * hh, rows[0], rows[1], rows[2], rows[3],
+        tma_gather4_mc(sV(st) + dst_off, &a.tm_v, x0 + 64 * hh, rows[0], rows[1], rows[2], rows[3],
                        bar(L::kVFull + st), kMaskW);
       }
     }
@@ -426,11 +431,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   }
 }
 
-template <bool MASK>
+template <bool MASK, bool RAGGED>
 cudaError_t launch_wide(const AttnArgs &a, cudaStream_t s) {
   static bool configured = false;
   if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_wide_kernel<MASK>,
+    cudaError_t e = cudaFuncSetAttribute(prefill_wide_kernel<MASK, RAGGED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          SmemW::kAlloc);
     if (e != cudaSuccess) return e;
@@ -449,7 +454,7 @@ cudaError_t launch_wide(const AttnArgs &a, cudaStream_t s) {
   attr[1] = chained_launch_attr();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, prefill_wide_kernel<MASK>, a);
+  return cudaLaunchKernelEx(&cfg, prefill_wide_kernel<MASK, RAGGED>, a);
 }
 
 } // namespace
@@ -457,7 +462,13 @@ cudaError_t launch_wide(const AttnArgs &a, cudaStream_t s) {
 cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s) {
   if (a.n_units == 0) return cudaSuccess;
   if (a.n_units % kCtasW != 0) return cudaErrorInvalidValue; // the planner groups every unit
-  return a.mask ? launch_wide<true>(a, s) : launch_wide<false>(a, s);
+  return a.mask ? launch_wide<true, false>(a, s) : launch_wide<false, false>(a, s);
+}
+
+cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s) {
+  if (a.n_units == 0) return cudaSuccess;
+  if (a.n_units % kCtasW != 0) return cudaErrorInvalidValue;
+  return launch_wide<false, true>(a, s);
 }
 
 } // namespace bia

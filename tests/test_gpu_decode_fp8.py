@@ -1,0 +1,246 @@
+"""Decode over the 8-bit paged cache against 64 bits, and its invariance."""
+import pytest
+import torch
+
+import invariant_paged_attention_gb300 as bia
+from tests import fp8_util as fu
+from tests.gpu_util import same_bits
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+# weights below 2^-12 of the largest lie under the second 8-bit term's last
+# place: off by at most half of 2^-19 of the largest weight, taken at the
+# largest value scale of the request (the sum |v| of the bound is taken there)
+FLOOR = 2.0 ** -19
+
+
+class Batch:
+    def __init__(self, lens, hq, hkv, d, page, seed=0, seeds=None, spread=1.0):
+        self.lens, self.page, self.hq = lens, page, hq
+        self.desc = bia.make_desc(hq, hkv, d, page)
+        self.indptr, self.idx, self.last, self.pages, total = fu.page_table(lens, page, seed)
+        rk, rv, q = [], [], []
+        for b, n in enumerate(lens):
+            g = torch.Generator(device=DEV).manual_seed(1000 + (seeds[b] if seeds else b))
+            rk.append((fu.rows((n, hkv, d), g).float() * spread).bfloat16())
+            rv.append(fu.rows((n, hkv, d), g))
+            q.append(fu.rows((1, hq, d), g))
+        self.cache = fu.make_cache(rk, rv, self.pages, page, total)
+        self.q = torch.cat(q)
+
+    def dev(self):
+        return self.indptr.to(DEV), self.idx.to(DEV), self.last.to(DEV)
+
+    def decode(self, split=0, lse=True, stream=None):
+        ws = torch.empty(bia.bia_decode_fp8_workspace_size(self.desc, self.indptr, self.last, split),
+                         dtype=torch.uint8, device=DEV)
+        out = torch.full_like(self.q, float("nan"))
+        l = torch.full(self.q.shape[:2], float("nan"), device=DEV) if lse else None
+        bia.bia_decode_paged_fp8(self.desc, self.q, *self.cache, *self.dev(), self.indptr, self.last,
+                                 ws, out, l, split_size=split, stream=stream)
+        assert bia.bia_read_status(ws, stream) == 0
+        return out, l
+
+    def rows_of(self, b):
+        kc, vc, ks, vs = self.cache
+        p = torch.arange(self.lens[b])
+        s = (self.pages[b].long()[p // self.page] * self.page + p % self.page).to(DEV)
+        hkv, d = kc.shape[2:]
+        take = lambda c, e: fu.cache_values(c.view(torch.uint8).view(-1, hkv, d)[s].view(fu.E4M3),
+                                            e.view(torch.uint8).view(-1, hkv)[s])
+        return take(kc, ks), take(vc, vs)
+
+    def check(self, out, lse):
+        for b in range(len(self.lens)):
+            k, v = self.rows_of(b)
+            # the floor is a share of the largest value scale: every |v| of a
+            # dim counts as that of the row with the largest scale
+            want = fu.attention_bounds(self.q[b:b + 1], k, v, floor=FLOOR)
+            big = v.abs().amax(-1, keepdim=True).amax(0, keepdim=True)  # [1, Hkv, 1]
+            big = big.repeat_interleave(self.hq // big.shape[1], 1)
+            p_max = torch.exp(self.p_top(b, k) - want[2])  # largest weight of each head
+            tol = want[1] + FLOOR * self.lens[b] * p_max[..., None] * big * 2
+            fu.check(out[b:b + 1], lse[b:b + 1], want[0], tol, want[2], want[3])
+
+    def p_top(self, b, k):
+        kh = k.repeat_interleave(self.hq // k.shape[1], 1)
+        x = torch.einsum("qhd,khd->qhk", self.q[b:b + 1].double(), kh) * self.q.shape[-1] ** -0.5
+        return x.amax(-1)
+
+
+LENS = [1, 2, 127, 128, 129, 255, 300, 2047, 2048, 2049, 5000]
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2), (8, 2), (16, 2), (32, 8)])
+def test_decode_against_64_bits(d, hq, hkv):
+    b = Batch(LENS, hq, hkv, d, 16, seed=d + hq)
+    b.check(*b.decode())
+
+
+@pytest.mark.parametrize("page", [1, 2, 32, 256])
+def test_decode_at_every_page_size(page):
+    b = Batch([1, 300, 130, 4097], 16, 4, 128, page, seed=page)
+    out, lse = b.decode()
+    b.check(out, lse)
+    other = Batch([1, 300, 130, 4097], 16, 4, 128, 16, seed=3)
+    o2, l2 = other.decode()
+    assert same_bits(out, o2) and same_bits(lse, l2)  # pages do not enter the bits
+
+
+@pytest.mark.parametrize("split", [128, 384, 2048, 4096])
+def test_decode_with_other_splits(split):
+    b = Batch([1, 384, 385, 3001], 8, 2, 128, 16, seed=split)
+    b.check(*b.decode(split))
+
+
+def test_steep_and_flat_scores():
+    for spread in (1e-3, 8.0, 60.0):
+        b = Batch([700, 2500], 8, 2, 128, 16, seed=4, spread=spread)
+        b.check(*b.decode())
+
+
+def test_a_request_has_its_bits_in_any_batch():
+    lens = [2049, 77, 6000, 1]
+    whole = Batch(lens, 16, 2, 128, 16, seed=1, seeds=[5, 6, 7, 8])
+    out, lse = whole.decode()
+    many = Batch([300] * 40 + lens[::-1], 16, 2, 128, 8, seed=2,
+                 seeds=list(range(20, 60)) + [8, 7, 6, 5])
+    o2, l2 = many.decode()
+    assert same_bits(o2[-4:].flip(0), out) and same_bits(l2[-4:].flip(0), lse)
+    for b, s in enumerate([5, 6, 7, 8]):
+        o1, l1 = Batch([lens[b]], 16, 2, 128, 1, seed=b, seeds=[s]).decode()
+        assert same_bits(o1, out[b:b + 1]) and same_bits(l1, lse[b:b + 1])
+
+
+def test_decode_twice_and_without_lse():
+    b = Batch([4097, 100, 2500], 32, 8, 128, 16)
+    out, lse = b.decode()
+    again, l2 = b.decode()
+    assert same_bits(out, again) and same_bits(lse, l2)
+    assert same_bits(b.decode(lse=False)[0], out)
+
+
+def test_a_dead_key_or_value_shows_only_where_it_reaches():
+    b = Batch([300, 200], 8, 2, 128, 16)
+    out, lse = b.decode()
+    kc, vc, ks, vs = [t.view(torch.uint8) for t in b.cache]
+    # request 0, key 20: a NaN in dim 7 of kv head 1's value row
+    page = int(b.pages[0][1])
+    vc[page, 4, 1, 7] = 0x7F
+    o2, l2 = b.decode()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, 4:, 7] = True
+    assert torch.isnan(o2[hit]).all() and torch.equal(o2[~hit], out[~hit]) and same_bits(l2, lse)
+    # and a NaN in a key row of kv head 0: its four heads are NaN
+    kc[page, 4, 0, 9] = 0xFF
+    o3, l3 = b.decode()
+    assert torch.isnan(o3[0, :4]).all() and torch.isnan(l3[0, :4]).all()
+    assert torch.equal(o3[1], out[1]) and torch.equal(l3[0, 4:], lse[0, 4:])
+
+
+def test_a_bad_page_reads_as_zeros_and_is_reported():
+    b = Batch([100, 60], 8, 2, 128, 16)
+    b.idx[2] = 1 << 20  # request 0, keys 32..47
+    indptr, idx, last = b.dev()
+    ws = torch.empty(bia.bia_decode_fp8_workspace_size(b.desc, b.indptr, b.last),
+                     dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=DEV)
+    bia.bia_decode_paged_fp8(b.desc, b.q, *b.cache, indptr, idx, last, b.indptr, b.last, ws, out, lse)
+    assert bia.bia_read_status(ws) == 1
+    k, v = b.rows_of(0)
+    k[32:48], v[32:48] = 0, 0
+    want = fu.attention_bounds(b.q[:1], k, v, floor=FLOOR * 200)
+    fu.check(out[:1], lse[:1], *want)
+
+
+def test_bounded_decode_replays_in_a_graph_with_the_exact_bits():
+    lens = [2040, 5, 130, 4090]
+    b = Batch([n + 12 for n in lens], 32, 8, 128, 16)
+    bounds = bia.make_bounds(max_kv_len=5000)
+    ws = torch.empty(bia.bia_decode_fp8_bounded_workspace_size(b.desc, bounds, 4),
+                     dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=DEV)
+    indptr, idx, last = b.dev()
+
+    def table(now):  # the same pages, `now` keys of each request visible
+        count = [-(-n // 16) for n in now]
+        ip = fu.indptr_of(count)
+        ids = torch.cat([b.pages[i][:c] for i, c in enumerate(count)])
+        la = torch.tensor([n - (c - 1) * 16 for n, c in zip(now, count)], dtype=torch.int32)
+        return ip, ids, la
+
+    def put(now):
+        ip, ids, la = table(now)
+        indptr.copy_(ip)
+        idx[:len(ids)].copy_(ids)
+        last.copy_(la)
+
+    put(lens)
+    call = lambda: bia.bia_decode_paged_fp8_bounded(b.desc, bounds, b.q, *b.cache, indptr, idx, last,
+                                                    ws, out, lse)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for step in (0, 1, 8, 12):
+        now = [n + step for n in lens]
+        put(now)
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bia.bia_read_status(ws) == 0
+        ip, ids, la = table(now)
+        w2 = torch.empty(bia.bia_decode_fp8_workspace_size(b.desc, ip, la), dtype=torch.uint8,
+                         device=DEV)
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        bia.bia_decode_paged_fp8(b.desc, b.q, *b.cache, ip.to(DEV), ids.to(DEV), la.to(DEV), ip, la,
+                                 w2, o2, l2)
+        assert same_bits(out, o2) and same_bits(lse, l2)
+    put([n + 12 if n != 5 else 0 for n in lens])  # a request without a key breaks a rule
+    last[1] = 0
+    graph.replay()
+    assert bia.bia_read_status(ws) & 2 and torch.isnan(out.float()).all() and torch.isnan(lse).all()
+
+
+def test_two_graphs_share_one_workspace():
+    a = Batch([2500, 300], 16, 4, 128, 16, seed=1)
+    c = Batch([5000, 1, 700], 16, 4, 128, 16, seed=2)
+    want = [a.decode(), c.decode()]
+    size = max(bia.bia_decode_fp8_workspace_size(x.desc, x.indptr, x.last) for x in (a, c))
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for x in (a, c):
+        out, lse = torch.empty_like(x.q), torch.empty(x.q.shape[:2], device=DEV)
+        dev = x.dev()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            bia.bia_decode_paged_fp8(x.desc, x.q, *x.cache, *dev, x.indptr, x.last, ws, out, lse)
+        graphs.append((graph, dev))
+        outs.append((out, lse))
+    for _ in range(3):
+        for graph, _ in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(outs, want):
+        assert same_bits(o, wo) and same_bits(l, wl)
+
+
+def test_calls_on_two_streams_with_their_own_workspaces():
+    a = Batch([6000, 300, 2049], 32, 8, 128, 16, seed=1)
+    c = Batch([700, 5000], 16, 2, 128, 1, seed=2)
+    want = [a.decode(), c.decode()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    torch.cuda.synchronize()
+    for x, st in ((a, streams[0]), (c, streams[1])) * 3:
+        with torch.cuda.stream(st):
+            ws = torch.empty(bia.bia_decode_fp8_workspace_size(x.desc, x.indptr, x.last),
+                             dtype=torch.uint8, device=DEV)
+            out, lse = torch.empty_like(x.q), torch.empty(x.q.shape[:2], device=DEV)
+            bia.bia_decode_paged_fp8(x.desc, x.q, *x.cache, *x.dev(), x.indptr, x.last, ws, out, lse)
+            got.append((out, lse, ws))
+    torch.cuda.synchronize()
+    for i, (o, l, _) in enumerate(got):
+        assert same_bits(o, want[i % 2][0]) and same_bits(l, want[i % 2][1])

@@ -1,0 +1,229 @@
+"""Attention of packed sequences over contiguous keys and values against 64
+bits, its strides, masks and invariance, and the 8-bit cache's calls run
+together."""
+import pytest
+import torch
+
+import invariant_paged_attention_gb300 as bia
+from tests import fp8_util as fu
+from tests.gpu_util import same_bits
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def run(q, k, v, q_lens, kv_lens, causal=True, split=0, lse=True, sm_scale=0.0, stream=None):
+    hq, d = q.shape[1:]
+    desc = bia.make_desc(hq, k.shape[1], d, 1, sm_scale)
+    qo, kv = fu.indptr_of(q_lens), fu.indptr_of(kv_lens)
+    ws = torch.empty(bia.bia_prefill_ragged_workspace_size(desc, qo, kv, causal, split),
+                     dtype=torch.uint8, device=DEV)
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    l = torch.full(q.shape[:2], float("nan"), device=DEV) if lse else None
+    bia.bia_prefill_ragged(desc, q, k, v, qo.to(DEV), kv.to(DEV), qo, kv, ws, out, l, causal=causal,
+                           split_size=split, stream=stream)
+    assert bia.bia_read_status(ws, stream) == 0
+    return out, l
+
+
+def check(q, k, v, q_lens, kv_lens, out, lse, causal=True, sm_scale=None):
+    qa = ka = 0
+    for ql, kl in zip(q_lens, kv_lens):
+        if ql:
+            want = fu.attention_bounds(q[qa:qa + ql], k[ka:ka + kl], v[ka:ka + kl],
+                                       kl - ql + 1 if causal else None, sm_scale)
+            fu.check(out[qa:qa + ql], lse[qa:qa + ql], *want)
+        qa, ka = qa + ql, ka + kl
+
+
+def draw(hq, hkv, d, q_lens, kv_lens, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (fu.rows((sum(q_lens), hq, d), g), fu.rows((sum(kv_lens), hkv, d), g),
+            fu.rows((sum(kv_lens), hkv, d), g))
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (4, 1), (16, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_against_64_bits(d, hq, hkv, causal):
+    q_lens = [1, 17, 128, 0, 129, 300, 513, 5]
+    kv_lens = [1, 17, 128, 0, 129, 300, 700, 400]
+    q, k, v = draw(hq, hkv, d, q_lens, kv_lens, d + hq)
+    out, lse = run(q, k, v, q_lens, kv_lens, causal)
+    check(q, k, v, q_lens, kv_lens, out, lse, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_without_keys(d):
+    q_lens, kv_lens = [5, 200, 3], [0, 130, 0]
+    q, k, v = draw(4, 2, d, q_lens, kv_lens)
+    out, lse = run(q, k, v, q_lens, kv_lens, causal=False)
+    check(q, k, v, q_lens, kv_lens, out, lse, False)
+    out, lse = run(q[:5], k[:0], v[:0], [5], [0], causal=False)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("d,split", [(64, 128), (128, 256), (128, 4096), (256, 256), (96, 384)])
+def test_long_keys_in_splits(d, split):
+    q_lens, kv_lens = [40, 300, 1], [5000, 1300, 4500]
+    q, k, v = draw(8, 2, d, q_lens, kv_lens, 3)
+    for causal in (True, False):
+        out, lse = run(q, k, v, q_lens, kv_lens, causal, split)
+        check(q, k, v, q_lens, kv_lens, out, lse, causal)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_slices_of_a_fused_projection(d):
+    hq, hkv, lens = 8, 2, [100, 1, 333]
+    g = torch.Generator(device=DEV).manual_seed(9)
+    rows = fu.rows((sum(lens), hq + 2 * hkv, d), g)
+    q, k, v = rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:]
+    out, lse = run(q, k, v, lens, lens)
+    o2, l2 = run(q.contiguous(), k.contiguous(), v.contiguous(), lens, lens)
+    assert same_bits(out, o2) and same_bits(lse, l2)
+    check(q, k, v, lens, lens, out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_neighbour_does_not_reach_a_request(d, bad):
+    # requests 0 and 2 hold nothing finite; request 1's rows keep their bits
+    q_lens, kv_lens = [70, 150, 40], [70, 150, 300]
+    q, k, v = draw(4, 2, d, q_lens, kv_lens, 5)
+    for causal in (True, False):
+        want, wl = run(q[70:220], k[70:220], v[70:220], [150], [150], causal)
+        for t in (k, v):
+            t[:70], t[220:] = bad, bad
+        q[:70], q[220:] = bad, bad
+        out, lse = run(q, k, v, q_lens, kv_lens, causal)
+        assert same_bits(out[70:220], want) and same_bits(lse[70:220], wl)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_row_has_its_bits_in_any_batch_and_chunking(d):
+    hq, hkv, n = 8, 2, 700
+    q, k, v = draw(hq, hkv, d, [n], [n], 6)
+    want, wl = run(q, k, v, [n], [n], split=256)
+    q2, k2, v2 = draw(hq, hkv, d, [300, 90], [310, 1000], 7)
+    out, lse = run(torch.cat([q2[:300], q, q2[300:]]), torch.cat([k2[:310], k, k2[310:]]),
+                   torch.cat([v2[:310], v, v2[310:]]), [300, n, 90], [310, n, 1000], split=256)
+    assert same_bits(out[300:300 + n], want) and same_bits(lse[300:300 + n], wl)
+    for chunk in (32, 100, 129, 1):  # on the q-tile grid and off it, one token too
+        for a in range(0, n, max(chunk, 150) if chunk == 1 else chunk):
+            e = min(n, a + chunk)
+            o, l = run(q[a:e], k[:e], v[:e], [e - a], [e], split=256)
+            assert same_bits(o, want[a:e]) and same_bits(l, wl[a:e]), (chunk, a)
+
+
+def test_scale_stream_and_lse():
+    lens = [257, 64]
+    q, k, v = draw(4, 4, 128, lens, lens, 8)
+    out, lse = run(q, k, v, lens, lens, sm_scale=0.3)
+    check(q, k, v, lens, lens, out, lse, sm_scale=0.3)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        o2, l2 = run(q, k, v, lens, lens, sm_scale=0.3)
+    st.synchronize()
+    assert same_bits(out, o2) and same_bits(lse, l2)
+    assert same_bits(run(q, k, v, lens, lens, sm_scale=0.3, lse=False)[0], out)
+
+
+def test_captured_prompt_replays():
+    lens = [300, 5000]
+    q, k, v = draw(8, 2, 128, lens, lens, 10)
+    want, wl = run(q, k, v, lens, lens)
+    desc = bia.make_desc(8, 2, 128, 1)
+    ip = fu.indptr_of(lens)
+    dev = ip.to(DEV)
+    ws = torch.empty(bia.bia_prefill_ragged_workspace_size(desc, ip, ip), dtype=torch.uint8,
+                     device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bia.bia_prefill_ragged(desc, q, k, v, dev, dev, ip, ip, ws, out, lse)
+    for _ in range(2):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(out, want) and same_bits(lse, wl)
+    q.copy_(q.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    check(q, k, v, lens, lens, out, lse)
+
+
+@pytest.mark.parametrize("d,hq,hkv,page", [(128, 32, 8, 16), (64, 8, 1, 1), (256, 4, 2, 32)])
+def test_a_server_with_an_8_bit_cache(d, hq, hkv, page):
+    """Prompts in two chunks (the second over the prefix read back), then
+    tokens one at a time, all from the 8-bit cache."""
+    desc = bia.make_desc(hq, hkv, d, page)
+    g = torch.Generator(device=DEV).manual_seed(21)
+    total = [150, 37, 400]
+    first = [100, 37, 256]  # the first chunk
+    steps = 4
+    full = [n + steps for n in total]
+    indptr_f, _, _, pages, n_pages = fu.page_table(full, page, 3)
+    proj = [fu.rows((n, hq + 2 * hkv, d), g) for n in full]  # each request's fused rows
+    kc, vc, ks, vs = fu.make_cache([p[:0, :hkv] for p in proj], [p[:0, :hkv] for p in proj],
+                                   [x[:0] for x in pages], page, n_pages)
+
+    def table(lens):
+        count = [-(-n // page) for n in lens]
+        ip = fu.indptr_of(count)
+        ids = torch.cat([pages[i][:c] for i, c in enumerate(count)])
+        last = torch.tensor([n - (c - 1) * page for n, c in zip(lens, count)], dtype=torch.int32)
+        return ip, ids, last
+
+    def values(b, n):  # what the cache has to hold of request b
+        c = []
+        for s in (slice(hq, hq + hkv), slice(hq + hkv, None)):
+            codes, e = fu.quantise(proj[b][:n, s])
+            c.append(codes * torch.exp2(e.double())[..., None])
+        return c
+
+    def put(lo, hi):
+        ip, ids, last = table(hi)
+        rows = torch.cat([p[a:e] for p, a, e in zip(proj, lo, hi)])
+        ap = fu.indptr_of([e - a for a, e in zip(lo, hi)])
+        bia.bia_append_paged_kv_fp8(desc, rows[:, hq:hq + hkv], rows[:, hq + hkv:], kc, vc, ks, vs,
+                                    ap.to(DEV), ip.to(DEV), ids.to(DEV), last.to(DEV), ap, ip, last)
+        return rows[:, :hq], ip, ids, last
+
+    lo = [0, 0, 0]
+    for hi in (first, total):
+        q, ip, ids, last = put(lo, hi)
+        kv = fu.indptr_of(hi)
+        k = torch.empty(sum(hi), hkv, d, dtype=torch.bfloat16, device=DEV)
+        v = torch.empty_like(k)
+        bia.bia_gather_paged_kv_fp8(desc, kc, vc, ks, vs, k, v, kv.to(DEV), ip.to(DEV), ids.to(DEV),
+                                    last.to(DEV), kv, ip, last)
+        q_lens = [e - a for a, e in zip(lo, hi)]
+        out, lse = run(q, k, v, q_lens, hi)
+        at = 0
+        for b in range(3):
+            kb, vb = values(b, hi[b])
+            assert torch.equal(k[kv[b]:kv[b + 1]].double(), kb)
+            n = q_lens[b]
+            if n:
+                fu.check(out[at:at + n], lse[at:at + n],
+                         *fu.attention_bounds(q[at:at + n], kb, vb, lo[b] + 1))
+            at += n
+        lo = hi
+    for _ in range(steps):
+        hi = [n + 1 for n in lo]
+        q, ip, ids, last = put(lo, hi)
+        q = q.contiguous()
+        ws = torch.empty(bia.bia_decode_fp8_workspace_size(desc, ip, last), dtype=torch.uint8,
+                         device=DEV)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+        bia.bia_decode_paged_fp8(desc, q, kc, vc, ks, vs, ip.to(DEV), ids.to(DEV), last.to(DEV), ip,
+                                 last, ws, out, lse)
+        for b in range(3):
+            kb, vb = values(b, hi[b])
+            want = fu.attention_bounds(q[b:b + 1], kb, vb)
+            # weights under the 8-bit terms' last place: 2^-19 of the largest
+            # weight (at most 1) for every key, at the largest value
+            tol = want[1] + 2.0 ** -18 * hi[b] * vb.abs().max()
+            fu.check(out[b:b + 1], lse[b:b + 1], want[0], tol, want[2], want[3])
+        lo = hi
