@@ -590,52 +590,122 @@ def bia_mla_prefill_paged(desc, q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, k
 
 
 # ---------------------------------------------------------------- 8-bit cache
+#
+# These calls are made once per layer and decode step, so what a well-formed
+# call pays on the host counts (a 32-token append's kernel takes about 3 us):
+# _not_ready looks every tensor over in one pass, and only a call that fails it
+# goes through the checks that find the reason.
+
+
+def _not_ready(stream, *specs):
+    """None when the tensors of `specs` ((name, tensor, dtype) or, for an
+    optional one, (name, tensor, dtype, True)) are contiguous, of their dtypes
+    and on the launch's device.  Else raises for a wrong dtype or layout, and
+    returns what _check_cuda takes, for after the shapes."""
+    device = None
+    for spec in specs:
+        t = spec[1]
+        if t is None and len(spec) > 3:
+            continue
+        if not isinstance(t, torch.Tensor):
+            break
+        at = t.get_device()
+        if device is None:
+            device = at
+        if (at != device or at < 0 or (spec[2] is not None and t.dtype is not spec[2]) or
+                not t.is_contiguous()):
+            break
+    else:
+        if stream is None and device == torch._C._cuda_getDevice():
+            return None
+    return _check_types(*specs)
+
+
+def _handle(stream):
+    """The raw handle of `stream`, or of the current device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _at(t):
+    """Address of a tensor (ctypes takes it as a void pointer), None of none."""
+    return None if t is None else t.data_ptr()
+
+
+def _last(t) -> int:
+    """Last entry of a host mirror."""
+    return ctypes.c_int32.from_address(t.data_ptr() + 4 * (t.numel() - 1)).value
+
+
+def _host(t) -> torch.Tensor:
+    """_host_i32 with at least one entry."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is I32 and t.is_contiguous() and
+            t.get_device() < 0):
+        t = _host_i32(t)
+    if t.numel() == 0:
+        raise ValueError("host mirrors hold at least one entry")
+    return t
 
 
 def _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale):
-    _check_caches(k_cache, v_cache)
-    want = (k_cache.shape[0], desc.page_size, desc.num_kv_heads, desc.head_dim)
-    if tuple(k_cache.shape) != want:
-        raise ValueError(f"the caches must be {want} (num_pages, page_size, num_kv_heads, "
-                         f"head_dim) for this descriptor, got {tuple(k_cache.shape)}")
-    if tuple(k_scale.shape) != want[:3] or tuple(v_scale.shape) != want[:3]:
-        raise ValueError(f"k_scale and v_scale must be {want[:3]}, got {tuple(k_scale.shape)} and "
+    rows = (k_cache.shape[0], desc.page_size, desc.num_kv_heads)
+    want = rows + (desc.head_dim,)
+    if k_cache.shape != want or v_cache.shape != want:
+        raise ValueError(f"k_cache and v_cache must be {want} (num_pages, page_size, "
+                         f"num_kv_heads, head_dim) for this descriptor, got "
+                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    if k_scale.shape != rows or v_scale.shape != rows:
+        raise ValueError(f"k_scale and v_scale must be {rows}, got {tuple(k_scale.shape)} and "
                          f"{tuple(v_scale.shape)}")
 
 
-def _check_lengths(batch, **arrays):
-    """Every index array holds the entries the call reads: batch + 1 of an
-    indptr, batch of a last page length."""
-    for name, t in arrays.items():
-        want = batch + ("indptr" in name)
-        if t.numel() != want:
+def _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp=None, last=None):
+    """The page table's arrays hold what a call of `batch` requests reads."""
+    for name, t, want in (("kv_indptr", kv_indptr, batch + 1),
+                          ("kv_last_page_len", kv_last_page_len, batch),
+                          ("kv_indptr_host", kvp, batch + 1),
+                          ("kv_last_page_len_host", last, batch)):
+        if t is not None and t.numel() != want:
             raise ValueError(f"{name} must hold {want} entries for {batch} requests, got "
                              f"{t.numel()}")
+    if kvp is not None and kv_indices.numel() < _last(kvp):
+        raise ValueError(f"kv_indices holds {kv_indices.numel()} pages, kv_indptr ends at "
+                         f"{_last(kvp)}")
 
 
-def _check_packed(name, t, heads, head_dim):
-    """(name, tensor) and token stride of packed bf16 rows [tokens, heads,
-    head_dim]: a token's heads and columns dense, any multiple of 8 elements
-    from one token to the next."""
-    if t is None:
-        raise TypeError(f"{name} is required")
+def _packed(name, t, heads, head_dim, tokens):
+    """Token stride of packed bf16 rows [tokens, heads, head_dim]: a token's
+    heads and columns dense, any multiple of 8 elements from one token to the
+    next, on the device of the contiguous tensors (checked by the caller)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != BF16:
+    if t.dtype is not BF16:
         raise TypeError(f"{name} must be {BF16}, got {t.dtype}")
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
-        raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}], got {tuple(t.shape)}")
+    if t.shape != (tokens, heads, head_dim):
+        raise ValueError(f"{name} must be [{tokens} tokens, {heads}, {head_dim}], got "
+                         f"{tuple(t.shape)}")
     row = heads * head_dim
-    if t.shape[0] == 0:
-        return (name, t), row
-    if (head_dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != head_dim):
+    if tokens == 0:
+        return row
+    step, head, col = t.stride()
+    if (head_dim > 1 and col != 1) or (heads > 1 and head != head_dim):
         raise ValueError(f"{name} must hold each token's heads one after the other, got strides "
                          f"{t.stride()}")
-    step = t.stride(0) if t.shape[0] > 1 else row
+    if tokens == 1:
+        return row
     if step < row or step % 8 != 0:
         raise ValueError(f"{name} must step a multiple of 8 elements, at least {row}, from token "
                          f"to token, got {step}")
-    return (name, t), step
+    return step
+
+
+def _on_device(unready, stream, like, **packed):
+    """The device checks of a call: what _not_ready left, and that the packed
+    rows are where `like` is."""
+    at = like.get_device()
+    if unready is not None or any(t.get_device() != at for t in packed.values()):
+        _check_cuda((unready or [("the other arguments", like)]) + list(packed.items()), stream)
 
 
 def bia_append_paged_kv_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_scale, append_indptr,
@@ -645,31 +715,28 @@ def bia_append_paged_kv_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_sca
     [num_pages, page_size, Hkv, D], scales torch.float8_e8m0fnu [num_pages,
     page_size, Hkv] (include/bia.h states the format).  k_new and v_new
     [total_new, Hkv, D] may be slices of a fused projection's rows."""
-    ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
-                      ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
-                      ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                      ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                      ("status", status, I32, True))
+    ap, kvp, last = (_host(append_indptr_host), _host(kv_indptr_host),
+                     _host(kv_last_page_len_host))
+    batch = ap.numel() - 1
+    total, hkv, d = _last(ap), desc.num_kv_heads, desc.head_dim
+    k_step = _packed("k_new", k_new, hkv, d, total)
+    v_step = _packed("v_new", v_new, hkv, d, total)
+    ts = _not_ready(stream, ("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                    ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                    ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                    ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                    ("status", status, I32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
-    k_given, k_step = _check_packed("k_new", k_new, desc.num_kv_heads, desc.head_dim)
-    v_given, v_step = _check_packed("v_new", v_new, desc.num_kv_heads, desc.head_dim)
-    ap, kvp, last = (_host_i32(append_indptr_host), _host_i32(kv_indptr_host),
-                     _host_i32(kv_last_page_len_host))
-    _check_lengths(len(ap) - 1, append_indptr=append_indptr, kv_indptr=kv_indptr,
-                   kv_last_page_len=kv_last_page_len, kv_indptr_host=kvp,
-                   kv_last_page_len_host=last)
-    if k_new.shape[0] != int(ap[-1]) or v_new.shape[0] != int(ap[-1]):
-        raise ValueError(f"k_new and v_new must hold append_indptr[batch] = {int(ap[-1])} tokens, "
-                         f"got {k_new.shape[0]} and {v_new.shape[0]}")
-    if kv_indices.numel() < int(kvp[-1]):
-        raise ValueError(f"kv_indices holds {kv_indices.numel()} pages, kv_indptr ends at "
-                         f"{int(kvp[-1])}")
-    _check_cuda(ts + [k_given, v_given], stream)
+    _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
+    if append_indptr.numel() != batch + 1:
+        raise ValueError(f"append_indptr must hold {batch + 1} entries, got "
+                         f"{append_indptr.numel()}")
+    _on_device(ts, stream, k_cache, k_new=k_new, v_new=v_new)
     rc = load().bia_append_paged_kv_fp8(
-        ctypes.byref(desc), _ptr(k_new), _ptr(v_new), k_step, v_step, _ptr(k_cache),
-        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(append_indptr),
-        _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(ap), _ptr(kvp),
-        _ptr(last), len(ap) - 1, _ptr(status), _stream(stream))
+        ctypes.byref(desc), _at(k_new), _at(v_new), k_step, v_step, _at(k_cache), _at(v_cache),
+        _at(k_scale), _at(v_scale), k_cache.shape[0], _at(append_indptr), _at(kv_indptr),
+        _at(kv_indices), _at(kv_last_page_len), _at(ap), _at(kvp), _at(last), batch, _at(status),
+        _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_append_paged_kv_fp8")
 
@@ -680,31 +747,28 @@ def bia_gather_paged_kv_fp8(desc, k_cache, v_cache, k_scale, v_scale, k_out, v_o
     """Reads the first out_indptr[b+1] - out_indptr[b] keys of each request
     back from the 8-bit cache into k_out / v_out [out_indptr[batch], Hkv, D]
     bf16, packed (include/bia.h states the rule)."""
-    ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
-                      ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
-                      ("k_out", k_out, BF16), ("v_out", v_out, BF16),
-                      ("out_indptr", out_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                      ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                      ("status", status, I32, True))
+    ts = _not_ready(stream, ("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                    ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                    ("k_out", k_out, BF16), ("v_out", v_out, BF16),
+                    ("out_indptr", out_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                    ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                    ("status", status, I32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
-    op, kvp, last = (_host_i32(out_indptr_host), _host_i32(kv_indptr_host),
-                     _host_i32(kv_last_page_len_host))
-    _check_lengths(len(op) - 1, out_indptr=out_indptr, kv_indptr=kv_indptr,
-                   kv_last_page_len=kv_last_page_len, kv_indptr_host=kvp,
-                   kv_last_page_len_host=last)
-    want = (int(op[-1]), desc.num_kv_heads, desc.head_dim)
-    if tuple(k_out.shape) != want or tuple(v_out.shape) != want:
+    op, kvp, last = _host(out_indptr_host), _host(kv_indptr_host), _host(kv_last_page_len_host)
+    batch = op.numel() - 1
+    _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
+    if out_indptr.numel() != batch + 1:
+        raise ValueError(f"out_indptr must hold {batch + 1} entries, got {out_indptr.numel()}")
+    want = (_last(op), desc.num_kv_heads, desc.head_dim)
+    if k_out.shape != want or v_out.shape != want:
         raise ValueError(f"k_out and v_out must be {want}, got {tuple(k_out.shape)} and "
                          f"{tuple(v_out.shape)}")
-    if kv_indices.numel() < int(kvp[-1]):
-        raise ValueError(f"kv_indices holds {kv_indices.numel()} pages, kv_indptr ends at "
-                         f"{int(kvp[-1])}")
-    _check_cuda(ts, stream)
+    _on_device(ts, stream, k_cache)
     rc = load().bia_gather_paged_kv_fp8(
-        ctypes.byref(desc), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        k_cache.shape[0], _ptr(out_indptr), _ptr(kv_indptr), _ptr(kv_indices),
-        _ptr(kv_last_page_len), _ptr(op), _ptr(kvp), _ptr(last), len(op) - 1, _ptr(k_out),
-        _ptr(v_out), _ptr(status), _stream(stream))
+        ctypes.byref(desc), _at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale),
+        k_cache.shape[0], _at(out_indptr), _at(kv_indptr), _at(kv_indices),
+        _at(kv_last_page_len), _at(op), _at(kvp), _at(last), batch, _at(k_out), _at(v_out),
+        _at(status), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_gather_paged_kv_fp8")
 
@@ -716,39 +780,36 @@ def bia_decode_fp8_workspace_size(desc, kv_indptr_host, kv_last_page_len_host,
                                                     len(kvp) - 1, int(split_size)))
 
 
-def _decode_fp8_tensors(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
-                        kv_last_page_len, workspace, out, lse, stream):
-    ts = _check_types(("q", q, BF16), ("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
-                      ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
-                      ("kv_indptr", kv_indptr, I32), ("kv_indices", kv_indices, I32),
-                      ("kv_last_page_len", kv_last_page_len, I32), ("workspace", workspace, None),
-                      ("out", out, BF16), ("lse", lse, F32, True))
+def _check_decode_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                      kv_last_page_len, workspace, out, lse, stream, kvp=None, last=None):
+    ts = _not_ready(stream, ("q", q, BF16), ("k_cache", k_cache, E4M3),
+                    ("v_cache", v_cache, E4M3), ("k_scale", k_scale, E8M0),
+                    ("v_scale", v_scale, E8M0), ("kv_indptr", kv_indptr, I32),
+                    ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                    ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
-    batch = kv_indptr.numel() - 1
-    if tuple(q.shape) != (batch, desc.num_qo_heads, desc.head_dim):
-        raise ValueError(f"q must be {(batch, desc.num_qo_heads, desc.head_dim)}, got "
-                         f"{tuple(q.shape)}")
-    _check_rows(q, out, lse)
-    _check_lengths(batch, kv_last_page_len=kv_last_page_len)
-    _check_cuda(ts, stream)
+    want = (kv_indptr.numel() - 1, desc.num_qo_heads, desc.head_dim)
+    if q.shape != want or out.shape != want:
+        raise ValueError(f"q and out must be {want}, got {tuple(q.shape)} and {tuple(out.shape)}")
+    if lse is not None and lse.numel() != want[0] * want[1]:
+        raise ValueError(f"lse must hold {want[0]} x {want[1]} floats")
+    _check_table(want[0], kv_indptr, kv_indices, kv_last_page_len, kvp, last)
+    _on_device(ts, stream, q)
 
 
 def bia_decode_paged_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
                          kv_last_page_len, kv_indptr_host, kv_last_page_len_host, workspace, out,
                          lse=None, split_size=0, stream=None):
     """bia_decode_paged over the 8-bit cache (include/bia.h states the format)."""
-    _decode_fp8_tensors(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
-                        kv_last_page_len, workspace, out, lse, stream)
-    kvp, last = _host_i32(kv_indptr_host), _host_i32(kv_last_page_len_host)
-    _check_lengths(q.shape[0], kv_indptr_host=kvp, kv_last_page_len_host=last)
-    if kv_indices.numel() < int(kvp[-1]):
-        raise ValueError(f"kv_indices holds {kv_indices.numel()} pages, kv_indptr ends at "
-                         f"{int(kvp[-1])}")
+    kvp, last = _host(kv_indptr_host), _host(kv_last_page_len_host)
+    _check_decode_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                      kv_last_page_len, workspace, out, lse, stream, kvp, last)
+    batch = q.shape[0]
     rc = load().bia_decode_paged_fp8(
-        ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        k_cache.shape[0], _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(kvp),
-        _ptr(last), len(kvp) - 1, int(split_size), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _stream(stream))
+        ctypes.byref(desc), _at(q), _at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale),
+        k_cache.shape[0], _at(kv_indptr), _at(kv_indices), _at(kv_last_page_len), _at(kvp),
+        _at(last), batch, int(split_size), _at(workspace),
+        workspace.numel() * workspace.element_size(), _at(out), _at(lse), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_decode_paged_fp8")
 
@@ -763,13 +824,14 @@ def bia_decode_paged_fp8_bounded(desc, bounds, q, k_cache, v_cache, k_scale, v_s
                                  split_size=0, stream=None):
     """bia_decode_paged_fp8 sized from `bounds` (max_kv_len): the index arrays
     are read on the device only, so a captured decode replays step after step."""
-    _decode_fp8_tensors(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
-                        kv_last_page_len, workspace, out, lse, stream)
+    _check_decode_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                      kv_last_page_len, workspace, out, lse, stream)
+    batch = q.shape[0]
     rc = load().bia_decode_paged_fp8_bounded(
-        ctypes.byref(desc), ctypes.byref(bounds), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(kv_indptr), _ptr(kv_indices),
-        _ptr(kv_last_page_len), q.shape[0], int(split_size), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _stream(stream))
+        ctypes.byref(desc), ctypes.byref(bounds), _at(q), _at(k_cache), _at(v_cache),
+        _at(k_scale), _at(v_scale), k_cache.shape[0], _at(kv_indptr), _at(kv_indices),
+        _at(kv_last_page_len), batch, int(split_size), _at(workspace),
+        workspace.numel() * workspace.element_size(), _at(out), _at(lse), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_decode_paged_fp8_bounded")
 
@@ -790,24 +852,26 @@ def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_i
     """Attention of packed sequences: q [total_q, Hq, D] over k, v [total_kv,
     Hkv, D], each dense or a slice of a fused projection's rows
     (include/bia.h states the rule)."""
-    ts = _check_types(("qo_indptr", qo_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                      ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
-    q_given, q_step = _check_packed("q", q, desc.num_qo_heads, desc.head_dim)
-    k_given, k_step = _check_packed("k", k, desc.num_kv_heads, desc.head_dim)
-    v_given, v_step = _check_packed("v", v, desc.num_kv_heads, desc.head_dim)
-    _check_rows(q, out, lse)
-    qo, kvp = _host_i32(qo_indptr_host), _host_i32(kv_indptr_host)
-    _check_lengths(len(qo) - 1, qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indptr_host=kvp)
-    if q.shape[0] != int(qo[-1]):
-        raise ValueError(f"q must hold qo_indptr[batch] = {int(qo[-1])} tokens, got {q.shape[0]}")
-    if k.shape[0] != int(kvp[-1]) or v.shape[0] != int(kvp[-1]):
-        raise ValueError(f"k and v must hold kv_indptr[batch] = {int(kvp[-1])} tokens, got "
-                         f"{k.shape[0]} and {v.shape[0]}")
-    _check_cuda(ts + [q_given, k_given, v_given], stream)
+    qo, kvp = _host(qo_indptr_host), _host(kv_indptr_host)
+    batch = qo.numel() - 1
+    hq, hkv, d = desc.num_qo_heads, desc.num_kv_heads, desc.head_dim
+    q_step = _packed("q", q, hq, d, _last(qo))
+    k_step = _packed("k", k, hkv, d, _last(kvp))
+    v_step = _packed("v", v, hkv, d, _last(kvp))
+    ts = _not_ready(stream, ("qo_indptr", qo_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                    ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+    if out.shape != q.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
+    if lse is not None and lse.numel() != q.shape[0] * hq:
+        raise ValueError(f"lse must hold {q.shape[0]} x {hq} floats")
+    for name, t in (("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("kv_indptr_host", kvp)):
+        if t.numel() != batch + 1:
+            raise ValueError(f"{name} must hold {batch + 1} entries, got {t.numel()}")
+    _on_device(ts, stream, out, q=q, k=k, v=v)
     rc = load().bia_prefill_ragged(
-        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), q_step, k_step, v_step, _ptr(qo_indptr),
-        _ptr(kv_indptr), _ptr(qo), _ptr(kvp), len(qo) - 1, int(bool(causal)), int(split_size),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
-        _stream(stream))
+        ctypes.byref(desc), _at(q), _at(k), _at(v), q_step, k_step, v_step, _at(qo_indptr),
+        _at(kv_indptr), _at(qo), _at(kvp), batch, int(bool(causal)), int(split_size),
+        _at(workspace), workspace.numel() * workspace.element_size(), _at(out), _at(lse),
+        _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_prefill_ragged")

@@ -159,7 +159,7 @@ def test_the_binding_checks_its_tensors(bia):
     with pytest.raises(ValueError, match="k_new"):
         put(k=torch.zeros(5, 2, 128, dtype=torch.bfloat16)[:, :, ::2])
     with pytest.raises(ValueError, match="k_new"):
-        put(k=torch.zeros(5, 129 + 3, dtype=torch.bfloat16)[:, :128].view(5, 2, 64))
+        put(k=torch.zeros(5, 132, dtype=torch.bfloat16)[:, :128].unflatten(1, (2, 64)))
     with pytest.raises(ValueError, match="tokens"):
         put(v=x[:4])
     with pytest.raises(ValueError, match="kv_indices"):
@@ -170,12 +170,12 @@ def test_the_binding_checks_its_tensors(bia):
         bia.bia_gather_paged_kv_fp8(d, kc, kc, ks, ks, x[:4], x[:4], *tail)
     q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
     ws = torch.zeros(4096, dtype=torch.uint8)
-    with pytest.raises(ValueError, match="q must be"):
+    with pytest.raises(ValueError, match="q and out must be"):
         bia.bia_decode_paged_fp8(d, q[:, :2].contiguous(), kc, kc, ks, ks, kvp, idx, last, kvp, last,
                                  ws, q[:, :2].contiguous())
     with pytest.raises(ValueError, match="CUDA"):
         bia.bia_decode_paged_fp8(d, q, kc, kc, ks, ks, kvp, idx, last, kvp, last, ws, q)
-    with pytest.raises(ValueError, match="q must hold"):
+    with pytest.raises(ValueError, match="q must be"):
         bia.bia_prefill_ragged(d, q, x, x, ip, ip, ip, ip, ws, q)
     qq = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="k must be"):
