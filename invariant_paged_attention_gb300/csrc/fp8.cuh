@@ -53,4 +53,30 @@ __device__ __forceinline__ void e4m3x2_values(uint32_t codes, float &lo, float &
       : "h"(static_cast<uint16_t>(codes)));
 }
 
+// ---------------------------------------------------------------- tensor cores
+// D[tmem] (+)= A[smem] * B[smem]^T of e4m3 codes (K = 32 a step), one elected
+// thread.
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "setp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator (bits 4-5 = 1),
+// e4m3 A and B (bits 7-9, 10-12 = 0), MN-major A / B (bits 15 / 16), N/8 at
+// bits 17-22, M/16 at bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// Shared-memory descriptor without swizzle (layout type 0): 8 x 16-byte core
+// matrices, `lbo` / `sbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
 } // namespace bia
