@@ -947,7 +947,7 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
               : host_plan(desc, nullptr, kvp_host, last_host, batch, 1, split, 1, 1, 1, 0, &hp);
   if (rc != BIA_OK) return rc;
   if (hp.n_units * desc->num_kv_heads > INT32_MAX) return BIA_ERR_UNSUPPORTED;
-  const WsLayout w = bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows,
+  const WsLayout w = bia::make_layout(batch, 0, hp.n_units, 0, hp.part_rows,
                                       desc->num_qo_heads, desc->head_dim);
   if (workspace_bytes < w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
   rc = check_resident({{"q", q},
@@ -970,15 +970,9 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   pa.kv_last_page_len = kv_last_page_len;
   pa.batch = batch;
   pa.page_size = desc->page_size;
-  pa.tile_tokens = pa.tiles_per_unit = pa.ctas = pa.causal = 1;
   pa.split = split;
   pa.bounded = bounds ? 1 : 0;
-  if (bounds) {
-    pa.max_q_len = 1;
-    pa.max_kv_len = bounds->max_kv_len;
-    pa.max_total_q = hp.total_q;
-  }
-  pa.n_groups_expected = hp.n_groups;
+  if (bounds) pa.max_kv_len = bounds->max_kv_len;
   pa.n_units_expected = hp.n_units;
   pa.part_rows_expected = hp.part_rows;
   pa.out = static_cast<uint16_t *>(out);
@@ -987,11 +981,8 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   pa.lse_elems = hp.total_q * desc->num_qo_heads;
   pa.status = reinterpret_cast<int32_t *>(ws + w.status);
   pa.reqs = reinterpret_cast<bia::ReqInfo *>(ws + w.reqs);
-  pa.group_off = reinterpret_cast<int32_t *>(ws + w.group_off);
-  pa.group_cnt = reinterpret_cast<int32_t *>(ws + w.group_cnt);
   pa.units = reinterpret_cast<bia::Unit *>(ws + w.units);
-  pa.sunits = reinterpret_cast<bia::Unit *>(ws + w.sunits);
-  cudaError_t e = bia::launch_plan(pa, st);
+  cudaError_t e = bia::launch_plan_decode_fp8(pa, st);
   if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
   __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
 
@@ -1005,9 +996,7 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   a.D = desc->head_dim;
   a.G = desc->num_qo_heads / desc->num_kv_heads;
   a.page_shift = log2i(desc->page_size);
-  a.causal = 1;
   a.split = split;
-  a.tile_tokens = 1;
   a.scale_log2 = effective_scale(desc);
   a.batch = batch;
   a.n_units = hp.n_units;
@@ -1036,7 +1025,7 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
     if (re != cudaSuccess) return cuda_fail("profile event record", re);
   }
   if (hp.part_rows > 0) {
-    e = bia::launch_merge_partials(a, st);
+    e = bia::launch_merge_decode_fp8(a, st);
     if (e != cudaSuccess) return cuda_fail("merge kernel launch", e);
     __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
   }
@@ -1053,7 +1042,7 @@ size_t decode_fp8_workspace(const bia_attn_desc *desc, const bia_bounds *bounds,
       bounds ? bounded_plan(bounds, batch, 1, split, 1, 1, 1, 0, true, &hp)
              : host_plan(desc, nullptr, kvp_host, last_host, batch, 1, split, 1, 1, 1, 0, &hp);
   if (rc != BIA_OK) return 0;
-  return bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows, desc->num_qo_heads,
+  return bia::make_layout(batch, 0, hp.n_units, 0, hp.part_rows, desc->num_qo_heads,
                           desc->head_dim)
       .total;
 }

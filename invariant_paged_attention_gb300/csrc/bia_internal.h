@@ -306,7 +306,9 @@ cudaError_t launch_decode_tc(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s); // head_dim 256
 cudaError_t launch_cache_fp8(const CacheFp8Args &a, bool append, cudaStream_t s);
+cudaError_t launch_plan_decode_fp8(const PlanArgs &p, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s);
+cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s);
 // Packed keys and values: head_dim 64, 96 and 128; 256
 cudaError_t launch_prefill_ragged(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s);

@@ -30,9 +30,13 @@
 // Persistent: one CTA per SM takes (unit, kv head) items from a counter and
 // posts them to its roles through a mailbox, as the bf16 decode does.  Roles:
 // warps 0-3 and 4-7 softmax + epilogue (WG 0 even blocks, WG 1 odd blocks;
-// the epilogue alternates by item), 8 the MMA issuer (owns TMEM), 9-12 the
-// scales of a block's keys and the q rows, 13.. the copies (16-byte cp.async
-// into the swizzled operand layout, page indices a block ahead).
+// the epilogue alternates by item), 8 issues P.V (owns TMEM), 9 issues S, 10-13
+// hand over the scales of a block's keys and the q rows, 14.. copy (16-byte
+// cp.async into the swizzled operand layout, page indices a block ahead).  S
+// and P.V come from two threads because each waits for its own inputs: from
+// one, S of a later block waited in front of a P.V that was ready (head_dim
+// 256, whose rings hold three blocks: 2.8 TB/s).  S also runs ahead into the
+// next item.
 #include <algorithm>
 
 #include "bia_internal.h"
@@ -46,15 +50,15 @@ namespace {
 constexpr int kKeys8 = 128;            // keys per block: the MMAs' M
 constexpr int kPiece8 = kKeys8 * 128;  // 128 rows x 128 codes, SW128
 constexpr int kN8 = 16;                // the MMAs' N: hi and lo of up to 8 heads
-constexpr int kMmaWarp8 = 8;
-constexpr int kAuxWarp8 = 9;           // four warps: thread t is key t
-constexpr int kCopyWarp8 = 13;
+constexpr int kPVWarp8 = 8;
+constexpr int kSWarp8 = 9;
+constexpr int kAuxWarp8 = 10;          // four warps: thread t is key t
+constexpr int kCopyWarp8 = 14;
 constexpr int kCopyWarps8 = 8;
 constexpr int kThreads8 = (kCopyWarp8 + kCopyWarps8) * 32;
 constexpr int kCopyThreads8 = kCopyWarps8 * 32;
 constexpr int kReaders8 = kCopyWarp8 + kCopyWarps8; // warps that read the mailbox
 constexpr int kScaleSlots8 = 8;
-constexpr int kAhead8 = 4;             // S runs up to this many blocks ahead of P.V
 // The running maximum moves when a block exceeds it by 2^2: weights stay
 // below 2^2, and 2^6 more fills e4m3's range (448).
 constexpr float kLazy8 = 2.0f;
@@ -158,12 +162,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
   };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kSlot);
 
-  grid_dep_wait();   // the plan is complete
-  grid_dep_launch(); // the next kernel of the call may start launching
   const int64_t n_work = a.n_units * a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == kMmaWarp8) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  if (warp == kPVWarp8) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   // q rows of heads that do not exist stay zero
   for (int i = tid; i < 2 * L::kQBuf / 16; i += kThreads8)
     reinterpret_cast<uint4 *>(smem + L::kQ)[i] = make_uint4(0, 0, 0, 0);
@@ -195,6 +197,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
     fence_mbar_init();
   }
+  grid_dep_launch(); // the merge may start launching
+  grid_dep_wait();   // the plan is complete (all of the above ran beside it)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -433,9 +437,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
         vb = vb1;
       }
     }
-  } else if (warp == kMmaWarp8) {
-    // ------------------------------------------------------------ MMA issuer
-    // Per item: S of the first blocks, then per block j: P.V(j), S(j + 4).
+  } else if (warp == kSWarp8) {
+    // ------------------------------------------------------------ S issuer
     if (lane == 0) {
       const int ksteps = a.D / 32 < 4 ? a.D / 32 : 4; // 32-code steps of a piece
       uint32_t jg = 0, ig = 0, cnt[2] = {0, 0};
@@ -447,15 +450,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (!it.live) continue;
         const uint32_t qb = qbuf(ig & 1);
         ok = mbar_wait(bar(L::bQFull + (ig & 1)), (ig >> 1) & 1, a.status);
-        // the item's O buffers are free once the epilogue of item ig - 2 read them
-        if (ok && ig >= 2) ok = mbar_wait(bar(L::bOFree + (ig & 1)), ((ig >> 1) - 1) & 1, a.status);
-        if (!ok) break;
-        auto issue_s = [&](int j) {
-          const uint32_t jj = jg + j;
-          const int s = static_cast<int>(jj % NS), wg = j & 1;
-          const uint32_t c = (wg ? cnt[1] : cnt[0]) + (j >> 1);
-          ok = mbar_wait(bar(L::bKFull + s), (jj / NS) & 1, a.status);
-          if (!ok) return;
+        for (int j = 0; j < it.nb && ok; ++j, ++jg) {
+          const int s = static_cast<int>(jg % NS), wg = j & 1;
+          const uint32_t c = wg ? cnt[1]++ : cnt[0]++;
+          // S buffer c % 2 is free once the softmax has read S(c - 2)
+          if (c >= 2)
+            ok = mbar_wait(bar(L::bPFull + 2 * wg + (c & 1)), ((c >> 1) - 1) & 1, a.status);
+          ok = ok && mbar_wait(bar(L::bKFull + s), (jg / NS) & 1, a.status);
+          if (!ok) break;
           fence_proxy_async(); // the rows were written by cp.async (generic proxy)
           tc_fence_after();
 #pragma unroll
@@ -466,13 +468,29 @@ __global__ void __launch_bounds__(kThreads8, 1)
                           (p | kk) != 0 ? 1u : 0u);
           mma_commit(bar(L::bKEmpty + s));
           mma_commit(bar(L::bSFull + 2 * wg + (c & 1)));
-        };
-        for (int j = 0; j < min(kAhead8, it.nb) && ok; ++j) issue_s(j);
-        for (int j = 0; j < it.nb && ok; ++j) {
-          const uint32_t jj = jg + j;
-          const int s = static_cast<int>(jj % NS), wg = j & 1;
-          const uint32_t c = (wg ? cnt[1] : cnt[0]) + (j >> 1);
-          ok = mbar_wait(bar(L::bVFull + s), (jj / NS) & 1, a.status) &&
+        }
+        if (!ok) break;
+        mma_commit(bar(L::bQEmpty + (ig & 1)));
+        ++ig;
+      }
+    }
+    __syncwarp();
+  } else if (warp == kPVWarp8) {
+    // ------------------------------------------------------------ P.V issuer
+    if (lane == 0) {
+      uint32_t jg = 0, ig = 0, cnt[2] = {0, 0};
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        const int64_t w = read_item(k, true);
+        if (w < 0) break;
+        const Item8 it = item8(a, w);
+        if (!it.live) continue;
+        // the item's O buffers are free once the epilogue of item ig - 2 read them
+        if (ig >= 2) ok = mbar_wait(bar(L::bOFree + (ig & 1)), ((ig >> 1) - 1) & 1, a.status);
+        for (int j = 0; j < it.nb && ok; ++j, ++jg) {
+          const int s = static_cast<int>(jg % NS), wg = j & 1;
+          const uint32_t c = wg ? cnt[1]++ : cnt[0]++;
+          ok = mbar_wait(bar(L::bVFull + s), (jg / NS) & 1, a.status) &&
                mbar_wait(bar(L::bPFull + 2 * wg + (c & 1)), (c >> 1) & 1, a.status);
           if (!ok) break;
           fence_proxy_async();
@@ -486,14 +504,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                           (j > 1 || kk > 0) ? 1u : 0u);
           mma_commit(bar(L::bVEmpty + s));
           mma_commit(bar(L::bPVDone + 2 * wg + (c & 1)));
-          if (j + kAhead8 < it.nb) issue_s(j + kAhead8);
         }
         if (!ok) break;
-        mma_commit(bar(L::bQEmpty + (ig & 1)));
         mma_commit(bar(L::bODone + (ig & 1)));
-        jg += it.nb;
-        cnt[0] += (it.nb + 1) >> 1;
-        cnt[1] += it.nb >> 1;
         ++ig;
       }
     }
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (e_up) eref = eb;
         // P buffer c % 2 is free once P.V(c - 2) is done; O may be rescaled
         // once P.V(c - 1) is done
-        if (j >= 4 || c >= 2)
+        if (c >= 2)
           bad = bad ||
                 !mbar_wait(bar(L::bPVDone + 2 * wg + (c & 1)), ((c >> 1) - 1) & 1, a.status);
         if (j > wg && (up != 0 || e_down != 1.f)) {
@@ -761,10 +774,219 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp8) {
+  if (warp == kPVWarp8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// ---------------------------------------------------------------- plan
+// One CTA turns the index arrays into per-request records and the units
+// (request, split), checks each request (and the bounds of a bounded call),
+// and clears the status word and the item counter.  A plan that does not fit
+// the launch retires every unit and fills the outputs with NaN.  The general
+// planner (plan.cu) does the same for every kind of call with four scans and
+// three passes over the units; a decode needs one scan.
+constexpr int kPlanThreads8 = 512;
+
+__device__ __forceinline__ bool keys_of(const PlanArgs &p, int b, int32_t &kv_len) {
+  const int64_t pages = static_cast<int64_t>(p.kv_indptr[b + 1]) - p.kv_indptr[b];
+  const int32_t last = p.kv_last_page_len[b];
+  const int64_t kl = pages > 0 ? (pages - 1) * p.page_size + last : 0;
+  const bool ok = pages > 0 && last >= 1 && last <= p.page_size && kl <= INT32_MAX / 2 &&
+                  (!p.bounded || kl <= p.max_kv_len);
+  kv_len = ok ? static_cast<int32_t>(kl) : 0;
+  return ok;
+}
+
+__global__ void __launch_bounds__(kPlanThreads8) plan_decode_fp8_kernel(const PlanArgs p) {
+  __shared__ int64_t s_warp[kPlanThreads8 / 32];
+  __shared__ int32_t s_off[kPlanThreads8 + 1]; // first unit of each request of the chunk
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_launch(); // the decode may set itself up meanwhile
+  grid_dep_wait();   // this kernel rewrites the workspace
+  // every request's check and the totals first: nothing is written past the
+  // capacities of the launch
+  bool bad = tid == 0 && p.kv_indptr[0] < 0;
+  int64_t units = 0, rows = 0; // unit and partial-row totals of this thread's requests
+  for (int b = tid; b < p.batch; b += kPlanThreads8) {
+    int32_t kv_len;
+    bad = !keys_of(p, b, kv_len) || bad;
+    const int32_t nsp = (kv_len + p.split - 1) / p.split;
+    units += nsp;
+    rows += nsp > 1 ? nsp : 0;
+  }
+  if (tid == 0) {
+    p.status[0] = 0;
+    p.status[kStatusWorkCounter] = 0;
+  }
+  auto block_sum = [&](int64_t v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    __syncthreads();
+    if (lane == 0) s_warp[warp] = v;
+    __syncthreads();
+    int64_t t = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads8 / 32; ++w) t += s_warp[w];
+    return t;
+  };
+  const bool any_bad = __syncthreads_or(bad) != 0;
+  const int64_t n_units = block_sum(units), n_rows = block_sum(rows);
+  const bool ok = !any_bad && (p.bounded ? n_units <= p.n_units_expected && n_rows <= p.part_rows_expected
+                                         : n_units == p.n_units_expected && n_rows == p.part_rows_expected);
+  if (!ok) {
+    if (tid == 0) atomicOr(p.status, kStatusPlanMismatch);
+    for (int64_t i = tid; i < p.n_units_expected; i += kPlanThreads8) p.units[i] = Unit{-1, 0, 0, 0};
+    for (int64_t i = tid; i < p.out_elems; i += kPlanThreads8) p.out[i] = 0x7fc0u; // bf16 NaN
+    for (int64_t i = tid; p.lse && i < p.lse_elems; i += kPlanThreads8)
+      p.lse[i] = __int_as_float(0x7fc00000);
+    return;
+  }
+  int64_t unit0 = 0, row0 = 0; // of the chunk of kPlanThreads8 requests
+  for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads8) {
+    const int b = b0 + tid;
+    int32_t kv_len = 0;
+    if (b < p.batch) keys_of(p, b, kv_len);
+    const int32_t nsp = (kv_len + p.split - 1) / p.split;
+    // units in the low half, partial rows in the high half (each below 2^31)
+    const int64_t mine = nsp + (static_cast<int64_t>(nsp > 1 ? nsp : 0) << 32);
+    int64_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += x;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads8 / 32; ++w) {
+      before += w < warp ? s_warp[w] : 0;
+      total += s_warp[w];
+    }
+    const int64_t excl = before + incl - mine;
+    s_off[tid] = static_cast<int32_t>(excl & 0xffffffff);
+    if (tid == 0) s_off[kPlanThreads8] = static_cast<int32_t>(total & 0xffffffff);
+    if (b < p.batch) {
+      ReqInfo r;
+      r.q_start = b;
+      r.q_len = 1;
+      r.kv_len = kv_len;
+      r.nsp = nsp;
+      r.rowbase = nsp > 1 ? row0 + (excl >> 32) : -1;
+      r.page_base = p.kv_indptr[b];
+      r.mbase = 0;
+      p.reqs[b] = r;
+    }
+    __syncthreads();
+    const int32_t n = s_off[kPlanThreads8], nb = min(kPlanThreads8, p.batch - b0);
+    for (int32_t i = tid; i < n; i += kPlanThreads8) {
+      int lo = 0, hi = nb - 1; // largest request with s_off <= i
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_off[mid] <= i) lo = mid;
+        else hi = mid - 1;
+      }
+      p.units[unit0 + i] = Unit{b0 + lo, 0, i - s_off[lo], 1};
+    }
+    unit0 += n;
+    row0 += total >> 32;
+  }
+  for (int64_t i = unit0 + tid; i < p.n_units_expected; i += kPlanThreads8)
+    p.units[i] = Unit{-1, 0, 0, 0}; // a bounded launch has room for more
+}
+
+// ---------------------------------------------------------------- merge
+// Joins a row's split states: with L = max lse_s and w_s = e^(lse_s - L),
+// o = sum w_s o_s / sum w_s in ascending split order.  A warp per (request, q
+// head); the weights of 32 splits come from their lanes at once and eight
+// states' loads are in flight, so a row costs a few memory latencies whatever
+// its number of splits (the streamed merge of the bf16 calls walks a token's
+// heads and splits one after the other in one CTA: 17 us for 8 requests).
+constexpr int kMergeWarps8 = 8;
+
+template <int V>
+__global__ void __launch_bounds__(kMergeWarps8 * 32) merge_decode_fp8_kernel(const AttnArgs a) {
+  constexpr int kChunk = V == 4 ? 8 : 4; // states in flight
+  const int lane = threadIdx.x & 31;
+  grid_dep_wait(); // the partials are complete
+  if (a.status[0] & kStatusPlanMismatch) return; // the outputs already hold NaN
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps8 + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(a.batch) * a.Hq) return;
+  const int b = static_cast<int>(row / a.Hq), h = static_cast<int>(row - static_cast<int64_t>(b) * a.Hq);
+  const ReqInfo r = a.reqs[b];
+  if (r.nsp <= 1) return; // the decode wrote the final row
+  const float *lse = a.part_lse + r.rowbase * a.Hq + h;
+  const float *part = a.part_o + (r.rowbase * a.Hq + h) * a.D + lane * 4;
+  const int64_t step = static_cast<int64_t>(a.Hq) * a.D;
+  float L = -INFINITY, sum = 0.f, o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+  for (int s0 = 0; s0 < r.nsp; s0 += 32) {
+    const int n = min(32, r.nsp - s0);
+    const float mine = lane < n ? __ldg(lse + static_cast<int64_t>(s0 + lane) * a.Hq) : -INFINITY;
+    const float top = fmaxf(L, warp_max(mine));
+    const float base = top == -INFINITY ? 0.f : top;
+    const float down = ex2((L - base) * kLog2e); // 0 for the first chunk
+    const float w = ex2((mine - base) * kLog2e); // 0 for a state without keys
+    float wsum = w;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
+    sum = __fadd_rn(__fmul_rn(sum, down), wsum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = __fmul_rn(o[i], down);
+    L = top;
+    for (int k0 = 0; k0 < n; k0 += kChunk) {
+      float4 v[kChunk][V / 4];
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c)
+#pragma unroll
+        for (int e = 0; e < V / 4; ++e) {
+          v[c][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 + c < n && e * 128 + lane * 4 < a.D)
+            v[c][e] = __ldg(reinterpret_cast<const float4 *>(part + (s0 + k0 + c) * step + e * 128));
+        }
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c) {
+        const float wc = __shfl_sync(0xffffffffu, w, (k0 + c) & 31); // 0 past the last state
+        if (k0 + c < n) {
+#pragma unroll
+          for (int e = 0; e < V / 4; ++e) {
+            o[4 * e] = __fmaf_rn(wc, v[c][e].x, o[4 * e]);
+            o[4 * e + 1] = __fmaf_rn(wc, v[c][e].y, o[4 * e + 1]);
+            o[4 * e + 2] = __fmaf_rn(wc, v[c][e].z, o[4 * e + 2]);
+            o[4 * e + 3] = __fmaf_rn(wc, v[c][e].w, o[4 * e + 3]);
+          }
+        }
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+#pragma unroll
+  for (int e = 0; e < V / 4; ++e)
+    if (e * 128 + lane * 4 < a.D) {
+      uint2 x;
+      x.x = pack_bf16(__fmul_rn(o[4 * e], inv), __fmul_rn(o[4 * e + 1], inv));
+      x.y = pack_bf16(__fmul_rn(o[4 * e + 2], inv), __fmul_rn(o[4 * e + 3], inv));
+      *reinterpret_cast<uint2 *>(a.out + row * a.D + e * 128 + lane * 4) = x;
+    }
+  if (a.lse && lane == 0)
+    a.lse[row] = sum == 0.f ? -INFINITY : __fadd_rn(L, __fmul_rn(lg2(sum), kLn2));
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*fn)(Params...), unsigned grid, unsigned block, cudaStream_t s,
+                           const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {chained_launch_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
 template <int G, int LPR>
@@ -799,6 +1021,20 @@ cudaError_t launch_f8_g(const DecodeFp8Args &f, cudaStream_t s) {
 }
 
 } // namespace
+
+cudaError_t launch_plan_decode_fp8(const PlanArgs &p, cudaStream_t s) {
+  return launch_chained(plan_decode_fp8_kernel, 1, kPlanThreads8, s, p);
+}
+
+cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.Hq;
+  const int64_t grid = (rows + kMergeWarps8 - 1) / kMergeWarps8;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return a.D <= 128 ? launch_chained(merge_decode_fp8_kernel<4>, static_cast<unsigned>(grid),
+                                     kMergeWarps8 * 32, s, a)
+                    : launch_chained(merge_decode_fp8_kernel<8>, static_cast<unsigned>(grid),
+                                     kMergeWarps8 * 32, s, a);
+}
 
 cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s) {
   if (f.a.n_units == 0) return cudaSuccess;
