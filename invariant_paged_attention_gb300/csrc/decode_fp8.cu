@@ -13,7 +13,7 @@
 // q is scaled by a power of two per head, so that q = hi + lo/16 is exact
 // down to 2^-11 of the row's largest element and off by at most 2^-22 of it
 // below; a weight keeps 8 significant bits (what a bf16 weight keeps) down to
-// 2^-13 of the largest.  The key's scale multiplies its score, the value's
+// 2^-10 of the largest.  The key's scale multiplies its score, the value's
 // scale its weight, relative to the block maximum of the value scales (a
 // power of two: exact).  Products, sums, the running maximum and the row sum
 // are fp32.  Converting the rows instead (8 -> 16 bits through registers and
@@ -57,12 +57,13 @@ constexpr int kCopyWarp8 = 14;
 constexpr int kCopyWarps8 = 8;
 constexpr int kThreads8 = (kCopyWarp8 + kCopyWarps8) * 32;
 constexpr int kCopyThreads8 = kCopyWarps8 * 32;
-constexpr int kReaders8 = kCopyWarp8 + kCopyWarps8; // warps that read the mailbox
+constexpr int kReaders8 = kThreads8 / 32;         // warps that read the mailbox
+constexpr int kCopyKeys8 = kKeys8 / kCopyWarps8;  // keys of a block a copy warp takes
 constexpr int kScaleSlots8 = 8;
-// The running maximum moves when a block exceeds it by 2^2: weights stay
-// below 2^2, and 2^6 more fills e4m3's range (448).
-constexpr float kLazy8 = 2.0f;
-constexpr int kBoost8 = 6;
+// The running maximum moves when a block exceeds it by 2^4: weights stay
+// below 2^4, and 2^4 more fills e4m3's range (448).
+constexpr float kLazy8 = 4.0f;
+constexpr int kBoost8 = 4;
 
 // LPR: lanes (16-byte chunks) per row: 4 (head_dim 64), 8 (96, 128), 16 (256)
 template <int LPR>
@@ -142,8 +143,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
   constexpr int NP = L::NP, NS = L::NS;
   constexpr int LO = G <= 4 ? 4 : 8; // column of a head's second term
   constexpr int NL = 2 * LO;         // columns in use
-  constexpr int kRows = kCopyThreads8 / LPR; // keys a pass of the copy threads takes
-  constexpr int NK = kKeys8 / kRows;         // keys a copy thread takes per block
   constexpr uint32_t kIdescS = idesc_e4m3(128, kN8, false, false);
   constexpr uint32_t kIdescPV = idesc_e4m3(128, kN8, true, true);
   constexpr uint32_t kTmemCols = NP == 1 ? 128 : 256;
@@ -225,9 +224,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
   if (warp >= kCopyWarp8) {
     // ------------------------------------------------------------ copies
-    // Thread pt copies chunk cc of keys kb, kb + kRows, ... of a block.
+    // A warp takes 16 keys of a block; lane l < 16 finds the row of one (its
+    // page index a block ahead) and hands it round, then the lanes copy chunk
+    // cc of every (32 / LPR)-th key.
     const int pt = tid - kCopyWarp8 * 32;
-    const int cc = pt % LPR, kb = pt / LPR;
+    const int cc = lane % LPR, kb = lane / LPR;
+    const int key_w = (pt >> 5) * kCopyKeys8; // the warp's first key of a block
     const int page_mask = (1 << a.page_shift) - 1;
     const bool in_row = cc * 16 < a.D; // head_dim 96: six of eight lanes
     const uint32_t piece_off = static_cast<uint32_t>(cc >> 3) * kPiece8;
@@ -264,32 +266,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
         post_next(k);
         continue;
       }
-      // page of each of this thread's keys of block j (-1: none); a block ahead
-      auto fetch = [&](int j, int32_t (&pg)[NK]) {
-#pragma unroll
-        for (int n = 0; n < NK; ++n) {
-          const int32_t key = it.key_begin + j * kKeys8 + kb + kRows * n;
-          pg[n] = key < it.key_end ? __ldg(a.kv_indices + it.r.page_base + (key >> a.page_shift))
-                                   : -1;
-        }
+      const int32_t key_l = lane < kCopyKeys8 ? it.key_begin + key_w + lane : INT32_MAX / 2;
+      auto page_of = [&](int32_t key) { // -1: no such key
+        return key < it.key_end ? __ldg(a.kv_indices + it.r.page_base + (key >> a.page_shift)) : -1;
       };
-      int32_t pg_next[NK];
-      fetch(0, pg_next);
+      int32_t page = page_of(key_l);
       for (int j = 0; j < it.nb; ++j, ++jg) {
-        int64_t row[NK];
-        uint32_t good = 0;
-#pragma unroll
-        for (int n = 0; n < NK; ++n) {
-          const int32_t key = it.key_begin + j * kKeys8 + kb + kRows * n;
-          const bool valid = key < it.key_end && pg_next[n] >= 0 && pg_next[n] < a.num_pages;
-          if (key < it.key_end && !valid) atomicOr(a.status, kStatusBadPage);
-          row[n] = valid ? ((static_cast<int64_t>(pg_next[n]) << a.page_shift) +
-                            (key & page_mask)) * a.Hkv + it.kvh
-                         : 0;
-          good |= static_cast<uint32_t>(valid) << n;
-        }
-        fetch(j + 1, pg_next); // in flight while this block's copies are issued
+        const int32_t key = key_l + j * kKeys8;
+        const bool good = page >= 0 && page < a.num_pages;
+        if (key < it.key_end && !good) atomicOr(a.status, kStatusBadPage);
+        // the lane's row (-1: zeros)
+        const int64_t row = good ? ((static_cast<int64_t>(page) << a.page_shift) +
+                                    (key & page_mask)) * a.Hkv + it.kvh
+                                 : -1;
+        page = page_of(key + kKeys8); // in flight while this block's copies are issued
         const int s = static_cast<int>(jg % NS);
+#pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           if (jg >= static_cast<uint32_t>(NS) &&
               !mbar_wait(bar((kv == 0 ? L::bKEmpty : L::bVEmpty) + s), ((jg / NS) - 1) & 1,
@@ -299,14 +291,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
           }
           const uint32_t base = (kv == 0 ? kstage(s) : vstage(s)) + piece_off;
           const uint8_t *src = (kv == 0 ? f.k_codes : f.v_codes) + cc * 16;
-          if (in_row) {
 #pragma unroll
-            for (int n = 0; n < NK; ++n) {
-              const int k8 = kb + kRows * n;
+          for (int i = 0; i < kCopyKeys8 * LPR / 32; ++i) {
+            const int kk = i * (32 / LPR) + kb; // key of the warp's 16
+            const int64_t r = __shfl_sync(0xffffffffu, row, kk);
+            const int k8 = key_w + kk;
+            if (in_row)
               cp_async16(base + static_cast<uint32_t>(k8) * 128 +
                              ((static_cast<uint32_t>(cc & 7) ^ static_cast<uint32_t>(k8 & 7)) << 4),
-                         src + row[n] * a.D, (good >> n) & 1u);
-            }
+                         src + (r < 0 ? 0 : r * a.D), r >= 0);
           }
           cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
         }

@@ -8,9 +8,9 @@ from tests.gpu_util import same_bits
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-# weights below 2^-12 of the largest lie under the second 8-bit term's last
-# place: off by at most half of 2^-19 of the largest weight, taken at the
-# largest value scale of the request (the sum |v| of the bound is taken there)
+# small weights lie under the second 8-bit term's last place: off by at most
+# half of 2^-17 of the largest weight, 2 * FLOOR below, taken at the largest
+# value scale of the request
 FLOOR = 2.0 ** -19
 
 
