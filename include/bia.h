@@ -100,6 +100,8 @@ extern "C" {
 /* Default fixed split-KV sizes ("sglang PR #10417", Modifications). */
 #define BIA_PREFILL_SPLIT 4096
 #define BIA_DECODE_SPLIT 2048
+/* Largest (and default) split-KV size of the 8-bit decode. */
+#define BIA_DECODE_FP8_SPLIT 1024
 
 typedef enum bia_status {
     BIA_OK = 0,
@@ -483,9 +485,11 @@ BIA_API int bia_gather_paged_kv_fp8(const bia_attn_desc *desc, const void *k_cac
 
 /*
  * bia_decode_paged over the 8-bit cache: q, out and lse, the page table, the
- * fixed split-KV tiles (0 = BIA_DECODE_SPLIT) and their ascending merge, the
- * ownership and the errors are the same.  The workspace is
- * bia_decode_fp8_workspace_size's.
+ * fixed split-KV tiles and their ascending merge, the ownership and the
+ * errors are the same.  split_size: a multiple of 128 up to
+ * BIA_DECODE_FP8_SPLIT, 0 = BIA_DECODE_FP8_SPLIT (a larger one:
+ * BIA_ERR_UNSUPPORTED, as are caches of 2^32 - 1 (key, kv head) rows and
+ * more).  The workspace is bia_decode_fp8_workspace_size's.
  */
 BIA_API int bia_decode_paged_fp8(const bia_attn_desc *desc, const void *q, const void *k_cache,
                          const void *v_cache, const void *k_scale, const void *v_scale,

@@ -31,6 +31,7 @@ BIA_ERR_CUDA = -4
 BIA_Q_TILE_ROWS = 128
 BIA_PREFILL_SPLIT = 4096
 BIA_DECODE_SPLIT = 2048
+BIA_DECODE_FP8_SPLIT = 1024
 
 # every symbol include/bia.h exports
 EXPORTS = ("bia_prefill_paged", "bia_prefill_workspace_size", "bia_decode_paged",

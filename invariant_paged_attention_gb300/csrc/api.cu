@@ -941,14 +941,18 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
       misaligned(v_cache, 16) || misaligned(out, 16) || misaligned(lse, 4) ||
       misaligned(kv_indptr, 4) || misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
     return BIA_ERR_INVALID_ARG;
-  if (split == 0) split = BIA_DECODE_SPLIT;
+  if (split == 0) split = BIA_DECODE_FP8_SPLIT;
+  if (split > BIA_DECODE_FP8_SPLIT) return BIA_ERR_UNSUPPORTED;
   HostPlan hp;
   rc = bounds ? bounded_plan(bounds, batch, 1, split, 1, 1, 1, 0, true, &hp)
               : host_plan(desc, nullptr, kvp_host, last_host, batch, 1, split, 1, 1, 1, 0, &hp);
   if (rc != BIA_OK) return rc;
   if (hp.n_units * desc->num_kv_heads > INT32_MAX) return BIA_ERR_UNSUPPORTED;
-  const WsLayout w = bia::make_layout(batch, 0, hp.n_units, 0, hp.part_rows,
-                                      desc->num_qo_heads, desc->head_dim);
+  // rows of the caches are numbered in 32 bits
+  if (num_pages > INT64_C(0xfffffffe) / (static_cast<int64_t>(desc->page_size) * desc->num_kv_heads))
+    return BIA_ERR_UNSUPPORTED;
+  const WsLayout w = bia::make_layout_fp8(batch, hp.n_units, hp.part_rows, desc->num_qo_heads,
+                                          desc->head_dim);
   if (workspace_bytes < w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
   rc = check_resident({{"q", q},
                        {"k_cache", k_cache},
@@ -981,8 +985,8 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   pa.lse_elems = hp.total_q * desc->num_qo_heads;
   pa.status = reinterpret_cast<int32_t *>(ws + w.status);
   pa.reqs = reinterpret_cast<bia::ReqInfo *>(ws + w.reqs);
-  pa.units = reinterpret_cast<bia::Unit *>(ws + w.units);
-  cudaError_t e = bia::launch_plan_decode_fp8(pa, st);
+  bia::UnitFp8 *units = reinterpret_cast<bia::UnitFp8 *>(ws + w.units);
+  cudaError_t e = bia::launch_plan_decode_fp8(pa, units, st);
   if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
   __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
 
@@ -1001,7 +1005,7 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   a.batch = batch;
   a.n_units = hp.n_units;
   a.reqs = pa.reqs;
-  a.units = pa.units;
+  f.units = units;
   a.part_o = reinterpret_cast<float *>(ws + w.part_o);
   a.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
   a.total_rows = hp.total_q;
@@ -1036,14 +1040,14 @@ size_t decode_fp8_workspace(const bia_attn_desc *desc, const bia_bounds *bounds,
                             const int32_t *kvp_host, const int32_t *last_host, int32_t batch,
                             int32_t split) {
   if (check_desc(desc) != BIA_OK) return 0;
-  if (split == 0) split = BIA_DECODE_SPLIT;
+  if (split == 0) split = BIA_DECODE_FP8_SPLIT;
+  if (split > BIA_DECODE_FP8_SPLIT) return 0;
   HostPlan hp;
   const int rc =
       bounds ? bounded_plan(bounds, batch, 1, split, 1, 1, 1, 0, true, &hp)
              : host_plan(desc, nullptr, kvp_host, last_host, batch, 1, split, 1, 1, 1, 0, &hp);
   if (rc != BIA_OK) return 0;
-  return bia::make_layout(batch, 0, hp.n_units, 0, hp.part_rows, desc->num_qo_heads,
-                          desc->head_dim)
+  return bia::make_layout_fp8(batch, hp.n_units, hp.part_rows, desc->num_qo_heads, desc->head_dim)
       .total;
 }
 

@@ -170,6 +170,11 @@ inline WsLayout make_layout(int batch, int64_t n_groups, int64_t n_units, int64_
   return w;
 }
 
+// The workspace of an 8-bit decode: two 16-byte unit records hold one UnitFp8.
+inline WsLayout make_layout_fp8(int batch, int64_t n_units, int64_t part_rows, int Hq, int D) {
+  return make_layout(batch, 0, 2 * n_units, 0, part_rows, Hq, D);
+}
+
 struct PlanArgs {
   const int32_t *qo_indptr;  // NULL for decode (one token per request)
   const int32_t *kv_indptr;
@@ -261,10 +266,21 @@ struct CacheFp8Args {
   int32_t *status; // may be NULL
 };
 
+// One split-KV tile of one request of an 8-bit decode.
+struct UnitFp8 {
+  int32_t b; // request; -1: retired
+  int32_t key_begin, key_end;
+  int32_t page_base; // kv_indptr[b]
+  int64_t prow;      // its partial row (of Hq heads); -1: the request's only tile
+  int64_t pad;
+};
+static_assert(sizeof(UnitFp8) == 32, "UnitFp8 layout");
+
 // Decode over the 8-bit paged cache: the geometry of the bf16 decode (the
-// cache pointers of `a` unused) and the codes and scales.
+// cache pointers and units of `a` unused) and the codes and scales.
 struct DecodeFp8Args {
   AttnArgs a;
+  const UnitFp8 *units;
   const uint8_t *k_codes, *v_codes; // e4m3 [num_pages, page_size, Hkv, D]
   const uint8_t *k_scale, *v_scale; // e8m0 [num_pages, page_size, Hkv]
 };
@@ -306,7 +322,7 @@ cudaError_t launch_decode_tc(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s); // head_dim 256
 cudaError_t launch_cache_fp8(const CacheFp8Args &a, bool append, cudaStream_t s);
-cudaError_t launch_plan_decode_fp8(const PlanArgs &p, cudaStream_t s);
+cudaError_t launch_plan_decode_fp8(const PlanArgs &p, UnitFp8 *units, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s);
 // Packed keys and values: head_dim 64, 96 and 128; 256

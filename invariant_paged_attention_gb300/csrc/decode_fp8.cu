@@ -1,6 +1,6 @@
 // Split-KV decode of one query token per request over the 8-bit paged cache
-// (fp8.cuh states the format) on the tensor cores, with the fixed split-KV
-// tiles and ascending merge of the bf16 decode ("sglang PR #10417 [POC]
+// (fp8.cuh states the format) on the tensor cores, with fixed split-KV tiles
+// joined in ascending order as the bf16 decode does ("sglang PR #10417 [POC]
 // Support deterministic inference", Modifications):
 //   s_j = sm_scale * 2^ek_j * <q, ck_j>,   o = sum_j softmax(s)_j 2^ev_j cv_j
 //
@@ -13,30 +13,32 @@
 // q is scaled by a power of two per head, so that q = hi + lo/16 is exact
 // down to 2^-11 of the row's largest element and off by at most 2^-22 of it
 // below; a weight keeps 8 significant bits (what a bf16 weight keeps) down to
-// 2^-10 of the largest.  The key's scale multiplies its score, the value's
-// scale its weight, relative to the block maximum of the value scales (a
-// power of two: exact).  Products, sums, the running maximum and the row sum
-// are fp32.  Converting the rows instead (8 -> 16 bits through registers and
-// shared memory) would cost more issue slots than the copies themselves.
+// 2^-14 of the largest.  The key's scale multiplies its score, the value's
+// scale its weight, relative to the largest value scale of the tile (a power
+// of two: exact).  Products, sums, the maximum and the row sum are fp32.
+// Converting the rows instead (8 -> 16 bits through registers and shared
+// memory) would cost more issue slots than the copies themselves.
 //
 // HBM bound: D + 1 bytes per key, head and cache.  At 6.5 TB/s an SM has
 // ~1450 cycles for a 128-key block of head_dim 128, half of what the bf16
-// decode has, so a block's latency chain (S, maximum, weights, P.V) does not
-// fit one after the other: two softmax warpgroups take alternate blocks, each
-// with its own running state and accumulator, joined in the item's epilogue
-// (the assignment goes by the block's index in its split, so the bits depend
-// on the split alone).
+// decode has, and an online softmax does not fit: per block its chain of
+// waits, maximum exchange and rescaling took ~5000 cycles of a warpgroup, 3.8
+// TB/s with two of them on alternate blocks.  So a tile (at most 1024 keys)
+// takes two passes: all its scores first, kept in TMEM (16 columns a block,
+// two tiles' worth), one maximum over the tile, then the weights.  Nothing is
+// rescaled, the weights of a tile are at most 1 and fill e4m3's range, and
+// the warps meet once a tile.  The key rows of a tile are copied before its
+// value rows, through a ring of their own each (one ring for both would let S
+// of the next tile wait on a stage two uses ahead, which an mbarrier's parity
+// cannot tell from the use before).
 //
-// Persistent: one CTA per SM takes (unit, kv head) items from a counter and
-// posts them to its roles through a mailbox, as the bf16 decode does.  Roles:
-// warps 0-3 and 4-7 softmax + epilogue (WG 0 even blocks, WG 1 odd blocks;
-// the epilogue alternates by item), 8 issues P.V (owns TMEM), 9 issues S, 10-13
-// hand over the scales of a block's keys and the q rows, 14.. copy (16-byte
-// cp.async into the swizzled operand layout, page indices a block ahead).  S
-// and P.V come from two threads because each waits for its own inputs: from
-// one, S of a later block waited in front of a P.V that was ready (head_dim
-// 256, whose rings hold three blocks: 2.8 TB/s).  S also runs ahead into the
-// next item.
+// Persistent: one CTA per SM takes (unit, kv head) items from a counter.
+// Warps 0-3 and 4-7 softmax (even and odd blocks; the epilogue alternates by
+// item), 8 issues P.V (owns TMEM), 9 issues S, 10-13 prepare an item: the
+// rows and scales of its keys, its q; 14-21 copy (16-byte cp.async into the
+// swizzled operand layout), 22 takes the items and posts them through a
+// mailbox in shared memory, one ahead of the copies.  An item's result
+// depends on its own keys alone, whichever CTA takes it.
 #include <algorithm>
 
 #include "bia_internal.h"
@@ -47,105 +49,93 @@ namespace bia {
 
 namespace {
 
-constexpr int kKeys8 = 128;            // keys per block: the MMAs' M
-constexpr int kPiece8 = kKeys8 * 128;  // 128 rows x 128 codes, SW128
-constexpr int kN8 = 16;                // the MMAs' N: hi and lo of up to 8 heads
+constexpr int kKeys8 = 128;           // keys per block: the MMAs' M
+constexpr int kPiece8 = kKeys8 * 128; // 128 rows x 128 codes, SW128
+constexpr int kN8 = 16;               // the MMAs' N: hi and lo of up to 8 heads
+constexpr int kBlocks8 = BIA_DECODE_FP8_SPLIT / kKeys8; // blocks of a tile
 constexpr int kPVWarp8 = 8;
 constexpr int kSWarp8 = 9;
-constexpr int kAuxWarp8 = 10;          // four warps: thread t is key t
+constexpr int kAuxWarp8 = 10;
 constexpr int kCopyWarp8 = 14;
 constexpr int kCopyWarps8 = 8;
-constexpr int kThreads8 = (kCopyWarp8 + kCopyWarps8) * 32;
+constexpr int kItemWarp8 = kCopyWarp8 + kCopyWarps8;
+constexpr int kThreads8 = (kItemWarp8 + 1) * 32;
 constexpr int kCopyThreads8 = kCopyWarps8 * 32;
-constexpr int kReaders8 = kThreads8 / 32;         // warps that read the mailbox
-constexpr int kCopyKeys8 = kKeys8 / kCopyWarps8;  // keys of a block a copy warp takes
-constexpr int kScaleSlots8 = 8;
-// The running maximum moves when a block exceeds it by 2^4: weights stay
-// below 2^4, and 2^4 more fills e4m3's range (448).
-constexpr float kLazy8 = 4.0f;
-constexpr int kBoost8 = 4;
+constexpr int kCopyKeys8 = kKeys8 / kCopyWarps8; // keys of a block a copy warp takes
+constexpr int kReaders8 = kItemWarp8;            // warps that read the mailbox
+constexpr int kBoost8 = 8; // weights <= 1 times 2^8 fill e4m3's range (448)
+constexpr uint32_t kNoRow8 = 0xffffffffu; // a key past the end or on a bad page: zeros
 
 // LPR: lanes (16-byte chunks) per row: 4 (head_dim 64), 8 (96, 128), 16 (256)
 template <int LPR>
 struct Smem8 {
   static constexpr int NP = LPR > 8 ? 2 : 1; // 128-code pieces of a row
-  static constexpr int kStage = NP * kPiece8;
-  static constexpr int NS = NP == 1 ? 6 : 3; // blocks in the key ring and in the value ring
+  // A ring stage holds SB blocks: two for rows of up to 128 codes, so that a
+  // barrier is waited for (~300 cycles even when it is complete) and the
+  // async proxy fenced every 256 keys
+  static constexpr int SB = NP == 1 ? 2 : 1;
+  static constexpr int kTileStages = kBlocks8 / SB;
+  static constexpr int kBlock = NP * kPiece8;
+  static constexpr int kStage = SB * kBlock;
+  static constexpr int NS = 3;  // stages in the key ring and in the value ring
+  static constexpr int NPS = 4; // stages of P
   static constexpr int kKRing = 0;
   static constexpr int kVRing = kKRing + NS * kStage;
   static constexpr int kQBuf = NP * kN8 * 128;
-  static constexpr int kQ = kVRing + NS * kStage; // 2 q buffers
-  static constexpr int kPBuf = kKeys8 * kN8;
-  static constexpr int kP = kQ + 2 * kQBuf;       // [WG][2]
-  static constexpr int kKs = kP + 4 * kPBuf;      // float [slot][128]
-  static constexpr int kVe = kKs + kScaleSlots8 * 512; // uint8 [slot][128]
-  static constexpr int kEmax = kVe + kScaleSlots8 * 128; // int [slot][4]
-  static constexpr int kQs = kEmax + kScaleSlots8 * 16;  // float [2][8]
-  static constexpr int kRed = kQs + 64;           // float [WG][2][4][8]
-  static constexpr int kLred = kRed + 512;        // float [WG][4][8]
-  static constexpr int kStat = kLred + 256;       // float [2][WG][2][8] m, l; then int [2][WG] E
-  static constexpr int kStatE = kStat + 256;
-  static constexpr int kItems = kStatE + 16;      // int64 [4]
-  static constexpr int kSlot = kItems + 32;
+  static constexpr int kQ = kVRing + NS * kStage; // [2]
+  static constexpr int kPBuf = SB * kKeys8 * kN8;
+  static constexpr int kP = kQ + 2 * kQBuf;      // [NPS]
+  static constexpr int kTile = kBlocks8 * kKeys8;
+  static constexpr int kRows = kP + NPS * kPBuf;      // uint32 [2][tile]: cache rows
+  static constexpr int kKe = kRows + 2 * kTile * 4;   // uint8 [2][tile]: key scales
+  static constexpr int kVe = kKe + 2 * kTile;         // uint8 [2][tile]: value scales
+  static constexpr int kEmax = kVe + 2 * kTile;       // int [2][kBlocks8]
+  static constexpr int kQs = kEmax + 2 * kBlocks8 * 4; // float [2][8]
+  static constexpr int kRed = kQs + 64;           // float [2][8 warps][8]
+  static constexpr int kStat = kRed + 512;        // float [2][8 warps][8]
+  static constexpr int kItems = kStat + 512;      // 32-byte records [4]
+  static constexpr int kSlot = kItems + 128;
   static constexpr int kBar = kSlot + 16;
   static constexpr int bKFull = 0, bKEmpty = bKFull + NS, bVFull = bKEmpty + NS,
                        bVEmpty = bVFull + NS, bQFull = bVEmpty + NS, bQEmpty = bQFull + 2,
-                       bSFull = bQEmpty + 2, bPFull = bSFull + 4, bPVDone = bPFull + 4,
-                       bODone = bPVDone + 4, bOFree = bODone + 2, bStat = bOFree + 2,
-                       bScFull = bStat + 2, bScEmpty = bScFull + kScaleSlots8,
-                       bItemFull = bScEmpty + kScaleSlots8, bItemEmpty = bItemFull + 4,
-                       kNumBars = bItemEmpty + 4;
+                       bRows = bQEmpty + 2, bRowsFree = bRows + 2, bAux = bRowsFree + 2,
+                       bAuxFree = bAux + 2, bMax = bAuxFree + 2, bStat = bMax + 2,
+                       bODone = bStat + 2, bOFree = bODone + 2, bSFull = bOFree + 2,
+                       bPFull = bSFull + 2 * kTileStages, bPVDone = bPFull + NPS,
+                       bItemFull = bPVDone + NPS,
+                       bItemEmpty = bItemFull + 4, bGo = bItemEmpty + 4, kNumBars = bGo + 1;
   static constexpr int kAlloc = kBar + kNumBars * 8 + 1024;
   static_assert(kAlloc <= 232448, "shared memory per CTA");
-  static_assert(kQ % 1024 == 0 && kQBuf % 1024 == 0, "q on the swizzle period");
+  static_assert(kQ % 1024 == 0 && kQBuf % 1024 == 0 && kBar % 8 == 0, "alignment");
 };
 
-// Work item w: unit w / Hkv, kv head w % Hkv.
+// One item: a tile of one request for one kv head.
 struct Item8 {
-  bool live;
-  int kvh;
-  Unit u;
-  ReqInfo r;
-  int32_t key_begin, key_end;
-  int nb; // 128-key blocks
+  int32_t nb;  // 128-key blocks; -1: no more items
+  int32_t kvh;
+  int32_t b;   // request
+  int32_t key_begin, key_end, page_base;
+  int64_t prow; // row of the partial states, in units of Hq heads; -1: one tile
 };
-
-__device__ __forceinline__ Item8 item8(const AttnArgs &a, int64_t w) {
-  Item8 it;
-  const int64_t unit = w / a.Hkv;
-  it.kvh = static_cast<int>(w - unit * a.Hkv);
-  it.u = a.units[unit];
-  it.live = it.u.b >= 0;
-  it.nb = 0;
-  if (!it.live) return it;
-  it.r = a.reqs[it.u.b];
-  it.key_begin = it.u.split * a.split;
-  it.key_end = min(it.key_begin + a.split, it.r.kv_len);
-  it.nb = (it.key_end - it.key_begin + kKeys8 - 1) / kKeys8;
-  return it;
-}
+static_assert(sizeof(Item8) == 32, "Item8 layout");
 
 template <int NL>
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[NL]) {
   if constexpr (NL == 8) tmem_ld8(taddr, r);
   else tmem_ld16(taddr, r);
 }
-template <int NL>
-__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[NL]) {
-  if constexpr (NL == 8) tmem_st8(taddr, r);
-  else tmem_st16(taddr, r);
-}
 
 template <int G, int LPR>
 __global__ void __launch_bounds__(kThreads8, 1)
     decode_fp8_kernel(const __grid_constant__ DecodeFp8Args f) {
   using L = Smem8<LPR>;
-  constexpr int NP = L::NP, NS = L::NS;
+  constexpr int NP = L::NP, NS = L::NS, SB = L::SB, NPS = L::NPS;
+  constexpr int kSBars = 2 * L::kTileStages; // S stages in TMEM: two tiles
   constexpr int LO = G <= 4 ? 4 : 8; // column of a head's second term
   constexpr int NL = 2 * LO;         // columns in use
   constexpr uint32_t kIdescS = idesc_e4m3(128, kN8, false, false);
   constexpr uint32_t kIdescPV = idesc_e4m3(128, kN8, true, true);
-  constexpr uint32_t kTmemCols = NP == 1 ? 128 : 256;
+  constexpr uint32_t kTmemCols = 512;
   const AttnArgs &a = f.a;
 
   extern __shared__ uint8_t smem_raw[];
@@ -153,15 +143,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + L::kBar + 8u * static_cast<uint32_t>(i); };
-  auto kstage = [&](int s) { return sbase + L::kKRing + static_cast<uint32_t>(s) * L::kStage; };
-  auto vstage = [&](int s) { return sbase + L::kVRing + static_cast<uint32_t>(s) * L::kStage; };
-  auto qbuf = [&](int i) { return sbase + L::kQ + static_cast<uint32_t>(i) * L::kQBuf; };
-  auto pbuf = [&](int w, uint32_t c) {
-    return sbase + L::kP + (2u * static_cast<uint32_t>(w) + (c & 1u)) * L::kPBuf;
-  };
+  auto kstage = [&](uint32_t s) { return sbase + L::kKRing + s * L::kStage; };
+  auto vstage = [&](uint32_t s) { return sbase + L::kVRing + s * L::kStage; };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kSlot);
-
-  const int64_t n_work = a.n_units * a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (warp == kPVWarp8) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -177,23 +161,27 @@ __global__ void __launch_bounds__(kThreads8, 1)
       mbar_init(bar(L::bVEmpty + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(L::bQFull + i), 4);      // the aux warps
-      mbar_init(bar(L::bQEmpty + i), 1 + 8); // the S MMAs, the softmax warps
+      mbar_init(bar(L::bQFull + i), 4);              // the aux warps
+      mbar_init(bar(L::bQEmpty + i), 1);             // the S MMAs
+      mbar_init(bar(L::bRows + i), 4);
+      mbar_init(bar(L::bRowsFree + i), kCopyWarps8);
+      mbar_init(bar(L::bAux + i), 4);
+      mbar_init(bar(L::bAuxFree + i), 8);            // the softmax warps, past pass 2
+      mbar_init(bar(L::bMax + i), 8);
+      mbar_init(bar(L::bStat + i), 8);
       mbar_init(bar(L::bODone + i), 1);
       mbar_init(bar(L::bOFree + i), 4);
-      mbar_init(bar(L::bStat + i), 2);
+    }
+    for (int i = 0; i < kSBars; ++i) mbar_init(bar(L::bSFull + i), 1);
+    for (int i = 0; i < NPS; ++i) {
+      mbar_init(bar(L::bPFull + i), 4 * SB); // the warps of the stage's blocks
+      mbar_init(bar(L::bPVDone + i), 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(L::bSFull + i), 1);
-      mbar_init(bar(L::bPFull + i), 4);
-      mbar_init(bar(L::bPVDone + i), 1);
       mbar_init(bar(L::bItemFull + i), 1);
       mbar_init(bar(L::bItemEmpty + i), kReaders8);
     }
-    for (int i = 0; i < kScaleSlots8; ++i) {
-      mbar_init(bar(L::bScFull + i), 4);
-      mbar_init(bar(L::bScEmpty + i), 4);
-    }
+    mbar_init(bar(L::bGo), 1);
     fence_mbar_init();
   }
   grid_dep_launch(); // the merge may start launching
@@ -202,148 +190,140 @@ __global__ void __launch_bounds__(kThreads8, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // TMEM columns: S^T buffers [WG][2] (lanes = keys) at 0..63, O^T buffers
-  // [item parity][WG][piece] (lanes = dims) from 64
-  auto tS = [&](int w, uint32_t c) {
-    return tmem + 16u * (2u * static_cast<uint32_t>(w) + (c & 1u));
+  // TMEM columns: S^T [item parity][block] (lanes = keys), then O^T [item
+  // parity][piece] (lanes = dims), 16 each
+  auto tS = [&](uint32_t ig, int j) {
+    return tmem + 16u * ((ig & 1u) * kBlocks8 + static_cast<uint32_t>(j));
   };
-  auto tO = [&](uint32_t ig, int w, int p) {
-    return tmem + 64u + 16u * (((ig & 1u) * 2u + static_cast<uint32_t>(w)) * NP + p);
+  auto tO = [&](uint32_t ig, int p) {
+    return tmem + 16u * (2 * kBlocks8 + (ig & 1u) * NP + static_cast<uint32_t>(p));
   };
-  volatile int64_t *items = reinterpret_cast<volatile int64_t *>(smem + L::kItems);
-  // the k-th item of this CTA (-1: no more, or a wait that ran out); read by a
-  // whole warp, or by one thread (single)
-  auto read_item = [&](uint32_t k, bool single) -> int64_t {
-    const int s = static_cast<int>(k & 3u);
-    int64_t w = -1;
-    if (mbar_wait(bar(L::bItemFull + s), (k >> 2) & 1u, a.status)) w = items[s];
-    if (!single) __syncwarp();
-    if (single || lane == 0) mbar_arrive(bar(L::bItemEmpty + s));
-    return w;
+  // the ig-th item of this CTA; nb = -1 also when the wait ran out
+  auto read_item = [&](uint32_t ig) {
+    const int s = static_cast<int>(ig & 3u);
+    Item8 it;
+    it.nb = -1;
+    if (mbar_wait(bar(L::bItemFull + s), (ig >> 2) & 1u, a.status))
+      it = *reinterpret_cast<const Item8 *>(smem + L::kItems + s * 32);
+    return it;
+  };
+  auto item_read = [&](uint32_t ig) { mbar_arrive(bar(L::bItemEmpty + static_cast<int>(ig & 3u))); };
+  // The warp-wide forms: the same answer on every lane, so that a wait that
+  // ran out takes the whole warp out (the others then run out of theirs).
+  auto wait = [&](int b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, a.status)) != 0;
+  };
+  auto warp_item = [&](uint32_t ig) {
+    Item8 it = read_item(ig);
+    if (__any_sync(0xffffffffu, it.nb < 0)) it.nb = -1;
+    if (lane == 0) item_read(ig);
+    return it;
   };
 
-  if (warp >= kCopyWarp8) {
-    // ------------------------------------------------------------ copies
-    // A warp takes 16 keys of a block; lane l < 16 finds the row of one (its
-    // page index a block ahead) and hands it round, then the lanes copy chunk
-    // cc of every (32 / LPR)-th key.
-    const int pt = tid - kCopyWarp8 * 32;
-    const int cc = lane % LPR, kb = lane / LPR;
-    const int key_w = (pt >> 5) * kCopyKeys8; // the warp's first key of a block
-    const int page_mask = (1 << a.page_shift) - 1;
-    const bool in_row = cc * 16 < a.D; // head_dim 96: six of eight lanes
-    const uint32_t piece_off = static_cast<uint32_t>(cc >> 3) * kPiece8;
-    uint32_t jg = 0;
-    bool ok = true;
-    // copy thread 0 fetches the items: the first is the CTA's own index, each
-    // next one is taken from the counter when the current item starts and
-    // posted once the item's first block of copies is issued
-    const bool fetcher = pt == 0;
-    if (fetcher) {
-      items[0] = blockIdx.x < n_work ? static_cast<int64_t>(blockIdx.x) : -1;
-      mbar_arrive(bar(L::bItemFull + 0));
-    }
-    int32_t taken = 0;
-    bool posted = false;
-    auto post_next = [&](uint32_t k) { // item k + 1
-      if (!fetcher || posted) return;
-      posted = true;
-      int64_t nw = static_cast<int64_t>(gridDim.x) + taken;
-      if (nw >= n_work) nw = -1;
-      const uint32_t kn = k + 1;
-      if (kn >= 4 && !mbar_wait(bar(L::bItemEmpty + (kn & 3u)), ((kn >> 2) - 1) & 1u, a.status))
-        nw = -1;
-      items[kn & 3u] = nw;
-      mbar_arrive(bar(L::bItemFull + (kn & 3u)));
-    };
-    for (uint32_t k = 0; ok; ++k) {
-      const int64_t w = read_item(k, false);
-      if (w < 0) break;
-      if (fetcher) taken = atomicAdd(a.status + kStatusWorkCounter, 1);
-      posted = false;
-      const Item8 it = item8(a, w);
-      if (!it.live) {
-        post_next(k);
-        continue;
-      }
-      const int32_t key_l = lane < kCopyKeys8 ? it.key_begin + key_w + lane : INT32_MAX / 2;
-      auto page_of = [&](int32_t key) { // -1: no such key
-        return key < it.key_end ? __ldg(a.kv_indices + it.r.page_base + (key >> a.page_shift)) : -1;
-      };
-      int32_t page = page_of(key_l);
-      for (int j = 0; j < it.nb; ++j, ++jg) {
-        const int32_t key = key_l + j * kKeys8;
-        const bool good = page >= 0 && page < a.num_pages;
-        if (key < it.key_end && !good) atomicOr(a.status, kStatusBadPage);
-        // the lane's row (-1: zeros)
-        const int64_t row = good ? ((static_cast<int64_t>(page) << a.page_shift) +
-                                    (key & page_mask)) * a.Hkv + it.kvh
-                                 : -1;
-        page = page_of(key + kKeys8); // in flight while this block's copies are issued
-        const int s = static_cast<int>(jg % NS);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (jg >= static_cast<uint32_t>(NS) &&
-              !mbar_wait(bar((kv == 0 ? L::bKEmpty : L::bVEmpty) + s), ((jg / NS) - 1) & 1,
-                         a.status)) {
-            ok = false;
-            break;
+  if (warp == kItemWarp8) {
+    // ------------------------------------------------------------ items
+    // The first item is the CTA's own index; each next one is taken from the
+    // counter when the copies of the current one start.
+    if (lane == 0) {
+      const int64_t n_work = a.n_units * a.Hkv;
+      int64_t w = blockIdx.x;
+      for (uint32_t ig = 0;; ++ig) {
+        Item8 it;
+        it.nb = -1;
+        if (w < n_work) {
+          const int64_t unit = w / a.Hkv;
+          const int4 u0 = __ldg(reinterpret_cast<const int4 *>(f.units + unit));
+          const int4 u1 = __ldg(reinterpret_cast<const int4 *>(f.units + unit) + 1);
+          if (u0.x >= 0) { // a retired unit: only retired ones follow
+            it.kvh = static_cast<int>(w - unit * a.Hkv);
+            it.b = u0.x;
+            it.key_begin = u0.y;
+            it.key_end = u0.z;
+            it.page_base = u0.w;
+            it.prow = static_cast<int64_t>(static_cast<uint32_t>(u1.x)) |
+                      (static_cast<int64_t>(u1.y) << 32);
+            it.nb = (it.key_end - it.key_begin + kKeys8 - 1) / kKeys8;
           }
-          const uint32_t base = (kv == 0 ? kstage(s) : vstage(s)) + piece_off;
-          const uint8_t *src = (kv == 0 ? f.k_codes : f.v_codes) + cc * 16;
+        }
+        const int s = static_cast<int>(ig & 3u);
+        if (ig >= 4 && !mbar_wait(bar(L::bItemEmpty + s), ((ig >> 2) - 1) & 1u, a.status)) it.nb = -1;
+        *reinterpret_cast<Item8 *>(smem + L::kItems + s * 32) = it;
+        mbar_arrive(bar(L::bItemFull + s));
+        if (it.nb < 0) break;
+        if (!mbar_wait(bar(L::bGo), ig & 1u, a.status)) w = n_work;
+        else w = static_cast<int64_t>(gridDim.x) + atomicAdd(a.status + kStatusWorkCounter, 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kCopyWarp8) {
+    // ------------------------------------------------------------ copies
+    // A warp copies 16 keys of each block: chunk cc of every (32 / LPR)-th.
+    const int cw = warp - kCopyWarp8;
+    const int cc = lane % LPR, kb = lane / LPR;
+    const bool in_row = cc * 16 < a.D; // head_dim 96: six of eight lanes
+    const uint32_t *rows = reinterpret_cast<const uint32_t *>(smem + L::kRows);
+    uint32_t sg = 0; // stages so far
+    bool ok = true;
+    for (uint32_t ig = 0; ok; ++ig) {
+      const Item8 it = warp_item(ig);
+      if (it.nb < 0) break;
+      const int nst = (it.nb + SB - 1) / SB;
+      if (cw == 0 && lane == 0) mbar_arrive(bar(L::bGo));
+      ok = wait(L::bRows + static_cast<int>(ig & 1), (ig >> 1) & 1);
+      for (int kv = 0; kv < 2 && ok; ++kv) {
+        const uint8_t *src = (kv == 0 ? f.k_codes : f.v_codes) + cc * 16;
+        const uint32_t *row_w = rows + (ig & 1) * L::kTile + cw * kCopyKeys8 + kb;
+        for (int st = 0; st < nst; ++st) {
+          const uint32_t ss = sg + st, s = ss % NS;
+          if (ss >= NS)
+            ok = wait((kv == 0 ? L::bKEmpty : L::bVEmpty) + static_cast<int>(s), ((ss / NS) - 1) & 1);
+          if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < kCopyKeys8 * LPR / 32; ++i) {
-            const int kk = i * (32 / LPR) + kb; // key of the warp's 16
-            const int64_t r = __shfl_sync(0xffffffffu, row, kk);
-            const int k8 = key_w + kk;
-            if (in_row)
-              cp_async16(base + static_cast<uint32_t>(k8) * 128 +
-                             ((static_cast<uint32_t>(cc & 7) ^ static_cast<uint32_t>(k8 & 7)) << 4),
-                         src + (r < 0 ? 0 : r * a.D), r >= 0);
+          for (int hb = 0; hb < SB; ++hb) {
+            const uint32_t dst = (kv == 0 ? kstage(s) : vstage(s)) + hb * L::kBlock +
+                                 static_cast<uint32_t>(cc >> 3) * kPiece8;
+#pragma unroll
+            for (int i = 0; i < kCopyKeys8 * LPR / 32; ++i) {
+              const int k8 = cw * kCopyKeys8 + i * (32 / LPR) + kb;
+              const uint32_t row = row_w[(st * SB + hb) * kKeys8 + i * (32 / LPR)];
+              if (in_row)
+                cp_async16(dst + static_cast<uint32_t>(k8) * 128 +
+                               ((static_cast<uint32_t>(cc & 7) ^ static_cast<uint32_t>(k8 & 7)) << 4),
+                           src + (row == kNoRow8 ? 0 : static_cast<uint64_t>(row) * a.D),
+                           row != kNoRow8);
+            }
           }
           cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
         }
-        if (!ok) break;
-        post_next(k); // after the first block
       }
-      post_next(k);
+      sg += nst;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::bRowsFree + static_cast<int>(ig & 1)));
     }
     cp_async_wait_all(); // no copy outlives the CTA
   } else if (warp >= kAuxWarp8) {
-    // ------------------------------------------------------------ scales and q
-    // Thread t hands key t's scales of each block to the softmax, up to
-    // kScaleSlots8 blocks ahead (the page index two blocks ahead, the bytes
-    // one); aux warp w also splits the q rows of heads w, w + 4.
-    const int aw = warp - kAuxWarp8, t = aw * 32 + lane;
+    // ------------------------------------------------------------ preparation
+    // Aux warp w finds the cache rows and the scales of the keys of blocks w
+    // and w + 4 (four keys a lane and block), and splits the q rows of heads
+    // w and w + 4, up to two items ahead of their use.
+    const int aw = warp - kAuxWarp8;
     const int page_mask = (1 << a.page_shift) - 1;
-    float *s_ks = reinterpret_cast<float *>(smem + L::kKs);
-    uint8_t *s_ve = smem + L::kVe;
+    uint32_t *s_rows = reinterpret_cast<uint32_t *>(smem + L::kRows);
     int32_t *s_emax = reinterpret_cast<int32_t *>(smem + L::kEmax);
     float *s_qs = reinterpret_cast<float *>(smem + L::kQs);
-    uint32_t jg = 0, ig = 0;
-    bool ok = true;
-    for (uint32_t k = 0; ok; ++k) {
-      const int64_t w = read_item(k, false);
-      if (w < 0) break;
-      const Item8 it = item8(a, w);
-      if (!it.live) continue;
-      auto page_of = [&](int j) {
-        const int32_t key = it.key_begin + j * kKeys8 + t;
-        return key < it.key_end ? __ldg(a.kv_indices + it.r.page_base + (key >> a.page_shift)) : -1;
-      };
-      // scale bytes of block j's key (past the end or on a bad page: zeros
-      // with a zero weight, outside the block's maximum)
-      auto bytes_of = [&](int j, int32_t page, uint32_t &kb, uint32_t &vb) {
-        kb = vb = 0;
-        if (page >= 0 && page < a.num_pages) {
-          const int32_t key = it.key_begin + j * kKeys8 + t;
-          const int64_t row =
-              ((static_cast<int64_t>(page) << a.page_shift) + (key & page_mask)) * a.Hkv + it.kvh;
-          kb = __ldg(f.k_scale + row);
-          vb = __ldg(f.v_scale + row);
+    for (uint32_t ig = 0;; ++ig) {
+      const Item8 it = warp_item(ig);
+      if (it.nb < 0) break;
+      const int par = static_cast<int>(ig & 1);
+      int32_t page[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int32_t key = it.key_begin + (aw + 4 * i) * kKeys8 + n * 32 + lane;
+          page[i][n] = key < it.key_end
+                           ? __ldg(a.kv_indices + it.page_base + (key >> a.page_shift)) : -1;
         }
-      };
-      int32_t pg1 = page_of(0), pg2 = page_of(1);
       // the q rows: 4 elements a lane and 128 columns
       constexpr int NH = G > 4 ? 2 : 1;
       uint2 qv[NH][NP];
@@ -355,11 +335,40 @@ __global__ void __launch_bounds__(kThreads8, 1)
           qv[i][p] = make_uint2(0, 0);
           if (h < G && col < a.D)
             qv[i][p] = __ldg(reinterpret_cast<const uint2 *>(
-                a.q + (static_cast<int64_t>(it.r.q_start) * a.Hq + it.kvh * G + h) * a.D + col));
+                a.q + (static_cast<int64_t>(it.b) * a.Hq + it.kvh * G + h) * a.D + col));
         }
-      uint32_t kb, vb;
-      bytes_of(0, pg1, kb, vb);
-      if (ig >= 2 && !mbar_wait(bar(L::bQEmpty + (ig & 1)), ((ig >> 1) - 1) & 1, a.status)) break;
+      // rows first: the copies wait for them
+      if (ig >= 2 && !wait(L::bRowsFree + par, ((ig >> 1) - 1) & 1)) break;
+      uint32_t row[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int t = (aw + 4 * i) * kKeys8 + n * 32 + lane;
+          const bool real = it.key_begin + t < it.key_end;
+          const bool good = real && page[i][n] >= 0 && page[i][n] < a.num_pages;
+          if (real && !good) atomicOr(a.status, kStatusBadPage);
+          row[i][n] = good ? static_cast<uint32_t>(((static_cast<int64_t>(page[i][n]) << a.page_shift) +
+                                                    ((it.key_begin + t) & page_mask)) * a.Hkv + it.kvh)
+                           : kNoRow8;
+          s_rows[par * L::kTile + t] = row[i][n];
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::bRows + par));
+      uint32_t kb[2][4], vb[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          kb[i][n] = vb[i][n] = 0; // no row: zeros with a zero weight, outside the maximum
+          if (row[i][n] != kNoRow8) {
+            kb[i][n] = __ldg(f.k_scale + row[i][n]);
+            vb[i][n] = __ldg(f.v_scale + row[i][n]);
+          }
+        }
+      // q: hi + lo/16 of the row scaled by 2^-e
+      if (ig >= 2 && !wait(L::bQEmpty + par, ((ig >> 1) - 1) & 1)) break;
+      if (ig >= 2 && !wait(L::bAuxFree + par, ((ig >> 1) - 1) & 1)) break;
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         const int h = aw + 4 * i;
@@ -383,18 +392,18 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             const int col = lane * 4;
-            float v[4], b[4];
+            float v[4], back[4];
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int c = 0; c < 4; ++c) v[c] = x[p][c] * inv;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               hi[c] = e4m3x2(v[2 * c], v[2 * c + 1]);
-              e4m3x2_values(hi[c], b[2 * c], b[2 * c + 1]);
-              lo[c] = e4m3x2((v[2 * c] - b[2 * c]) * 16.f, (v[2 * c + 1] - b[2 * c + 1]) * 16.f);
+              e4m3x2_values(hi[c], back[2 * c], back[2 * c + 1]);
+              lo[c] = e4m3x2((v[2 * c] - back[2 * c]) * 16.f, (v[2 * c + 1] - back[2 * c + 1]) * 16.f);
             }
             if (p * 128 + col < a.D) {
-              uint8_t *q0 = smem + L::kQ + (ig & 1) * L::kQBuf + p * (kN8 * 128);
+              uint8_t *q0 = smem + L::kQ + par * L::kQBuf + p * (kN8 * 128);
               auto at = [&](int rr) { // row rr, 16-byte chunk col / 16
                 return rr * 128 + (((col >> 4) ^ (rr & 7)) << 4) + (col & 15);
               };
@@ -402,245 +411,192 @@ __global__ void __launch_bounds__(kThreads8, 1)
               *reinterpret_cast<uint32_t *>(q0 + at(LO + h)) = lo[0] | (lo[1] << 16);
             }
           }
-          if (lane == 0) s_qs[(ig & 1) * 8 + h] = a.scale_log2 * exp2_int(e);
+          if (lane == 0) s_qs[par * 8 + h] = a.scale_log2 * exp2_int(e);
         }
       }
       fence_proxy_async(); // q is read by the MMA (async proxy)
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::bQFull + (ig & 1)));
-      ++ig;
-      for (int j = 0; j < it.nb; ++j, ++jg) {
-        const int s = static_cast<int>(jg % kScaleSlots8);
-        pg1 = pg2;
-        pg2 = page_of(j + 2);
-        uint32_t kb1, vb1;
-        bytes_of(j + 1, pg1, kb1, vb1);
-        if (jg >= kScaleSlots8 &&
-            !mbar_wait(bar(L::bScEmpty + s), ((jg / kScaleSlots8) - 1) & 1, a.status)) {
-          ok = false;
-          break;
+      if (lane == 0) mbar_arrive(bar(L::bQFull + par));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t big = 0;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int t = par * L::kTile + (aw + 4 * i) * kKeys8 + n * 32 + lane;
+          smem[L::kKe + t] = static_cast<uint8_t>(kb[i][n]);
+          smem[L::kVe + t] = static_cast<uint8_t>(vb[i][n]);
+          big = max(big, vb[i][n] == 255u ? 0u : vb[i][n]);
         }
-        s_ks[s * 128 + t] = e8m0_value(kb);
-        s_ve[s * 128 + t] = static_cast<uint8_t>(vb);
-        const uint32_t big = __reduce_max_sync(0xffffffffu, vb == 255u ? 0u : vb);
-        if (lane == 0) s_emax[s * 4 + aw] = static_cast<int32_t>(big);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bScFull + s));
-        kb = kb1;
-        vb = vb1;
+        big = __reduce_max_sync(0xffffffffu, big);
+        if (lane == 0) s_emax[par * kBlocks8 + aw + 4 * i] = static_cast<int32_t>(big);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::bAux + par));
     }
   } else if (warp == kSWarp8) {
     // ------------------------------------------------------------ S issuer
     if (lane == 0) {
       const int ksteps = a.D / 32 < 4 ? a.D / 32 : 4; // 32-code steps of a piece
-      uint32_t jg = 0, ig = 0, cnt[2] = {0, 0};
+      uint32_t sg = 0;
       bool ok = true;
-      for (uint32_t k = 0; ok; ++k) {
-        const int64_t w = read_item(k, true);
-        if (w < 0) break;
-        const Item8 it = item8(a, w);
-        if (!it.live) continue;
-        const uint32_t qb = qbuf(ig & 1);
+      for (uint32_t ig = 0; ok; ++ig) {
+        const Item8 it = read_item(ig);
+        item_read(ig);
+        if (it.nb < 0) break;
+        const uint32_t qb = sbase + L::kQ + (ig & 1) * L::kQBuf;
         ok = mbar_wait(bar(L::bQFull + (ig & 1)), (ig >> 1) & 1, a.status);
-        for (int j = 0; j < it.nb && ok; ++j, ++jg) {
-          const int s = static_cast<int>(jg % NS), wg = j & 1;
-          const uint32_t c = wg ? cnt[1]++ : cnt[0]++;
-          // S buffer c % 2 is free once the softmax has read S(c - 2)
-          if (c >= 2)
-            ok = mbar_wait(bar(L::bPFull + 2 * wg + (c & 1)), ((c >> 1) - 1) & 1, a.status);
-          ok = ok && mbar_wait(bar(L::bKFull + s), (jg / NS) & 1, a.status);
+        // the item's S columns are free once the softmax is through item ig - 2
+        if (ok && ig >= 2) ok = mbar_wait(bar(L::bAuxFree + (ig & 1)), ((ig >> 1) - 1) & 1, a.status);
+        for (int j = 0; j < it.nb && ok; ++sg) {
+          const uint32_t s = sg % NS;
+          ok = mbar_wait(bar(L::bKFull + s), (sg / NS) & 1, a.status);
           if (!ok) break;
           fence_proxy_async(); // the rows were written by cp.async (generic proxy)
           tc_fence_after();
+          for (int hb = 0; hb < SB && j < it.nb; ++hb, ++j)
 #pragma unroll
-          for (int p = 0; p < NP; ++p)
-            for (int kk = 0; kk < ksteps; ++kk)
-              mma_e4m3_ss(tS(wg, c), desc_sw128(kstage(s) + p * kPiece8 + kk * 32, 16, 1024),
-                          desc_sw128(qb + p * (kN8 * 128) + kk * 32, 16, 1024), kIdescS,
-                          (p | kk) != 0 ? 1u : 0u);
+            for (int p = 0; p < NP; ++p)
+              for (int kk = 0; kk < ksteps; ++kk)
+                mma_e4m3_ss(tS(ig, j),
+                            desc_sw128(kstage(s) + hb * L::kBlock + p * kPiece8 + kk * 32, 16, 1024),
+                            desc_sw128(qb + p * (kN8 * 128) + kk * 32, 16, 1024), kIdescS,
+                            (p | kk) != 0 ? 1u : 0u);
           mma_commit(bar(L::bKEmpty + s));
-          mma_commit(bar(L::bSFull + 2 * wg + (c & 1)));
+          mma_commit(bar(L::bSFull + sg % kSBars));
         }
         if (!ok) break;
         mma_commit(bar(L::bQEmpty + (ig & 1)));
-        ++ig;
       }
     }
     __syncwarp();
   } else if (warp == kPVWarp8) {
     // ------------------------------------------------------------ P.V issuer
     if (lane == 0) {
-      uint32_t jg = 0, ig = 0, cnt[2] = {0, 0};
+      uint32_t sg = 0;
       bool ok = true;
-      for (uint32_t k = 0; ok; ++k) {
-        const int64_t w = read_item(k, true);
-        if (w < 0) break;
-        const Item8 it = item8(a, w);
-        if (!it.live) continue;
-        // the item's O buffers are free once the epilogue of item ig - 2 read them
+      for (uint32_t ig = 0; ok; ++ig) {
+        const Item8 it = read_item(ig);
+        item_read(ig);
+        if (it.nb < 0) break;
+        // the item's O buffer is free once the epilogue of item ig - 2 read it
         if (ig >= 2) ok = mbar_wait(bar(L::bOFree + (ig & 1)), ((ig >> 1) - 1) & 1, a.status);
-        for (int j = 0; j < it.nb && ok; ++j, ++jg) {
-          const int s = static_cast<int>(jg % NS), wg = j & 1;
-          const uint32_t c = wg ? cnt[1]++ : cnt[0]++;
-          ok = mbar_wait(bar(L::bVFull + s), (jg / NS) & 1, a.status) &&
-               mbar_wait(bar(L::bPFull + 2 * wg + (c & 1)), (c >> 1) & 1, a.status);
+        for (int j = 0; j < it.nb && ok; ++sg) {
+          const uint32_t s = sg % NS, ps = sg % NPS;
+          ok = mbar_wait(bar(L::bVFull + s), (sg / NS) & 1, a.status) &&
+               mbar_wait(bar(L::bPFull + ps), (sg / NPS) & 1, a.status);
           if (!ok) break;
           fence_proxy_async();
           tc_fence_after();
+          for (int hb = 0; hb < SB && j < it.nb; ++hb, ++j)
 #pragma unroll
-          for (int p = 0; p < NP; ++p)
+            for (int p = 0; p < NP; ++p)
 #pragma unroll
-            for (int kk = 0; kk < kKeys8 / 32; ++kk)
-              mma_e4m3_ss(tO(ig, wg, p), desc_sw128(vstage(s) + p * kPiece8 + kk * 4096, 16384, 1024),
-                          desc_plain(pbuf(wg, c) + kk * 512, 128, 128), kIdescPV,
-                          (j > 1 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < kKeys8 / 32; ++kk)
+                mma_e4m3_ss(tO(ig, p),
+                            desc_sw128(vstage(s) + hb * L::kBlock + p * kPiece8 + kk * 4096, 16384, 1024),
+                            desc_plain(sbase + L::kP + ps * L::kPBuf + hb * (kKeys8 * kN8) + kk * 512,
+                                       128, 128),
+                            kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
           mma_commit(bar(L::bVEmpty + s));
-          mma_commit(bar(L::bPVDone + 2 * wg + (c & 1)));
+          if constexpr (NPS < L::kTileStages) mma_commit(bar(L::bPVDone + ps));
         }
         if (!ok) break;
         mma_commit(bar(L::bODone + (ig & 1)));
-        ++ig;
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    // A wait that runs out marks its thread; the warpgroup's named barriers
-    // reduce the marks, so its four warps leave at the same barrier.
     const int wg = warp >> 2, qd = warp & 3; // TMEM lanes 32qd .. 32qd+31
     const int t = qd * 32 + lane;            // key of the block, dim of the output
     const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
-    const uint32_t nbar = 1 + wg;
-    float *red = reinterpret_cast<float *>(smem + L::kRed) + wg * 64;
-    float *lr = reinterpret_cast<float *>(smem + L::kLred) + wg * 32;
-    float *stat = reinterpret_cast<float *>(smem + L::kStat); // [parity][WG][m, l][8]
-    int32_t *stat_e = reinterpret_cast<int32_t *>(smem + L::kStatE);
-    const float *s_ks = reinterpret_cast<const float *>(smem + L::kKs);
-    const uint8_t *s_ve = smem + L::kVe;
-    const int4 *s_emax = reinterpret_cast<const int4 *>(smem + L::kEmax);
+    float *s_red = reinterpret_cast<float *>(smem + L::kRed);
+    float *s_stat = reinterpret_cast<float *>(smem + L::kStat);
+    const int32_t *s_emax = reinterpret_cast<const int32_t *>(smem + L::kEmax);
     const float *s_qs = reinterpret_cast<const float *>(smem + L::kQs);
-    uint32_t jg = 0, ig = 0, c = 0; // c: blocks this warpgroup has taken
-    bool failed = false;            // the same on every thread of the warpgroup
-    for (uint32_t k = 0; !failed; ++k) {
-      const int64_t w = read_item(k, false);
-      if (bar_any_named(nbar, 128, w < 0)) break;
-      const Item8 it = item8(a, w);
-      if (!it.live) continue;
-      bool bad = !mbar_wait(bar(L::bQFull + (ig & 1)), (ig >> 1) & 1, a.status);
-      float m[G], l[G], qs[G];
+    uint32_t sg = 0;
+    for (uint32_t ig = 0;; ++ig) {
+      const Item8 it = warp_item(ig);
+      if (it.nb < 0) break;
+      const int nst = (it.nb + SB - 1) / SB;
+      const int par = static_cast<int>(ig & 1);
+      if (!wait(L::bAux + par, (ig >> 1) & 1)) break;
+      const uint8_t *ke = smem + L::kKe + par * L::kTile + t;
+      const uint8_t *ve = smem + L::kVe + par * L::kTile + t;
+      float qs[G];
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-        qs[h] = s_qs[(ig & 1) * 8 + h];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::bQEmpty + (ig & 1)));
-      int32_t eref = -1; // value-scale byte the accumulator is relative to
-      for (int j = wg; j < it.nb; j += 2, ++c) {
-        const uint32_t jj = jg + j;
-        const int ss = static_cast<int>(jj % kScaleSlots8);
-        bad = bad || !mbar_wait(bar(L::bScFull + ss), (jj / kScaleSlots8) & 1, a.status);
-        const float ks = s_ks[ss * 128 + t];
-        const uint32_t ve = s_ve[ss * 128 + t];
-        const int4 em = s_emax[ss];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bScEmpty + ss));
-        bad = bad || !mbar_wait(bar(L::bSFull + 2 * wg + (c & 1)), (c >> 1) & 1, a.status);
+      for (int h = 0; h < G; ++h) qs[h] = s_qs[par * 8 + h];
+      bool ok = true;
+      // ---- pass 1: the tile's largest score of each head
+      float m[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) m[h] = -INFINITY;
+      for (int j = wg; j < it.nb; j += 2) {
+        const uint32_t ss = sg + j / SB;
+        ok = wait(L::bSFull + static_cast<int>(ss % kSBars), (ss / kSBars) & 1);
+        if (!ok) break;
         tc_fence_after();
         uint32_t v[NL];
-        if (__any_sync(0xffffffffu, bad)) {
-          bad = true;
-#pragma unroll
-          for (int i = 0; i < NL; ++i) v[i] = 0;
-        } else {
-          tmem_ld_n<NL>(tS(wg, c) + lane_base, v);
-          tmem_wait_ld();
-        }
+        tmem_ld_n<NL>(tS(ig, j) + lane_base, v);
+        const float ks = e8m0_value(ke[j * kKeys8]);
         const bool valid = it.key_begin + j * kKeys8 + t < it.key_end;
-        float s[G], p[G];
+        tmem_wait_ld();
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float raw = fmaf(__uint_as_float(v[LO + h]), 0.0625f, __uint_as_float(v[h]));
-          s[h] = valid ? raw * (ks * qs[h]) : -INFINITY;
+          m[h] = fmaxf(m[h], valid ? raw * (ks * qs[h]) : -INFINITY);
         }
-        // weights against the running max while the block max is exchanged
+      }
+      if (!ok) break;
+      float mine = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float wm = warp_max(m[h]);
+        mine = lane == h ? wm : mine;
+      }
+      if (lane < 8) s_red[(par * 8 + warp) * 8 + lane] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::bMax + par));
+      int32_t eref = 0; // the tile's largest value scale
+#pragma unroll
+      for (int j = 0; j < kBlocks8; ++j) eref = max(eref, s_emax[par * kBlocks8 + j]);
+      if (!wait(L::bMax + par, (ig >> 1) & 1)) break;
+#pragma unroll
+      for (int h = 0; h < G; ++h) m[h] = s_red[par * 64 + h];
+#pragma unroll
+      for (int w = 1; w < 8; ++w)
+#pragma unroll
+        for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], s_red[(par * 8 + w) * 8 + h]);
+      // ---- pass 2: the weights 2^(s - m), times 2^(ev - eref + 8) in two
+      // e4m3 terms
+      float l[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) l[h] = 0.f;
+      // P of item ig - 1 has been read (its slots are the tile's, or fewer)
+      if (ig >= 1 && !wait(L::bODone + (par ^ 1), ((ig - 1) >> 1) & 1)) break;
+      for (int j = wg; j < it.nb; j += 2) {
+        const int st = j / SB;
+        const uint32_t ss = sg + st, ps = ss % NPS;
+        uint32_t v[NL];
+        tmem_ld_n<NL>(tS(ig, j) + lane_base, v);
+        const float ks = e8m0_value(ke[j * kKeys8]);
+        const uint32_t vb = ve[j * kKeys8];
+        const int32_t de = static_cast<int32_t>(vb) - eref + kBoost8 + 127;
+        const float vf = vb == 255u ? NAN : de > 0 ? __uint_as_float(de << 23) : 0.f;
+        const bool valid = it.key_begin + j * kKeys8 + t < it.key_end;
+        tmem_wait_ld();
+        float w[G];
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          const float ms = m[h] == -INFINITY ? 0.f : m[h];
-          p[h] = s[h] == -INFINITY ? 0.f : ex2(s[h] - ms);
+          const float raw = fmaf(__uint_as_float(v[LO + h]), 0.0625f, __uint_as_float(v[h]));
+          const float p = valid ? ex2(fmaf(raw, ks * qs[h], -m[h])) : 0.f;
+          l[h] += p;
+          w[h] = p * vf;
         }
-        float *rd = red + (c & 1) * 32;
-        float mine = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          const float wm = warp_max(s[h]);
-          mine = lane == h ? wm : mine;
-        }
-        if (lane < G) rd[qd * 8 + lane] = mine;
-        if (bar_any_named(nbar, 128, bad)) {
-          failed = true;
-          break;
-        }
-        uint32_t up = 0; // heads whose running max moves (the same on every thread)
-        float bmv[G], alpha[G];
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          bmv[h] = fmaxf(fmaxf(rd[h], rd[8 + h]), fmaxf(rd[16 + h], rd[24 + h]));
-          alpha[h] = 1.f;
-          if (bmv[h] > m[h] + kLazy8 || (m[h] == -INFINITY && bmv[h] != -INFINITY)) up |= 1u << h;
-        }
-        if (up != 0) {
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            if ((up >> h) & 1u) {
-              alpha[h] = ex2(m[h] - bmv[h]); // 0 when m == -inf
-              m[h] = bmv[h];
-              p[h] = s[h] == -INFINITY ? 0.f : ex2(s[h] - m[h]);
-            }
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < G; ++h) l[h] = fmaf(l[h], alpha[h], p[h]);
-        const int32_t eb = max(max(em.x, em.y), max(em.z, em.w));
-        const bool e_up = eb > eref;
-        const float e_down = e_up && eref >= 0 ? exp2_int(max(eref - eb, -126)) : 1.f;
-        if (e_up) eref = eb;
-        // P buffer c % 2 is free once P.V(c - 2) is done; O may be rescaled
-        // once P.V(c - 1) is done
-        if (c >= 2)
-          bad = bad ||
-                !mbar_wait(bar(L::bPVDone + 2 * wg + (c & 1)), ((c >> 1) - 1) & 1, a.status);
-        if (j > wg && (up != 0 || e_down != 1.f)) {
-          bad = bad || !mbar_wait(bar(L::bPVDone + 2 * wg + ((c - 1) & 1)), ((c - 1) >> 1) & 1,
-                                  a.status);
-          tc_fence_after();
-          if (!__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-            for (int pp = 0; pp < NP; ++pp) {
-              uint32_t o[NL];
-              tmem_ld_n<NL>(tO(ig, wg, pp) + lane_base, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int h = 0; h < G; ++h) {
-                const float x = alpha[h] * e_down;
-                o[h] = __float_as_uint(__uint_as_float(o[h]) * x);
-                o[LO + h] = __float_as_uint(__uint_as_float(o[LO + h]) * x);
-              }
-              tmem_st_n<NL>(tO(ig, wg, pp) + lane_base, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        if (bad) continue; // the next barrier takes everyone out
-        // weight times 2^(ev - eref + 6), in two e4m3 terms
-        const int32_t de = static_cast<int32_t>(ve) - eref + kBoost8 + 127;
-        const float vf = ve == 255u ? NAN : de > 0 ? __uint_as_float(de << 23) : 0.f;
         uint32_t pk[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < G; h += 2) {
-          const float w0 = p[h] * vf, w1 = h + 1 < G ? p[h + 1 < G ? h + 1 : h] * vf : 0.f;
+          const float w0 = w[h], w1 = h + 1 < G ? w[h + 1 < G ? h + 1 : h] : 0.f;
           const uint32_t hi = e4m3x2(w0, w1);
           float b0, b1;
           e4m3x2_values(hi, b0, b1);
@@ -648,120 +604,82 @@ __global__ void __launch_bounds__(kThreads8, 1)
           pk[h >> 2] |= hi << (8 * (h & 3));
           pk[(LO + h) >> 2] |= lo << (8 * (h & 3));
         }
-        *reinterpret_cast<uint4 *>(smem + L::kP + (2 * wg + (c & 1)) * L::kPBuf + t * 16) =
+        // more stages than P slots: the slot's last P.V of this item is done
+        if (NPS < L::kTileStages && st >= NPS) {
+          ok = wait(L::bPVDone + static_cast<int>(ps), ((ss / NPS) - 1) & 1);
+          if (!ok) break;
+        }
+        *reinterpret_cast<uint4 *>(smem + L::kP + ps * L::kPBuf + (j % SB) * (kKeys8 * kN8) + t * 16) =
             make_uint4(pk[0], pk[1], pk[2], pk[3]);
         fence_proxy_async(); // P is read by the MMA (async proxy)
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bPFull + 2 * wg + (c & 1)));
+        if (lane == 0) mbar_arrive(bar(L::bPFull + static_cast<int>(ps)));
       }
-      if (failed) break;
-
-      // ---- the warpgroup's state: row sums over its threads (warp butterfly,
-      // then the four warps in order), its maxima and its scale reference
+      if (SB == 2 && wg == 1 && (it.nb & 1) && lane == 0) // no block in the last stage
+        mbar_arrive(bar(L::bPFull + static_cast<int>((sg + nst - 1) % NPS)));
+      if (!ok) break;
+      // ---- row sums: warp butterfly, then the eight warps in order
 #pragma unroll
       for (int h = 0; h < G; ++h)
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-      float lw = 0.f, mw = 0.f;
+      float lw = 0.f;
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        lw = lane == h ? l[h] : lw;
-        mw = lane == h ? m[h] : mw;
+      for (int h = 0; h < G; ++h) lw = lane == h ? l[h] : lw;
+      if (lane < 8) s_stat[(par * 8 + warp) * 8 + lane] = lw;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(L::bAuxFree + par));
+        mbar_arrive(bar(L::bStat + par));
       }
-      // the epilogue of item ig - 2 (the other reader of this slot) is done:
-      // its OFree preceded this item's first MMA
-      if (bar_any_named(nbar, 128, bad)) {
-        failed = true;
-        break;
-      }
-      if (lane < G) lr[qd * 8 + lane] = lw;
-      bar_sync_named(nbar, 128);
-      float *st = stat + ((ig & 1) * 2 + wg) * 16;
-      if (t < G) {
-        st[t] = mw;
-        st[8 + t] = __fadd_rn(__fadd_rn(__fadd_rn(lr[t], lr[8 + t]), lr[16 + t]), lr[24 + t]);
-      }
-      if (t == 0) stat_e[(ig & 1) * 2 + wg] = eref;
-      if (qd == 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bStat + (ig & 1)));
-      }
-      if (static_cast<int>(ig & 1) == wg) {
-        // ---- epilogue of this item: the two states joined, o = O^T / l
-        bad = !mbar_wait(bar(L::bStat + (ig & 1)), (ig >> 1) & 1, a.status) ||
-              !mbar_wait(bar(L::bODone + (ig & 1)), (ig >> 1) & 1, a.status);
-        if (bar_any_named(nbar, 128, bad)) {
-          failed = true;
-          break;
-        }
+      if (par == wg) {
+        // ---- epilogue: o = O^T / l
+        if (!wait(L::bStat + par, (ig >> 1) & 1) || !wait(L::bODone + par, (ig >> 1) & 1)) break;
         tc_fence_after();
-        const float *s0 = stat + (ig & 1) * 32, *s1 = s0 + 16;
-        const int32_t e0 = stat_e[(ig & 1) * 2], e1 = stat_e[(ig & 1) * 2 + 1];
-        const bool two = it.nb > 1; // the odd blocks' state exists
-        const int32_t em = two ? max(e0, e1) : e0;
-        const float g0 = exp2_int(max(e0 - em, -126));
-        const float g1 = two ? exp2_int(max(e1 - em, -126)) : 0.f;
-        const float e_val = __fmul_rn(e8m0_value(static_cast<uint32_t>(em)), 1.f);
-        float f0[G], f1[G], lse_mine = 0.f;
+        const float e_val = e8m0_value(static_cast<uint32_t>(eref));
+        const bool single = it.prow < 0; // one tile: the final row
+        const int64_t head0 = static_cast<int64_t>(single ? it.b : it.prow) * a.Hq + it.kvh * G;
+        float inv[G], lse_mine = 0.f;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          const float m0 = s0[h], m1 = two ? s1[h] : -INFINITY;
-          const float M = fmaxf(m0, m1);
-          const float a0 = m0 == M ? 1.f : ex2(m0 - M);
-          const float a1 = !two ? 0.f : m1 == M ? 1.f : ex2(m1 - M);
-          const float ls = two ? __fadd_rn(__fmul_rn(a0, s0[8 + h]), __fmul_rn(a1, s1[8 + h]))
-                               : s0[8 + h];
-          const float inv = ls == 0.f ? 0.f : __frcp_rn(ls);
-          f0[h] = __fmul_rn(__fmul_rn(a0, g0), inv);
-          f1[h] = __fmul_rn(__fmul_rn(a1, g1), inv);
-          const float lse = ls == 0.f ? -INFINITY : __fmul_rn(__fadd_rn(M, lg2(ls)), kLn2);
+          float ls = s_stat[par * 64 + h];
+#pragma unroll
+          for (int w = 1; w < 8; ++w) ls = __fadd_rn(ls, s_stat[(par * 8 + w) * 8 + h]);
+          inv[h] = ls == 0.f ? 0.f : __frcp_rn(ls);
+          const float lse = ls == 0.f ? -INFINITY : __fmul_rn(__fadd_rn(m[h], lg2(ls)), kLn2);
           lse_mine = t == h ? lse : lse_mine;
         }
-        const bool single = (it.r.kv_len - 1) / a.split == 0; // one split: the final row
-        const int64_t head0 = static_cast<int64_t>(it.r.q_start) * a.Hq + it.kvh * G;
-        const int64_t prow0 = (it.r.rowbase + it.u.split) * static_cast<int64_t>(a.Hq) + it.kvh * G;
 #pragma unroll
         for (int pp = 0; pp < NP; ++pp) {
-          uint32_t o0[NL], o1[NL];
-          tmem_ld_n<NL>(tO(ig, 0, pp) + lane_base, o0);
-          if (two) tmem_ld_n<NL>(tO(ig, 1, pp) + lane_base, o1);
+          uint32_t o[NL];
+          tmem_ld_n<NL>(tO(ig, pp) + lane_base, o);
           tmem_wait_ld();
           if (pp == NP - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::bOFree + (ig & 1))); // O read
+            if (lane == 0) mbar_arrive(bar(L::bOFree + par)); // O read
           }
           const int dim = pp * 128 + t;
           if (dim < a.D) {
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-              const float x0 =
-                  fmaf(__uint_as_float(o0[LO + h]), 0.0625f, __uint_as_float(o0[h]));
-              float val = __fmul_rn(x0, f0[h]);
-              if (two) {
-                const float x1 =
-                    fmaf(__uint_as_float(o1[LO + h]), 0.0625f, __uint_as_float(o1[h]));
-                val = __fmaf_rn(x1, f1[h], val);
-              }
-              val = __fmul_rn(__fmul_rn(val, 1.f / (1 << kBoost8)), e_val);
+              const float x = fmaf(__uint_as_float(o[LO + h]), 0.0625f, __uint_as_float(o[h]));
+              const float val =
+                  __fmul_rn(__fmul_rn(__fmul_rn(x, inv[h]), 1.f / (1 << kBoost8)), e_val);
               if (single)
                 a.out[(head0 + h) * a.D + dim] = to_bf16(val);
               else
-                a.part_o[(prow0 + h) * a.D + dim] = val;
+                a.part_o[(head0 + h) * a.D + dim] = val;
             }
           }
         }
         if (t < G) {
-          if (single) {
-            if (a.lse) a.lse[head0 + t] = lse_mine;
-          } else {
-            a.part_lse[prow0 + t] = lse_mine;
-          }
+          if (!single) a.part_lse[head0 + t] = lse_mine;
+          else if (a.lse) a.lse[head0 + t] = lse_mine;
         }
       }
-      jg += it.nb;
-      ++ig;
+      sg += nst;
     }
   }
 
@@ -792,9 +710,12 @@ __device__ __forceinline__ bool keys_of(const PlanArgs &p, int b, int32_t &kv_le
   return ok;
 }
 
-__global__ void __launch_bounds__(kPlanThreads8) plan_decode_fp8_kernel(const PlanArgs p) {
+__global__ void __launch_bounds__(kPlanThreads8)
+    plan_decode_fp8_kernel(const PlanArgs p, UnitFp8 *units_out) {
   __shared__ int64_t s_warp[kPlanThreads8 / 32];
   __shared__ int32_t s_off[kPlanThreads8 + 1]; // first unit of each request of the chunk
+  __shared__ int32_t s_keys[kPlanThreads8], s_page[kPlanThreads8];
+  __shared__ int64_t s_row[kPlanThreads8]; // its first partial row, -1: one split
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_launch(); // the decode may set itself up meanwhile
   grid_dep_wait();   // this kernel rewrites the workspace
@@ -830,7 +751,7 @@ __global__ void __launch_bounds__(kPlanThreads8) plan_decode_fp8_kernel(const Pl
                                          : n_units == p.n_units_expected && n_rows == p.part_rows_expected);
   if (!ok) {
     if (tid == 0) atomicOr(p.status, kStatusPlanMismatch);
-    for (int64_t i = tid; i < p.n_units_expected; i += kPlanThreads8) p.units[i] = Unit{-1, 0, 0, 0};
+    for (int64_t i = tid; i < p.n_units_expected; i += kPlanThreads8) units_out[i].b = -1;
     for (int64_t i = tid; i < p.out_elems; i += kPlanThreads8) p.out[i] = 0x7fc0u; // bf16 NaN
     for (int64_t i = tid; p.lse && i < p.lse_elems; i += kPlanThreads8)
       p.lse[i] = __int_as_float(0x7fc00000);
@@ -872,6 +793,9 @@ __global__ void __launch_bounds__(kPlanThreads8) plan_decode_fp8_kernel(const Pl
       r.page_base = p.kv_indptr[b];
       r.mbase = 0;
       p.reqs[b] = r;
+      s_keys[tid] = kv_len;
+      s_page[tid] = r.page_base;
+      s_row[tid] = r.rowbase;
     }
     __syncthreads();
     const int32_t n = s_off[kPlanThreads8], nb = min(kPlanThreads8, p.batch - b0);
@@ -882,13 +806,21 @@ __global__ void __launch_bounds__(kPlanThreads8) plan_decode_fp8_kernel(const Pl
         if (s_off[mid] <= i) lo = mid;
         else hi = mid - 1;
       }
-      p.units[unit0 + i] = Unit{b0 + lo, 0, i - s_off[lo], 1};
+      const int32_t split = i - s_off[lo];
+      UnitFp8 u;
+      u.b = b0 + lo;
+      u.key_begin = split * p.split;
+      u.key_end = min(u.key_begin + p.split, s_keys[lo]);
+      u.page_base = s_page[lo];
+      u.prow = s_row[lo] < 0 ? -1 : s_row[lo] + split;
+      u.pad = 0;
+      units_out[unit0 + i] = u;
     }
     unit0 += n;
     row0 += total >> 32;
   }
   for (int64_t i = unit0 + tid; i < p.n_units_expected; i += kPlanThreads8)
-    p.units[i] = Unit{-1, 0, 0, 0}; // a bounded launch has room for more
+    units_out[i].b = -1; // a bounded launch has room for more
 }
 
 // ---------------------------------------------------------------- merge
@@ -1015,8 +947,8 @@ cudaError_t launch_f8_g(const DecodeFp8Args &f, cudaStream_t s) {
 
 } // namespace
 
-cudaError_t launch_plan_decode_fp8(const PlanArgs &p, cudaStream_t s) {
-  return launch_chained(plan_decode_fp8_kernel, 1, kPlanThreads8, s, p);
+cudaError_t launch_plan_decode_fp8(const PlanArgs &p, UnitFp8 *units, cudaStream_t s) {
+  return launch_chained(plan_decode_fp8_kernel, 1, kPlanThreads8, s, p, units);
 }
 
 cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s) {

@@ -94,6 +94,7 @@ def test_decode_refuses(bia):
     assert decode(bia, d, [0, 2], [4], q=FAKE + 8) == inv
     assert decode(bia, d, [0, 2], [4], ws=FAKE + 16) == inv
     assert decode(bia, d, [0, 2], [4], split=100) == uns
+    assert decode(bia, d, [0, 2], [4], split=bia.BIA_DECODE_FP8_SPLIT + 128) == uns
     assert decode(bia, bia.make_desc(48, 3, 128, 16), [0, 2], [4]) == uns
     assert decode(bia, d, [0, 2], [4], ws_bytes=256) == bia.BIA_ERR_WORKSPACE_TOO_SMALL
     assert bia.load().bia_decode_paged_fp8_bounded(

@@ -78,6 +78,18 @@ def test_decode_against_64_bits(d, hq, hkv):
     b.check(*b.decode())
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 8), (96, 32, 8), (128, 64, 8), (256, 16, 8)])
+def test_many_tiles_per_sm(d, hq, hkv):
+    # about a dozen (tile, kv head) items for each SM, whole and ragged ones in
+    # turn, so that every ring and double buffer of the kernel goes round
+    lens = [(i * 397) % 2900 + 1 for i in range(90)] + [6000, 128, 1024]
+    b = Batch(lens, hq, hkv, d, 16, seed=d)
+    out, lse = b.decode()
+    b.check(out, lse)
+    again, l2 = b.decode()
+    assert same_bits(out, again) and same_bits(lse, l2)
+
+
 @pytest.mark.parametrize("page", [1, 2, 32, 256])
 def test_decode_at_every_page_size(page):
     b = Batch([1, 300, 130, 4097], 16, 4, 128, page, seed=page)
@@ -88,7 +100,7 @@ def test_decode_at_every_page_size(page):
     assert same_bits(out, o2) and same_bits(lse, l2)  # pages do not enter the bits
 
 
-@pytest.mark.parametrize("split", [128, 384, 2048, 4096])
+@pytest.mark.parametrize("split", [128, 384, 768, 1024])
 def test_decode_with_other_splits(split):
     b = Batch([1, 384, 385, 3001], 8, 2, 128, 16, seed=split)
     b.check(*b.decode(split))
