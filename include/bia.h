@@ -429,6 +429,7 @@ BIA_API int bia_append_paged_kv(const bia_attn_desc *desc, const void *k_new, co
  *   k_scale, v_scale  [num_pages, page_size, num_kv_heads] e8m0 scales: one
  *                     power of two, 2^(byte - 127), per (key, kv head) row
  *   row value d = code_d * scale
+ * (the codes start on a 16-byte boundary, the scales on a 2-byte one).
  * The append below writes a row with e = the smallest integer >= -120 for
  * which the row's largest finite magnitude is at most 448 * 2^e, codes
  * rounded to nearest even, and the byte e + 127; a non-finite element is

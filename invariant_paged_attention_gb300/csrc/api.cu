@@ -862,7 +862,8 @@ int check_cache_fp8(const bia_attn_desc *desc, const void *k_rows, const void *v
         !kv_indptr || !kv_indices || !kv_last_page_len || num_pages <= 0)
       return BIA_ERR_INVALID_ARG;
     if (misaligned(k_rows, 16) || misaligned(v_rows, 16) || misaligned(k_cache, 16) ||
-        misaligned(v_cache, 16) || misaligned(row_indptr, 4) || misaligned(kv_indptr, 4) ||
+        misaligned(v_cache, 16) || misaligned(k_scale, 2) || misaligned(v_scale, 2) ||
+        misaligned(row_indptr, 4) || misaligned(kv_indptr, 4) ||
         misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
       return BIA_ERR_INVALID_ARG;
     // one group of lanes per (token, head) row of K and of V
@@ -938,8 +939,9 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
       !kv_last_page_len || !out || !workspace || num_pages <= 0)
     return BIA_ERR_INVALID_ARG;
   if (misaligned(workspace, 256) || misaligned(q, 16) || misaligned(k_cache, 16) ||
-      misaligned(v_cache, 16) || misaligned(out, 16) || misaligned(lse, 4) ||
-      misaligned(kv_indptr, 4) || misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
+      misaligned(v_cache, 16) || misaligned(k_scale, 2) || misaligned(v_scale, 2) ||
+      misaligned(out, 16) || misaligned(lse, 4) || misaligned(kv_indptr, 4) ||
+      misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
     return BIA_ERR_INVALID_ARG;
   if (split == 0) split = BIA_DECODE_FP8_SPLIT;
   if (split > BIA_DECODE_FP8_SPLIT) return BIA_ERR_UNSUPPORTED;

@@ -324,6 +324,10 @@ cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s); // head_dim 
 cudaError_t launch_cache_fp8(const CacheFp8Args &a, bool append, cudaStream_t s);
 cudaError_t launch_plan_decode_fp8(const PlanArgs &p, UnitFp8 *units, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s);
+cudaError_t launch_decode_fp8_g1(const DecodeFp8Args &f, cudaStream_t s); // by group size
+cudaError_t launch_decode_fp8_g2(const DecodeFp8Args &f, cudaStream_t s);
+cudaError_t launch_decode_fp8_g4(const DecodeFp8Args &f, cudaStream_t s);
+cudaError_t launch_decode_fp8_g8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s);
 // Packed keys and values: head_dim 64, 96 and 128; 256
 cudaError_t launch_prefill_ragged(const AttnArgs &a, cudaStream_t s);

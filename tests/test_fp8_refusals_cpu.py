@@ -73,6 +73,7 @@ def test_append_refuses_rows_off_their_grid(bia):
     d = bia.make_desc(32, 8, 128, 16)
     assert append(bia, d, [0, 5], [0, 1], [5], k=FAKE + 8) == inv
     assert append(bia, d, [0, 5], [0, 1], [5], cache=FAKE + 8) == inv
+    assert append(bia, d, [0, 5], [0, 1], [5], scale=FAKE + 1) == inv
     assert append(bia, d, [0, 5], [0, 1], [5], status=FAKE + 2) == inv
     assert gather(bia, d, [0, 5], [0, 1], [5], out=FAKE + 8) == inv
 
@@ -91,6 +92,7 @@ def test_decode_refuses(bia):
     assert decode(bia, d, [0, 2, 1], [1, 1]) == inv
     assert decode(bia, d, [0, 2], [17]) == inv
     assert decode(bia, d, [0, 2], [4], scale=0) == inv
+    assert decode(bia, d, [0, 2], [4], scale=FAKE + 1) == inv
     assert decode(bia, d, [0, 2], [4], q=FAKE + 8) == inv
     assert decode(bia, d, [0, 2], [4], ws=FAKE + 16) == inv
     assert decode(bia, d, [0, 2], [4], split=100) == uns

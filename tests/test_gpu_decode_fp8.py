@@ -72,13 +72,15 @@ LENS = [1, 2, 127, 128, 129, 255, 300, 2047, 2048, 2049, 5000]
 
 
 @pytest.mark.parametrize("d", [64, 96, 128, 256])
-@pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2), (8, 2), (16, 2), (32, 8)])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2), (8, 2), (16, 2), (32, 8), (3, 3), (2, 1), (12, 3),
+                                    (8, 1)])
 def test_decode_against_64_bits(d, hq, hkv):
     b = Batch(LENS, hq, hkv, d, 16, seed=d + hq)
     b.check(*b.decode())
 
 
-@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 8), (96, 32, 8), (128, 64, 8), (256, 16, 8)])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 8), (96, 32, 8), (128, 64, 8), (256, 16, 8),
+                                      (64, 28, 7), (96, 40, 5), (128, 14, 7), (256, 7, 7)])
 def test_many_tiles_per_sm(d, hq, hkv):
     # about a dozen (tile, kv head) items for each SM, whole and ragged ones in
     # turn, so that every ring and double buffer of the kernel goes round
