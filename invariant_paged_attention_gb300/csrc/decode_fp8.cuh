@@ -28,8 +28,8 @@
 // first, kept in TMEM, one maximum over the part, then the weights.  Nothing
 // is rescaled, the weights of a part are at most 1 and fill e4m3's range, and
 // the warps meet once a part; the parts' states (each with its own O columns)
-// are joined in the epilogue.  A part's key rows are copied before its value
-// rows, through a ring of their own each (one ring for both would let S of the
+// are joined in the epilogue.  The key rows of a part are copied before the
+// value rows of the part before it, through a ring of their own each (one ring for both would let S of the
 // next part wait on a stage two uses ahead, which an mbarrier's parity cannot
 // tell from the use before).
 //
@@ -135,6 +135,30 @@ template <int NL>
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[NL]) {
   if constexpr (NL == 8) tmem_ld8(taddr, r);
   else tmem_ld16(taddr, r);
+}
+
+// Sums of G values over the 32 lanes of a warp: lane h < G gets the sum of
+// v[h].  Each step halves the values a lane carries (it sends the others to
+// its partner), so it takes G - 1 + log2(32 / G) shuffles instead of 5 G; the
+// order of the additions is fixed.
+template <int G>
+__device__ __forceinline__ float warp_sums(const float (&v)[G], int lane) {
+  float x[G];
+#pragma unroll
+  for (int h = 0; h < G; ++h) x[h] = v[h];
+#pragma unroll
+  for (int n = G / 2; n >= 1; n /= 2) { // partner: lane bit n; keep the half it names
+    const bool up = (lane & n) != 0;
+#pragma unroll
+    for (int h = 0; h < n; ++h) {
+      const float give = up ? x[h] : x[h + n], keep = up ? x[h + n] : x[h];
+      x[h] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, n));
+    }
+  }
+#pragma unroll
+  for (int off = G; off < 32; off *= 2)
+    x[0] = __fadd_rn(x[0], __shfl_xor_sync(0xffffffffu, x[0], off));
+  return x[0];
 }
 
 template <int G, int DW, int HB>
@@ -285,46 +309,59 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const int piece = DW == 64 ? 0 : DW == 256 ? cc >> 3 : cc / chunks;
     const uint32_t pc = static_cast<uint32_t>(DW == 128 ? cc - piece * chunks : cc & 7); // in the piece
     const uint32_t *rows = reinterpret_cast<const uint32_t *>(smem + L::kRows);
-    uint32_t sg = 0, ug = 0; // stages and parts so far
-    bool ok = true;
-    for (uint32_t ig = 0; ok; ++ig) {
-      const Item8 it = warp_item(ig);
-      if (it.nb < 0) break;
-      if (cw == 0 && lane == 0) mbar_arrive(bar(L::bGo));
-      for (int part = 0; part < parts_of(it) && ok; ++part, ++ug) {
-        const int par = static_cast<int>(ug & 1), nst = (blocks_of(it, part) + SB - 1) / SB;
-        ok = wait(L::bRows + par, (ug >> 1) & 1);
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const uint8_t *src = (kv == 0 ? f.k_codes : f.v_codes) + cc * 16;
-          const uint32_t *row_w = rows + par * kPart8 + cw * kCopyKeys8 + kb;
-          for (int st = 0; st < nst; ++st) {
-            const uint32_t ss = sg + st, s = ss % NS;
-            if (ss >= NS)
-              ok = wait((kv == 0 ? L::bKEmpty : L::bVEmpty) + static_cast<int>(s), ((ss / NS) - 1) & 1);
-            if (!ok) break;
+    // Copies one part's key or value rows; sg counts the stages of each ring.
+    uint32_t sg[2] = {0, 0}, ug[2] = {0, 0};
+    auto copy_part = [&](int kv, int nst) {
+      const int par = static_cast<int>(ug[kv] & 1);
+      if (kv == 0 && !wait(L::bRows + par, (ug[0] >> 1) & 1)) return false;
+      const uint8_t *src = (kv == 0 ? f.k_codes : f.v_codes) + cc * 16;
+      const uint32_t *row_w = rows + par * kPart8 + cw * kCopyKeys8 + kb;
+      for (int st = 0; st < nst; ++st, ++sg[kv]) {
+        const uint32_t ss = sg[kv], s = ss % NS;
+        if (ss >= NS &&
+            !wait((kv == 0 ? L::bKEmpty : L::bVEmpty) + static_cast<int>(s), ((ss / NS) - 1) & 1))
+          return false;
 #pragma unroll
-            for (int hb = 0; hb < SB; ++hb) {
-              const uint32_t dst = (kv == 0 ? kstage(s) : vstage(s)) + hb * L::kBlock +
-                                   static_cast<uint32_t>(piece) * kPiece8;
+        for (int hb = 0; hb < SB; ++hb) {
+          const uint32_t dst = (kv == 0 ? kstage(s) : vstage(s)) + hb * L::kBlock +
+                               static_cast<uint32_t>(piece) * kPiece8;
 #pragma unroll
-              for (int i = 0; i < kCopyKeys8 * LPR / 32; ++i) {
-                const int k8 = cw * kCopyKeys8 + i * (32 / LPR) + kb;
-                const uint32_t row = row_w[(st * SB + hb) * kKeys8 + i * (32 / LPR)];
-                if (in_row)
-                  cp_async16(dst + static_cast<uint32_t>(k8) * 128 +
-                                 ((pc ^ static_cast<uint32_t>(k8 & 7)) << 4),
-                             src + (row == kNoRow8 ? 0 : static_cast<uint64_t>(row) * a.D),
-                             row != kNoRow8);
-              }
-            }
-            cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
+          for (int i = 0; i < kCopyKeys8 * LPR / 32; ++i) {
+            const int k8 = cw * kCopyKeys8 + i * (32 / LPR) + kb;
+            const uint32_t row = row_w[(st * SB + hb) * kKeys8 + i * (32 / LPR)];
+            if (in_row)
+              cp_async16(dst + static_cast<uint32_t>(k8) * 128 +
+                             ((pc ^ static_cast<uint32_t>(k8 & 7)) << 4),
+                         src + (row == kNoRow8 ? 0 : static_cast<uint64_t>(row) * a.D),
+                         row != kNoRow8);
           }
         }
-        sg += nst;
+        cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
+      }
+      ++ug[kv];
+      if (kv == 1) { // the part's rows have been read
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::bRowsFree + par));
       }
+      return true;
+    };
+    // K(0), then K(u + 1), V(u): a part's value rows follow the next part's
+    // key rows, so that they find ring stages that P.V has freed meanwhile
+    int nst_v = 0; // stages of the part whose V comes next (0: none yet)
+    bool ok = true;
+    for (uint32_t ig = 0; ok; ++ig) {
+      const Item8 it = warp_item(ig);
+      if (it.nb >= 0 && cw == 0 && lane == 0) mbar_arrive(bar(L::bGo));
+      const int n_parts = it.nb < 0 ? 0 : parts_of(it);
+      for (int part = 0; part < n_parts && ok; ++part) {
+        const int nst = (blocks_of(it, part) + SB - 1) / SB;
+        ok = copy_part(0, nst);
+        if (ok && nst_v > 0) ok = copy_part(1, nst_v);
+        nst_v = nst;
+      }
+      if (it.nb < 0) break;
     }
+    if (ok && nst_v > 0) copy_part(1, nst_v);
     cp_async_wait_all(); // no copy outlives the CTA
   } else if (warp >= kAuxWarp8) {
     // ------------------------------------------------------------ preparation
@@ -686,16 +723,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
           mbar_arrive(bar(L::bPFull + static_cast<int>((sg + nst - 1) % ST)));
         sg += nst;
         // ---- the part's state: row sums of the warps, maxima, scale
+        const float lw = warp_sums<G>(l, lane); // lane h < G: head h
+        float mw = 0.f;
 #pragma unroll
-        for (int h = 0; h < G; ++h)
-#pragma unroll
-          for (int off = 16; off >= 1; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-        float lw = 0.f, mw = 0.f;
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          lw = lane == h ? l[h] : lw;
-          mw = lane == h ? m[h] : mw;
-        }
+        for (int h = 0; h < G; ++h) mw = lane == h ? m[h] : mw;
         if (lane < 8) {
           s_stat[(par * 8 + warp) * 8 + lane] = lw;
           if (warp == wf) s_m[(par * HB + hh) * 8 + lane] = mw;
@@ -721,25 +752,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const int32_t e0 = s_e[p0 * HB + hh], e1 = s_e[p1 * HB + hh], em = max(e0, e1);
         const float g0 = exp2_int(max(e0 - em, -126)), g1 = exp2_int(max(e1 - em, -126));
         const float e_val = e8m0_value(static_cast<uint32_t>(em));
-        float f0[G], f1[G], lse_mine = 0.f;
+        // lane h < G: the join of head h (lanes past G repeat one)
+        const int hl = lane & (G - 1);
+        const float m0 = s_m[(p0 * HB + hh) * 8 + hl], m1 = s_m[(p1 * HB + hh) * 8 + hl];
+        const float M = fmaxf(m0, m1);
+        const float a0 = m0 == M ? 1.f : ex2(m0 - M), a1 = m1 == M ? 1.f : ex2(m1 - M);
+        float l0 = s_stat[(p0 * 8 + wf) * 8 + hl], l1 = s_stat[(p1 * 8 + wf) * 8 + hl];
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          const float m0 = s_m[(p0 * HB + hh) * 8 + h], m1 = s_m[(p1 * HB + hh) * 8 + h];
-          const float M = fmaxf(m0, m1);
-          const float a0 = m0 == M ? 1.f : ex2(m0 - M), a1 = m1 == M ? 1.f : ex2(m1 - M);
-          float l0 = s_stat[(p0 * 8 + wf) * 8 + h], l1 = s_stat[(p1 * 8 + wf) * 8 + h];
-#pragma unroll
-          for (int w = 1; w < WH; ++w) {
-            l0 = __fadd_rn(l0, s_stat[(p0 * 8 + wf + w) * 8 + h]);
-            l1 = __fadd_rn(l1, s_stat[(p1 * 8 + wf + w) * 8 + h]);
-          }
-          const float ls = two ? __fadd_rn(__fmul_rn(a0, l0), __fmul_rn(a1, l1)) : l0;
-          const float inv = ls == 0.f ? 0.f : __frcp_rn(ls);
-          f0[h] = __fmul_rn(__fmul_rn(a0, g0), inv);
-          f1[h] = __fmul_rn(__fmul_rn(a1, g1), inv);
-          const float lse = ls == 0.f ? -INFINITY : __fmul_rn(__fadd_rn(M, lg2(ls)), kLn2);
-          lse_mine = t == h ? lse : lse_mine;
+        for (int w = 1; w < WH; ++w) {
+          l0 = __fadd_rn(l0, s_stat[(p0 * 8 + wf + w) * 8 + hl]);
+          l1 = __fadd_rn(l1, s_stat[(p1 * 8 + wf + w) * 8 + hl]);
         }
+        const float ls = two ? __fadd_rn(__fmul_rn(a0, l0), __fmul_rn(a1, l1)) : l0;
+        const float inv = ls == 0.f ? 0.f : __frcp_rn(ls);
+        const float f0_mine = __fmul_rn(__fmul_rn(a0, g0), inv);
+        const float f1_mine = __fmul_rn(__fmul_rn(a1, g1), inv);
+        const float lse_mine = ls == 0.f ? -INFINITY : __fmul_rn(__fadd_rn(M, lg2(ls)), kLn2);
         const bool single = it.prow < 0; // one tile: the final row
         const int64_t head0 =
             static_cast<int64_t>(single ? it.b : it.prow) * a.Hq + (it.kvh + hh) * G;
@@ -755,20 +783,19 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (lane == 0) mbar_arrive(bar(L::bOFree + static_cast<int>(ig & 1))); // O read
           }
           const int dim = p * 128 + t - (DW == 64 ? 64 * hh : 0);
-          if (dim >= 0 && dim < a.D) {
+          const bool real = dim >= 0 && dim < a.D;
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
-              float val = __fmul_rn(
-                  fmaf(__uint_as_float(o0[LO + h]), 0.0625f, __uint_as_float(o0[h])), f0[h]);
-              if (two)
-                val = __fmaf_rn(
-                    fmaf(__uint_as_float(o1[LO + h]), 0.0625f, __uint_as_float(o1[h])), f1[h], val);
-              val = __fmul_rn(__fmul_rn(val, 1.f / (1 << kBoost8)), e_val);
-              if (single)
-                a.out[(head0 + h) * a.D + dim] = to_bf16(val);
-              else
-                a.part_o[(head0 + h) * a.D + dim] = val;
-            }
+          for (int h = 0; h < G; ++h) {
+            const float f0 = __shfl_sync(0xffffffffu, f0_mine, h);
+            const float f1 = __shfl_sync(0xffffffffu, f1_mine, h);
+            float val =
+                __fmul_rn(fmaf(__uint_as_float(o0[LO + h]), 0.0625f, __uint_as_float(o0[h])), f0);
+            if (two)
+              val = __fmaf_rn(fmaf(__uint_as_float(o1[LO + h]), 0.0625f, __uint_as_float(o1[h])), f1,
+                              val);
+            val = __fmul_rn(__fmul_rn(val, 1.f / (1 << kBoost8)), e_val);
+            if (real && single) a.out[(head0 + h) * a.D + dim] = to_bf16(val);
+            if (real && !single) a.part_o[(head0 + h) * a.D + dim] = val;
           }
         }
         if (t < G) {
