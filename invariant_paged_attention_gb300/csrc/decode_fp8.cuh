@@ -512,14 +512,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
   } else if (warp == kSWarp8) {
     // ------------------------------------------------------------ S issuer
     if (lane == 0) {
-      const int ksteps = a.D / 32 < 4 ? a.D / 32 : 4; // 32-code steps of a piece
+      // 32-code steps of a head's piece.  The descriptors are built once: a
+      // step only adds to the start-address field (16-byte units; every
+      // address is below 2^18, so the field never carries), since the thread
+      // executes an instruction only about every ten cycles and building each
+      // descriptor anew took longer than the MMAs.
+      constexpr int KS = DW == 64 ? 2 : 4;
+      const bool all_steps = a.D != 96;
+      const uint64_t dk0 = desc_sw128(kstage(0), 16, 1024);
+      const uint64_t dq0 = desc_sw128(sbase + L::kQ, 16, 1024);
       uint32_t sg = 0, ug = 0;
       bool ok = true;
       for (uint32_t ig = 0; ok; ++ig) {
         const Item8 it = read_item(ig);
         item_read(ig);
         if (it.nb < 0) break;
-        const uint32_t qb = sbase + L::kQ + (ig & 1) * L::kQBuf;
+        const uint64_t dq = dq0 + ((ig & 1) * L::kQBuf >> 4);
         ok = mbar_wait(bar(L::bQFull + (ig & 1)), (ig >> 1) & 1, a.status);
         for (int part = 0; part < parts_of(it) && ok; ++part, ++ug) {
           const int nb = blocks_of(it, part);
@@ -531,18 +539,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (!ok) break;
             fence_proxy_async(); // the rows were written by cp.async (generic proxy)
             tc_fence_after();
-            for (int hb = 0; hb < SB && j < nb; ++hb, ++j) {
+            const uint64_t dk = dk0 + (s * L::kStage >> 4);
+#pragma unroll
+            for (int hb = 0; hb < SB; ++hb, ++j) {
+              if (j >= nb) break;
+              const uint32_t ts = tS(ug, j, 0);
 #pragma unroll
               for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
                 for (int p = 0; p < PH; ++p)
-                  for (int kk = 0; kk < ksteps; ++kk) {
-                    const uint32_t pc = DW == 64 ? 0 : DW == 256 ? p : hh; // piece
+#pragma unroll
+                  for (int kk = 0; kk < KS; ++kk) {
+                    const uint32_t pc = DW == 64 ? 0 : DW == 256 ? p : hh;  // piece
                     const uint32_t co = (DW == 64 ? hh * 64 : 0) + kk * 32; // column
-                    mma_e4m3_ss(tS(ug, j, hh),
-                                desc_sw128(kstage(s) + hb * L::kBlock + pc * kPiece8 + co, 16, 1024),
-                                desc_sw128(qb + pc * (kN8 * 128) + co, 16, 1024), kIdescS,
-                                (p | kk) != 0 ? 1u : 0u);
+                    if (kk < 3 || all_steps)
+                      mma_e4m3_ss(ts + 16 * hh, dk + ((hb * L::kBlock + pc * kPiece8 + co) >> 4),
+                                  dq + ((pc * (kN8 * 128) + co) >> 4), kIdescS, p + kk > 0);
                   }
             }
             mma_commit(bar(L::bKEmpty + s));
@@ -557,6 +569,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
   } else if (warp == kPVWarp8) {
     // ------------------------------------------------------------ P.V issuer
     if (lane == 0) {
+      const uint64_t dv0 = desc_sw128(vstage(0), 16384, 1024);
+      const uint64_t dp0 = desc_plain(sbase + L::kP, 128, 128);
       uint32_t sg = 0, ug = 0;
       bool ok = true;
       for (uint32_t ig = 0; ok; ++ig) {
@@ -574,7 +588,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (!ok) break;
             fence_proxy_async();
             tc_fence_after();
-            for (int hb = 0; hb < SB && j < nb; ++hb, ++j)
+            const uint64_t dv = dv0 + (s * L::kStage >> 4);
+            const uint64_t dp = dp0 + (ps * (SB * HB * L::kPBlock) >> 4);
+            const uint32_t to = tO(ig, part, 0, 0);
+#pragma unroll
+            for (int hb = 0; hb < SB; ++hb, ++j) {
+              if (j >= nb) break;
 #pragma unroll
               for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
@@ -582,13 +601,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                   for (int kk = 0; kk < kKeys8 / 32; ++kk) {
                     const uint32_t pc = DW == 64 ? 0 : DW == 256 ? p : hh; // piece
-                    mma_e4m3_ss(tO(ig, part, hh, p),
-                                desc_sw128(vstage(s) + hb * L::kBlock + pc * kPiece8 + kk * 4096,
-                                           16384, 1024),
-                                desc_plain(sbase + L::kP + ((ps * SB + hb) * HB + hh) * L::kPBlock +
-                                               kk * 512, 128, 128),
-                                kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+                    mma_e4m3_ss(to + 16 * (hh * PH + p),
+                                dv + ((hb * L::kBlock + pc * kPiece8 + kk * 4096) >> 4),
+                                dp + (((hb * HB + hh) * L::kPBlock + kk * 512) >> 4), kIdescPV,
+                                (j > 0 || kk > 0) ? 1u : 0u);
                   }
+            }
             mma_commit(bar(L::bVEmpty + s));
           }
           if (ok) mma_commit(bar(L::bPart + (ug & 1)));
