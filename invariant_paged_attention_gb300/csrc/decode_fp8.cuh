@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const uint32_t pc = static_cast<uint32_t>(DW == 128 ? cc - piece * chunks : cc & 7); // in the piece
     const uint32_t *rows = reinterpret_cast<const uint32_t *>(smem + L::kRows);
     // Copies one part's key or value rows; sg counts the stages of each ring.
+    const uint64_t once = policy_evict_first();
     uint32_t sg[2] = {0, 0}, ug[2] = {0, 0};
     auto copy_part = [&](int kv, int nst) {
       const int par = static_cast<int>(ug[kv] & 1);
@@ -330,10 +331,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const int k8 = cw * kCopyKeys8 + i * (32 / LPR) + kb;
             const uint32_t row = row_w[(st * SB + hb) * kKeys8 + i * (32 / LPR)];
             if (in_row)
-              cp_async16(dst + static_cast<uint32_t>(k8) * 128 +
+              cp_async16_hint(dst + static_cast<uint32_t>(k8) * 128 +
                              ((pc ^ static_cast<uint32_t>(k8 & 7)) << 4),
                          src + (row == kNoRow8 ? 0 : static_cast<uint64_t>(row) * a.D),
-                         row != kNoRow8);
+                         row != kNoRow8, once);
           }
         }
         cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     uint32_t *s_rows = reinterpret_cast<uint32_t *>(smem + L::kRows);
     int32_t *s_emax = reinterpret_cast<int32_t *>(smem + L::kEmax);
     float *s_qs = reinterpret_cast<float *>(smem + L::kQs);
+    const uint64_t keep = policy_evict_last();
     uint32_t ug = 0;
     bool ok = true;
     for (uint32_t ig = 0; ok; ++ig) {
@@ -410,11 +412,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
           ke[n] = ve[n] = 0;
           if (row[n] != kNoRow8) {
             if constexpr (HB == 2) { // an even row (the host checks the arrays' alignment)
-              ke[n] = __ldg(reinterpret_cast<const uint16_t *>(f.k_scale + row[n]));
-              ve[n] = __ldg(reinterpret_cast<const uint16_t *>(f.v_scale + row[n]));
+              ke[n] = ld_scale_u16(f.k_scale + row[n], keep);
+              ve[n] = ld_scale_u16(f.v_scale + row[n], keep);
             } else {
-              ke[n] = __ldg(f.k_scale + row[n]);
-              ve[n] = __ldg(f.v_scale + row[n]);
+              ke[n] = ld_scale_u8(f.k_scale + row[n], keep);
+              ve[n] = ld_scale_u8(f.v_scale + row[n], keep);
             }
           }
         }

@@ -53,6 +53,42 @@ __device__ __forceinline__ void e4m3x2_values(uint32_t codes, float &lo, float &
       : "h"(static_cast<uint16_t>(codes)));
 }
 
+// ---------------------------------------------------------------- cache policy
+// Codes are read once and scales by every head's CTA and, in a randomly paged
+// cache, line by line for many keys in turn: the codes' lines leave L2 first.
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_evict_last() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+// Loads of scale bytes that bring their whole 128-byte line into L2.
+__device__ __forceinline__ uint32_t ld_scale_u8(const uint8_t *p, uint64_t policy) {
+  uint16_t v;
+  asm("{\n\t.reg .u32 t;\n\t"
+      "ld.global.nc.L1::no_allocate.L2::cache_hint.L2::128B.u8 t, [%1], %2;\n\t"
+      "cvt.u16.u32 %0, t;\n\t}"
+      : "=h"(v) : "l"(p), "l"(policy));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_scale_u16(const uint8_t *p, uint64_t policy) {
+  uint16_t v;
+  asm("ld.global.nc.L1::no_allocate.L2::cache_hint.L2::128B.u16 %0, [%1], %2;"
+      : "=h"(v) : "l"(p), "l"(policy));
+  return v;
+}
+// 16-byte global->shared copy with a cache policy; zero-fills when !valid.
+__device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void *src, bool valid,
+                                                uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(valid ? 16 : 0), "l"(policy)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- tensor cores
 // D[tmem] (+)= A[smem] * B[smem]^T of e4m3 codes (K = 32 a step), one elected
 // thread.
