@@ -28,8 +28,8 @@
 // first, kept in TMEM, one maximum over the part, then the weights.  Nothing
 // is rescaled, the weights of a part are at most 1 and fill e4m3's range, and
 // the warps meet once a part; the parts' states (each with its own O columns)
-// are joined in the epilogue.  The key rows of a part are copied before the
-// value rows of the part before it, through a ring of their own each (one ring for both would let S of the
+// are joined in the epilogue.  Key and value rows are copied by warps of their
+// own through a ring of their own each (one ring for both would let S of the
 // next part wait on a stage two uses ahead, which an mbarrier's parity cannot
 // tell from the use before).
 //
@@ -42,9 +42,10 @@
 //
 // Persistent: one CTA per SM takes (tile, kv heads) items from a counter.
 // Warps 0-3 and 4-7 softmax + epilogue, 8 issues P.V (owns TMEM), 9 issues S,
-// 10-13 prepare: the rows and scales of a part's keys, the item's q; 14-21
-// copy (16-byte cp.async into the swizzled operand layout), 22 takes the items
-// and posts them through a mailbox in shared memory, one ahead of the copies.
+// 10-13 prepare: the rows and scales of a part's keys, the item's q; 14-21 and
+// 22-29 copy keys and values (16-byte cp.async into the swizzled operand
+// layout), 30 takes the items and posts them through a mailbox in shared
+// memory, one ahead of the copies.
 // An item's result depends on its own keys alone, whichever CTA takes it.
 #pragma once
 
@@ -69,10 +70,15 @@ constexpr int kPVWarp8 = 8;
 constexpr int kSWarp8 = 9;
 constexpr int kAuxWarp8 = 10;
 constexpr int kCopyWarp8 = 14;
-constexpr int kCopyWarps8 = 8;
-constexpr int kItemWarp8 = kCopyWarp8 + kCopyWarps8;
-constexpr int kThreads8 = (kItemWarp8 + 1) * 32;
+constexpr int kCopyWarps8 = 8;                           // for keys, and as many for values
+constexpr int kItemWarp8 = kCopyWarp8 + 2 * kCopyWarps8;
+constexpr int kThreads8 = 1024; // the last warp idles
 constexpr int kCopyThreads8 = kCopyWarps8 * 32;
+// Registers of the softmax warps and of the others: 8 * 112 + 24 * 48 = 32 * 64,
+// what the launch has
+constexpr int kSoftRegs8 = 112, kOtherRegs8 = 48;
+static_assert(8 * kSoftRegs8 + (kThreads8 / 32 - 8) * kOtherRegs8 <= 65536 / 32, "register split");
+static_assert(kItemWarp8 < kThreads8 / 32, "warps");
 constexpr int kCopyKeys8 = kKeys8 / kCopyWarps8; // keys of a block a copy warp takes
 constexpr int kReaders8 = kItemWarp8;            // warps that read the mailbox
 constexpr int kBoost8 = 8; // weights <= 1 times 2^8 fill e4m3's range (448)
@@ -114,7 +120,7 @@ struct Smem8 {
                        bRows = bQEmpty + 2, bRowsFree = bRows + 2, bAux = bRowsFree + 2,
                        bAuxFree = bAux + 2, bMax = bAuxFree + 2, bStat = bMax + 2 * HB,
                        bPart = bStat + 2 * HB, bOFree = bPart + 2, bSFull = bOFree + 2,
-                       bPFull = bSFull + 2 * kStages, bItemFull = bPFull + kStages,
+                       bPFull = bSFull + 2, bItemFull = bPFull + kStages,
                        bItemEmpty = bItemFull + 4, bGo = bItemEmpty + 4, kNumBars = bGo + 1;
   static constexpr int kAlloc = kBar + kNumBars * 8 + 1024;
   static_assert(kAlloc <= 232448, "shared memory per CTA");
@@ -169,6 +175,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
   constexpr int LO = G <= 4 ? 4 : 8; // column of a head's second term
   constexpr int NL = 2 * LO;         // columns in use
   constexpr int WH = 8 / HB;         // softmax warps that share a kv head
+  constexpr int NB = kPartBlocks8 * HB / 2; // blocks of a part a softmax warp takes
+  constexpr bool kKeep = NB * G <= 16;      // their scores stay in registers
   constexpr uint32_t kIdescS = idesc_e4m3(128, kN8, false, false);
   constexpr uint32_t kIdescPV = idesc_e4m3(128, kN8, true, true);
   constexpr uint32_t kTmemCols = 512;
@@ -200,9 +208,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
       mbar_init(bar(L::bQFull + i), 4);              // the aux warps
       mbar_init(bar(L::bQEmpty + i), 1);             // the S MMAs
       mbar_init(bar(L::bRows + i), 4);
-      mbar_init(bar(L::bRowsFree + i), kCopyWarps8);
+      mbar_init(bar(L::bRowsFree + i), 2 * kCopyWarps8);
       mbar_init(bar(L::bAux + i), 4);
       mbar_init(bar(L::bAuxFree + i), 8);            // the softmax warps, past pass 2
+      mbar_init(bar(L::bSFull + i), 1);              // a part's S
       mbar_init(bar(L::bPart + i), 1);               // a part's P.V
       mbar_init(bar(L::bOFree + i), 4 * HB);
     }
@@ -210,7 +219,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
       mbar_init(bar(L::bMax + i), WH);
       mbar_init(bar(L::bStat + i), WH);
     }
-    for (int i = 0; i < 2 * ST; ++i) mbar_init(bar(L::bSFull + i), 1);
     for (int i = 0; i < ST; ++i)
       mbar_init(bar(L::bPFull + i), HB == 2 ? 8 : 4 * SB); // the warps of the stage's P
     for (int i = 0; i < 4; ++i) {
@@ -262,6 +270,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
     return min(kPartBlocks8, it.nb - part * kPartBlocks8);
   };
 
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs8));
   if (warp == kItemWarp8) {
     // ------------------------------------------------------------ items
     // The first item is the CTA's own index; each next one is taken from the
@@ -298,11 +308,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= kCopyWarp8) {
+  } else if (warp >= kCopyWarp8 && warp < kItemWarp8) {
     // ------------------------------------------------------------ copies
-    // A warp copies 16 keys of each block: chunk cc of every (32 / LPR)-th.
-    // A chunk goes to its head's piece (head_dim 64: both heads in one).
-    const int cw = warp - kCopyWarp8;
+    // Eight warps copy key rows, eight value rows, at their own pace.  A warp
+    // copies 16 keys of each block: chunk cc of every (32 / LPR)-th.  A chunk
+    // goes to its head's piece (head_dim 64: both heads in one).
+    const int kv = (warp - kCopyWarp8) / kCopyWarps8, cw = (warp - kCopyWarp8) % kCopyWarps8;
     const int cc = lane % LPR, kb = lane / LPR;
     const int chunks = a.D / 16; // of a head
     const bool in_row = cc < HB * chunks; // head_dim 96: 6 of 8 lanes a head
@@ -311,60 +322,46 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const uint32_t *rows = reinterpret_cast<const uint32_t *>(smem + L::kRows);
     // Copies one part's key or value rows; sg counts the stages of each ring.
     const uint64_t once = policy_evict_first();
-    uint32_t sg[2] = {0, 0}, ug[2] = {0, 0};
-    auto copy_part = [&](int kv, int nst) {
-      const int par = static_cast<int>(ug[kv] & 1);
-      if (kv == 0 && !wait(L::bRows + par, (ug[0] >> 1) & 1)) return false;
-      const uint8_t *src = (kv == 0 ? f.k_codes : f.v_codes) + cc * 16;
-      const uint32_t *row_w = rows + par * kPart8 + cw * kCopyKeys8 + kb;
-      for (int st = 0; st < nst; ++st, ++sg[kv]) {
-        const uint32_t ss = sg[kv], s = ss % NS;
-        if (ss >= NS &&
-            !wait((kv == 0 ? L::bKEmpty : L::bVEmpty) + static_cast<int>(s), ((ss / NS) - 1) & 1))
-          return false;
-#pragma unroll
-        for (int hb = 0; hb < SB; ++hb) {
-          const uint32_t dst = (kv == 0 ? kstage(s) : vstage(s)) + hb * L::kBlock +
-                               static_cast<uint32_t>(piece) * kPiece8;
-#pragma unroll
-          for (int i = 0; i < kCopyKeys8 * LPR / 32; ++i) {
-            const int k8 = cw * kCopyKeys8 + i * (32 / LPR) + kb;
-            const uint32_t row = row_w[(st * SB + hb) * kKeys8 + i * (32 / LPR)];
-            if (in_row)
-              cp_async16_hint(dst + static_cast<uint32_t>(k8) * 128 +
-                             ((pc ^ static_cast<uint32_t>(k8 & 7)) << 4),
-                         src + (row == kNoRow8 ? 0 : static_cast<uint64_t>(row) * a.D),
-                         row != kNoRow8, once);
-          }
-        }
-        cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
-      }
-      ++ug[kv];
-      if (kv == 1) { // the part's rows have been read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bRowsFree + par));
-      }
-      return true;
-    };
-    // K(0), then K(u + 1), V(u): a part's value rows follow the next part's
-    // key rows, so that they find ring stages that P.V has freed meanwhile
-    int nst_v = 0; // stages of the part whose V comes next (0: none yet)
+    const int b_full = kv == 0 ? L::bKFull : L::bVFull, b_empty = kv == 0 ? L::bKEmpty : L::bVEmpty;
+    const uint32_t ring = (kv == 0 ? kstage(0) : vstage(0)) + static_cast<uint32_t>(piece) * kPiece8;
+    const uint8_t *src = (kv == 0 ? f.k_codes : f.v_codes) + cc * 16;
+    uint32_t sg = 0, ug = 0; // stages and parts so far
     bool ok = true;
     for (uint32_t ig = 0; ok; ++ig) {
       const Item8 it = warp_item(ig);
-      if (it.nb >= 0 && cw == 0 && lane == 0) mbar_arrive(bar(L::bGo));
-      const int n_parts = it.nb < 0 ? 0 : parts_of(it);
-      for (int part = 0; part < n_parts && ok; ++part) {
-        const int nst = (blocks_of(it, part) + SB - 1) / SB;
-        ok = copy_part(0, nst);
-        if (ok && nst_v > 0) ok = copy_part(1, nst_v);
-        nst_v = nst;
-      }
       if (it.nb < 0) break;
+      if (warp == kCopyWarp8 && lane == 0) mbar_arrive(bar(L::bGo));
+      const int n_parts = parts_of(it);
+      for (int part = 0; part < n_parts && ok; ++part, ++ug) {
+        const int par = static_cast<int>(ug & 1), nst = (blocks_of(it, part) + SB - 1) / SB;
+        ok = wait(L::bRows + par, (ug >> 1) & 1);
+        const uint32_t *row_w = rows + par * kPart8 + cw * kCopyKeys8 + kb;
+        for (int st = 0; st < nst && ok; ++st, ++sg) {
+          const uint32_t s = sg % NS;
+          if (sg >= NS) ok = wait(b_empty + static_cast<int>(s), ((sg / NS) - 1) & 1);
+          if (!ok) break;
+#pragma unroll
+          for (int hb = 0; hb < SB; ++hb) {
+            const uint32_t dst = ring + s * L::kStage + hb * L::kBlock;
+#pragma unroll
+            for (int i = 0; i < kCopyKeys8 * LPR / 32; ++i) {
+              const int k8 = cw * kCopyKeys8 + i * (32 / LPR) + kb;
+              const uint32_t row = row_w[(st * SB + hb) * kKeys8 + i * (32 / LPR)];
+              if (in_row)
+                cp_async16_hint(dst + static_cast<uint32_t>(k8) * 128 +
+                                    ((pc ^ static_cast<uint32_t>(k8 & 7)) << 4),
+                                src + (row == kNoRow8 ? 0 : static_cast<uint64_t>(row) * a.D),
+                                row != kNoRow8, once);
+            }
+          }
+          cp_async_arrive(bar(b_full + static_cast<int>(s)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bRowsFree + par)); // the part's rows have been read
+      }
     }
-    if (ok && nst_v > 0) copy_part(1, nst_v);
     cp_async_wait_all(); // no copy outlives the CTA
-  } else if (warp >= kAuxWarp8) {
+  } else if (warp >= kAuxWarp8 && warp < kCopyWarp8) {
     // ------------------------------------------------------------ preparation
     // Aux warp w finds the cache rows and the scales of the keys of block w of
     // a part (four a lane) and splits q heads w, w + 4, ... of an item, up to
@@ -560,8 +557,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                   }
             }
             mma_commit(bar(L::bKEmpty + s));
-            mma_commit(bar(L::bSFull + sg % (2 * ST)));
           }
+          if (ok) mma_commit(bar(L::bSFull + (ug & 1)));
         }
         if (!ok) break;
         mma_commit(bar(L::bQEmpty + (ig & 1)));
@@ -616,7 +613,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
       }
     }
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs8));
     // ------------------------------------------------------------ softmax
     // Thread t is key t of a block and dim t of the output.  HB = 2:
     // warpgroup w has head w and every block; HB = 1: both have the one head,
@@ -649,27 +648,48 @@ __global__ void __launch_bounds__(kThreads8, 1)
         float qs[G];
 #pragma unroll
         for (int h = 0; h < G; ++h) qs[h] = s_qs[(static_cast<int>(ig & 1) * HB + hh) * 8 + h];
-        // ---- pass 1: the part's largest score of each head
-        float m[G];
-#pragma unroll
-        for (int h = 0; h < G; ++h) m[h] = -INFINITY;
-        for (int j = HB == 2 ? 0 : wg; j < nb; j += 3 - HB) {
-          const uint32_t ss = sg + j / SB;
-          ok = wait(L::bSFull + static_cast<int>(ss % (2 * ST)), (ss / (2 * ST)) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          uint32_t v[NL];
-          tmem_ld_n<NL>(tS(ug, j, hh) + lane_base, v);
+        // ---- pass 1: the scores, and the part's largest of each head.  They
+        // stay in registers where 16 hold them, else pass 2 reads S again.
+        ok = wait(L::bSFull + par, (ug >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        auto block = [&](int i) { return HB == 2 ? i : 2 * i + wg; };
+        auto scores = [&](int j, const uint32_t (&v)[NL], float (&sc)[G]) {
           const float ks = e8m0_value(ke[j * kKeys8]);
-          const bool valid = key0 + j * kKeys8 < it.key_end;
-          tmem_wait_ld();
+          const bool valid = key0 + j * kKeys8 < it.key_end; // false past the part's blocks
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             const float raw = fmaf(__uint_as_float(v[LO + h]), 0.0625f, __uint_as_float(v[h]));
-            m[h] = fmaxf(m[h], valid ? raw * (ks * qs[h]) : -INFINITY);
+            sc[h] = valid ? raw * (ks * qs[h]) : -INFINITY;
+          }
+        };
+        float m[G], sc[NB][G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) m[h] = -INFINITY;
+        if constexpr (kKeep) {
+          uint32_t v[NB][NL];
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            if (block(i) < nb) tmem_ld_n<NL>(tS(ug, block(i), hh) + lane_base, v[i]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            scores(block(i), v[i], sc[i]);
+#pragma unroll
+            for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], sc[i][h]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            if (block(i) >= nb) break;
+            uint32_t v[NL];
+            tmem_ld_n<NL>(tS(ug, block(i), hh) + lane_base, v);
+            tmem_wait_ld();
+            scores(block(i), v, sc[0]);
+#pragma unroll
+            for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], sc[0][h]);
           }
         }
-        if (!ok) break;
         float mine = -INFINITY;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -693,28 +713,33 @@ __global__ void __launch_bounds__(kThreads8, 1)
           for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], s_red[(par * 8 + wf + w) * 8 + h]);
         // ---- pass 2: the weights 2^(s - m), times 2^(ev - eref + 8) in two
         // e4m3 terms
-        float l[G];
+        // row sums: even blocks, odd blocks (HB = 1 with two warpgroups on
+        // them adds in the same order: both forms give the same bits)
+        float l[2][G];
 #pragma unroll
-        for (int h = 0; h < G; ++h) l[h] = 0.f;
+        for (int h = 0; h < G; ++h) l[0][h] = l[1][h] = 0.f;
         // P of part ug - 1 has been read
         if (ug >= 1) ok = wait(L::bPart + (par ^ 1), ((ug - 1) >> 1) & 1);
         if (!ok) break;
-        for (int j = HB == 2 ? 0 : wg; j < nb; j += 3 - HB) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int j = block(i);
+          if (j >= nb) break;
           const uint32_t ps = (sg + j / SB) % ST;
-          uint32_t v[NL];
-          tmem_ld_n<NL>(tS(ug, j, hh) + lane_base, v);
-          const float ks = e8m0_value(ke[j * kKeys8]);
+          if constexpr (!kKeep) {
+            uint32_t v[NL];
+            tmem_ld_n<NL>(tS(ug, j, hh) + lane_base, v);
+            tmem_wait_ld();
+            scores(j, v, sc[0]);
+          }
           const uint32_t vb = ve[j * kKeys8];
           const int32_t de = static_cast<int32_t>(vb) - eref + kBoost8 + 127;
           const float vf = vb == 255u ? NAN : de > 0 ? __uint_as_float(de << 23) : 0.f;
-          const bool valid = key0 + j * kKeys8 < it.key_end;
-          tmem_wait_ld();
           float w[G];
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float raw = fmaf(__uint_as_float(v[LO + h]), 0.0625f, __uint_as_float(v[h]));
-            const float p = valid ? ex2(fmaf(raw, ks * qs[h], -m[h])) : 0.f;
-            l[h] += p;
+            const float p = ex2(sc[kKeep ? i : 0][h] - m[h]); // 0 for a key that is not there
+            l[i & (HB - 1)][h] += p;
             w[h] = p * vf;
           }
           uint32_t pk[4] = {0, 0, 0, 0};
@@ -743,7 +768,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
           mbar_arrive(bar(L::bPFull + static_cast<int>((sg + nst - 1) % ST)));
         sg += nst;
         // ---- the part's state: row sums of the warps, maxima, scale
-        const float lw = warp_sums<G>(l, lane); // lane h < G: head h
+        float lw = warp_sums<G>(l[0], lane); // lane h < G: head h
+        if (HB == 2) lw = __fadd_rn(lw, warp_sums<G>(l[1], lane));
         float mw = 0.f;
 #pragma unroll
         for (int h = 0; h < G; ++h) mw = lane == h ? m[h] : mw;
@@ -777,11 +803,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const float m0 = s_m[(p0 * HB + hh) * 8 + hl], m1 = s_m[(p1 * HB + hh) * 8 + hl];
         const float M = fmaxf(m0, m1);
         const float a0 = m0 == M ? 1.f : ex2(m0 - M), a1 = m1 == M ? 1.f : ex2(m1 - M);
-        float l0 = s_stat[(p0 * 8 + wf) * 8 + hl], l1 = s_stat[(p1 * 8 + wf) * 8 + hl];
+        float l0 = 0.f, l1 = 0.f; // the quadrants in order, each even + odd blocks
 #pragma unroll
-        for (int w = 1; w < WH; ++w) {
-          l0 = __fadd_rn(l0, s_stat[(p0 * 8 + wf + w) * 8 + hl]);
-          l1 = __fadd_rn(l1, s_stat[(p1 * 8 + wf + w) * 8 + hl]);
+        for (int w = 0; w < 4; ++w) {
+          float x0 = s_stat[(p0 * 8 + wf + w) * 8 + hl], x1 = s_stat[(p1 * 8 + wf + w) * 8 + hl];
+          if (HB == 1) {
+            x0 = __fadd_rn(x0, s_stat[(p0 * 8 + 4 + w) * 8 + hl]);
+            x1 = __fadd_rn(x1, s_stat[(p1 * 8 + 4 + w) * 8 + hl]);
+          }
+          l0 = __fadd_rn(l0, x0);
+          l1 = __fadd_rn(l1, x1);
         }
         const float ls = two ? __fadd_rn(__fmul_rn(a0, l0), __fmul_rn(a1, l1)) : l0;
         const float inv = ls == 0.f ? 0.f : __frcp_rn(ls);
@@ -854,11 +885,17 @@ cudaError_t launch_f8(const DecodeFp8Args &f, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<G, DW, HB>, f);
 }
 
-// Two kv heads an item where they pair up (a rule on the head layout alone:
-// the two forms add up a row's weights in different orders).
+// Two kv heads an item where they pair up, unless one head an item still gives
+// every item an SM of its own (one request of 4097 keys, 8 kv heads: 16.4
+// instead of 20.5 us on twice the SMs; one of 32768: 24.6 instead of 22.5 us).
+// Both forms give the same bits.
 template <int G>
 cudaError_t launch_f8_g(const DecodeFp8Args &f, cudaStream_t s) {
-  const bool pairs = f.a.Hkv % 2 == 0;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const bool pairs = f.a.Hkv % 2 == 0 && f.a.n_units * f.a.Hkv > sms;
   if (f.a.D == 64) return pairs ? launch_f8<G, 64, 2>(f, s) : launch_f8<G, 64, 1>(f, s);
   if (f.a.D <= 128) return pairs ? launch_f8<G, 128, 2>(f, s) : launch_f8<G, 128, 1>(f, s);
   return launch_f8<G, 256, 1>(f, s);

@@ -127,6 +127,18 @@ def test_a_request_has_its_bits_in_any_batch():
         assert same_bits(o1, out[b:b + 1]) and same_bits(l1, lse[b:b + 1])
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(64, 16, 2), (96, 4, 4), (128, 8, 8), (128, 16, 4)])
+def test_small_and_large_calls_take_the_same_bits(d, hq, hkv):
+    # one kv head an item while every item has an SM, two above that
+    lens = [1024, 600, 3000]
+    few = Batch(lens, hq, hkv, d, 16, seed=1, seeds=[5, 6, 7])
+    assert len(lens) * hkv < 100
+    out, lse = few.decode()
+    many = Batch(lens + [777] * 160, hq, hkv, d, 16, seed=2, seeds=[5, 6, 7] + list(range(20, 180)))
+    o2, l2 = many.decode()
+    assert same_bits(o2[:3], out) and same_bits(l2[:3], lse)
+
+
 def test_decode_twice_and_without_lse():
     b = Batch([4097, 100, 2500], 32, 8, 128, 16)
     out, lse = b.decode()
