@@ -914,7 +914,7 @@ bia::CacheFp8Args cache_fp8_args(const bia_attn_desc *desc, void *k_cache, void 
   a.batch = batch;
   a.Hkv = desc->num_kv_heads;
   a.D = desc->head_dim;
-  a.page_size = desc->page_size;
+  a.page_shift = log2i(desc->page_size);
   a.status = status;
   return a;
 }

@@ -262,7 +262,7 @@ struct CacheFp8Args {
   uint8_t *k_scale, *v_scale;   // e8m0 [num_pages, page_size, Hkv]
   const int32_t *row_indptr, *kv_indptr, *kv_indices, *kv_last_page_len;
   int64_t num_pages, total;
-  int32_t batch, Hkv, D, page_size;
+  int32_t batch, Hkv, D, page_shift;
   int32_t *status; // may be NULL
 };
 
