@@ -1053,18 +1053,42 @@ size_t decode_fp8_workspace(const bia_attn_desc *desc, const bia_bounds *bounds,
       .total;
 }
 
-// Packed keys: the descriptor with its page size (not used) replaced by 1.
+// Packed keys: the descriptor with its page size (not used) replaced by 1,
+// the plan and the split it is made with.  A call whose q tile pairs keep
+// every SM busy for a while is planned without splits: the attention kernel
+// runs through a pair's splits and folds them itself, in one state per CTA.
 int ragged_plan(const bia_attn_desc *desc, const int32_t *qo_host, const int32_t *kv_host,
-                int32_t batch, int32_t causal, int32_t split, bia_attn_desc *d, HostPlan *hp) {
+                int32_t batch, int32_t causal, int32_t split, bia_attn_desc *d, HostPlan *hp,
+                int32_t *plan_split, WsLayout *w) {
   if (!desc || !qo_host || !kv_host) return BIA_ERR_INVALID_ARG;
   *d = *desc;
   d->page_size = 1;
-  const int rc = check_desc(d);
+  int rc = check_desc(d);
   if (rc != BIA_OK) return rc;
   if (kv_host[0] != 0) return BIA_ERR_INVALID_ARG;
-  return host_plan(d, qo_host, kv_host, nullptr, batch, causal, split,
-                   bia::kTileRows / (d->num_qo_heads / d->num_kv_heads),
-                   bia::ragged_tiles_per_unit(d->head_dim), bia::ragged_ctas(d->head_dim), 0, hp);
+  auto plan = [&](int32_t sp) {
+    return host_plan(d, qo_host, kv_host, nullptr, batch, causal, sp,
+                     bia::kTileRows / (d->num_qo_heads / d->num_kv_heads),
+                     bia::ragged_tiles_per_unit(d->head_dim), bia::ragged_ctas(d->head_dim), 0,
+                     hp);
+  };
+  rc = plan(split);
+  if (rc != BIA_OK) return rc;
+  *plan_split = split;
+  int64_t state_rows = hp->part_rows;
+  if (d->head_dim != 256 && hp->part_rows > 0 &&
+      hp->n_groups * d->num_kv_heads >= bia::kFoldItems) {
+    *plan_split = 1 << 30; // no request has more keys
+    rc = plan(*plan_split);
+    if (rc != BIA_OK) return rc;
+    const int64_t row = static_cast<int64_t>(d->num_qo_heads) * d->head_dim;
+    const int64_t states = static_cast<int64_t>(bia::kFoldCtas) * 2 * bia::kTileRows *
+                           (d->head_dim > 64 ? 128 : 64);
+    state_rows = (states + row - 1) / row;
+  }
+  *w = bia::make_layout(batch, hp->n_groups, hp->n_units, 0, state_rows, d->num_qo_heads,
+                        d->head_dim);
+  return BIA_OK;
 }
 } // namespace
 
@@ -1169,15 +1193,16 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
     return BIA_ERR_INVALID_ARG;
   bia_attn_desc d;
   HostPlan hp;
-  int rc = ragged_plan(desc, qo_indptr_host, kv_indptr_host, batch, causal, split_size, &d, &hp);
+  int32_t plan_split;
+  WsLayout w;
+  int rc = ragged_plan(desc, qo_indptr_host, kv_indptr_host, batch, causal, split_size, &d, &hp,
+                       &plan_split, &w);
   if (rc != BIA_OK) return rc;
   const int D = d.head_dim, Hq = d.num_qo_heads, Hkv = d.num_kv_heads, G = Hq / Hkv;
   rc = token_stride(q_stride, static_cast<int64_t>(Hq) * D, &q_stride);
   if (rc == BIA_OK) rc = token_stride(k_stride, static_cast<int64_t>(Hkv) * D, &k_stride);
   if (rc == BIA_OK) rc = token_stride(v_stride, static_cast<int64_t>(Hkv) * D, &v_stride);
   if (rc != BIA_OK) return rc;
-  const WsLayout w =
-      bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows, Hq, D);
   if (workspace_bytes < w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
   if (hp.total_q == 0) return BIA_OK;
   const int64_t total_kv = kv_indptr_host[batch];
@@ -1203,7 +1228,7 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
   pa.tiles_per_unit = bia::ragged_tiles_per_unit(D);
   pa.ctas = bia::ragged_ctas(D);
   pa.causal = causal;
-  pa.split = split_size;
+  pa.split = plan_split;
   pa.n_groups_expected = hp.n_groups;
   pa.n_units_expected = hp.n_units;
   pa.part_rows_expected = hp.part_rows;
@@ -1282,12 +1307,12 @@ size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc, const int32_
   if (split_size == 0) split_size = BIA_PREFILL_SPLIT;
   bia_attn_desc d;
   HostPlan hp;
-  if (ragged_plan(desc, qo_indptr_host, kv_indptr_host, batch, causal ? 1 : 0, split_size, &d,
-                  &hp) != BIA_OK)
+  int32_t plan_split;
+  WsLayout w;
+  if (ragged_plan(desc, qo_indptr_host, kv_indptr_host, batch, causal ? 1 : 0, split_size, &d, &hp,
+                  &plan_split, &w) != BIA_OK)
     return 0;
-  return bia::make_layout(batch, hp.n_groups, hp.n_units, 0, hp.part_rows, d.num_qo_heads,
-                          d.head_dim)
-      .total;
+  return w.total;
 }
 
 } // extern "C"

@@ -330,6 +330,10 @@ cudaError_t launch_decode_fp8_g4(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s);
 // Packed keys and values: head_dim 64, 96 and 128; 256
+// (q tile pair, kv head) items from which a packed prefill folds a pair's
+// splits in the CTA instead of merging states: four a CTA of the 152 SMs.
+constexpr int64_t kFoldCtas = 152;
+constexpr int64_t kFoldItems = 4 * kFoldCtas;
 cudaError_t launch_prefill_ragged(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s);
 inline int ragged_tiles_per_unit(int head_dim) {

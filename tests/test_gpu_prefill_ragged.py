@@ -115,6 +115,51 @@ def test_a_row_has_its_bits_in_any_batch_and_chunking(d):
             assert same_bits(o, want[a:e]) and same_bits(l, wl[a:e]), (chunk, a)
 
 
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_items_than_sms(d, causal):
+    """Several items a CTA, of every size from a row to eight blocks, each
+    with a V tail of its own: against 64 bits, and bit for bit as alone."""
+    g = torch.Generator().manual_seed(d)
+    q_lens = torch.randint(0, 130, (60,), generator=g).tolist()
+    extra = torch.randint(0, 900, (60,), generator=g).tolist()
+    kv_lens = [x + (e if i % 3 else 0) for i, (x, e) in enumerate(zip(q_lens, extra))]
+    q, k, v = draw(8, 4, d, q_lens, kv_lens, d)
+    out, lse = run(q, k, v, q_lens, kv_lens, causal)
+    check(q, k, v, q_lens, kv_lens, out, lse, causal)
+    qa = ka = 0
+    for i, (x, y) in enumerate(zip(q_lens, kv_lens)):
+        if i % 7 == 0 and x:
+            one, l = run(q[qa:qa + x], k[ka:ka + y], v[ka:ka + y], [x], [y], causal)
+            assert same_bits(one, out[qa:qa + x]) and same_bits(l, lse[qa:qa + x])
+        qa, ka = qa + x, ka + y
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_splits_folded_in_the_cta_have_the_merge_s_bits(d, causal):
+    """A batch with enough q tiles folds each row's splits where they are
+    computed; one request of it alone has them merged by a kernel."""
+    hq, hkv, split = 32, 8, 256
+    q_lens, kv_lens = [1500, 700, 1, 64, 0, 1100, 900, 1500], [1500, 2900, 1300, 64, 7, 1101, 900, 1700]
+    q, k, v = draw(hq, hkv, d, q_lens, kv_lens, 5)
+    desc = bia.make_desc(hq, hkv, d, 1)
+    need = [bia.bia_prefill_ragged_workspace_size(desc, fu.indptr_of(a), fu.indptr_of(b), causal, split)
+            for a, b in ((q_lens, kv_lens), (q_lens[1:2], kv_lens[1:2]))]
+    assert need[0] < need[1]  # one state a CTA, not one a row and split
+    out, lse = run(q, k, v, q_lens, kv_lens, causal, split)
+    qa = ka = 0
+    for x, y in zip(q_lens, kv_lens):
+        if x:
+            one, l = run(q[qa:qa + x], k[ka:ka + y], v[ka:ka + y], [x], [y], causal, split)
+            assert same_bits(one, out[qa:qa + x]) and same_bits(l, lse[qa:qa + x])
+        qa, ka = qa + x, ka + y
+    for i in (1, 2, 5):
+        qa, ka = sum(q_lens[:i]), sum(kv_lens[:i])
+        x, y = q_lens[i], kv_lens[i]
+        check(q[qa:qa + x], k[ka:ka + y], v[ka:ka + y], [x], [y], out[qa:qa + x], lse[qa:qa + x], causal)
+
+
 def test_scale_stream_and_lse():
     lens = [257, 64]
     q, k, v = draw(4, 4, 128, lens, lens, 8)
