@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbia.so")
 SOURCES = ["api.cu", "plan.cu", "merge.cu", "decode.cu", "decode_tc.cu", "prefill.cu", "static_ws.cu", "append.cu", "prefill_wide.cu", "mla_decode.cu",
            "cache_fp8.cu", "decode_fp8.cu", "decode_fp8_g1.cu", "decode_fp8_g2.cu",
-           "decode_fp8_g4.cu", "decode_fp8_g8.cu", "prefill_ragged.cu"]
+           "decode_fp8_g4.cu", "decode_fp8_g8.cu", "prefill_ragged.cu", "plan_ragged.cu"]
 HEADERS = ["bia_internal.h", "ptx.cuh", "fold.cuh", "softmax_rows.cuh", "fp8.cuh",
            "decode_fp8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

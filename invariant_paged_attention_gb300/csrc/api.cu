@@ -1242,7 +1242,7 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
   pa.group_cnt = reinterpret_cast<int32_t *>(ws + w.group_cnt);
   pa.units = reinterpret_cast<bia::Unit *>(ws + w.units);
   pa.sunits = reinterpret_cast<bia::Unit *>(ws + w.sunits);
-  cudaError_t e = bia::launch_plan(pa, st);
+  cudaError_t e = bia::launch_plan_ragged(pa, st);
   if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
   __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
 

@@ -178,7 +178,7 @@ inline WsLayout make_layout_fp8(int batch, int64_t n_units, int64_t part_rows, i
 struct PlanArgs {
   const int32_t *qo_indptr;  // NULL for decode (one token per request)
   const int32_t *kv_indptr;
-  const int32_t *kv_last_page_len; // NULL: every page is full (packed keys, page_size 1)
+  const int32_t *kv_last_page_len; // NULL: packed keys
   int32_t batch, page_size, tile_tokens, tiles_per_unit, ctas, causal, split;
   int32_t stream; // 1: single-token tail tiles become streamed units (prefill)
   // 0: the launch was sized from the host mirrors and the device plan must
@@ -331,9 +331,14 @@ cudaError_t launch_decode_fp8_g8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s);
 // Packed keys and values: head_dim 64, 96 and 128; 256
 // (q tile pair, kv head) items from which a packed prefill folds a pair's
-// splits in the CTA instead of merging states: four a CTA of the 152 SMs.
+// splits in the CTA instead of merging states: two a CTA of the 152 SMs.
+// Below, the splits balance the CTAs.  Folded against merged, 128-wide heads:
+// 512 items of a 16384-token prompt 472 / 554 us, of 4 x 2048 tokens behind
+// 16383 keys 1074 / 1037; 256 items of 4 x 1024 such tokens 552 / 535; 160 of
+// 5 x 512 would take two rounds of whole rows where their splits need one.
 constexpr int64_t kFoldCtas = 152;
-constexpr int64_t kFoldItems = 4 * kFoldCtas;
+constexpr int64_t kFoldItems = 2 * kFoldCtas;
+cudaError_t launch_plan_ragged(const PlanArgs &p, cudaStream_t s);
 cudaError_t launch_prefill_ragged(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s);
 inline int ragged_tiles_per_unit(int head_dim) {

@@ -43,7 +43,7 @@ __device__ inline bool request_geometry(const PlanArgs &a, int b, int32_t &q_sta
     ql = 1;
   }
   const int64_t pages = static_cast<int64_t>(a.kv_indptr[b + 1]) - a.kv_indptr[b];
-  const int32_t last = a.kv_last_page_len ? a.kv_last_page_len[b] : a.page_size;
+  const int32_t last = a.kv_last_page_len[b];
   const int64_t kl = pages > 0 ? (pages - 1) * a.page_size + last : 0;
   bool ok = ql >= 0 && pages >= 0 && (pages == 0 || (last >= 1 && last <= a.page_size)) &&
             kl <= INT32_MAX / 2 && ql <= INT32_MAX / 2 && (!a.causal || ql <= kl) &&

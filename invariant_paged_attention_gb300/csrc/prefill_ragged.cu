@@ -98,6 +98,11 @@ __global__ void __launch_bounds__(kThreadsR, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (warp == kMmaWarpR) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  if (warp == kProdWarpR && lane < (a.kv_rows > 0 ? 3 : 1)) // without keys there is only q's
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0   ? &a.tm_q
+                                                  : lane == 1 ? &a.tm_k
+                                                              : &a.tm_v)
+                 : "memory");
   if (tid == 0) {
     mbar_init(bar(L::kQFull), 1);
     mbar_init(bar(L::kQEmpty), 1);
@@ -150,69 +155,90 @@ __global__ void __launch_bounds__(kThreadsR, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegsR));
     if (warp == kItemWarpR) {
       // ------------------------------------------------------------ items
-      if (lane == 0) {
-        const int64_t n_items = a.n_units * a.Hkv;
-        int64_t w = blockIdx.x; // the CTA's first item is its own, the others come from a counter
-        auto take = [&]() {
-          w = gridDim.x < n_items
-                  ? gridDim.x + static_cast<int64_t>(atomicAdd(a.status + kStatusWorkCounter, 1))
-                  : n_items;
-        };
-        ItemR x{};
-        x.kvh = -1;
-        int ns[2] = {0, 0}; // splits of the two tiles
-        bool more = false;  // the folded item has another split
-        for (int i = 0;; ++i) {
-          if (more) {
-            ++x.split;
-            x.key_begin += a.split;
-            x.row0 += a.split;
-          } else {
-            x.kvh = -1;
-            while (w < n_items) {
-              const Unit u = a.units[w / a.Hkv];
-              if (u.b >= 0) { // not retired by the plan
-                const ReqInfo r = a.reqs[u.b];
-                x.kvh = static_cast<int32_t>(w % a.Hkv);
-                x.tile = u.tile;
-                x.split = u.split;
-                x.q_start = r.q_start;
-                x.q_len = r.q_len;
-                x.kv_len = r.kv_len;
-                x.key_begin = u.split * a.split;
-                x.row0 = r.page_base + x.key_begin;
-                x.rowbase = r.rowbase;
-                x.nsp = r.nsp;
+      const int64_t n_items = a.n_units * a.Hkv;
+      int64_t w = blockIdx.x; // the CTA's first item is its own, the others come from a counter
+      auto take = [&]() {
+        if (gridDim.x >= n_items) {
+          w = n_items;
+          return;
+        }
+        int k = 0;
+        if (lane == 0) k = atomicAdd(a.status + kStatusWorkCounter, 1);
+        w = gridDim.x + static_cast<int64_t>(__shfl_sync(0xffffffffu, k, 0));
+      };
+      // up to 32 requests' records stay in the lanes: an item is then one
+      // memory latency away, not two
+      ReqInfo mine{};
+      if (a.batch <= 32 && lane < a.batch) mine = a.reqs[lane];
+      auto request = [&](int b) {
+        if (a.batch > 32) return a.reqs[b];
+        ReqInfo r;
+        r.q_start = __shfl_sync(0xffffffffu, mine.q_start, b);
+        r.q_len = __shfl_sync(0xffffffffu, mine.q_len, b);
+        r.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, b);
+        r.nsp = __shfl_sync(0xffffffffu, mine.nsp, b);
+        r.rowbase = __shfl_sync(0xffffffffu, mine.rowbase, b);
+        r.page_base = __shfl_sync(0xffffffffu, mine.page_base, b);
+        return r;
+      };
+      ItemR x{};
+      x.kvh = -1;
+      int ns[2] = {0, 0}; // splits of the two tiles
+      bool more = false;  // the folded item has another split
+      for (int i = 0;; ++i) {
+        if (more) {
+          ++x.split;
+          x.key_begin += a.split;
+          x.row0 += a.split;
+        } else {
+          x.kvh = -1;
+          while (w < n_items) {
+            const Unit u = a.units[w / a.Hkv];
+            if (u.b >= 0) { // not retired by the plan
+              const ReqInfo r = request(u.b);
+              x.kvh = static_cast<int32_t>(w % a.Hkv);
+              x.tile = u.tile;
+              x.split = u.split;
+              x.q_start = r.q_start;
+              x.q_len = r.q_len;
+              x.kv_len = r.kv_len;
+              x.key_begin = u.split * a.split;
+              x.row0 = r.page_base + x.key_begin;
+              x.rowbase = r.rowbase;
+              x.nsp = r.nsp;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                  ns[t] = t < u.ntiles ? tile_splits(r.q_len, r.kv_len, u.tile + t, T, a.causal,
-                                                     a.split) : 0;
-                break;
-              }
-              take();
+              for (int t = 0; t < 2; ++t)
+                ns[t] = t < u.ntiles ? tile_splits(r.q_len, r.kv_len, u.tile + t, T, a.causal,
+                                                   a.split) : 0;
+              break;
             }
+            take();
           }
+        }
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const bool has = x.split < ns[t];
-            const int32_t last = tile_last_key(x.q_len, x.kv_len, x.tile + t, T, a.causal);
-            const int32_t end = min(x.key_begin + a.split, last + 1);
-            x.n_splits[t] = has ? ns[t] : 0;
-            x.n_blocks[t] =
-                has && end > x.key_begin ? (end - x.key_begin + kKvBlock - 1) / kKvBlock : 0;
-          }
-          more = x.kvh >= 0 && x.rowbase < 0 && x.split + 1 < max(ns[0], ns[1]);
-          const int sl = i % kItemsR;
-          if (i >= kItemsR && !mbar_wait(bar(L::kIEmpty + sl), (i / kItemsR - 1) & 1, a.status))
-            break;
+        for (int t = 0; t < 2; ++t) {
+          const bool has = x.split < ns[t];
+          const int32_t last = tile_last_key(x.q_len, x.kv_len, x.tile + t, T, a.causal);
+          const int32_t end = min(x.key_begin + a.split, last + 1);
+          x.n_splits[t] = has ? ns[t] : 0;
+          x.n_blocks[t] =
+              has && end > x.key_begin ? (end - x.key_begin + kKvBlock - 1) / kKvBlock : 0;
+        }
+        more = x.kvh >= 0 && x.rowbase < 0 && x.split + 1 < max(ns[0], ns[1]);
+        const int sl = i % kItemsR;
+        if (i >= kItemsR &&
+            !__all_sync(0xffffffffu,
+                        mbar_wait(bar(L::kIEmpty + sl), (i / kItemsR - 1) & 1, a.status)))
+          break;
+        if (lane == 0) {
           items[sl] = x;
           mbar_arrive(bar(L::kIFull + sl));
-          if (x.kvh < 0) break;
-          // the loads ask three blocks before they end: late enough for the
-          // counter to balance the CTAs, early enough to hide the fetch
-          if (!mbar_wait(bar(L::kIAsk), i & 1, a.status)) break;
-          if (!more) take();
         }
+        if (x.kvh < 0) break;
+        // the loads ask three blocks before they end: late enough for the
+        // counter to balance the CTAs, early enough to hide the fetch
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kIAsk), i & 1, a.status))) break;
+        if (!more) take();
       }
     } else if (warp == kProdWarpR) {
       // ------------------------------------------------------------ loads
