@@ -9,17 +9,27 @@ namespace {
 
 // ---------------------------------------------------------------- plan
 // One CTA turns the index arrays into per-request records and the units
-// (request, group of q tiles, split; one per CTA of a cluster), a request's
-// last groups first as they carry the most keys, checks each request and
-// clears the status word and the item counter.  Requests in chunks of the
-// block: one scan gives their first groups, partial rows and merge rows, a
-// second one, over the groups, their first units.  Nothing is written past
-// the capacities of the launch; a plan that differs from the host's retires
-// every unit and fills the outputs with NaN.  (The general planner, plan.cu,
-// takes five scans and looks its groups up in global memory: 8 us a call
-// of a few requests, this one 6.)
+// (request, group of q tiles, split; one per CTA of a cluster), checks each
+// request and clears the status word and the item counter.  Requests and
+// their groups are taken in chunks of the block: one scan gives the requests'
+// first groups, partial rows and merge rows; then the chunk's units are
+// sorted by their key blocks, the most first, into bins of 1/8 octave, as the
+// CTAs take units off the list one by one and short ones fill the end best
+// (one prompt of 8192 tokens, 8 heads over 2: 163 -> 156 us).  Units of a bin come in any order:
+// they are computed alike wherever they stand.  Nothing is written past the
+// capacities of the launch; a plan that differs from the host's retires every
+// unit and fills the outputs with NaN.  (The general planner, plan.cu, takes
+// five scans and looks its groups up in global memory: 8 us a call of a few
+// requests, this one 6.)
 constexpr int kPlanThreadsR = 512;
 constexpr int kPlanWarpsR = kPlanThreadsR / 32;
+constexpr int kBinsR = 192; // bin_of(2^23 blocks of 128 keys) is 175
+
+__device__ __forceinline__ int bin_of(int32_t blocks) {
+  if (blocks < 8) return max(blocks, 0);
+  const int k = 31 - __clz(blocks);
+  return 8 + (k - 3) * 8 + ((blocks >> (k - 3)) & 7);
+}
 
 struct RaggedRequest {
   int32_t q_start, q_len, kv_begin, kv_len, groups, nsp;
@@ -74,6 +84,7 @@ __global__ void __launch_bounds__(kPlanThreadsR) plan_ragged_kernel(const PlanAr
   __shared__ int64_t s_warp[kPlanWarpsR], s_rows[kPlanWarpsR];
   __shared__ int32_t s_group[kPlanThreadsR + 1]; // first group of each request of the chunk
   __shared__ int32_t s_q[kPlanThreadsR], s_kv[kPlanThreadsR];
+  __shared__ int32_t s_bin[kBinsR]; // units of each bin, then the next one's place
   const int tid = threadIdx.x;
   grid_dep_launch(); // the attention kernel may set itself up meanwhile
   grid_dep_wait();   // this kernel rewrites the workspace
@@ -128,14 +139,33 @@ __global__ void __launch_bounds__(kPlanThreadsR) plan_ragged_kernel(const PlanAr
         n = tile_splits(s_q[lo], s_kv[lo], min(t0 + gt, tiles) - 1, p.tile_tokens, p.causal,
                         p.split);
       }
+      const int32_t keys =
+          n > 0 ? tile_last_key(s_q[lo], s_kv[lo], min(t0 + gt, tiles) - 1, p.tile_tokens,
+                                p.causal) + 1 : 0;
+      auto bin = [&](int32_t s) {
+        const int64_t left = keys - static_cast<int64_t>(s) * p.split;
+        return bin_of((static_cast<int32_t>(min(left, static_cast<int64_t>(p.split))) +
+                       kKvBlock - 1) / kKvBlock);
+      };
+      if (tid < kBinsR) s_bin[tid] = 0;
+      __syncthreads();
+      for (int32_t s = 0; s < n; ++s) atomicAdd(&s_bin[bin(s)], 1);
+      __syncthreads();
       int64_t total;
-      int64_t u = units + block_scan(static_cast<int64_t>(n) * p.ctas, s_warp, total);
-      for (int32_t s = 0; s < n; ++s)
-        for (int32_t c = 0; c < p.ctas; ++c, ++u) {
+      const int64_t place =
+          block_scan(tid < kBinsR ? s_bin[kBinsR - 1 - tid] : 0, s_warp, total);
+      if (tid < kBinsR) s_bin[kBinsR - 1 - tid] = static_cast<int32_t>(place);
+      __syncthreads();
+      for (int32_t s = 0; s < n; ++s) {
+        const int64_t u = units + static_cast<int64_t>(atomicAdd(&s_bin[bin(s)], 1)) * p.ctas;
+        for (int32_t c = 0; c < p.ctas; ++c) {
           const int32_t tile = t0 + c * p.tiles_per_unit;
-          if (u < p.n_units_expected)
-            p.units[u] = Unit{b0 + lo, tile, s, max(0, min(p.tiles_per_unit, tiles - tile))};
+          if (u + c < p.n_units_expected)
+            p.units[u + c] = Unit{b0 + lo, tile, s, max(0, min(p.tiles_per_unit, tiles - tile))};
         }
+      }
+      __syncthreads(); // the bins are read
+      total *= p.ctas;
       units += total;
     }
     groups += n_groups;
