@@ -15,12 +15,12 @@ namespace {
 // first groups, partial rows and merge rows; then the chunk's units are
 // sorted by their key blocks, the most first, into bins of 1/8 octave, as the
 // CTAs take units off the list one by one and short ones fill the end best
-// (one prompt of 8192 tokens, 8 heads over 2: 163 -> 156 us).  Units of a bin come in any order:
-// they are computed alike wherever they stand.  Nothing is written past the
-// capacities of the launch; a plan that differs from the host's retires every
-// unit and fills the outputs with NaN.  (The general planner, plan.cu, takes
-// five scans and looks its groups up in global memory: 8 us a call of a few
-// requests, this one 6.)
+// (one prompt of 8192 tokens, 8 heads over 2: 163 -> 156 us).  Units of a bin
+// come in any order: they are computed alike wherever they stand.  Nothing is
+// written past the capacities of the launch; a plan that differs from the
+// host's retires every unit and fills the outputs with NaN.  (The general
+// planner, plan.cu, takes five scans and looks its groups up in global
+// memory: 8 us a call of a few requests, this one 6.)
 constexpr int kPlanThreadsR = 512;
 constexpr int kPlanWarpsR = kPlanThreadsR / 32;
 constexpr int kBinsR = 192; // bin_of(2^23 blocks of 128 keys) is 175

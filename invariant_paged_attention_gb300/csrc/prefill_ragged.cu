@@ -66,8 +66,7 @@ struct SmemR {
   static constexpr int kTile = kTileRows * D * 2; // one Q, K or V tile
   static constexpr int kQ = 0;
   static constexpr int kKV = 2 * kTile; // stage s: K at kKV + 2s*kTile, V after it
-  static constexpr int kOut = 6 * kTile; // per softmax warp: 32 rows x 128 B on their way out
-  static constexpr int kItem = kOut + kSoftWarpsR * 4096;
+  static constexpr int kItem = 6 * kTile;
   static constexpr int kBar = kItem + kItemsR * static_cast<int>(sizeof(ItemR));
   static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kVFull = 4, kKEmpty = 6, kVEmpty = 8,
                        kSFull = 10, kPFull = 12, kODone = 14, kVGo = 16, kVTail = 18,
@@ -76,6 +75,24 @@ struct SmemR {
   static constexpr int kSlot = kBar + kNumBars * 8;
   static constexpr int kAlloc = kSlot + 16 + 1024;
 };
+
+// N words of a thread's row, 32 bytes a store where out allows it
+template <int N>
+__device__ __forceinline__ void store_row(void *p, const uint32_t (&w)[N]) {
+  uint32_t *d = static_cast<uint32_t *>(p);
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + i),
+                   "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                   "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<uint4 *>(d + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsR, 1)
@@ -413,7 +430,6 @@ __global__ void __launch_bounds__(kThreadsR, 1)
     const int gs = __ffs(G) - 1; // G is a power of two
     int ns = 0, no = 0;        // S blocks and O tiles of this q tile so far
     float run_lse = -INFINITY; // of the splits folded so far
-    uint8_t *stg = smem + L::kOut + warp * 4096;
     while (const ItemR *xp = next()) {
       const int nb = xp->n_blocks[t];
       // the row's visible keys, counted from the split's first
@@ -503,9 +519,10 @@ __global__ void __launch_bounds__(kThreadsR, 1)
         if (lane == 0) mbar_arrive(bar(L::kPFull + t));
       }
       // epilogue: o_s = O / l; bf16 when the tile has one split or this is the
-      // last of the folded ones, else the fp32 state.  A thread has a row; rows
-      // leave through shared memory, where a warp stores 128 bytes of four rows
-      // at a time (a thread storing its own row costs an L1 cycle per 16 bytes)
+      // last of the folded ones, else the fp32 state.  A thread stores its own
+      // row: a store instruction costs the SM an L1 cycle per row, so 32 bytes
+      // of it each (6 prompts of 100 to 2048 tokens: 70 us with 16-byte stores
+      // through shared memory, 68)
       const ItemR &x = *xp;
       int ln = lane; // opaque: what follows from it is not kept over the blocks
       asm volatile("" : "+r"(ln));
@@ -537,26 +554,8 @@ __global__ void __launch_bounds__(kThreadsR, 1)
             (last ? static_cast<int64_t>(x.q_start) : x.rowbase + x.split) * a.Hq + x.kvh * G;
         const int64_t row_step = last ? a.Hq : static_cast<int64_t>(x.nsp) * a.Hq;
         const int tok0 = (x.tile + t) * T, q_len = x.q_len;
-        const int r0 = (warp & 3) * 32 + (ln >> 3); // the first row this lane stores
-        // 128 bytes of the warp's 32 rows, from shared memory to column byte cb
-        // of rows of row_bytes
-        auto put = [&](uint8_t *base, int cb, int row_bytes) {
-          __syncwarp();
-          uint4 w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            w[i] = *reinterpret_cast<const uint4 *>(stg + ((r0 + 4 * i) & 31) * 128 +
-                                                    (((ln & 7) ^ ((r0 + 4 * i) & 7)) << 4));
-          const int c = cb + (ln & 7) * 16;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 4 * i, tok = tok0 + (r >> gs);
-            if (tok < q_len && c < row_bytes)
-              *reinterpret_cast<uint4 *>(base + (row_base + tok * row_step + (r & (G - 1))) *
-                                                    row_bytes + c) = w[i];
-          }
-          __syncwarp();
-        };
+        const int64_t dst = (row_base + (tok0 + (row >> gs)) * row_step + (row & (G - 1))) * Dr;
+        const bool store = tok0 + (row >> gs) < q_len;
         // the running state, this CTA's own: float4 column x tile row
         float4 *run = reinterpret_cast<float4 *>(a.part_o) +
                       static_cast<int64_t>(blockIdx.x) * (2 * kTileRows * D / 4) +
@@ -590,29 +589,22 @@ __global__ void __launch_bounds__(kThreadsR, 1)
                     fold_value(how, wa, wb, o[i], __uint_as_float(v[q * 4 + i])));
             }
           }
-          if (last) { // 64 bytes of the row: two of these make a chunk
-            const int half = (c & 1) * 4;
+          if (last) {
+            if (store && c * 32 < Dr) {
+              uint32_t w[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              auto two = [&](int i) {
-                return pack_bf16(__uint_as_float(v[q * 8 + i]), __uint_as_float(v[q * 8 + i + 1]));
-              };
-              *reinterpret_cast<uint4 *>(stg + ln * 128 + (((half + q) ^ (ln & 7)) << 4)) =
-                  make_uint4(two(0), two(2), two(4), two(6));
+              for (int i = 0; i < 16; ++i)
+                w[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+              store_row(a.out + dst + c * 32, w);
             }
-            if (half) put(reinterpret_cast<uint8_t *>(a.out), (c >> 1) * 128, Dr * 2);
           } else if (folds) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               run[(c * 8 + q) * kTileRows] =
                   make_float4(__uint_as_float(v[q * 4]), __uint_as_float(v[q * 4 + 1]),
                               __uint_as_float(v[q * 4 + 2]), __uint_as_float(v[q * 4 + 3]));
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<uint4 *>(stg + ln * 128 + ((q ^ (ln & 7)) << 4)) =
-                  make_uint4(v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]);
-            put(reinterpret_cast<uint8_t *>(a.part_o), c * 128, Dr * 4);
+          } else if (store && c * 32 < Dr) {
+            store_row(a.part_o + dst + c * 32, v);
           }
         }
         if (t_row < q_len && (last || !folds)) {
