@@ -50,7 +50,10 @@ constexpr int kSoftRegsR = 216, kOtherRegsR = 72;
 static_assert(8 * kSoftRegsR + 4 * kOtherRegsR <= 12 * 168, "registers of the launch");
 constexpr int kItemsR = 3;              // items in flight: loads run ahead of the stores
 constexpr int kAtomR = kTileRows * 128; // one SW128 column block: 128 rows x 64 bf16
-constexpr float kRescaleR = 8.0f;       // log2 units
+// log2 units the running max may lag a block's: weights reach 2^16 (bf16 and
+// fp32 sums keep their relative precision), and fewer blocks rescale O than at
+// 8 (16384 tokens: 1.65 -> 1.62 ms; nothing more at 40)
+constexpr float kRescaleR = 16.0f;
 
 // One (unit, kv head): what the roles need of it.  kvh < 0 ends the list.
 struct alignas(16) ItemR {
@@ -363,8 +366,8 @@ __global__ void __launch_bounds__(kThreadsR, 1)
           }
           mma_commit(bar(L::kSFull + t));
         };
-        auto issue_pv = [&](int t, int st, int &np, bool first, bool last) {
-          ok = ok && mbar_wait(bar(L::kPFull + t), np & 1, a.status);
+        auto issue_pv = [&](int t, int st, int &np, bool first, bool last, bool rdy) {
+          ok = ok && (rdy || mbar_wait(bar(L::kPFull + t), np & 1, a.status));
           if (!ok) return;
           ++np;
           tc_fence_after();
@@ -398,19 +401,24 @@ __global__ void __launch_bounds__(kThreadsR, 1)
           if (nb == 1) mma_commit(bar(L::kQEmpty));
           for (int j = 0; j < nb && ok; ++j, ++g) {
             const int st = g & 1, s1 = st ^ 1, j1 = j + 1;
-            ok = mbar_wait(bar(L::kVFull + st), (g >> 1) & 1, a.status);
+            // a barrier's answer takes ~170 cycles even when its phase is complete:
+            // ask for the three at once (16384 tokens: 1.68 -> 1.65 ms)
+            const bool v_rdy = mbar_try(bar(L::kVFull + st), (g >> 1) & 1);
+            const bool pa_rdy = j < nb0 && mbar_try(bar(L::kPFull + 0), np0 & 1);
+            const bool k_rdy = j1 < nb && mbar_try(bar(L::kKFull + s1), ((g + 1) >> 1) & 1);
+            ok = v_rdy || mbar_wait(bar(L::kVFull + st), (g >> 1) & 1, a.status);
             if (ok && v_tail && j1 == nb) {
               ok = mbar_wait(bar(L::kVTail + st), (tails >> st) & 1, a.status);
               tails ^= 1u << st;
             }
             if (!ok) break;
-            if (j < nb0) issue_pv(0, st, np0, j == 0, j1 == nb0);
+            if (j < nb0) issue_pv(0, st, np0, j == 0, j1 == nb0, pa_rdy);
             if (ok && j1 < nb) {
-              ok = mbar_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1, a.status);
+              ok = k_rdy || mbar_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1, a.status);
               if (ok) tc_fence_after();
             }
             if (ok && j1 < nb0) issue_s(0, s1);
-            if (j < nb1) issue_pv(1, st, np1, j == 0, j1 == nb1);
+            if (j < nb1) issue_pv(1, st, np1, j == 0, j1 == nb1, false);
             if (!ok) break;
             if (j1 < nb1) issue_s(1, s1);
             mma_commit(bar(L::kVEmpty + st));
