@@ -1229,6 +1229,8 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
   pa.ctas = bia::ragged_ctas(D);
   pa.causal = causal;
   pa.split = plan_split;
+  pa.max_total_q = hp.total_q;
+  pa.max_kv_len = static_cast<int32_t>(total_kv);
   pa.n_groups_expected = hp.n_groups;
   pa.n_units_expected = hp.n_units;
   pa.part_rows_expected = hp.part_rows;

@@ -186,8 +186,9 @@ struct PlanArgs {
   // capacities), every request must lie within them, and the units the
   // actual lengths do not need are retired
   int32_t bounded;
-  int32_t max_q_len, max_kv_len; // per-request bounds (bounded calls)
-  int64_t max_total_q;            // q tokens of the call (bounded calls)
+  // per-request bounds (bounded calls); max_kv_len of packed keys: all of them
+  int32_t max_q_len, max_kv_len;
+  int64_t max_total_q; // q tokens of the call (bounded calls, packed keys)
   int64_t n_groups_expected, n_units_expected, n_sunits_expected, part_rows_expected;
   // the call's outputs: filled with NaN when the plan fails its checks, so a
   // failure shows in the data and not only in the status word

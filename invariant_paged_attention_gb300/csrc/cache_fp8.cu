@@ -8,13 +8,14 @@
 // the reverse).  A warp takes up to 32 consecutive tokens: each lane finds the
 // cache slot of one (its request by a search over the lanes' copy of the index
 // arrays, then one load of its page), and the warp runs through their rows,
-// the K heads and then the V heads of each token, four steps' loads in
-// flight.  Nothing is read or written twice: 2*D bytes in and D + 1 out per
-// row, HBM bound.  44213 tokens of 8 heads x 128 (272 MB, 40 us at the copy
-// rate): see the two kernels.  With a group of lanes per row, each finding its
-// slot by binary search and 64-bit divisions, the index work bound them: 123
-// and 94 us; with a warp a token, a slot's three dependent loads: 54 us for
-// gather, 29 for the append of one 64-wide head (17 MB).
+// the K heads and then the V heads of each token, two steps' loads in flight.
+// Nothing is read or written twice: 2*D bytes in and D + 1 out per row, HBM
+// bound.  44213 tokens of 8 heads x 128 (272 MB, 40 us at the copy rate): 45
+// us for the append, 47 for the gather.  With a group of lanes per row, each
+// finding its slot by binary search and 64-bit divisions, the index work bound
+// them: 123 and 94 us; with a warp a token, a slot's three dependent loads did
+// where tokens are short: 29 us for the append of one 64-wide head (17 MB),
+// 11 now.
 #include <algorithm>
 
 #include "bia_internal.h"
@@ -92,7 +93,7 @@ struct RowAt {
   }
 };
 
-// 16 elements of a row quantised; big: the row's largest |x| bits.
+// 16 elements of a row as codes; inv: 2^-e of the row.
 __device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], float inv) {
   const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
   uint32_t c[8];

@@ -93,7 +93,10 @@ __global__ void __launch_bounds__(kPlanThreadsR) plan_ragged_kernel(const PlanAr
     p.status[0] = 0;
     p.status[kStatusWorkCounter] = 0;
   }
-  bool bad = tid == 0 && (p.kv_indptr[0] < 0 || p.qo_indptr[0] != 0);
+  // the ends too: the rows of the buffers are counted from the host's arrays
+  bool bad = tid == 0 && (p.kv_indptr[0] < 0 || p.qo_indptr[0] != 0 ||
+                          p.qo_indptr[p.batch] != p.max_total_q ||
+                          p.kv_indptr[p.batch] != p.max_kv_len);
   int64_t groups = 0, rows = 0, merges = 0, units = 0; // of the chunks before
   for (int b0 = 0; b0 < p.batch; b0 += kPlanThreadsR) {
     const int b = b0 + tid;

@@ -198,6 +198,25 @@ def test_captured_prompt_replays():
     check(q, k, v, lens, lens, out, lse)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("which", ["q", "kv"])
+def test_device_lengths_that_end_elsewhere_compute_nothing(d, which):
+    """Device arrays that count the same tiles and splits as the host's but end
+    at another row: the buffers are as long as the host's say."""
+    lens = [100, 100]
+    q, k, v = draw(4, 2, d, lens, lens, 1)
+    desc = bia.make_desc(4, 2, d, 1)
+    ip = fu.indptr_of(lens)
+    other = fu.indptr_of([100, 99])
+    ws = torch.empty(bia.bia_prefill_ragged_workspace_size(desc, ip, ip), dtype=torch.uint8, device=DEV)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device=DEV)
+    qo, kv = ((other, ip) if which == "q" else (ip, other))
+    bia.bia_prefill_ragged(desc, q, k, v, qo.to(DEV), kv.to(DEV), ip, ip, ws, out, lse,
+                           causal=which == "q")
+    assert bia.bia_read_status(ws) != 0
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
 @pytest.mark.parametrize("d,hq,hkv,page", [(128, 32, 8, 16), (64, 8, 1, 1), (256, 4, 2, 32)])
 def test_a_server_with_an_8_bit_cache(d, hq, hkv, page):
     """Prompts in two chunks (the second over the prefix read back), then
