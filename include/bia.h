@@ -100,6 +100,8 @@ extern "C" {
 /* Default fixed split-KV sizes ("sglang PR #10417", Modifications). */
 #define BIA_PREFILL_SPLIT 4096
 #define BIA_DECODE_SPLIT 2048
+/* Largest split-KV size of bia_prefill_ragged. */
+#define BIA_RAGGED_MAX_SPLIT 16777216
 /* Largest (and default) split-KV size of the 8-bit decode. */
 #define BIA_DECODE_FP8_SPLIT 1024
 
@@ -537,8 +539,10 @@ BIA_API size_t bia_decode_fp8_bounded_workspace_size(const bia_attn_desc *desc,
  * Request b's q tokens are the last q_len of its kv_len keys (the rule of
  * bia_prefill_paged); causal calls need q_len <= kv_len, and without causal a
  * request without keys gives out 0 and lse -inf.  page_size of desc is not
- * used.  Tiles, split_size (0 = BIA_PREFILL_SPLIT), merge, workspace,
- * ownership and errors as for bia_prefill_paged; a row's bits depend only on
+ * used.  Tiles, split_size (0 = BIA_PREFILL_SPLIT; at most
+ * BIA_RAGGED_MAX_SPLIT, so that a tile's time stays far below the limit of
+ * the kernel's waits, else BIA_ERR_UNSUPPORTED), merge, workspace, ownership
+ * and errors as for bia_prefill_paged; a row's bits depend only on
  * its own request up to its position, under any chunking, on the q-tile grid
  * or off it.  What lies past a request's last key never reaches its rows; a
  * non-finite key or value of the request itself may reach every row of the

@@ -30,6 +30,7 @@ BIA_ERR_WORKSPACE_TOO_SMALL = -3
 BIA_ERR_CUDA = -4
 BIA_Q_TILE_ROWS = 128
 BIA_PREFILL_SPLIT = 4096
+BIA_RAGGED_MAX_SPLIT = 1 << 24
 BIA_DECODE_SPLIT = 2048
 BIA_DECODE_FP8_SPLIT = 1024
 

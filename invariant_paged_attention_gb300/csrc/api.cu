@@ -1066,6 +1066,7 @@ int ragged_plan(const bia_attn_desc *desc, const int32_t *qo_host, const int32_t
   int rc = check_desc(d);
   if (rc != BIA_OK) return rc;
   if (kv_host[0] != 0) return BIA_ERR_INVALID_ARG;
+  if (split > BIA_RAGGED_MAX_SPLIT) return BIA_ERR_UNSUPPORTED;
   auto plan = [&](int32_t sp) {
     return host_plan(d, qo_host, kv_host, nullptr, batch, causal, sp,
                      bia::kTileRows / (d->num_qo_heads / d->num_kv_heads),

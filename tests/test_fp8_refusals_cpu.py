@@ -130,6 +130,11 @@ def test_packed_prefill_refuses(bia):
     assert prompt(bia, d, [0, 10], [0, 10], q_stride=4092) == inv  # below a token's row
     assert prompt(bia, d, [0, 10], [0, 10], k_stride=1028) == inv  # off the 16-byte grid
     assert prompt(bia, d, [0, 10], [0, 10], split=64) == uns
+    most = bia.BIA_RAGGED_MAX_SPLIT
+    assert prompt(bia, d, [0, 10], [0, 10], split=most + 128) == uns
+    assert prompt(bia, d, [0, 10], [0, 10], split=most, ws_bytes=64) == bia.BIA_ERR_WORKSPACE_TOO_SMALL
+    header = os.path.join(os.path.dirname(__file__), "..", "include", "bia.h")
+    assert f"#define BIA_RAGGED_MAX_SPLIT {most}\n" in open(header).read()
     assert prompt(bia, bia.make_desc(32, 8, 112, 1), [0, 10], [0, 10]) == uns
     assert prompt(bia, bia.make_desc(36, 12, 128, 1), [0, 10], [0, 10]) == uns
     assert prompt(bia, d, [0, 10], [0, 10], ws_bytes=64) == bia.BIA_ERR_WORKSPACE_TOO_SMALL

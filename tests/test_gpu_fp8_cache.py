@@ -119,6 +119,41 @@ def test_gather_reads_back_exactly(hkv, d, page, lens, take):
             assert torch.equal(out[op[b]:op[b] + n].double(), want)
 
 
+def test_a_cache_past_32_bits():
+    """Codes on both sides of byte 2^32 of the cache and at its end: what is
+    appended there reads back, and decodes to the bits a small cache gives."""
+    hkv, d, page, n_pages = 8, 128, 16, 300_000  # 4.9 GB of codes each
+    at = 2 ** 32 // (page * hkv * d)
+    far = torch.tensor([at - 1, at, n_pages - 1, 0], dtype=torch.int32)
+    lens = [60]
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k, v, q = fu.rows((60, hkv, d), g), fu.rows((60, hkv, d), g), fu.rows((1, 32, d), g)
+    desc = bia.make_desc(32, hkv, d, page)
+    indptr, last = fu.indptr_of([4]), torch.tensor([12], dtype=torch.int32)
+    got = []
+    for pages, ids in ((n_pages, far), (4, torch.arange(4, dtype=torch.int32))):
+        cache = [torch.empty((pages, page, hkv, d), dtype=torch.uint8, device=DEV).view(fu.E4M3)
+                 for _ in "kv"]
+        scale = [torch.empty((pages, page, hkv), dtype=torch.uint8, device=DEV).view(fu.E8M0)
+                 for _ in "kv"]
+        append(desc, k, v, *cache, *scale, lens, (indptr, ids, last))
+        slots = slots_of(ids, page, 0, 60)
+        for c, e, r in zip(cache, scale, (k, v)):
+            expect(c, e, slots, r)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        op, dev = fu.indptr_of(lens), (indptr.to(DEV), ids.to(DEV), last.to(DEV))
+        bia.bia_gather_paged_kv_fp8(desc, *cache, *scale, ko, vo, op.to(DEV), *dev, op, indptr, last)
+        ws = torch.empty(bia.bia_decode_fp8_workspace_size(desc, indptr, last), dtype=torch.uint8,
+                         device=DEV)
+        out, lse = torch.empty_like(q), torch.empty((1, 32), device=DEV)
+        bia.bia_decode_paged_fp8(desc, q, *cache, *scale, *dev, indptr, last, ws, out, lse)
+        assert bia.bia_read_status(ws) == 0
+        got.append((ko, vo, out, lse))
+        del cache, scale
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_a_whole_code_table_reads_back_exactly():
     # every code under every scale byte that append can write, and the e8m0
     # bytes 0 and 255 of a foreign cache

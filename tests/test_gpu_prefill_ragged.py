@@ -160,6 +160,28 @@ def test_splits_folded_in_the_cta_have_the_merge_s_bits(d, causal):
         check(q[qa:qa + x], k[ka:ka + y], v[ka:ka + y], [x], [y], out[qa:qa + x], lse[qa:qa + x], causal)
 
 
+def test_rows_past_32_bits_and_more_requests_than_a_plan_s_chunk():
+    """2700 requests, q and out of more than 2^31 elements: as each alone."""
+    hq, hkv, d = 64, 8, 128
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 201, (2700,), generator=g).tolist()
+    assert sum(lens) * hq * d > 2 ** 31
+    gd = torch.Generator(device=DEV).manual_seed(4)
+    q, k, v = (torch.empty((sum(lens), h, d), dtype=torch.bfloat16, device=DEV).normal_(generator=gd)
+               for h in (hq, hkv, hkv))
+    out, lse = run(q, k, v, lens, lens)
+    at = fu.indptr_of(lens).tolist()
+    for i in (0, 1, 511, 512, 1024, 1500, 2698, 2699):
+        a, b = at[i], at[i + 1]
+        if a == b:
+            continue
+        one, l = run(q[a:b], k[a:b], v[a:b], lens[i:i + 1], lens[i:i + 1])
+        assert same_bits(one, out[a:b]) and same_bits(l, lse[a:b])
+    a, b = at[2690], at[2700]
+    check(q[a:b], k[a:b], v[a:b], lens[2690:], lens[2690:], out[a:b], lse[a:b])
+    assert torch.isfinite(lse).all()
+
+
 def test_scale_stream_and_lse():
     lens = [257, 64]
     q, k, v = draw(4, 4, 128, lens, lens, 8)
