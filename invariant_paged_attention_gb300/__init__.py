@@ -594,33 +594,25 @@ def bia_mla_prefill_paged(desc, q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, k
 # ---------------------------------------------------------------- 8-bit cache
 #
 # These calls are made once per layer and decode step, so what a well-formed
-# call pays on the host counts (a 32-token append's kernel takes about 3 us):
-# _not_ready looks every tensor over in one pass, and only a call that fails it
-# goes through the checks that find the reason.
+# call pays on the host counts (a 32-token append's kernel takes about 5 us):
+# _dense looks the tensors over, and only a call that fails it goes through
+# the checks that find the reason.
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _not_ready(stream, *specs):
-    """None when the tensors of `specs` ((name, tensor, dtype) or, for an
-    optional one, (name, tensor, dtype, True)) are contiguous, of their dtypes
-    and on the launch's device.  Else raises for a wrong dtype or layout, and
-    returns what _check_cuda takes, for after the shapes."""
-    device = None
-    for spec in specs:
-        t = spec[1]
-        if t is None and len(spec) > 3:
-            continue
-        if not isinstance(t, torch.Tensor):
-            break
-        at = t.get_device()
-        if device is None:
-            device = at
-        if (at != device or at < 0 or (spec[2] is not None and t.dtype is not spec[2]) or
+def _index(t) -> int:
+    """CUDA device index of a tensor, -1 of anything else."""
+    return t.get_device() if type(t) is torch.Tensor else -1
+
+
+def _dense(device, dtype, *tensors) -> bool:
+    """Whether all are contiguous tensors of `dtype` on CUDA device `device`."""
+    for t in tensors:
+        if (type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != device or
                 not t.is_contiguous()):
-            break
-    else:
-        if stream is None and device == torch._C._cuda_getDevice():
-            return None
-    return _check_types(*specs)
+            return False
+    return True
 
 
 def _handle(stream):
@@ -702,14 +694,6 @@ def _packed(name, t, heads, head_dim, tokens):
     return step
 
 
-def _on_device(unready, stream, like, **packed):
-    """The device checks of a call: what _not_ready left, and that the packed
-    rows are where `like` is."""
-    at = like.get_device()
-    if unready is not None or any(t.get_device() != at for t in packed.values()):
-        _check_cuda((unready or [("the other arguments", like)]) + list(packed.items()), stream)
-
-
 def bia_append_paged_kv_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_scale, append_indptr,
                             kv_indptr, kv_indices, kv_last_page_len, append_indptr_host,
                             kv_indptr_host, kv_last_page_len_host, status=None, stream=None):
@@ -723,17 +707,24 @@ def bia_append_paged_kv_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_sca
     total, hkv, d = _last(ap), desc.num_kv_heads, desc.head_dim
     k_step = _packed("k_new", k_new, hkv, d, total)
     v_step = _packed("v_new", v_new, hkv, d, total)
-    ts = _not_ready(stream, ("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
-                    ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
-                    ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                    ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                    ("status", status, I32, True))
+    at, ts = _index(k_cache), None
+    if not (stream is None and _dense(at, E4M3, k_cache, v_cache) and
+            _dense(at, E8M0, k_scale, v_scale) and
+            _dense(at, I32, append_indptr, kv_indptr, kv_indices, kv_last_page_len) and
+            (status is None or _dense(at, I32, status)) and at >= 0 and
+            at == _current_device()):
+        ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                        ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                        ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                        ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                        ("status", status, I32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
     _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
     if append_indptr.numel() != batch + 1:
         raise ValueError(f"append_indptr must hold {batch + 1} entries, got "
                          f"{append_indptr.numel()}")
-    _on_device(ts, stream, k_cache, k_new=k_new, v_new=v_new)
+    if ts is not None or k_new.get_device() != at or v_new.get_device() != at:
+        _check_cuda((ts or [("k_cache", k_cache)]) + [("k_new", k_new), ("v_new", v_new)], stream)
     rc = load().bia_append_paged_kv_fp8(
         ctypes.byref(desc), _at(k_new), _at(v_new), k_step, v_step, _at(k_cache), _at(v_cache),
         _at(k_scale), _at(v_scale), k_cache.shape[0], _at(append_indptr), _at(kv_indptr),
@@ -749,12 +740,18 @@ def bia_gather_paged_kv_fp8(desc, k_cache, v_cache, k_scale, v_scale, k_out, v_o
     """Reads the first out_indptr[b+1] - out_indptr[b] keys of each request
     back from the 8-bit cache into k_out / v_out [out_indptr[batch], Hkv, D]
     bf16, packed (include/bia.h states the rule)."""
-    ts = _not_ready(stream, ("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
-                    ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
-                    ("k_out", k_out, BF16), ("v_out", v_out, BF16),
-                    ("out_indptr", out_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                    ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                    ("status", status, I32, True))
+    at, ts = _index(k_cache), None
+    if not (stream is None and _dense(at, E4M3, k_cache, v_cache) and
+            _dense(at, E8M0, k_scale, v_scale) and _dense(at, BF16, k_out, v_out) and
+            _dense(at, I32, out_indptr, kv_indptr, kv_indices, kv_last_page_len) and
+            (status is None or _dense(at, I32, status)) and at >= 0 and
+            at == _current_device()):
+        ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                        ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                        ("k_out", k_out, BF16), ("v_out", v_out, BF16),
+                        ("out_indptr", out_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                        ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                        ("status", status, I32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
     op, kvp, last = _host(out_indptr_host), _host(kv_indptr_host), _host(kv_last_page_len_host)
     batch = op.numel() - 1
@@ -765,7 +762,8 @@ def bia_gather_paged_kv_fp8(desc, k_cache, v_cache, k_scale, v_scale, k_out, v_o
     if k_out.shape != want or v_out.shape != want:
         raise ValueError(f"k_out and v_out must be {want}, got {tuple(k_out.shape)} and "
                          f"{tuple(v_out.shape)}")
-    _on_device(ts, stream, k_cache)
+    if ts is not None:
+        _check_cuda(ts, stream)
     rc = load().bia_gather_paged_kv_fp8(
         ctypes.byref(desc), _at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale),
         k_cache.shape[0], _at(out_indptr), _at(kv_indptr), _at(kv_indices),
@@ -784,11 +782,17 @@ def bia_decode_fp8_workspace_size(desc, kv_indptr_host, kv_last_page_len_host,
 
 def _check_decode_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
                       kv_last_page_len, workspace, out, lse, stream, kvp=None, last=None):
-    ts = _not_ready(stream, ("q", q, BF16), ("k_cache", k_cache, E4M3),
-                    ("v_cache", v_cache, E4M3), ("k_scale", k_scale, E8M0),
-                    ("v_scale", v_scale, E8M0), ("kv_indptr", kv_indptr, I32),
-                    ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                    ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+    at, ts = _index(q), None
+    if not (stream is None and _dense(at, BF16, q, out) and _dense(at, E4M3, k_cache, v_cache) and
+            _dense(at, E8M0, k_scale, v_scale) and
+            _dense(at, I32, kv_indptr, kv_indices, kv_last_page_len) and
+            (lse is None or _dense(at, F32, lse)) and at >= 0 and
+            _index(workspace) == at == _current_device() and workspace.is_contiguous()):
+        ts = _check_types(("q", q, BF16), ("k_cache", k_cache, E4M3),
+                        ("v_cache", v_cache, E4M3), ("k_scale", k_scale, E8M0),
+                        ("v_scale", v_scale, E8M0), ("kv_indptr", kv_indptr, I32),
+                        ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
+                        ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
     want = (kv_indptr.numel() - 1, desc.num_qo_heads, desc.head_dim)
     if q.shape != want or out.shape != want:
@@ -796,7 +800,8 @@ def _check_decode_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv
     if lse is not None and lse.numel() != want[0] * want[1]:
         raise ValueError(f"lse must hold {want[0]} x {want[1]} floats")
     _check_table(want[0], kv_indptr, kv_indices, kv_last_page_len, kvp, last)
-    _on_device(ts, stream, q)
+    if ts is not None:
+        _check_cuda(ts, stream)
 
 
 def bia_decode_paged_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
@@ -860,8 +865,12 @@ def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_i
     q_step = _packed("q", q, hq, d, _last(qo))
     k_step = _packed("k", k, hkv, d, _last(kvp))
     v_step = _packed("v", v, hkv, d, _last(kvp))
-    ts = _not_ready(stream, ("qo_indptr", qo_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                    ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+    at, ts = _index(out), None
+    if not (stream is None and _dense(at, I32, qo_indptr, kv_indptr) and _dense(at, BF16, out) and
+            (lse is None or _dense(at, F32, lse)) and at >= 0 and
+            _index(workspace) == at == _current_device() and workspace.is_contiguous()):
+        ts = _check_types(("qo_indptr", qo_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                        ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
     if out.shape != q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
     if lse is not None and lse.numel() != q.shape[0] * hq:
@@ -869,7 +878,8 @@ def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_i
     for name, t in (("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("kv_indptr_host", kvp)):
         if t.numel() != batch + 1:
             raise ValueError(f"{name} must hold {batch + 1} entries, got {t.numel()}")
-    _on_device(ts, stream, out, q=q, k=k, v=v)
+    if ts is not None or q.get_device() != at or k.get_device() != at or v.get_device() != at:
+        _check_cuda((ts or [("out", out)]) + [("q", q), ("k", k), ("v", v)], stream)
     rc = load().bia_prefill_ragged(
         ctypes.byref(desc), _at(q), _at(k), _at(v), q_step, k_step, v_step, _at(qo_indptr),
         _at(kv_indptr), _at(qo), _at(kvp), batch, int(bool(causal)), int(split_size),

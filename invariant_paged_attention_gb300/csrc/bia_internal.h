@@ -3,6 +3,7 @@
 // launchers.  Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -331,6 +332,28 @@ cudaError_t launch_decode_fp8_g4(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s);
 // Packed keys and values: head_dim 64, 96 and 128; 256
+// Looked up once per device: its SM count, and (smem > 0) whether `fn` may use
+// that much dynamic shared memory there; `ready` holds a bit per device.
+inline cudaError_t prepare_launch(const void *fn, int smem, std::atomic<uint64_t> &ready,
+                                  int *sms) {
+  static std::atomic<int> counts[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev < 64;
+  *sms = kept ? counts[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms == 0) {
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (kept) counts[dev].store(*sms, std::memory_order_relaxed);
+  }
+  const uint64_t bit = kept ? uint64_t{1} << dev : 0;
+  if (smem == 0 || (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // (q tile pair, kv head) items from which a packed prefill folds a pair's
 // splits in the CTA instead of merging states: two a CTA of the 152 SMs.
 // Below, the splits balance the CTAs.  Folded against merged, 128-wide heads:

@@ -867,12 +867,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
 template <int G, int DW, int HB>
 cudaError_t launch_f8(const DecodeFp8Args &f, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decode_fp8_kernel<G, DW, HB>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem8<DW, HB>::kAlloc);
+  static std::atomic<uint64_t> ready{0};
+  int sms = 0;
+  const cudaError_t e =
+      prepare_launch(reinterpret_cast<const void *>(decode_fp8_kernel<G, DW, HB>),
+                     Smem8<DW, HB>::kAlloc, ready, &sms);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(f.a.n_units * (f.a.Hkv / HB), sms)));
@@ -891,9 +890,9 @@ cudaError_t launch_f8(const DecodeFp8Args &f, cudaStream_t s) {
 // Both forms give the same bits.
 template <int G>
 cudaError_t launch_f8_g(const DecodeFp8Args &f, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<uint64_t> none{0};
+  int sms = 0;
+  const cudaError_t e = prepare_launch(nullptr, 0, none, &sms);
   if (e != cudaSuccess) return e;
   const bool pairs = f.a.Hkv % 2 == 0 && f.a.n_units * f.a.Hkv > sms;
   if (f.a.D == 64) return pairs ? launch_f8<G, 64, 2>(f, s) : launch_f8<G, 64, 1>(f, s);

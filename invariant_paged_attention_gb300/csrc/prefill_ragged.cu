@@ -639,12 +639,10 @@ __global__ void __launch_bounds__(kThreadsR, 1)
 template <int D>
 cudaError_t launch_ragged_d(const AttnArgs &a, cudaStream_t s) {
   using L = SmemR<D>;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(prefill_ragged_kernel<D>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  static std::atomic<uint64_t> ready{0};
+  int sms = 0;
+  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(prefill_ragged_kernel<D>),
+                                       L::kAlloc, ready, &sms);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min({static_cast<int64_t>(sms), kFoldCtas, a.n_units * a.Hkv})));
