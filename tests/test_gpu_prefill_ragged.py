@@ -220,6 +220,65 @@ def test_captured_prompt_replays():
     check(q, k, v, lens, lens, out, lse)
 
 
+def two_calls():
+    """A call that folds its splits in the CTAs and one that merges them."""
+    calls = []
+    for i, (hq, hkv, q_lens, kv_lens) in enumerate((
+            (32, 8, [2000, 1500], [2000, 6000]), (8, 2, [100, 1, 300], [5000, 4500, 300]))):
+        calls.append((hq, hkv, q_lens, kv_lens, draw(hq, hkv, 128, q_lens, kv_lens, 20 + i)))
+    return calls
+
+
+def enqueue(hq, hkv, q_lens, kv_lens, rows, ws=None):
+    desc = bia.make_desc(hq, hkv, 128, 1)
+    qo, kv = fu.indptr_of(q_lens), fu.indptr_of(kv_lens)
+    if ws is None:
+        ws = torch.empty(bia.bia_prefill_ragged_workspace_size(desc, qo, kv), dtype=torch.uint8,
+                         device=DEV)
+    out, lse = torch.empty_like(rows[0]), torch.empty(rows[0].shape[:2], device=DEV)
+    dev = qo.to(DEV), kv.to(DEV)
+
+    def call():
+        bia.bia_prefill_ragged(desc, *rows, *dev, qo, kv, ws, out, lse)
+    return call, out, lse, ws
+
+
+def test_two_graphs_share_one_workspace():
+    calls = two_calls()
+    want = [run(*rows, ql, kl) for _, _, ql, kl, rows in calls]
+    ws = torch.empty(max(enqueue(*c)[3].numel() for c in calls), dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for c in calls:
+        call, out, lse, _ = enqueue(*c, ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append((graph, call))
+        outs.append((out, lse))
+    for _ in range(3):
+        for graph, _ in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(outs, want):
+        assert same_bits(o, wo) and same_bits(l, wl)
+
+
+def test_calls_on_two_streams_with_their_own_workspaces():
+    calls = two_calls()
+    want = [run(*rows, ql, kl) for _, _, ql, kl, rows in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            call, out, lse, ws = enqueue(*calls[i % 2])
+            call()
+            got.append((out, lse, ws))
+    torch.cuda.synchronize()
+    for i, (o, l, _) in enumerate(got):
+        assert same_bits(o, want[i % 2][0]) and same_bits(l, want[i % 2][1])
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("which", ["q", "kv"])
 def test_device_lengths_that_end_elsewhere_compute_nothing(d, which):
