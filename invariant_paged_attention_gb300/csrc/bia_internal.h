@@ -357,9 +357,10 @@ inline cudaError_t prepare_launch(const void *fn, int smem, std::atomic<uint64_t
 // (q tile pair, kv head) items from which a packed prefill folds a pair's
 // splits in the CTA instead of merging states: two a CTA of the 152 SMs.
 // Below, the splits balance the CTAs.  Folded against merged, 128-wide heads:
-// 512 items of a 16384-token prompt 472 / 554 us, of 4 x 2048 tokens behind
-// 16383 keys 1074 / 1037; 256 items of 4 x 1024 such tokens 552 / 535; 160 of
-// 5 x 512 would take two rounds of whole rows where their splits need one.
+// 512 items of a 16384-token prompt 447 / 531 us, of 4 x 2048 tokens behind
+// 16383 keys 1030 / 980; 256 items of 4 x 1024 such tokens 520 / 498, of an
+// 8192-token prompt 138 / 158; a little over 152 equal items would take two
+// rounds of whole rows where their splits need one.
 constexpr int64_t kFoldCtas = 152;
 constexpr int64_t kFoldItems = 2 * kFoldCtas;
 cudaError_t launch_plan_ragged(const PlanArgs &p, cudaStream_t s);
