@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreadsR, 1)
       // ------------------------------------------------------------ loads
       if (lane == 0) {
         bool ok = true;
-        int g = 0, nq = 0; // blocks and q tile pairs loaded
+        int g = 0, nk = 0, nq = 0; // blocks, K blocks and q tile pairs loaded
         while (const ItemR *xp = next()) {
           const ItemR x = *xp;
           release();
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreadsR, 1)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
               tma_load_3d(sK(st) + h * kAtomR, &a.tm_k, 64 * h, x.kvh, row, bar(L::kKFull + st));
+            nk = g + 1;
             if (j == 0) {
               // q of this item while the previous one is still in its last P.V
               ok = nq == 0 || mbar_wait(bar(L::kQEmpty), (nq - 1) & 1, a.status);
@@ -313,10 +314,12 @@ __global__ void __launch_bounds__(kThreadsR, 1)
         // no copy and no commit outlives the CTA, also when a wait ran out
         if (nq > 0) mbar_wait(bar(L::kQFull), (nq - 1) & 1, a.status);
         if (nq > 0 && ok) mbar_wait(bar(L::kQEmpty), (nq - 1) & 1, a.status);
-        for (int b = max(0, g - 2); b < g; ++b) {
+        for (int b = max(0, nk - 2); b < nk; ++b) {
           mbar_wait(bar(L::kKFull + (b & 1)), (b >> 1) & 1, a.status);
-          mbar_wait(bar(L::kVFull + (b & 1)), (b >> 1) & 1, a.status);
           if (ok) mbar_wait(bar(L::kKEmpty + (b & 1)), (b >> 1) & 1, a.status);
+        }
+        for (int b = max(0, g - 2); b < g; ++b) {
+          mbar_wait(bar(L::kVFull + (b & 1)), (b >> 1) & 1, a.status);
           if (ok) mbar_wait(bar(L::kVEmpty + (b & 1)), (b >> 1) & 1, a.status);
         }
       }
