@@ -993,7 +993,7 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
 
   bia::DecodeFp8Args f{};
-  AttnArgs &a = f.a;
+  bia::DecodeGeometry &a = f.a;
   a.q = static_cast<const uint16_t *>(q);
   a.kv_indices = kv_indices;
   a.num_pages = num_pages;
@@ -1002,7 +1002,6 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   a.D = desc->head_dim;
   a.G = desc->num_qo_heads / desc->num_kv_heads;
   a.page_shift = log2i(desc->page_size);
-  a.split = split;
   a.scale_log2 = effective_scale(desc);
   a.batch = batch;
   a.n_units = hp.n_units;
@@ -1010,7 +1009,6 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   f.units = units;
   a.part_o = reinterpret_cast<float *>(ws + w.part_o);
   a.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
-  a.total_rows = hp.total_q;
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.status = pa.status;

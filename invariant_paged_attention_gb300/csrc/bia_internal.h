@@ -278,10 +278,25 @@ struct UnitFp8 {
 };
 static_assert(sizeof(UnitFp8) == 32, "UnitFp8 layout");
 
-// Decode over the 8-bit paged cache: the geometry of the bf16 decode (the
-// cache pointers and units of `a` unused) and the codes and scales.
+// Geometry of a decode over the 8-bit paged cache (AttnArgs' fields of the
+// same names, without its 900 bytes of tensor maps).
+struct DecodeGeometry {
+  const uint16_t *q;
+  const int32_t *kv_indices;
+  int64_t num_pages;
+  int32_t Hq, Hkv, D, G, page_shift;
+  float scale_log2;
+  int32_t batch;
+  int64_t n_units;
+  const ReqInfo *reqs;
+  float *part_o, *part_lse;
+  uint16_t *out;
+  float *lse;
+  int32_t *status;
+};
+
 struct DecodeFp8Args {
-  AttnArgs a;
+  DecodeGeometry a;
   const UnitFp8 *units;
   const uint8_t *k_codes, *v_codes; // e4m3 [num_pages, page_size, Hkv, D]
   const uint8_t *k_scale, *v_scale; // e8m0 [num_pages, page_size, Hkv]
@@ -330,7 +345,7 @@ cudaError_t launch_decode_fp8_g1(const DecodeFp8Args &f, cudaStream_t s); // by 
 cudaError_t launch_decode_fp8_g2(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g4(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g8(const DecodeFp8Args &f, cudaStream_t s);
-cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_merge_decode_fp8(const DecodeGeometry &a, cudaStream_t s);
 // Packed keys and values: head_dim 64, 96 and 128; 256
 // Looked up once per device: its SM count, and (smem > 0) whether `fn` may use
 // that much dynamic shared memory there; `ready` holds a bit per device.

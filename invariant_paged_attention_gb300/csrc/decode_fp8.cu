@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads8)
 constexpr int kMergeWarps8 = 8;
 
 template <int V>
-__global__ void __launch_bounds__(kMergeWarps8 * 32) merge_decode_fp8_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kMergeWarps8 * 32) merge_decode_fp8_kernel(const DecodeGeometry a) {
   constexpr int kChunk = V == 4 ? 8 : 4; // states in flight
   const int lane = threadIdx.x & 31;
   grid_dep_wait(); // the partials are complete
@@ -238,7 +238,7 @@ cudaError_t launch_plan_decode_fp8(const PlanArgs &p, UnitFp8 *units, cudaStream
   return launch_chained(plan_decode_fp8_kernel, 1, kPlanThreads8, s, p, units);
 }
 
-cudaError_t launch_merge_decode_fp8(const AttnArgs &a, cudaStream_t s) {
+cudaError_t launch_merge_decode_fp8(const DecodeGeometry &a, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.batch) * a.Hq;
   const int64_t grid = (rows + kMergeWarps8 - 1) / kMergeWarps8;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;

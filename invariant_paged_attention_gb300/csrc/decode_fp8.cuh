@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   constexpr uint32_t kIdescS = idesc_e4m3(128, kN8, false, false);
   constexpr uint32_t kIdescPV = idesc_e4m3(128, kN8, true, true);
   constexpr uint32_t kTmemCols = 512;
-  const AttnArgs &a = f.a;
+  const DecodeGeometry &a = f.a;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
