@@ -1243,9 +1243,13 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
   pa.group_cnt = reinterpret_cast<int32_t *>(ws + w.group_cnt);
   pa.units = reinterpret_cast<bia::Unit *>(ws + w.units);
   pa.sunits = reinterpret_cast<bia::Unit *>(ws + w.sunits);
-  cudaError_t e = bia::launch_plan_ragged(pa, st);
+  bool itself = false;
+  cudaError_t e = bia::ragged_plans_itself(D, batch, hp.n_units * Hkv, hp.part_rows, &itself);
+  if (e == cudaSuccess && !itself) {
+    e = bia::launch_plan_ragged(pa, st);
+    if (e == cudaSuccess) __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  }
   if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
-  __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
 
   AttnArgs a{};
   a.q = static_cast<const uint16_t *>(q);
@@ -1287,7 +1291,8 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
     const cudaError_t re = cudaEventRecord(g_attn_begin, st);
     if (re != cudaSuccess) return cuda_fail("profile event record", re);
   }
-  e = D == 256 ? bia::launch_prefill_ragged_wide(a, st) : bia::launch_prefill_ragged(a, st);
+  e = D == 256 ? bia::launch_prefill_ragged_wide(a, st)
+               : bia::launch_prefill_ragged(a, itself ? kv_indptr : nullptr, st);
   if (e != cudaSuccess) return cuda_fail("packed prefill kernel launch", e);
   if (hp.n_units > 0) __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
   if (profile) {

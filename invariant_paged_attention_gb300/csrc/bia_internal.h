@@ -379,7 +379,12 @@ inline cudaError_t prepare_launch(const void *fn, int smem, std::atomic<uint64_t
 constexpr int64_t kFoldCtas = 152;
 constexpr int64_t kFoldItems = 2 * kFoldCtas;
 cudaError_t launch_plan_ragged(const PlanArgs &p, cudaStream_t s);
-cudaError_t launch_prefill_ragged(const AttnArgs &a, cudaStream_t s);
+// Whether a packed prefill needs no plan kernel: its CTAs, one an item, find
+// their units themselves.
+cudaError_t ragged_plans_itself(int head_dim, int batch, int64_t items, int64_t part_rows,
+                                bool *itself);
+// kv_indptr: for a call that plans itself, else NULL
+cudaError_t launch_prefill_ragged(const AttnArgs &a, const int32_t *kv_indptr, cudaStream_t s);
 cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s);
 inline int ragged_tiles_per_unit(int head_dim) {
   return head_dim == 256 ? 1 : kPrefillTilesPerUnit;

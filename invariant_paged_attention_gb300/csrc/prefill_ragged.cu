@@ -31,6 +31,10 @@
 // tokens, 32/8 heads x 128: 1350 TFLOP/s, 79 % of the sustained cuBLAS rate;
 // 6 prompts of 100 to 2048 tokens (4 to 5 blocks an item) 61 us, 730 TFLOP/s.
 //
+// A call of up to 32 requests without splits to merge and with an SM for
+// every item has no plan: each CTA's item warp works its unit out of the index
+// arrays (a prompt of 256 tokens: 18 -> 14 us).
+//
 // Invariance: as for prefill.cu; single-token tiles run here too, so a row's
 // bits do not depend on where a chunk boundary falls at all.
 #include "bia_internal.h"
@@ -59,6 +63,22 @@ constexpr int kAtomR = kTileRows * 128; // one SW128 column block: 128 rows x 64
 // fp32 sums keep their relative precision), and fewer blocks rescale O than at
 // 8 (16384 tokens: 1.65 -> 1.62 ms; nothing more at 40)
 constexpr float kRescaleR = 16.0f;
+
+// What the kernel needs of AttnArgs, without the tensor maps it does not use.
+struct RaggedArgs {
+  int32_t Hq, Hkv, D, G, causal, split, tile_tokens, batch, kv_rows;
+  float scale_log2;
+  int64_t n_units;
+  const ReqInfo *reqs;
+  const Unit *units;
+  const int32_t *qo_indptr, *kv_indptr; // of a call that plans itself, else kv_indptr NULL
+  int64_t total_q;
+  float *part_o, *part_lse;
+  uint16_t *out;
+  float *lse;
+  int32_t *status;
+  CUtensorMap tm_q, tm_k, tm_v;
+};
 
 // One (unit, kv head): what the roles need of it.  kvh < 0 ends the list.
 struct alignas(16) ItemR {
@@ -104,7 +124,7 @@ __device__ __forceinline__ void store_row(void *p, const uint32_t (&w)[N]) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsR, 1)
-    prefill_ragged_kernel(const __grid_constant__ AttnArgs a) {
+    prefill_ragged_kernel(const __grid_constant__ RaggedArgs a) {
   using L = SmemR<D>;
   constexpr uint32_t kIdescS = idesc_bf16(128, kKvBlock, false);
   constexpr uint32_t kIdescPV = idesc_bf16(128, D, true);
@@ -194,7 +214,51 @@ __global__ void __launch_bounds__(kThreadsR, 1)
       // up to 32 requests' records stay in the lanes: an item is then one
       // memory latency away, not two
       ReqInfo mine{};
-      if (a.batch <= 32 && lane < a.batch) mine = a.reqs[lane];
+      Unit own{-1, 0, 0, 0}; // the only unit of a CTA that plans itself
+      if (a.kv_indptr) {
+        const bool live = lane < a.batch;
+        const int r = live ? lane : a.batch;
+        const int32_t q0 = a.qo_indptr[r], k0 = a.kv_indptr[r];
+        const int64_t ql = static_cast<int64_t>(a.qo_indptr[live ? r + 1 : r]) - q0;
+        const int64_t kl = static_cast<int64_t>(a.kv_indptr[live ? r + 1 : r]) - k0;
+        bool ok = ql >= 0 && kl >= 0 && kl <= INT32_MAX / 2 && ql <= INT32_MAX / 2 &&
+                  (!a.causal || ql <= kl) && (lane > 0 || (q0 == 0 && k0 >= 0)) &&
+                  (lane != a.batch - 1 || (q0 + ql == a.total_q && k0 + kl == a.kv_rows));
+        mine.q_start = q0;
+        mine.q_len = ok ? static_cast<int32_t>(ql) : 0;
+        mine.kv_len = ok ? static_cast<int32_t>(kl) : 0;
+        mine.nsp = 1;
+        mine.rowbase = -1;
+        mine.page_base = k0;
+        const int32_t tiles = (mine.q_len + T - 1) / T, groups = (tiles + 1) / 2;
+        ok = ok && (tiles == 0 ||
+                    tile_splits(mine.q_len, mine.kv_len, tiles - 1, T, a.causal, a.split) == 1);
+        int64_t end = groups; // of the request's groups
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, end, off);
+          if (lane >= off) end += x;
+        }
+        ok = __all_sync(0xffffffffu, ok) && __shfl_sync(0xffffffffu, end, 31) == a.n_units;
+        // no other error can be noted before: the kernel's waits last seconds
+        if (blockIdx.x == 0 && lane == 0) a.status[0] = ok ? 0 : kStatusPlanMismatch;
+        if (ok) {
+          const int64_t g = w / a.Hkv;
+          const int b = __popc(__ballot_sync(0xffffffffu, end <= g)); // the first that ends past g
+          own.b = b;
+          own.tile = 2 * static_cast<int32_t>(g - __shfl_sync(0xffffffffu, end - groups, b));
+          own.ntiles = min(2, __shfl_sync(0xffffffffu, tiles, b) - own.tile);
+        } else { // as the planner: NaN instead of stale values
+          w = n_items;
+          const int64_t step = static_cast<int64_t>(gridDim.x) * 32, rows = a.total_q * a.Hq;
+          for (int64_t e = blockIdx.x * 32 + lane; e < rows * a.D; e += step)
+            a.out[e] = 0x7fc0u; // bf16 NaN
+          for (int64_t e = blockIdx.x * 32 + lane; a.lse && e < rows; e += step)
+            a.lse[e] = __int_as_float(0x7fc00000);
+        }
+      } else if (a.batch <= 32 && lane < a.batch) {
+        mine = a.reqs[lane];
+      }
       auto request = [&](int b) {
         if (a.batch > 32) return a.reqs[b];
         ReqInfo r;
@@ -218,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsR, 1)
         } else {
           x.kvh = -1;
           while (w < n_items) {
-            const Unit u = a.units[w / a.Hkv];
+            const Unit u = a.kv_indptr ? own : a.units[w / a.Hkv];
             if (u.b >= 0) { // not retired by the plan
               const ReqInfo r = request(u.b);
               x.kvh = static_cast<int32_t>(w % a.Hkv);
@@ -645,7 +709,7 @@ __global__ void __launch_bounds__(kThreadsR, 1)
 }
 
 template <int D>
-cudaError_t launch_ragged_d(const AttnArgs &a, cudaStream_t s) {
+cudaError_t launch_ragged_d(const RaggedArgs &a, cudaStream_t s) {
   using L = SmemR<D>;
   static std::atomic<uint64_t> ready{0};
   int sms = 0;
@@ -665,11 +729,46 @@ cudaError_t launch_ragged_d(const AttnArgs &a, cudaStream_t s) {
 
 } // namespace
 
-cudaError_t launch_prefill_ragged(const AttnArgs &a, cudaStream_t s) {
+cudaError_t ragged_plans_itself(int head_dim, int batch, int64_t items, int64_t part_rows,
+                                bool *itself) {
+  static std::atomic<uint64_t> none{0};
+  int sms = 0;
+  const cudaError_t e = prepare_launch(nullptr, 0, none, &sms);
+  *itself = head_dim != 256 && batch <= 32 && part_rows == 0 &&
+            items <= std::min<int64_t>(sms, kFoldCtas);
+  return e;
+}
+
+cudaError_t launch_prefill_ragged(const AttnArgs &a, const int32_t *kv_indptr, cudaStream_t s) {
   if (a.n_units == 0) return cudaSuccess;
+  RaggedArgs r{};
+  r.Hq = a.Hq;
+  r.Hkv = a.Hkv;
+  r.D = a.D;
+  r.G = a.G;
+  r.causal = a.causal;
+  r.split = a.split;
+  r.tile_tokens = a.tile_tokens;
+  r.batch = a.batch;
+  r.kv_rows = a.kv_rows;
+  r.scale_log2 = a.scale_log2;
+  r.n_units = a.n_units;
+  r.reqs = a.reqs;
+  r.units = a.units;
+  r.qo_indptr = a.qo_indptr;
+  r.kv_indptr = kv_indptr;
+  r.total_q = a.total_rows;
+  r.part_o = a.part_o;
+  r.part_lse = a.part_lse;
+  r.out = a.out;
+  r.lse = a.lse;
+  r.status = a.status;
+  r.tm_q = a.tm_q;
+  r.tm_k = a.tm_k;
+  r.tm_v = a.tm_v;
   // head_dim 96 runs on the 128-wide layout: the tensor maps read columns
   // 96..127 as zeros
-  return a.D > 64 ? launch_ragged_d<128>(a, s) : launch_ragged_d<64>(a, s);
+  return r.D > 64 ? launch_ragged_d<128>(r, s) : launch_ragged_d<64>(r, s);
 }
 
 } // namespace bia

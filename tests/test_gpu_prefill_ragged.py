@@ -279,6 +279,29 @@ def test_calls_on_two_streams_with_their_own_workspaces():
         assert same_bits(o, want[i % 2][0]) and same_bits(l, want[i % 2][1])
 
 
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_calls_with_and_without_a_plan_take_the_same_bits(d):
+    """32 requests find their units themselves, 33 and more have them planned,
+    as have calls with more items than SMs: the same rows either way."""
+    g = torch.Generator().manual_seed(8)
+    lens = torch.randint(0, 40, (33,), generator=g).tolist()
+    lens[0], lens[5], lens[31], lens[32] = 0, 300, 0, 9
+    kv_lens = [x + 50 * (i % 4) for i, x in enumerate(lens)]
+    q, k, v = draw(4, 2, d, lens, kv_lens, 6)
+    out, lse = run(q, k, v, lens, kv_lens)  # planned
+    n, m = sum(lens[:32]), sum(kv_lens[:32])
+    one, l = run(q[:n], k[:m], v[:m], lens[:32], kv_lens[:32])  # not
+    assert same_bits(one, out[:n]) and same_bits(l, lse[:n])
+    check(q, k, v, lens, kv_lens, out, lse)
+    launches = []
+    for count in (32, 33):
+        before = bia.bia_launch_count()
+        a, b = sum(lens[:count]), sum(kv_lens[:count])
+        run(q[:a], k[:b], v[:b], lens[:count], kv_lens[:count])
+        launches.append(bia.bia_launch_count() - before)
+    assert launches == [1, 2]
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("which", ["q", "kv"])
 def test_device_lengths_that_end_elsewhere_compute_nothing(d, which):
