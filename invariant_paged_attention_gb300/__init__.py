@@ -656,6 +656,10 @@ def _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale):
 
 def _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp=None, last=None):
     """The page table's arrays hold what a call of `batch` requests reads."""
+    if (kv_indptr.numel() == batch + 1 and kv_last_page_len.numel() == batch and
+            (kvp is None or (kvp.numel() == batch + 1 and last.numel() == batch and
+                             kv_indices.numel() >= _last(kvp)))):
+        return
     for name, t, want in (("kv_indptr", kv_indptr, batch + 1),
                           ("kv_last_page_len", kv_last_page_len, batch),
                           ("kv_indptr_host", kvp, batch + 1),
@@ -714,10 +718,11 @@ def bia_append_paged_kv_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_sca
             (status is None or _dense(at, I32, status)) and at >= 0 and
             at == _current_device()):
         ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
-                        ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
-                        ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                        ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                        ("status", status, I32, True))
+                          ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                          ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                          ("kv_indices", kv_indices, I32),
+                          ("kv_last_page_len", kv_last_page_len, I32),
+                          ("status", status, I32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
     _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
     if append_indptr.numel() != batch + 1:
@@ -726,10 +731,11 @@ def bia_append_paged_kv_fp8(desc, k_new, v_new, k_cache, v_cache, k_scale, v_sca
     if ts is not None or k_new.get_device() != at or v_new.get_device() != at:
         _check_cuda((ts or [("k_cache", k_cache)]) + [("k_new", k_new), ("v_new", v_new)], stream)
     rc = load().bia_append_paged_kv_fp8(
-        ctypes.byref(desc), _at(k_new), _at(v_new), k_step, v_step, _at(k_cache), _at(v_cache),
-        _at(k_scale), _at(v_scale), k_cache.shape[0], _at(append_indptr), _at(kv_indptr),
-        _at(kv_indices), _at(kv_last_page_len), _at(ap), _at(kvp), _at(last), batch, _at(status),
-        _handle(stream))
+        ctypes.byref(desc), k_new.data_ptr(), v_new.data_ptr(), k_step, v_step, k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_cache.shape[0],
+        append_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
+        kv_last_page_len.data_ptr(), ap.data_ptr(), kvp.data_ptr(), last.data_ptr(), batch,
+        _at(status), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_append_paged_kv_fp8")
 
@@ -747,11 +753,12 @@ def bia_gather_paged_kv_fp8(desc, k_cache, v_cache, k_scale, v_scale, k_out, v_o
             (status is None or _dense(at, I32, status)) and at >= 0 and
             at == _current_device()):
         ts = _check_types(("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
-                        ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
-                        ("k_out", k_out, BF16), ("v_out", v_out, BF16),
-                        ("out_indptr", out_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                        ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                        ("status", status, I32, True))
+                          ("k_scale", k_scale, E8M0), ("v_scale", v_scale, E8M0),
+                          ("k_out", k_out, BF16), ("v_out", v_out, BF16),
+                          ("out_indptr", out_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                          ("kv_indices", kv_indices, I32),
+                          ("kv_last_page_len", kv_last_page_len, I32),
+                          ("status", status, I32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
     op, kvp, last = _host(out_indptr_host), _host(kv_indptr_host), _host(kv_last_page_len_host)
     batch = op.numel() - 1
@@ -765,10 +772,10 @@ def bia_gather_paged_kv_fp8(desc, k_cache, v_cache, k_scale, v_scale, k_out, v_o
     if ts is not None:
         _check_cuda(ts, stream)
     rc = load().bia_gather_paged_kv_fp8(
-        ctypes.byref(desc), _at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale),
-        k_cache.shape[0], _at(out_indptr), _at(kv_indptr), _at(kv_indices),
-        _at(kv_last_page_len), _at(op), _at(kvp), _at(last), batch, _at(k_out), _at(v_out),
-        _at(status), _handle(stream))
+        ctypes.byref(desc), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), k_cache.shape[0], out_indptr.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_last_page_len.data_ptr(), op.data_ptr(), kvp.data_ptr(),
+        last.data_ptr(), batch, k_out.data_ptr(), v_out.data_ptr(), _at(status), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_gather_paged_kv_fp8")
 
@@ -789,10 +796,11 @@ def _check_decode_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv
             (lse is None or _dense(at, F32, lse)) and at >= 0 and
             _index(workspace) == at == _current_device() and workspace.is_contiguous()):
         ts = _check_types(("q", q, BF16), ("k_cache", k_cache, E4M3),
-                        ("v_cache", v_cache, E4M3), ("k_scale", k_scale, E8M0),
-                        ("v_scale", v_scale, E8M0), ("kv_indptr", kv_indptr, I32),
-                        ("kv_indices", kv_indices, I32), ("kv_last_page_len", kv_last_page_len, I32),
-                        ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+                          ("v_cache", v_cache, E4M3), ("k_scale", k_scale, E8M0),
+                          ("v_scale", v_scale, E8M0), ("kv_indptr", kv_indptr, I32),
+                          ("kv_indices", kv_indices, I32),
+                          ("kv_last_page_len", kv_last_page_len, I32),
+                          ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
     want = (kv_indptr.numel() - 1, desc.num_qo_heads, desc.head_dim)
     if q.shape != want or out.shape != want:
@@ -813,10 +821,11 @@ def bia_decode_paged_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr,
                       kv_last_page_len, workspace, out, lse, stream, kvp, last)
     batch = q.shape[0]
     rc = load().bia_decode_paged_fp8(
-        ctypes.byref(desc), _at(q), _at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale),
-        k_cache.shape[0], _at(kv_indptr), _at(kv_indices), _at(kv_last_page_len), _at(kvp),
-        _at(last), batch, int(split_size), _at(workspace),
-        workspace.numel() * workspace.element_size(), _at(out), _at(lse), _handle(stream))
+        ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), k_cache.shape[0], kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_last_page_len.data_ptr(), kvp.data_ptr(), last.data_ptr(), batch,
+        int(split_size), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        out.data_ptr(), _at(lse), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_decode_paged_fp8")
 
@@ -835,10 +844,11 @@ def bia_decode_paged_fp8_bounded(desc, bounds, q, k_cache, v_cache, k_scale, v_s
                       kv_last_page_len, workspace, out, lse, stream)
     batch = q.shape[0]
     rc = load().bia_decode_paged_fp8_bounded(
-        ctypes.byref(desc), ctypes.byref(bounds), _at(q), _at(k_cache), _at(v_cache),
-        _at(k_scale), _at(v_scale), k_cache.shape[0], _at(kv_indptr), _at(kv_indices),
-        _at(kv_last_page_len), batch, int(split_size), _at(workspace),
-        workspace.numel() * workspace.element_size(), _at(out), _at(lse), _handle(stream))
+        ctypes.byref(desc), ctypes.byref(bounds), q.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_cache.shape[0],
+        kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_last_page_len.data_ptr(), batch,
+        int(split_size), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        out.data_ptr(), _at(lse), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_decode_paged_fp8_bounded")
 
@@ -870,7 +880,7 @@ def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_i
             (lse is None or _dense(at, F32, lse)) and at >= 0 and
             _index(workspace) == at == _current_device() and workspace.is_contiguous()):
         ts = _check_types(("qo_indptr", qo_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                        ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+                          ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
     if out.shape != q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
     if lse is not None and lse.numel() != q.shape[0] * hq:
@@ -881,9 +891,9 @@ def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_i
     if ts is not None or q.get_device() != at or k.get_device() != at or v.get_device() != at:
         _check_cuda((ts or [("out", out)]) + [("q", q), ("k", k), ("v", v)], stream)
     rc = load().bia_prefill_ragged(
-        ctypes.byref(desc), _at(q), _at(k), _at(v), q_step, k_step, v_step, _at(qo_indptr),
-        _at(kv_indptr), _at(qo), _at(kvp), batch, int(bool(causal)), int(split_size),
-        _at(workspace), workspace.numel() * workspace.element_size(), _at(out), _at(lse),
-        _handle(stream))
+        ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_step, k_step, v_step,
+        qo_indptr.data_ptr(), kv_indptr.data_ptr(), qo.data_ptr(), kvp.data_ptr(), batch,
+        int(bool(causal)), int(split_size), workspace.data_ptr(), workspace.numel() *
+        workspace.element_size(), out.data_ptr(), _at(lse), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_prefill_ragged")
