@@ -800,7 +800,8 @@ def _check_decode_fp8(desc, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv
                           ("v_scale", v_scale, E8M0), ("kv_indptr", kv_indptr, I32),
                           ("kv_indices", kv_indices, I32),
                           ("kv_last_page_len", kv_last_page_len, I32),
-                          ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+                          ("workspace", workspace, None), ("out", out, BF16),
+                          ("lse", lse, F32, True))
     _check_caches_fp8(desc, k_cache, v_cache, k_scale, v_scale)
     want = (kv_indptr.numel() - 1, desc.num_qo_heads, desc.head_dim)
     if q.shape != want or out.shape != want:
@@ -880,7 +881,8 @@ def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_i
             (lse is None or _dense(at, F32, lse)) and at >= 0 and
             _index(workspace) == at == _current_device() and workspace.is_contiguous()):
         ts = _check_types(("qo_indptr", qo_indptr, I32), ("kv_indptr", kv_indptr, I32),
-                          ("workspace", workspace, None), ("out", out, BF16), ("lse", lse, F32, True))
+                          ("workspace", workspace, None), ("out", out, BF16),
+                          ("lse", lse, F32, True))
     if out.shape != q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
     if lse is not None and lse.numel() != q.shape[0] * hq:
