@@ -988,9 +988,14 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   pa.status = reinterpret_cast<int32_t *>(ws + w.status);
   pa.reqs = reinterpret_cast<bia::ReqInfo *>(ws + w.reqs);
   bia::UnitFp8 *units = reinterpret_cast<bia::UnitFp8 *>(ws + w.units);
-  cudaError_t e = bia::launch_plan_decode_fp8(pa, units, st);
+  bool itself = false;
+  const int64_t items = hp.n_units * desc->num_kv_heads;
+  cudaError_t e = bia::decode_plans_itself(batch, items, hp.part_rows, &itself);
+  if (e == cudaSuccess && !itself) {
+    e = bia::launch_plan_decode_fp8(pa, units, st);
+    if (e == cudaSuccess) __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  }
   if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
-  __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
 
   bia::DecodeFp8Args f{};
   bia::DecodeGeometry &a = f.a;
@@ -1012,6 +1017,15 @@ int run_decode_fp8(const bia_attn_desc *desc, const bia_bounds *bounds, const vo
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.status = pa.status;
+  if (itself) {
+    a.slots = reinterpret_cast<int32_t *>(ws + w.group_cnt);
+    a.n_slots = static_cast<int32_t>(items);
+    a.kv_indptr = kv_indptr;
+    a.kv_last_page_len = kv_last_page_len;
+    a.split = split;
+    a.max_kv_len = pa.max_kv_len;
+    a.part_rows = hp.part_rows;
+  }
   f.k_codes = static_cast<const uint8_t *>(k_cache);
   f.v_codes = static_cast<const uint8_t *>(v_cache);
   f.k_scale = static_cast<const uint8_t *>(k_scale);

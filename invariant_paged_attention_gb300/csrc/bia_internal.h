@@ -171,9 +171,12 @@ inline WsLayout make_layout(int batch, int64_t n_groups, int64_t n_units, int64_
   return w;
 }
 
-// The workspace of an 8-bit decode: two 16-byte unit records hold one UnitFp8.
+// The workspace of an 8-bit decode: two 16-byte unit records hold one
+// UnitFp8; the group counts' place takes a status word per CTA of a decode
+// that plans itself (one of the 152 SMs at most).
+constexpr int64_t kDecodeSlots = 152;
 inline WsLayout make_layout_fp8(int batch, int64_t n_units, int64_t part_rows, int Hq, int D) {
-  return make_layout(batch, 0, 2 * n_units, 0, part_rows, Hq, D);
+  return make_layout(batch, kDecodeSlots, 2 * n_units, 0, part_rows, Hq, D);
 }
 
 struct PlanArgs {
@@ -293,6 +296,13 @@ struct DecodeGeometry {
   uint16_t *out;
   float *lse;
   int32_t *status;
+  // A decode that plans itself: a status word per CTA, which the merge joins
+  // (no CTA may clear a shared one while another notes a bad page); else NULL.
+  int32_t *slots;
+  const int32_t *kv_indptr, *kv_last_page_len;
+  int32_t split, n_slots;
+  int32_t max_kv_len; // of a bounded call, else 0
+  int64_t part_rows;  // of the workspace
 };
 
 struct DecodeFp8Args {
@@ -346,6 +356,9 @@ cudaError_t launch_decode_fp8_g2(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g4(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_merge_decode_fp8(const DecodeGeometry &a, cudaStream_t s);
+// Whether a decode needs no plan kernel: its CTAs, one an item, find their
+// units themselves, and the merge that follows joins their status words.
+cudaError_t decode_plans_itself(int batch, int64_t items, int64_t part_rows, bool *itself);
 // Packed keys and values: head_dim 64, 96 and 128; 256
 // Looked up once per device: its SM count, and (smem > 0) whether `fn` may use
 // that much dynamic shared memory there; `ready` holds a bit per device.
@@ -368,6 +381,46 @@ inline cudaError_t prepare_launch(const void *fn, int smem, std::atomic<uint64_t
   if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
+
+// Request `lane` of a call of up to 32: its keys and split tiles (nsp), the
+// units and partial rows (requests with several tiles) of it and those before;
+// false (on every lane) when an index array breaks a rule or the totals do
+// not fit the launch.
+#ifdef __CUDACC__
+struct LaneRequest {
+  int32_t page_base, kv_len, nsp, units_end, rows_end;
+};
+
+__device__ __forceinline__ bool lane_requests(const DecodeGeometry &a, int lane, LaneRequest &r) {
+  bool ok = true;
+  r.page_base = r.kv_len = 0;
+  if (lane < a.batch) {
+    r.page_base = a.kv_indptr[lane];
+    const int64_t pages = static_cast<int64_t>(a.kv_indptr[lane + 1]) - r.page_base;
+    const int32_t last = a.kv_last_page_len[lane];
+    const int64_t keys = ((pages - 1) << a.page_shift) + last;
+    ok = (lane > 0 || r.page_base >= 0) && pages > 0 && last >= 1 &&
+         last <= (1 << a.page_shift) && keys <= INT32_MAX / 2 &&
+         (a.max_kv_len == 0 || keys <= a.max_kv_len);
+    r.kv_len = ok ? static_cast<int32_t>(keys) : 0;
+  }
+  r.nsp = (r.kv_len + a.split - 1) / a.split;
+  r.units_end = r.nsp;
+  r.rows_end = r.nsp > 1 ? r.nsp : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int32_t u = __shfl_up_sync(0xffffffffu, r.units_end, off);
+    const int32_t w = __shfl_up_sync(0xffffffffu, r.rows_end, off);
+    r.units_end += lane >= off ? u : 0;
+    r.rows_end += lane >= off ? w : 0;
+  }
+  const int64_t units = __shfl_sync(0xffffffffu, r.units_end, 31);
+  const int64_t rows = __shfl_sync(0xffffffffu, r.rows_end, 31);
+  ok = ok && (a.max_kv_len ? units <= a.n_units && rows <= a.part_rows
+                           : units == a.n_units && rows == a.part_rows);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+#endif
 
 // (q tile pair, kv head) items from which a packed prefill folds a pair's
 // splits in the CTA instead of merging states: two a CTA of the 152 SMs.

@@ -155,11 +155,24 @@ __global__ void __launch_bounds__(kMergeWarps8 * 32) merge_decode_fp8_kernel(con
   constexpr int kChunk = V == 4 ? 8 : 4; // states in flight
   const int lane = threadIdx.x & 31;
   grid_dep_wait(); // the partials are complete
-  if (a.status[0] & kStatusPlanMismatch) return; // the outputs already hold NaN
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps8 + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(a.batch) * a.Hq) return;
   const int b = static_cast<int>(row / a.Hq), h = static_cast<int>(row - static_cast<int64_t>(b) * a.Hq);
-  const ReqInfo r = a.reqs[b];
+  ReqInfo r{};
+  if (a.slots) { // the decode planned itself: so does the merge, and joins the status
+    int32_t noted = 0;
+    for (int i = lane; i < a.n_slots; i += 32) noted |= a.slots[i];
+    LaneRequest mine;
+    const bool ok = lane_requests(a, lane, mine);
+    noted = __reduce_or_sync(0xffffffffu, noted);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.status[0] = noted;
+    if (!ok || (noted & kStatusPlanMismatch)) return; // the outputs already hold NaN
+    r.nsp = __shfl_sync(0xffffffffu, mine.nsp, b & 31);
+    r.rowbase = __shfl_sync(0xffffffffu, mine.rows_end, b & 31) - r.nsp;
+  } else if (a.status[0] & kStatusPlanMismatch) {
+    return; // the outputs already hold NaN
+  }
+  if (row >= static_cast<int64_t>(a.batch) * a.Hq) return;
+  if (!a.slots) r = a.reqs[b];
   if (r.nsp <= 1) return; // the decode wrote the final row
   const float *lse = a.part_lse + r.rowbase * a.Hq + h;
   const float *part = a.part_o + (r.rowbase * a.Hq + h) * a.D + lane * 4;
@@ -246,6 +259,14 @@ cudaError_t launch_merge_decode_fp8(const DecodeGeometry &a, cudaStream_t s) {
                                      kMergeWarps8 * 32, s, a)
                     : launch_chained(merge_decode_fp8_kernel<8>, static_cast<unsigned>(grid),
                                      kMergeWarps8 * 32, s, a);
+}
+
+cudaError_t decode_plans_itself(int batch, int64_t items, int64_t part_rows, bool *itself) {
+  static std::atomic<uint64_t> none{0};
+  int sms = 0;
+  const cudaError_t e = prepare_launch(nullptr, 0, none, &sms);
+  *itself = batch <= 32 && part_rows > 0 && items <= std::min<int64_t>(sms, kDecodeSlots);
+  return e;
 }
 
 cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s) {

@@ -230,6 +230,93 @@ def test_bounded_decode_replays_in_a_graph_with_the_exact_bits():
     assert bia.bia_read_status(ws) & 2 and torch.isnan(out.float()).all() and torch.isnan(lse).all()
 
 
+@pytest.mark.parametrize("n", [1, 33])
+def test_device_lengths_other_than_the_host_s_compute_nothing(n):
+    """One request finds its units itself, 33 have them planned."""
+    x = Batch([2058] + [300] * (n - 1), 8, 2, 128, 16)
+    ws = torch.empty(bia.bia_decode_fp8_workspace_size(x.desc, x.indptr, x.last), dtype=torch.uint8,
+                     device=DEV)
+    out, lse = torch.zeros_like(x.q), torch.zeros(x.q.shape[:2], device=DEV)
+    indptr, idx, last = x.dev()
+    indptr, last = indptr.clone(), last.clone()
+    indptr[0] += 1  # the first request: 2048 keys, two tiles instead of three
+    last[0] = 16
+    bia.bia_decode_paged_fp8(x.desc, x.q, *x.cache, indptr, idx, last, x.indptr, x.last, ws, out, lse)
+    assert bia.bia_read_status(ws) != 0
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def test_small_calls_take_no_plan_and_the_same_bits():
+    """Up to 32 requests with an SM for every tile and head find their units
+    themselves; the same requests beside others have them planned."""
+    lens = [3000, 1, 1024, 1025]
+    small, large = Batch(lens, 8, 2, 128, 16), Batch(lens + [700] * 30, 8, 2, 128, 16)
+    counts, got = [], []
+    for x in (small, large):
+        before = bia.bia_launch_count()
+        got.append(x.decode())
+        counts.append(bia.bia_launch_count() - before)
+    assert counts == [2, 3]
+    for i in range(2):
+        assert same_bits(got[0][i], got[1][i][:4])
+    small.check(*got[0])
+
+
+def test_a_bad_page_of_a_call_without_a_plan_is_reported():
+    b = Batch([1500, 60], 8, 2, 128, 16)
+    b.idx[2] = 1 << 20  # request 0, keys 32..47
+    b.idx[93] = -1      # and keys 1488..1499
+    indptr, idx, last = b.dev()
+    ws = torch.empty(bia.bia_decode_fp8_workspace_size(b.desc, b.indptr, b.last),
+                     dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=DEV)
+    for clean in (False, True, False):
+        good = idx.clone()
+        if clean:
+            good[2], good[93] = good[3], good[92]
+        bia.bia_decode_paged_fp8(b.desc, b.q, *b.cache, indptr, good, last, b.indptr, b.last, ws, out,
+                                 lse)
+        assert bia.bia_read_status(ws) == (0 if clean else 1)
+    k, v = b.rows_of(0)
+    k[32:48], v[32:48], k[1488:], v[1488:] = 0, 0, 0, 0
+    want = fu.attention_bounds(b.q[:1], k, v, floor=FLOOR * 3000)
+    fu.check(out[:1], lse[:1], *want)
+
+
+def test_bounded_calls_without_a_plan_replay_with_the_exact_bits():
+    lens = [2040, 5, 130]
+    b = Batch([n + 12 for n in lens], 8, 2, 128, 16)
+    bounds = bia.make_bounds(max_kv_len=4000)
+    ws = torch.empty(bia.bia_decode_fp8_bounded_workspace_size(b.desc, bounds, 3),
+                     dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=DEV)
+    indptr, idx, last = b.dev()
+    graph = torch.cuda.CUDAGraph()
+    before = bia.bia_launch_count()
+    with torch.cuda.graph(graph):
+        bia.bia_decode_paged_fp8_bounded(b.desc, bounds, b.q, *b.cache, indptr, idx, last, ws, out, lse)
+    assert bia.bia_launch_count() - before == 2
+    for step in (12, 0, 9):
+        now = [n + step for n in lens]
+        count = [-(-n // 16) for n in now]
+        ip = fu.indptr_of(count)
+        ids = torch.cat([b.pages[i][:c] for i, c in enumerate(count)])
+        la = torch.tensor([n - (c - 1) * 16 for n, c in zip(now, count)], dtype=torch.int32)
+        indptr.copy_(ip)
+        idx[:len(ids)].copy_(ids)
+        last.copy_(la)
+        out.fill_(float("nan"))
+        graph.replay()
+        assert bia.bia_read_status(ws) == 0
+        w2 = torch.empty(bia.bia_decode_fp8_workspace_size(b.desc, ip, la), dtype=torch.uint8, device=DEV)
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        bia.bia_decode_paged_fp8(b.desc, b.q, *b.cache, ip.to(DEV), ids.to(DEV), la.to(DEV), ip, la, w2, o2, l2)
+        assert same_bits(out, o2) and same_bits(lse, l2)
+    last[1] = 17  # breaks a rule
+    graph.replay()
+    assert bia.bia_read_status(ws) & 2 and torch.isnan(out.float()).all() and torch.isnan(lse).all()
+
+
 def test_two_graphs_share_one_workspace():
     a = Batch([2500, 300], 16, 4, 128, 16, seed=1)
     c = Batch([5000, 1, 700], 16, 4, 128, 16, seed=2)
