@@ -12,10 +12,15 @@
 //   O^T += V^T [p_hi; p_lo]   M = 128 dims, N = 16, K = 128 keys
 // q is scaled by a power of two per head, so that q = hi + lo/16 is exact
 // down to 2^-11 of the row's largest element and off by at most 2^-22 of it
-// below; a weight keeps 8 significant bits (what a bf16 weight keeps) down to
-// 2^-14 of the largest.  The key's scale multiplies its score, the value's
-// scale its weight, relative to the largest value scale of the part (a power
-// of two: exact).  Products, sums, the maximum and the row sum are fp32.
+// below.  The key's scale multiplies its score.  The value's scale 2^ev
+// multiplies its weight: P holds p_j * 2^(ev_j - c + 8), with c the integer
+// next above the largest of (score + ev) less the largest score, each over the
+// part's keys, so that a head's largest entry lies in (2^7, 2^8].  An entry
+// keeps 8 significant bits (what a bf16 weight keeps) down to 2^-6 and is off
+// by at most 2^-14, 2^-21 of the largest, below: only what adds little to the
+// result is held coarsely.  (Scaled by the part's largest value scale instead,
+// a row 2^22 times the others in magnitude took every bit from them, attended
+// or not.)  Products, sums, the maxima and the row sum are fp32.
 // Converting the rows instead (8 -> 16 bits through registers and shared
 // memory) would cost more issue slots than the copies themselves.
 //
@@ -25,8 +30,8 @@
 // waits, maximum exchange and rescaling took ~5000 cycles of a warpgroup, 3.8
 // TB/s with two of them on alternate blocks.  So a tile (at most 1024 keys)
 // is taken in parts of 512 keys, and a part in two passes: all its scores
-// first, kept in TMEM, one maximum over the part, then the weights.  Nothing
-// is rescaled, the weights of a part are at most 1 and fill e4m3's range, and
+// first, kept in TMEM, the maxima over the part, then the weights.  Nothing
+// is rescaled, the entries of P are at most 2^8 and fill e4m3's range, and
 // the warps meet once a part; the parts' states (each with its own O columns)
 // are joined in the epilogue.  Key and value rows are copied by warps of their
 // own through a ring of their own each (one ring for both would let S of the
@@ -85,7 +90,7 @@ static_assert(8 * kSoftRegs8 + (kThreads8 / 32 - 8) * kOtherRegs8 <= 65536 / 32,
 static_assert(kItemWarp8 < kThreads8 / 32, "warps");
 constexpr int kCopyKeys8 = kKeys8 / kCopyWarps8; // keys of a block a copy warp takes
 constexpr int kReaders8 = kItemWarp8;            // warps that read the mailbox
-constexpr int kBoost8 = 8; // weights <= 1 times 2^8 fill e4m3's range (448)
+constexpr int kBoost8 = 8; // entries of P are at most 2^8: e4m3 ends at 448
 constexpr uint32_t kNoRow8 = 0xffffffffu; // a key past the end or on a bad page: zeros
 
 // DW: 64, 128 (head_dim 96 too) or 256; HB: kv heads of an item.
@@ -111,12 +116,11 @@ struct Smem8 {
   static constexpr int kRows = kP + kPartBlocks8 * HB * kPBlock; // uint32 [2][part]: cache rows
   static constexpr int kKe = kRows + 2 * kPart8 * 4;   // uint8 [2][HB][part]: key scales
   static constexpr int kVe = kKe + 2 * HB * kPart8;    // uint8 [2][HB][part]: value scales
-  static constexpr int kEmax = kVe + 2 * HB * kPart8;  // int [2][HB][blocks]
-  static constexpr int kQs = kEmax + 2 * HB * kPartBlocks8 * 4; // float [2][HB][8]
-  static constexpr int kRed = kQs + 2 * HB * 32;  // float [2][8 warps][8]
-  static constexpr int kStat = kRed + 512;        // float [2][8 warps][8]
-  static constexpr int kStatM = kStat + 512;      // float [2][HB][8], then int [2][HB] scale
-  static constexpr int kItems = (kStatM + 2 * HB * 36 + 31) / 32 * 32; // 32-byte records [4]
+  static constexpr int kQs = kVe + 2 * HB * kPart8; // float [2][HB][8]
+  static constexpr int kMax = kQs + 2 * HB * 32;  // int [3][HB][16]: a part's maxima
+  static constexpr int kStat = kMax + 3 * HB * 64; // float [2][8 warps][8]
+  static constexpr int kStatM = kStat + 512;      // float [2][HB][8] maximum, then as many c
+  static constexpr int kItems = (kStatM + 4 * HB * 32 + 31) / 32 * 32; // 32-byte records [4]
   static constexpr int kSlot = kItems + 128;
   static constexpr int kBar = kSlot + 16;
   static constexpr int bKFull = 0, bKEmpty = bKFull + NS, bVFull = bKEmpty + NS,
@@ -128,7 +132,8 @@ struct Smem8 {
                        bItemEmpty = bItemFull + 4, bGo = bItemEmpty + 4, kNumBars = bGo + 1;
   static constexpr int kAlloc = kBar + kNumBars * 8 + 1024;
   static_assert(kAlloc <= 232448, "shared memory per CTA");
-  static_assert(kQ % 1024 == 0 && kQBuf % 1024 == 0 && kBar % 8 == 0, "alignment");
+  static_assert(kQ % 1024 == 0 && kQBuf % 1024 == 0 && kMax % 16 == 0 && kBar % 8 == 0,
+                "alignment");
 };
 
 // One item: a tile of one request for HB kv heads.
@@ -171,6 +176,35 @@ __device__ __forceinline__ float warp_sums(const float (&v)[G], int lane) {
   return x[0];
 }
 
+// fp32 as int32 in the same order (for atomicMax), and back.
+__device__ __forceinline__ int32_t ordered(float x) {
+  const int32_t b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_ordered(int32_t b) {
+  return __int_as_float(b ^ ((b >> 31) & 0x7fffffff));
+}
+constexpr int32_t kNoMax8 = static_cast<int32_t>(0xff800000u ^ 0x7fffffffu); // ordered(-inf)
+
+// Element-wise on the G heads' values of a key, two an instruction.
+template <int G>
+__device__ __forceinline__ void add_heads(const float (&x)[G], const float (&y)[G], float (&z)[G]) {
+  if constexpr (G == 1) {
+    z[0] = x[0] + y[0];
+  } else {
+#pragma unroll
+    for (int h = 0; h < G; h += 2)
+      f32x2_split(fadd2(f32x2(x[h], x[h + 1]), f32x2(y[h], y[h + 1])), z[h], z[h + 1]);
+  }
+}
+template <int G>
+__device__ __forceinline__ void add_heads(const float (&x)[G], float y, float (&z)[G]) {
+  float all[G];
+#pragma unroll
+  for (int h = 0; h < G; ++h) all[h] = y;
+  add_heads(x, all, z);
+}
+
 template <int G, int DW, int HB>
 __global__ void __launch_bounds__(kThreads8, 1)
     decode_fp8_kernel(const __grid_constant__ DecodeFp8Args f) {
@@ -200,6 +234,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   // q rows of heads that do not exist stay zero
   for (int i = tid; i < 2 * L::kQBuf / 16; i += kThreads8)
     reinterpret_cast<uint4 *>(smem + L::kQ)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 3 * HB * 16) reinterpret_cast<int32_t *>(smem + L::kMax)[tid] = kNoMax8;
   fence_proxy_async();
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -406,7 +441,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const int aw = warp - kAuxWarp8;
     const int page_mask = (1 << a.page_shift) - 1;
     uint32_t *s_rows = reinterpret_cast<uint32_t *>(smem + L::kRows);
-    int32_t *s_emax = reinterpret_cast<int32_t *>(smem + L::kEmax);
     float *s_qs = reinterpret_cast<float *>(smem + L::kQs);
     const uint64_t keep = policy_evict_last();
     uint32_t ug = 0;
@@ -438,8 +472,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::bRows + par));
-        // scale bytes of the HB heads; no row: zeros with a zero weight,
-        // outside the maximum
+        // scale bytes of the HB heads; no row: zeros
         uint32_t ke[4], ve[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -528,19 +561,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
           if (lane == 0) mbar_arrive(bar(L::bQFull + qp));
         }
 #pragma unroll
-        for (int hh = 0; hh < HB; ++hh) {
-          uint32_t big = 0;
+        for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             const int t = (par * HB + hh) * kPart8 + aw * kKeys8 + n * 32 + lane;
-            const uint32_t v = (ve[n] >> (8 * hh)) & 0xffu;
             smem[L::kKe + t] = static_cast<uint8_t>(ke[n] >> (8 * hh));
-            smem[L::kVe + t] = static_cast<uint8_t>(v);
-            big = max(big, v == 255u ? 0u : v);
+            smem[L::kVe + t] = static_cast<uint8_t>(ve[n] >> (8 * hh));
           }
-          big = __reduce_max_sync(0xffffffffu, big);
-          if (lane == 0) s_emax[(par * HB + hh) * kPartBlocks8 + aw] = static_cast<int32_t>(big);
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::bAux + par));
       }
@@ -662,13 +689,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const int hh = HB == 2 ? wg : 0;
     const int wf = HB == 2 ? 4 * wg : 0; // first warp of the head's
     const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
-    float *s_red = reinterpret_cast<float *>(smem + L::kRed);
+    int32_t *s_max = reinterpret_cast<int32_t *>(smem + L::kMax) + hh * 16;
     float *s_stat = reinterpret_cast<float *>(smem + L::kStat);
     float *s_m = reinterpret_cast<float *>(smem + L::kStatM);
-    int32_t *s_e = reinterpret_cast<int32_t *>(smem + L::kStatM + 2 * HB * 32);
-    const int32_t *s_emax = reinterpret_cast<const int32_t *>(smem + L::kEmax);
+    float *s_c = s_m + 2 * HB * 8;
     const float *s_qs = reinterpret_cast<const float *>(smem + L::kQs);
     uint32_t sg = 0, ug = 0;
+    int max_at = 0; // ug % 3, times a part's maxima
     bool ok = true;
     for (uint32_t ig = 0; ok; ++ig) {
       const Item8 it = warp_item(ig);
@@ -685,8 +712,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
         float qs[G];
 #pragma unroll
         for (int h = 0; h < G; ++h) qs[h] = s_qs[(static_cast<int>(ig & 1) * HB + hh) * 8 + h];
-        // ---- pass 1: the scores, and the part's largest of each head.  They
-        // stay in registers where 16 hold them, else pass 2 reads S again.
+        // ---- pass 1: the scores, and of each head the part's largest score
+        // and largest score + ev.  The scores stay in registers where 16 hold
+        // them, else pass 2 reads S again.
         ok = wait(L::bSFull + par, (ug >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -694,15 +722,36 @@ __global__ void __launch_bounds__(kThreads8, 1)
         auto scores = [&](int j, const uint32_t (&v)[NL], float (&sc)[G]) {
           const float ks = e8m0_value(ke[j * kKeys8]);
           const bool valid = key0 + j * kKeys8 < it.key_end; // false past the part's blocks
+          if constexpr (G == 1) {
+            const float raw = fmaf(__uint_as_float(v[LO]), 0.0625f, __uint_as_float(v[0]));
+            sc[0] = raw * (ks * qs[0]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < G; h += 2) {
+              const uint64_t raw =
+                  ffma2r(f32x2(__uint_as_float(v[LO + h]), __uint_as_float(v[LO + h + 1])),
+                         f32x2(0.0625f, 0.0625f),
+                         f32x2(__uint_as_float(v[h]), __uint_as_float(v[h + 1])));
+              f32x2_split(fmul2(raw, fmul2(f32x2(ks, ks), f32x2(qs[h], qs[h + 1]))), sc[h], sc[h + 1]);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < G; ++h) sc[h] = valid ? sc[h] : -INFINITY;
+        };
+        float m[G], r[G], sc[NB][G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) m[h] = r[h] = -INFINITY;
+        auto maxima = [&](int j, const float (&x)[G]) {
+          const uint32_t vb = ve[j * kKeys8];
+          const float ev = vb == 255u ? -INFINITY : static_cast<float>(vb); // a NaN scale: nowhere
+          float y[G];
+          add_heads(x, ev, y);
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float raw = fmaf(__uint_as_float(v[LO + h]), 0.0625f, __uint_as_float(v[h]));
-            sc[h] = valid ? raw * (ks * qs[h]) : -INFINITY;
+            m[h] = fmaxf(m[h], x[h]);
+            r[h] = fmaxf(r[h], y[h]);
           }
         };
-        float m[G], sc[NB][G];
-#pragma unroll
-        for (int h = 0; h < G; ++h) m[h] = -INFINITY;
         if constexpr (kKeep) {
           uint32_t v[NB][NL];
 #pragma unroll
@@ -712,8 +761,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
             scores(block(i), v[i], sc[i]);
-#pragma unroll
-            for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], sc[i][h]);
+            maxima(block(i), sc[i]);
           }
         } else {
 #pragma unroll
@@ -723,33 +771,50 @@ __global__ void __launch_bounds__(kThreads8, 1)
             tmem_ld_n<NL>(tS(ug, block(i), hh) + lane_base, v);
             tmem_wait_ld();
             scores(block(i), v, sc[0]);
-#pragma unroll
-            for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], sc[0][h]);
+            maxima(block(i), sc[0]);
           }
         }
-        float mine = -INFINITY;
+        // The warps' maxima meet in shared memory, lane h < G that of head h,
+        // lane 8 + h its score + ev.  Three sets in turn: the next part's is
+        // cleared before this part's barrier, behind the barrier of the last
+        // part (past which nobody reads it) and before any warp can add to it.
+        int32_t mine = kNoMax8;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          const float wm = warp_max(m[h]);
-          mine = lane == h ? wm : mine;
+          const float wm = warp_max(m[h]), wr = warp_max(r[h]);
+          mine = lane == h ? ordered(wm) : lane == 8 + h ? ordered(wr) : mine;
         }
-        if (lane < 8) s_red[(par * 8 + warp) * 8 + lane] = mine;
+        if (lane < 16 && (lane & 7) < G) atomicMax(s_max + max_at + lane, mine);
+        const int max_next = max_at == 2 * HB * 16 ? 0 : max_at + HB * 16;
+        if (warp == wf && lane < 16) s_max[max_next + lane] = kNoMax8;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::bMax + par * HB + hh));
-        int32_t eref = 0; // the part's largest value scale
-#pragma unroll
-        for (int j = 0; j < kPartBlocks8; ++j)
-          eref = max(eref, s_emax[(par * HB + hh) * kPartBlocks8 + j]);
         ok = wait(L::bMax + par * HB + hh, (ug >> 1) & 1);
         if (!ok) break;
+        // c is 0 .. 254, as the key of the largest score has an ev of 0 or more
+        // (0 where an infinite score makes it NaN)
+        auto c_of = [](float most, float top) {
+          return fminf(fmaxf(ceilf(most - top), 0.f), 254.f);
+        };
+        float m_neg[G], c_neg[G];
+        int32_t all[16];
 #pragma unroll
-        for (int h = 0; h < G; ++h) m[h] = s_red[(par * 8 + wf) * 8 + h];
+        for (int h = 0; h < 16; h += 4)
+          if ((h & 7) < G)
+            *reinterpret_cast<int4 *>(all + h) = *reinterpret_cast<const int4 *>(s_max + max_at + h);
 #pragma unroll
-        for (int w = 1; w < WH; ++w)
-#pragma unroll
-          for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], s_red[(par * 8 + wf + w) * 8 + h]);
-        // ---- pass 2: the weights 2^(s - m), times 2^(ev - eref + 8) in two
-        // e4m3 terms
+        for (int h = 0; h < G; ++h) {
+          m_neg[h] = -from_ordered(all[h]);
+          c_neg[h] = -c_of(from_ordered(all[8 + h]), -m_neg[h]);
+        }
+        if (warp == wf && lane < G) { // of the part's state
+          const float top = from_ordered(s_max[max_at + lane]);
+          s_m[(par * HB + hh) * 8 + lane] = top;
+          s_c[(par * HB + hh) * 8 + lane] = c_of(from_ordered(s_max[max_at + 8 + lane]), top);
+        }
+        max_at = max_next;
+        // ---- pass 2: the weights 2^(s - m), and 2^(s - m + ev - c + 8) in two
+        // e4m3 terms (an exponential of its own: the weight alone may underflow)
         // row sums: even blocks, odd blocks (HB = 1 with two warpgroups on
         // them adds in the same order: both forms give the same bits)
         float l[2][G];
@@ -770,15 +835,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
             scores(j, v, sc[0]);
           }
           const uint32_t vb = ve[j * kKeys8];
-          const int32_t de = static_cast<int32_t>(vb) - eref + kBoost8 + 127;
-          const float vf = vb == 255u ? NAN : de > 0 ? __uint_as_float(de << 23) : 0.f;
-          float w[G];
+          const float ev = vb == 255u ? NAN : static_cast<float>(static_cast<int>(vb) + kBoost8);
+          float x[G], y[G], w[G];
+          add_heads(sc[kKeep ? i : 0], m_neg, x); // -inf for a key that is not there
+          add_heads(c_neg, ev, w);
+          add_heads(x, w, y);
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float p = ex2(sc[kKeep ? i : 0][h] - m[h]); // 0 for a key that is not there
-            l[i & (HB - 1)][h] += p;
-            w[h] = p * vf;
+            x[h] = ex2(x[h]);
+            w[h] = ex2(y[h]);
           }
+          add_heads(l[i & (HB - 1)], x, l[i & (HB - 1)]);
           uint32_t pk[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int h = 0; h < G; h += 2) {
@@ -804,17 +871,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (HB == 1 && SB == 2 && wg == 1 && (nb & 1) && lane == 0)
           mbar_arrive(bar(L::bPFull + static_cast<int>((sg + nst - 1) % ST)));
         sg += nst;
-        // ---- the part's state: row sums of the warps, maxima, scale
+        // ---- the part's state: the row sums of the warps
         float lw = warp_sums<G>(l[0], lane); // lane h < G: head h
         if (HB == 2) lw = __fadd_rn(lw, warp_sums<G>(l[1], lane));
-        float mw = 0.f;
-#pragma unroll
-        for (int h = 0; h < G; ++h) mw = lane == h ? m[h] : mw;
-        if (lane < 8) {
-          s_stat[(par * 8 + warp) * 8 + lane] = lw;
-          if (warp == wf) s_m[(par * HB + hh) * 8 + lane] = mw;
-          if (warp == wf && lane == 0) s_e[par * HB + hh] = eref;
-        }
+        if (lane < 8) s_stat[(par * 8 + warp) * 8 + lane] = lw;
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(L::bAuxFree + par));
@@ -832,14 +892,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
         tc_fence_after();
         const bool two = n_parts == 2;
         const int p0 = static_cast<int>(u0 & 1), p1 = static_cast<int>(u1 & 1);
-        const int32_t e0 = s_e[p0 * HB + hh], e1 = s_e[p1 * HB + hh], em = max(e0, e1);
-        const float g0 = exp2_int(max(e0 - em, -126)), g1 = exp2_int(max(e1 - em, -126));
-        const float e_val = e8m0_value(static_cast<uint32_t>(em));
         // lane h < G: the join of head h (lanes past G repeat one)
         const int hl = lane & (G - 1);
         const float m0 = s_m[(p0 * HB + hh) * 8 + hl], m1 = s_m[(p1 * HB + hh) * 8 + hl];
         const float M = fmaxf(m0, m1);
-        const float a0 = m0 == M ? 1.f : ex2(m0 - M), a1 = m1 == M ? 1.f : ex2(m1 - M);
+        const float d0 = m0 == M ? 0.f : m0 - M, d1 = m1 == M ? 0.f : m1 - M;
+        const float a0 = ex2(d0), a1 = ex2(d1);
+        // O of a part counts 2^(d + c): that much over the larger of the two
+        const float x0 = d0 + s_c[(p0 * HB + hh) * 8 + hl], x1 = d1 + s_c[(p1 * HB + hh) * 8 + hl];
+        const float top = fminf(ceilf(fmaxf(x0, x1)), 254.f); // >= 0: that of the larger maximum
+        const float e_mine = e8m0_value(static_cast<uint32_t>(top));
         float l0 = 0.f, l1 = 0.f; // the quadrants in order, each even + odd blocks
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -853,8 +915,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         const float ls = two ? __fadd_rn(__fmul_rn(a0, l0), __fmul_rn(a1, l1)) : l0;
         const float inv = ls == 0.f ? 0.f : __frcp_rn(ls);
-        const float f0_mine = __fmul_rn(__fmul_rn(a0, g0), inv);
-        const float f1_mine = __fmul_rn(__fmul_rn(a1, g1), inv);
+        const float f0_mine = __fmul_rn(ex2(x0 - top), inv); // one part: 2^0
+        const float f1_mine = __fmul_rn(ex2(x1 - top), inv);
         const float lse_mine = ls == 0.f ? -INFINITY : __fmul_rn(__fadd_rn(M, lg2(ls)), kLn2);
         const bool single = it.prow < 0; // one tile: the final row
         const int64_t head0 =
@@ -876,6 +938,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
           for (int h = 0; h < G; ++h) {
             const float f0 = __shfl_sync(0xffffffffu, f0_mine, h);
             const float f1 = __shfl_sync(0xffffffffu, f1_mine, h);
+            const float e_val = __shfl_sync(0xffffffffu, e_mine, h);
             float val =
                 __fmul_rn(fmaf(__uint_as_float(o0[LO + h]), 0.0625f, __uint_as_float(o0[h])), f0);
             if (two)
