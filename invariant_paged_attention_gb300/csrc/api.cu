@@ -141,11 +141,11 @@ int check_desc(const bia_attn_desc *d) {
 // Validates the host mirrors and computes the same plan sizes the device
 // planner will produce.  qo == nullptr: decode (one query per request).
 // stream: single-token tail tiles become streamed units (prefill).
-// last == nullptr with page_size 1: packed keys (every "page" is one key).
+// packed: keys without pages (page_size 1 and no last lengths).
 int host_plan(const bia_attn_desc *d, const int32_t *qo, const int32_t *kvp,
               const int32_t *last, int32_t batch, int32_t causal, int32_t split, int tile_tokens,
-              int tiles_per_unit, int ctas, int stream, HostPlan *hp) {
-  if (batch <= 0 || !kvp || (!last && d->page_size != 1)) return BIA_ERR_INVALID_ARG;
+              int tiles_per_unit, int ctas, int stream, HostPlan *hp, bool packed = false) {
+  if (batch <= 0 || !kvp || (!last && !packed)) return BIA_ERR_INVALID_ARG;
   if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
   if (qo && qo[0] != 0) return BIA_ERR_INVALID_ARG;
   if (kvp[0] < 0) return BIA_ERR_INVALID_ARG;
@@ -154,7 +154,7 @@ int host_plan(const bia_attn_desc *d, const int32_t *qo, const int32_t *kvp,
     const int64_t q_len = qo ? static_cast<int64_t>(qo[b + 1]) - qo[b] : 1;
     const int64_t pages = static_cast<int64_t>(kvp[b + 1]) - kvp[b];
     if (q_len < 0 || pages < 0) return BIA_ERR_INVALID_ARG;
-    const int32_t last_len = last ? last[b] : 1;
+    const int32_t last_len = packed ? 1 : last[b];
     if (pages > 0 && (last_len < 1 || last_len > d->page_size)) return BIA_ERR_INVALID_ARG;
     const int64_t kv_len = pages > 0 ? (pages - 1) * d->page_size + last_len : 0;
     if (kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
@@ -1083,7 +1083,7 @@ int ragged_plan(const bia_attn_desc *desc, const int32_t *qo_host, const int32_t
     return host_plan(d, qo_host, kv_host, nullptr, batch, causal, sp,
                      bia::kTileRows / (d->num_qo_heads / d->num_kv_heads),
                      bia::ragged_tiles_per_unit(d->head_dim), bia::ragged_ctas(d->head_dim), 0,
-                     hp);
+                     hp, true);
   };
   rc = plan(split);
   if (rc != BIA_OK) return rc;
