@@ -556,8 +556,9 @@ BIA_API int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const v
                        size_t workspace_bytes, void *out, float *lse, void *stream);
 
 /* Workspace bytes bia_prefill_ragged needs for this call (0 on invalid input).
- * Of these lengths: a call with many q tiles keeps a state per CTA instead of
- * one per row and split, so a longer call may need less than a shorter one. */
+ * Of these lengths: a call with many q tiles of like lengths keeps a state per
+ * CTA instead of one per row and split, so a longer call may need less than a
+ * shorter one. */
 BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
                                          const int32_t *qo_indptr_host,
                                          const int32_t *kv_indptr_host, int32_t batch,
