@@ -359,24 +359,28 @@ cudaError_t launch_merge_decode_fp8(const DecodeGeometry &a, cudaStream_t s);
 // Whether a decode needs no plan kernel: its CTAs, one an item, find their
 // units themselves, and the merge that follows joins their status words.
 cudaError_t decode_plans_itself(int batch, int64_t items, int64_t part_rows, bool *itself);
-// Packed keys and values: head_dim 64, 96 and 128; 256
-// Looked up once per device: its SM count, and (smem > 0) whether `fn` may use
-// that much dynamic shared memory there; `ready` holds a bit per device.
-inline cudaError_t prepare_launch(const void *fn, int smem, std::atomic<uint64_t> &ready,
-                                  int *sms) {
+// SM count of the current device, looked up once per device.
+inline cudaError_t device_sms(int *sms) {
   static std::atomic<int> counts[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool kept = dev < 64;
-  *sms = kept ? counts[dev].load(std::memory_order_relaxed) : 0;
-  if (*sms == 0) {
-    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    if (kept) counts[dev].store(*sms, std::memory_order_relaxed);
-  }
-  const uint64_t bit = kept ? uint64_t{1} << dev : 0;
-  if (smem == 0 || (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  *sms = dev < 64 ? counts[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms != 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) counts[dev].store(*sms, std::memory_order_relaxed);
+  return e;
+}
+// Allows kernel `fn` `smem` bytes of dynamic shared memory on the current
+// device, once per device: `ready` holds a bit for each.
+inline cudaError_t prepare_launch(const void *fn, int smem, std::atomic<uint64_t> &ready,
+                                  int *sms = nullptr) {
+  int dev = 0;
+  cudaError_t e = sms ? device_sms(sms) : cudaSuccess;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
@@ -436,9 +440,10 @@ cudaError_t launch_plan_ragged(const PlanArgs &p, cudaStream_t s);
 // their units themselves.
 cudaError_t ragged_plans_itself(int head_dim, int batch, int64_t items, int64_t part_rows,
                                 bool *itself);
-// kv_indptr: for a call that plans itself, else NULL
+// Packed keys and values, head_dim 64, 96 and 128; kv_indptr: of a call that
+// plans itself, else NULL.
 cudaError_t launch_prefill_ragged(const AttnArgs &a, const int32_t *kv_indptr, cudaStream_t s);
-cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_prefill_ragged_wide(const AttnArgs &a, cudaStream_t s); // head_dim 256
 inline int ragged_tiles_per_unit(int head_dim) {
   return head_dim == 256 ? 1 : kPrefillTilesPerUnit;
 }

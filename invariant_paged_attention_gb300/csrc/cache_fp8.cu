@@ -238,9 +238,8 @@ cudaError_t launch_tokens(const CacheFp8Args &a, bool append, cudaStream_t s) {
   // Tokens a warp: kRounds rounds of loads, as far as the call still has a
   // warp for each of the SMs' schedulers; one for small calls, where latency
   // counts.
-  static std::atomic<uint64_t> none{0};
   int sms = 0;
-  const cudaError_t e = prepare_launch(nullptr, 0, none, &sms);
+  const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
   const int64_t round = std::max<int64_t>(1, kRounds * kInFlight * (32 / LPR) / (2 * a.Hkv));
   const int per = static_cast<int>(

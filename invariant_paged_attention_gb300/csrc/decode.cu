@@ -472,13 +472,10 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
 template <int D, int G, bool MASK>
 cudaError_t launch_decode_dgm(const AttnArgs &a, cudaStream_t s) {
   using L = DecSmem<D>;
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, G, MASK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(decode_kernel<D, G, MASK>),
+                                       L::kAlloc, ready);
+  if (e != cudaSuccess) return e;
   const int64_t blocks = a.n_units * a.Hkv;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};

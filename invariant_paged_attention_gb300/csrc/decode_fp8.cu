@@ -262,9 +262,8 @@ cudaError_t launch_merge_decode_fp8(const DecodeGeometry &a, cudaStream_t s) {
 }
 
 cudaError_t decode_plans_itself(int batch, int64_t items, int64_t part_rows, bool *itself) {
-  static std::atomic<uint64_t> none{0};
   int sms = 0;
-  const cudaError_t e = prepare_launch(nullptr, 0, none, &sms);
+  const cudaError_t e = device_sms(&sms);
   *itself = batch <= 32 && part_rows > 0 && items <= std::min<int64_t>(sms, kDecodeSlots);
   return e;
 }

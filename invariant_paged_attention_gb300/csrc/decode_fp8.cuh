@@ -990,9 +990,8 @@ cudaError_t launch_f8(const DecodeFp8Args &f, cudaStream_t s) {
 // Both forms give the same bits.
 template <int G>
 cudaError_t launch_f8_g(const DecodeFp8Args &f, cudaStream_t s) {
-  static std::atomic<uint64_t> none{0};
   int sms = 0;
-  const cudaError_t e = prepare_launch(nullptr, 0, none, &sms);
+  const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
   const bool pairs = f.a.Hkv % 2 == 0 && f.a.n_units * f.a.Hkv > sms;
   if (f.a.D == 64) return pairs ? launch_f8<G, 64, 2>(f, s) : launch_f8<G, 64, 1>(f, s);

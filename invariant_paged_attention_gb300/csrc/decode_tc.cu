@@ -618,18 +618,11 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
 
 template <int G, bool MASK>
 cudaError_t launch_tc(const AttnArgs &a, cudaStream_t s) {
-  static bool configured = false;
-  static int sms = 0;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<G, MASK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DecTcSmem::kAlloc);
-    int dev = 0;
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  int sms = 0;
+  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(decode_tc_kernel<G, MASK>),
+                                       DecTcSmem::kAlloc, ready, &sms);
+  if (e != cudaSuccess) return e;
   const int64_t work = a.n_units * a.Hkv;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(work, sms)));

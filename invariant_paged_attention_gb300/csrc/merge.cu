@@ -381,13 +381,9 @@ cudaError_t launch_merge_partials(const AttnArgs &a, cudaStream_t st) {
   if (a.total_rows == 0) return cudaSuccess;
   // two CTAs per SM (all resident at once) share out the rows the planner
   // lists (at most one per q token)
-  static int sms = 0;
-  if (sms == 0) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-  }
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.total_rows, 2LL * sms)));
   cfg.blockDim = dim3(kMergeWarps * 32);
@@ -396,17 +392,13 @@ cudaError_t launch_merge_partials(const AttnArgs &a, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (a.Hq % 4 == 0 && merge_chunk_heads(a.Hq, a.D) >= 1) { // streamed through shared memory
-    static bool configured[3] = {false, false, false};
+    static std::atomic<uint64_t> ready[3] = {};
     const int vi = a.D <= 128 ? 0 : a.D <= 256 ? 1 : 2;
     const void *fn = vi == 0 ? reinterpret_cast<const void *>(merge_stream_kernel<4>)
                      : vi == 1 ? reinterpret_cast<const void *>(merge_stream_kernel<8>)
                                : reinterpret_cast<const void *>(merge_stream_kernel<16>);
-    if (!configured[vi]) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMSmem);
-      if (e != cudaSuccess) return e;
-      configured[vi] = true;
-    }
+    e = prepare_launch(fn, kMSmem, ready[vi]);
+    if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(kMThreads);
     cfg.dynamicSmemBytes = kMSmem;
     if (vi == 0) return cudaLaunchKernelEx(&cfg, merge_stream_kernel<4>, a);

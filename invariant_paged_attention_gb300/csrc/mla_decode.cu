@@ -561,13 +561,10 @@ __global__ void __launch_bounds__(MlaCfg<HG>::kThreads, 1)
 template <int HG>
 cudaError_t launch_mla_hg(const AttnArgs &a, cudaStream_t s) {
   using L = MlaSmem<HG>;
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<HG>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e =
+      prepare_launch(reinterpret_cast<const void *>(mla_decode_kernel<HG>), L::kAlloc, ready);
+  if (e != cudaSuccess) return e;
   const int64_t blocks = a.n_units * ((a.Hq + HG - 1) / HG);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};

@@ -483,13 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 template <int D, bool MASK>
 cudaError_t launch_prefill_d(const AttnArgs &a, cudaStream_t s) {
   using L = Smem<D>;
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, MASK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(prefill_kernel<D, MASK>),
+                                       L::kAlloc, ready);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.n_units), static_cast<unsigned>(a.Hkv));
   cfg.blockDim = dim3(kThreads);

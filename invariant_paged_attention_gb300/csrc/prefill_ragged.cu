@@ -731,9 +731,8 @@ cudaError_t launch_ragged_d(const RaggedArgs &a, cudaStream_t s) {
 
 cudaError_t ragged_plans_itself(int head_dim, int batch, int64_t items, int64_t part_rows,
                                 bool *itself) {
-  static std::atomic<uint64_t> none{0};
   int sms = 0;
-  const cudaError_t e = prepare_launch(nullptr, 0, none, &sms);
+  const cudaError_t e = device_sms(&sms);
   *itself = head_dim != 256 && batch <= 32 && part_rows == 0 &&
             items <= std::min<int64_t>(sms, kFoldCtas);
   return e;

@@ -433,14 +433,10 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 
 template <bool MASK, bool RAGGED>
 cudaError_t launch_wide(const AttnArgs &a, cudaStream_t s) {
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_wide_kernel<MASK, RAGGED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SmemW::kAlloc);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = prepare_launch(
+      reinterpret_cast<const void *>(prefill_wide_kernel<MASK, RAGGED>), SmemW::kAlloc, ready);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.n_units), static_cast<unsigned>(a.Hkv));
   cfg.blockDim = dim3(kThreadsW);
