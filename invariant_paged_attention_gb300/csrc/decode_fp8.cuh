@@ -14,11 +14,11 @@
 // down to 2^-11 of the row's largest element and off by at most 2^-22 of it
 // below.  The key's scale multiplies its score.  The value's scale 2^ev
 // multiplies its weight: P holds p_j * 2^(ev_j - c + 8), with c the integer
-// next above the largest of (score + ev) less the largest score, each over the
-// part's keys, so that a head's largest entry lies in (2^7, 2^8].  An entry
-// keeps 8 significant bits (what a bf16 weight keeps) down to 2^-6 and is off
-// by at most 2^-14, 2^-21 of the largest, below: only what adds little to the
-// result is held coarsely.  (Scaled by the part's largest value scale instead,
+// nearest to the largest of (score + ev) less the largest score, each over the
+// part's keys, so that a head's largest entry lies about 2^8 (2^7.5 .. 2^8.5;
+// e4m3 ends at 2^8.8).  An entry keeps 8 significant bits (what a bf16 weight
+// keeps) down to 2^-6 and is off by at most 2^-14, 2^-21 of the largest, below:
+// only what adds little to the result is held coarsely.  (Scaled by the part's largest value scale instead,
 // a row 2^22 times the others in magnitude took every bit from them, attended
 // or not.)  Products, sums, the maxima and the row sum are fp32.
 // Converting the rows instead (8 -> 16 bits through registers and shared
@@ -31,7 +31,7 @@
 // TB/s with two of them on alternate blocks.  So a tile (at most 1024 keys)
 // is taken in parts of 512 keys, and a part in two passes: all its scores
 // first, kept in TMEM, the maxima over the part, then the weights.  Nothing
-// is rescaled, the entries of P are at most 2^8 and fill e4m3's range, and
+// is rescaled, the entries of P fill e4m3's range, and
 // the warps meet once a part; the parts' states (each with its own O columns)
 // are joined in the epilogue.  Key and value rows are copied by warps of their
 // own through a ring of their own each (one ring for both would let S of the
@@ -90,7 +90,8 @@ static_assert(8 * kSoftRegs8 + (kThreads8 / 32 - 8) * kOtherRegs8 <= 65536 / 32,
 static_assert(kItemWarp8 < kThreads8 / 32, "warps");
 constexpr int kCopyKeys8 = kKeys8 / kCopyWarps8; // keys of a block a copy warp takes
 constexpr int kReaders8 = kItemWarp8;            // warps that read the mailbox
-constexpr int kBoost8 = 8; // entries of P are at most 2^8: e4m3 ends at 448
+constexpr int kMaxima8 = 20; // 8 heads' scores, 8 score + ev, the ev, up to 16 bytes
+constexpr int kBoost8 = 8; // entries of P are at most 2^8.5: e4m3 ends at 448
 constexpr uint32_t kNoRow8 = 0xffffffffu; // a key past the end or on a bad page: zeros
 
 // DW: 64, 128 (head_dim 96 too) or 256; HB: kv heads of an item.
@@ -117,8 +118,8 @@ struct Smem8 {
   static constexpr int kKe = kRows + 2 * kPart8 * 4;   // uint8 [2][HB][part]: key scales
   static constexpr int kVe = kKe + 2 * HB * kPart8;    // uint8 [2][HB][part]: value scales
   static constexpr int kQs = kVe + 2 * HB * kPart8; // float [2][HB][8]
-  static constexpr int kMax = kQs + 2 * HB * 32;  // int [3][HB][16]: a part's maxima
-  static constexpr int kStat = kMax + 3 * HB * 64; // float [2][8 warps][8]
+  static constexpr int kMax = kQs + 2 * HB * 32;  // int [3][HB][kMaxima8]: a part's maxima
+  static constexpr int kStat = kMax + 3 * HB * kMaxima8 * 4; // float [2][8 warps][8]
   static constexpr int kStatM = kStat + 512;      // float [2][HB][8] maximum, then as many c
   static constexpr int kItems = (kStatM + 4 * HB * 32 + 31) / 32 * 32; // 32-byte records [4]
   static constexpr int kSlot = kItems + 128;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   // q rows of heads that do not exist stay zero
   for (int i = tid; i < 2 * L::kQBuf / 16; i += kThreads8)
     reinterpret_cast<uint4 *>(smem + L::kQ)[i] = make_uint4(0, 0, 0, 0);
-  if (tid < 3 * HB * 16) reinterpret_cast<int32_t *>(smem + L::kMax)[tid] = kNoMax8;
+  if (tid < 3 * HB * kMaxima8) reinterpret_cast<int32_t *>(smem + L::kMax)[tid] = kNoMax8;
   fence_proxy_async();
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const int hh = HB == 2 ? wg : 0;
     const int wf = HB == 2 ? 4 * wg : 0; // first warp of the head's
     const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
-    int32_t *s_max = reinterpret_cast<int32_t *>(smem + L::kMax) + hh * 16;
+    int32_t *s_max = reinterpret_cast<int32_t *>(smem + L::kMax) + hh * kMaxima8;
     float *s_stat = reinterpret_cast<float *>(smem + L::kStat);
     float *s_m = reinterpret_cast<float *>(smem + L::kStatM);
     float *s_c = s_m + 2 * HB * 8;
@@ -739,11 +740,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
           for (int h = 0; h < G; ++h) sc[h] = valid ? sc[h] : -INFINITY;
         };
         float m[G], r[G], sc[NB][G];
+        uint32_t ev_most = 0;
 #pragma unroll
         for (int h = 0; h < G; ++h) m[h] = r[h] = -INFINITY;
         auto maxima = [&](int j, const float (&x)[G]) {
           const uint32_t vb = ve[j * kKeys8];
           const float ev = vb == 255u ? -INFINITY : static_cast<float>(vb); // a NaN scale: nowhere
+          ev_most = max(ev_most, vb == 255u ? 0u : vb);
           float y[G];
           add_heads(x, ev, y);
 #pragma unroll
@@ -775,42 +778,50 @@ __global__ void __launch_bounds__(kThreads8, 1)
           }
         }
         // The warps' maxima meet in shared memory, lane h < G that of head h,
-        // lane 8 + h its score + ev.  Three sets in turn: the next part's is
-        // cleared before this part's barrier, behind the barrier of the last
-        // part (past which nobody reads it) and before any warp can add to it.
-        int32_t mine = kNoMax8;
+        // lane 8 + h its score + ev, lane 16 the ev.  Three sets in turn: the
+        // next part's is cleared before this part's barrier, behind the barrier
+        // of the last part (past which nobody reads it) and before any warp can
+        // add to it.
+        int32_t mine = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, ev_most));
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float wm = warp_max(m[h]), wr = warp_max(r[h]);
           mine = lane == h ? ordered(wm) : lane == 8 + h ? ordered(wr) : mine;
         }
-        if (lane < 16 && (lane & 7) < G) atomicMax(s_max + max_at + lane, mine);
-        const int max_next = max_at == 2 * HB * 16 ? 0 : max_at + HB * 16;
-        if (warp == wf && lane < 16) s_max[max_next + lane] = kNoMax8;
+        if (lane <= 16 && (lane & 7) < G) atomicMax(s_max + max_at + lane, mine);
+        const int max_next = max_at == 2 * HB * kMaxima8 ? 0 : max_at + HB * kMaxima8;
+        if (warp == wf && lane <= 16) s_max[max_next + lane] = kNoMax8;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::bMax + par * HB + hh));
         ok = wait(L::bMax + par * HB + hh, (ug >> 1) & 1);
         if (!ok) break;
-        // c is 0 .. 254, as the key of the largest score has an ev of 0 or more
-        // (0 where an infinite score makes it NaN)
-        auto c_of = [](float most, float top) {
-          return fminf(fmaxf(ceilf(most - top), 0.f), 254.f);
+        // c: at least 0, as the key of the largest score has an ev of 0 or more
+        // (0 too where an infinite score makes it NaN).  (score + ev) was
+        // rounded, by at most 2^-24 of it: c makes up for that, so that no entry
+        // passes 2^8.5 however large the scores are, and is at most the part's
+        // largest ev, with which no entry passes 2^8.
+        const float c_top = static_cast<float>(s_max[max_at + 16]);
+        auto c_of = [&](float most, float top) {
+          const float c = ceilf(fmaf(fabsf(most), 0x1p-23f, most - top) - 0.5f);
+          return fminf(fmaxf(c, 0.f), c_top);
         };
+        // lane h (and 8 + h, ...) works out head h's
+        const float m_mine = from_ordered(s_max[max_at + (lane & 7)]);
+        const float c_mine = c_of(from_ordered(s_max[max_at + 8 + (lane & 7)]), m_mine);
+        if (warp == wf && lane < G) { // of the part's state
+          s_m[(par * HB + hh) * 8 + lane] = m_mine;
+          s_c[(par * HB + hh) * 8 + lane] = c_mine;
+        }
         float m_neg[G], c_neg[G];
-        int32_t all[16];
-#pragma unroll
-        for (int h = 0; h < 16; h += 4)
-          if ((h & 7) < G)
-            *reinterpret_cast<int4 *>(all + h) = *reinterpret_cast<const int4 *>(s_max + max_at + h);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          m_neg[h] = -from_ordered(all[h]);
-          c_neg[h] = -c_of(from_ordered(all[8 + h]), -m_neg[h]);
-        }
-        if (warp == wf && lane < G) { // of the part's state
-          const float top = from_ordered(s_max[max_at + lane]);
-          s_m[(par * HB + hh) * 8 + lane] = top;
-          s_c[(par * HB + hh) * 8 + lane] = c_of(from_ordered(s_max[max_at + 8 + lane]), top);
+          if constexpr (G == 8) { // shuffles take ptxas past its registers
+            m_neg[h] = -from_ordered(s_max[max_at + h]);
+            c_neg[h] = -c_of(from_ordered(s_max[max_at + 8 + h]), -m_neg[h]);
+          } else {
+            m_neg[h] = -__shfl_sync(0xffffffffu, m_mine, h);
+            c_neg[h] = -__shfl_sync(0xffffffffu, c_mine, h);
+          }
         }
         max_at = max_next;
         // ---- pass 2: the weights 2^(s - m), and 2^(s - m + ev - c + 8) in two

@@ -144,3 +144,48 @@ def test_one_magnitude_at_either_end_of_the_range():
         size = lambda b, n, h, g: torch.full((n, h, 1), e, dtype=fu.F64, device=DEV)
         r = Requests([1, 700, 3000], 8, 2, 128, seed=6, size=size)
         r.check(*r.decode())
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (8, 1)])
+@pytest.mark.parametrize("up", [12, 16, 20, 24, 40])
+def test_huge_scores(hq, hkv, up):
+    # one key a part scores 2^up times the ordinary and takes all the weight:
+    # the output is its value row, whatever the spacing of such scores is; the
+    # largest value row of the part stands elsewhere
+    lens = [300, 513, 1024, 2500]
+    r = Requests(lens, hq, hkv, 128, seed=up)
+    r.q[:, :, 0] = 8.0
+    for b, n in enumerate(lens):
+        s = r.slots(b)
+        rows = list(range(77, n, 512))
+        for i, key in enumerate(rows):
+            r.codes[0][s[key]] = 0
+            r.codes[0][s[key], :, 0] = 0x38 + i  # 1, 1.125, 1.25, ... in e4m3
+            r.scale[0][s[key]] = 127 + up
+            r.scale[1][s[key] if i % 2 else s[key - 1]] += 9
+        out, lse = r.decode()
+        v = fu.cache_values(r.codes[1].view(fu.E4M3), r.scale[1].view(fu.E8M0))
+        want = v[s[rows[-1]]].repeat_interleave(hq // hkv, 0)
+        # 8 significant bits of the weight, the output's rounding
+        assert ((out[b].double() - want).abs() <= 2.02 * 2.0 ** -8 * want.abs()).all()
+
+
+@pytest.mark.parametrize("byte", [0, 1, 3, 254])
+def test_the_ends_of_the_scale_bytes(byte):
+    # foreign caches: values down to 2^-136 (bf16 ends at 2^-133) and up to 2^127
+    lens = [1, 600]
+    r = Requests(lens, 4, 2, 64, seed=byte)
+    for b in range(2):
+        s = r.slots(b)
+        r.scale[1][s] = byte
+        if byte == 254:  # 1.75 and less, finite in bf16
+            r.codes[1][s] &= 0xBF
+    out, lse = r.decode()
+    for b in range(2):
+        s = r.slots(b)
+        want, tol, l, l_tol = fb.decode_bounds(r.q[b:b + 1], r.codes[0][s].view(fu.E4M3),
+                                               r.scale[0][s].view(fu.E8M0),
+                                               r.codes[1][s].view(fu.E4M3),
+                                               r.scale[1][s].view(fu.E8M0))
+        # half a step of bf16's smallest values, and fp32's in between
+        fu.check(out[b:b + 1], lse[b:b + 1], want, tol + 2.0 ** -134 + 2.0 ** -148, l, l_tol)
