@@ -42,10 +42,12 @@ __device__ __forceinline__ RaggedRequest ragged_request(const PlanArgs &p, int b
   RaggedRequest r;
   r.q_start = p.qo_indptr[b];
   r.kv_begin = p.kv_indptr[b];
-  const int64_t ql = static_cast<int64_t>(p.qo_indptr[b + 1]) - r.q_start;
-  const int64_t kl = static_cast<int64_t>(p.kv_indptr[b + 1]) - r.kv_begin;
+  const int32_t q_end = p.qo_indptr[b + 1], kv_end = p.kv_indptr[b + 1];
+  const int64_t ql = static_cast<int64_t>(q_end) - r.q_start;
+  const int64_t kl = static_cast<int64_t>(kv_end) - r.kv_begin;
   r.ok = ql >= 0 && kl >= 0 && kl <= INT32_MAX / 2 && ql <= INT32_MAX / 2 &&
-         (!p.causal || ql <= kl);
+         (!p.causal || ql <= kl) && r.q_start >= 0 && q_end <= p.max_total_q && r.kv_begin >= 0 &&
+         kv_end <= p.max_kv_len;
   r.q_len = r.ok ? static_cast<int32_t>(ql) : 0;
   r.kv_len = r.ok ? static_cast<int32_t>(kl) : 0;
   const int32_t tiles = (r.q_len + p.tile_tokens - 1) / p.tile_tokens;
@@ -103,7 +105,11 @@ __global__ void __launch_bounds__(kPlanThreadsR) plan_ragged_kernel(const PlanAr
     RaggedRequest r{};
     r.ok = true;
     if (b < p.batch) r = ragged_request(p, b, gt);
-    bad = bad || !r.ok;
+    // a chunk whose requests follow one another within the host's totals has no
+    // more groups and splits than fit those: the loops below end in time,
+    // whatever the arrays hold
+    bad = __syncthreads_or(bad || !r.ok) != 0;
+    if (bad) break;
     // groups in the low half, merge rows in the high half (each below 2^31)
     int64_t n_gm, n_rows;
     const int64_t gm = block_scan(r.groups + (static_cast<int64_t>(r.merge) << 32), s_warp, n_gm);
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreadsR) plan_ragged_kernel(const PlanAr
     merges += n_gm >> 32;
     rows += n_rows;
   }
-  const bool ok = __syncthreads_or(bad) == 0 && groups == p.n_groups_expected &&
+  const bool ok = !bad && groups == p.n_groups_expected &&
                   rows == p.part_rows_expected && units == p.n_units_expected;
   if (tid == 0) p.status[kStatusMergeRows] = ok ? static_cast<int32_t>(merges) : 0;
   if (ok) return;
