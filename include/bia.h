@@ -55,10 +55,9 @@
  * call does comes after the work already on `stream` and before the work
  * enqueued there next.  During a graph capture of `stream` the fork is
  * captured with the call (if that thread's side stream does not exist yet,
- * the call stays on `stream`).  A process drives one GPU: each kernel's shared-memory limit is
- * raised on its first launch, for the device current then, and a later
- * launch on another device fails with BIA_ERR_CUDA (one process per GPU is
- * the intended deployment).
+ * the call stays on `stream`).  Calls run on the current device; each kernel is
+ * set up on its first launch there (one process per GPU is the intended
+ * deployment).
  *
  * Errors: every entry point returns BIA_OK or a negative bia_status and never
  * aborts.  Host-side checks run before anything is enqueued.  A page index
@@ -439,8 +438,8 @@ BIA_API int bia_append_paged_kv(const bia_attn_desc *desc, const void *k_new, co
  * reaches).  A row's codes and scale depend on that row alone, so what the
  * cache holds, and every result from it, is free of batch, page and chunk.
  * With those scales every value is exact in bf16: reading back rounds nothing
- * (an element above 248 * 2^120, 3.29e38, is stored as 2^128, which reads back
- * as an infinity).
+ * (but an element above 248 * 2^120, 3.29e38, is stored as 2^128, which reads
+ * back as an infinity).
  * head_dim, page sizes and head counts are those of the bf16 calls.
  */
 
@@ -451,7 +450,10 @@ BIA_API int bia_append_paged_kv(const bia_attn_desc *desc, const void *k_new, co
  *                 aligned; k_stride / v_stride elements from one token to the
  *                 next (a multiple of 8, at least the row; 0: dense), so that
  *                 both may lie inside a fused projection's rows
- * Everything else, the status word included, as for bia_append_paged_kv.
+ * Everything else, the status word included, as for bia_append_paged_kv; as
+ * there, the device arrays are the ones gone by (a captured append follows them
+ * as they change), so kv_indices must hold the kv_indptr[batch] entries that the
+ * device array asks for.
  * append_indptr[batch] * num_kv_heads must stay below 2^30 (else
  * BIA_ERR_UNSUPPORTED).
  */
@@ -488,8 +490,15 @@ BIA_API int bia_gather_paged_kv_fp8(const bia_attn_desc *desc, const void *k_cac
 
 /*
  * bia_decode_paged over the 8-bit cache: q, out and lse, the page table, the
- * fixed split-KV tiles and their ascending merge, the ownership and the
- * errors are the same.  split_size: a multiple of 128 up to
+ * fixed split-KV tiles (anchored at key 0), the ownership and the errors are the
+ * same.  The tiles' states are joined in a fixed order of this call's own:
+ * weights and their sum over 32 tiles at a time, one division at the end.
+ * Where the values are rounded: softmax weights, each times its value row's
+ * scale, keep 8 significant bits (what bf16 keeps) down to 2^-13 of the largest
+ * such product among the 512 keys it shares a part of a tile with, and are off
+ * by at most 2^-21 of that one below; sums are fp32, out is bf16.  So the scale
+ * of a row should fit its codes, as the append's does: a row of small codes
+ * under a large scale counts as a large one.  split_size: a multiple of 128 up to
  * BIA_DECODE_FP8_SPLIT, 0 = BIA_DECODE_FP8_SPLIT (a larger one:
  * BIA_ERR_UNSUPPORTED, as are caches of 2^32 - 1 (key, kv head) rows and
  * more).  The workspace is bia_decode_fp8_workspace_size's.
@@ -544,7 +553,8 @@ BIA_API size_t bia_decode_fp8_bounded_workspace_size(const bia_attn_desc *desc,
  * the kernel's waits, else BIA_ERR_UNSUPPORTED), merge, workspace, ownership
  * and errors as for bia_prefill_paged; a row's bits depend only on
  * its own request up to its position, under any chunking, on the q-tile grid
- * or off it.  What lies past a request's last key never reaches its rows; a
+ * or off it.  Weights lag the running maximum by up to 2^16 before they are
+ * divided by their sum, in fp32: values above 2^80 may overflow.  What lies past a request's last key never reaches its rows; a
  * non-finite key or value of the request itself may reach every row of the
  * 128-row q tiles that see its 128-key block.
  */

@@ -24,7 +24,12 @@
 // Converting the rows instead (8 -> 16 bits through registers and shared
 // memory) would cost more issue slots than the copies themselves.
 //
-// HBM bound: D + 1 bytes per key, head and cache.  At 6.5 TB/s an SM has
+// HBM bound at 128 and 256 columns with up to 4 heads a group: D + 1 bytes per
+// key, head and cache (64 requests of 1024 to 32768 keys, 8 kv heads x 128, page
+// 16: 6.1 TB/s with 2 heads a group, 5.8 with 4).  Narrower heads and 8 heads a
+// group are bound by the softmax warps, whose time for a part hardly depends on
+// its bytes: 64 columns 344 us where 128 take 390 (3.3 TB/s), 96 378 us (4.5),
+// 8 heads a group 456 us (5.0).  At 6.5 TB/s an SM has
 // ~1450 cycles for a 128-key block of one 128-wide head, half of what the bf16
 // decode has, and an online softmax does not fit: per block its chain of
 // waits, maximum exchange and rescaling took ~5000 cycles of a warpgroup, 3.8

@@ -8,7 +8,8 @@
 // A power of two costs a floating code no accuracy (scaling by it is exact),
 // takes one byte a row, and makes the value exact in bf16: a code has 4
 // significant bits, and with e >= -120 its last place (2^(e-9)) is at least
-// bf16's smallest subnormal.  A row's codes and scale depend on that row
+// bf16's smallest subnormal.  (At the top, elements above 248 * 2^120 round to
+// the code 256 under e = 120: 2^128, in bf16 an infinity.)  A row's codes and scale depend on that row
 // alone, so what a cache holds never depends on batch, page or chunk.
 #pragma once
 

@@ -28,7 +28,9 @@
 // Bound by the chain of a q tile: S, softmax (1350 cycles), P.V and the waits
 // between them take ~3400 cycles a block where the two tiles' MMAs take 2048
 // alone (2800 with the S operands' shared-memory reads at their limit).  16384
-// tokens, 32/8 heads x 128: 1350 TFLOP/s, 79 % of the sustained cuBLAS rate;
+// tokens, 32/8 heads x 128: 1662 us a call, 1320 TFLOP/s, 77 % of the sustained
+// cuBLAS rate; three prompts of 4096 to 8192 tokens 1250 (950 at 96 columns, 760
+// at 64, where a block's MMAs halve and its softmax does not);
 // 6 prompts of 100 to 2048 tokens (4 to 5 blocks an item) 61 us, 730 TFLOP/s.
 //
 // A call of up to 32 requests without splits to merge and with an SM for
