@@ -547,7 +547,8 @@ BIA_API size_t bia_decode_fp8_bounded_workspace_size(const bia_attn_desc *desc,
  *         q tokens qo_indptr[b] .. and keys kv_indptr[b] ..
  * Request b's q tokens are the last q_len of its kv_len keys (the rule of
  * bia_prefill_paged); causal calls need q_len <= kv_len, and without causal a
- * request without keys gives out 0 and lse -inf.  page_size of desc is not
+ * request without keys gives out 0 and lse -inf.  A call without a q token does
+ * nothing (q and out may be NULL; the status word is not touched).  page_size of desc is not
  * used.  Tiles, split_size (0 = BIA_PREFILL_SPLIT; at most
  * BIA_RAGGED_MAX_SPLIT, so that a tile's time stays far below the limit of
  * the kernel's waits, else BIA_ERR_UNSUPPORTED), merge, workspace, ownership

@@ -1218,7 +1218,7 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
                        size_t workspace_bytes, void *out, float *lse, void *stream) {
   causal = causal ? 1 : 0;
   if (split_size == 0) split_size = BIA_PREFILL_SPLIT;
-  if (!q || !qo_indptr || !kv_indptr || !out || !workspace) return BIA_ERR_INVALID_ARG;
+  if (!qo_indptr || !kv_indptr || !workspace) return BIA_ERR_INVALID_ARG;
   if (misaligned(workspace, 256) || misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) ||
       misaligned(out, 16) || misaligned(lse, 4) || misaligned(qo_indptr, 4) ||
       misaligned(kv_indptr, 4))
@@ -1238,7 +1238,7 @@ int bia_prefill_ragged(const bia_attn_desc *desc, const void *q, const void *k, 
   if (workspace_bytes < w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
   if (hp.total_q == 0) return BIA_OK;
   const int64_t total_kv = kv_indptr_host[batch];
-  if (total_kv > 0 && (!k || !v)) return BIA_ERR_INVALID_ARG;
+  if (!q || !out || (total_kv > 0 && (!k || !v))) return BIA_ERR_INVALID_ARG;
   rc = check_resident({{"q", q},
                        {"k", k},
                        {"v", v},
