@@ -189,3 +189,39 @@ def test_the_ends_of_the_scale_bytes(byte):
                                                r.scale[1][s].view(fu.E8M0))
         # half a step of bf16's smallest values, and fp32's in between
         fu.check(out[b:b + 1], lse[b:b + 1], want, tol + 2.0 ** -134 + 2.0 ** -148, l, l_tol)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 8), (128, 16, 2), (128, 32, 8), (256, 8, 2)])
+@pytest.mark.parametrize("many", [False, True])
+def test_non_finite_inputs_stay_with_their_heads(d, hq, hkv, many):
+    lens = [700, 1500, 2500] + [600] * (100 if many else 0)
+    r = Requests(lens, hq, hkv, d, seed=d + hkv)
+    out, lse = r.decode()
+    g = hq // hkv
+    clean = torch.ones_like(out, dtype=torch.bool)
+    # a query element of head 1 of request 0: that head alone
+    r.q[0, 1, 5] = float("inf")
+    clean[0, 1] = False
+    # a NaN value scale, kv head 1 of request 1: its heads' outputs, not their lse
+    r.scale[1][r.slots(1)[1200], 1] = 255
+    clean[1, g:2 * g] = False
+    # a NaN key scale, kv head 0 of request 2: its heads
+    r.scale[0][r.slots(2)[40], 0] = 255
+    clean[2, :g] = False
+    o2, l2 = r.decode()
+    assert torch.isnan(o2[~clean]).all()
+    assert torch.equal(o2[clean], out[clean])
+    dead = torch.zeros_like(lse, dtype=torch.bool)
+    dead[0, 1] = True
+    dead[2, :g] = True
+    assert torch.isnan(l2[dead]).all() and torch.equal(l2[~dead], lse[~dead])
+
+
+def test_more_requests_than_a_plan_s_chunk():
+    lens = [(i * 131) % 300 + 1 for i in range(1300)]
+    for b in (0, 511, 512, 1024, 1299):
+        lens[b] = 1500 + b
+    r = Requests(lens, 8, 2, 64, seed=9)
+    out, lse = r.decode()
+    r.check(out, lse, (0, 1, 510, 511, 512, 513, 1023, 1024, 1025, 1298, 1299))
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
