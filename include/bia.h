@@ -575,6 +575,101 @@ BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
                                          const int32_t *kv_indptr_host, int32_t batch,
                                          int32_t causal, int32_t split_size);
 
+/*
+ * Rotary positions, with the norm of each query and key head in the same pass:
+ * what stands between a model's projection and the calls above.  A head x of
+ * head_dim columns becomes, in fp32 and rounded once at the end,
+ *   y = x * weight / sqrt(mean(x^2) + norm_eps)     (without a weight: y = x)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)        for each pair of columns
+ * Frequency i in 0 .. rot_dim/2 - 1 turns columns i and i + rot_dim/2, or
+ * (interleaved) 2i and 2i + 1; the columns from rot_dim on pass unturned.
+ *   table:     fp32 [num_positions, rot_dim], 16-byte aligned: row p holds
+ *              cos(p * w_i) for every i, then sin(p * w_i), so that any scheme
+ *              of frequencies (and their scaling) is the caller's
+ *   positions: int32 [num_axes, total]: a token's position on each axis
+ *              (one for text; time, height and width for images and video);
+ *              frequency i follows axis freq_axis[i].  A position outside
+ *              0 .. num_positions - 1 turns by NaN and sets bit 3 of *status
+ *   q_weight, k_weight: fp32 [head_dim], 16-byte aligned, of the norms of
+ *              queries and of keys; NULL: no norm of theirs
+ * Squares above the range of fp32 (elements above 1.8e19) make a normed head
+ * zero or NaN.  A head's bits depend on that head, its position and the table
+ * alone.
+ */
+typedef struct bia_rope {
+    int32_t rot_dim;       /* columns that turn: a multiple of 16 up to head_dim */
+    int32_t interleaved;   /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1) */
+    int32_t num_axes;      /* 1..4 */
+    int32_t num_positions; /* rows of the table */
+    float norm_eps;        /* finite, >= 0 */
+    uint8_t freq_axis[128]; /* axis of frequency i; not read with one axis */
+} bia_rope;
+
+/*
+ * Rows to rows: the queries and keys of packed tokens, for bia_prefill_ragged
+ * and the appends above.
+ *   q [total, num_qo_heads, head_dim], k [total, num_kv_heads, head_dim] bf16,
+ *   q_out and k_out the same; 16-byte aligned, *_stride elements from one
+ *   token to the next (a multiple of 8, at least the row; 0: dense), so that q
+ *   and k may be parts of a fused projection.  q_out == q with the same stride
+ *   rotates in place (k_out == k as well); any other overlap is the caller's
+ *   error.  q and q_out, or k and k_out, may be NULL together.
+ *   status: NULL, or a device int32 that the call zeroes first
+ * desc gives the head counts and head_dim (its page size is not used).
+ * total * (num_qo_heads + 2 num_kv_heads) must stay below 2^31 (else
+ * BIA_ERR_UNSUPPORTED), here and below.
+ */
+BIA_API int bia_norm_rope(const bia_attn_desc *desc, const bia_rope *rope, const float *table,
+                  const int32_t *positions, const void *q, const void *k, int64_t q_stride,
+                  int64_t k_stride, const float *q_weight, const float *k_weight, int64_t total,
+                  void *q_out, void *k_out, int64_t q_out_stride, int64_t k_out_stride,
+                  int32_t *status, void *stream);
+
+/*
+ * bia_append_paged_kv with the norm and the rotation on the way: the new keys
+ * are normed, turned and written into their pages, the values as they are, and
+ * the queries of the same tokens to q_out, ready for the attention calls.
+ *   q [total, num_qo_heads, head_dim], k_new, v_new [total, num_kv_heads,
+ *   head_dim] bf16 with token strides as above, total = append_indptr[batch];
+ *   q and q_out may be NULL together
+ *   positions: as above, or NULL: a token's position on every axis is its
+ *   key's, kv_len(b) - n_new(b) + (t - append_indptr[b])
+ * The page table, append_indptr and the status word are those of
+ * bia_append_paged_kv (a token without a page is skipped, its query is not).
+ * The bits are those of bia_norm_rope followed by bia_append_paged_kv.
+ */
+BIA_API int bia_append_paged_kv_rope(const bia_attn_desc *desc, const bia_rope *rope,
+                             const float *table, const int32_t *positions, const void *q,
+                             const void *k_new, const void *v_new, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float *q_weight,
+                             const float *k_weight, void *k_cache, void *v_cache,
+                             int64_t num_pages, const int32_t *append_indptr,
+                             const int32_t *kv_indptr, const int32_t *kv_indices,
+                             const int32_t *kv_last_page_len, const int32_t *append_indptr_host,
+                             const int32_t *kv_indptr_host, const int32_t *kv_last_page_len_host,
+                             int32_t batch, void *q_out, int64_t q_out_stride, int32_t *status,
+                             void *stream);
+
+/*
+ * The same into the 8-bit cache (the format of bia_append_paged_kv_fp8): a key
+ * row is quantised from its fp32 values, without a rounding to bf16 between.
+ *   k_out: NULL, or bf16 rows [total, num_kv_heads, head_dim] that the turned
+ *          keys are also written to, for bia_prefill_ragged over the prompt
+ */
+BIA_API int bia_append_paged_kv_fp8_rope(const bia_attn_desc *desc, const bia_rope *rope,
+                                 const float *table, const int32_t *positions, const void *q,
+                                 const void *k_new, const void *v_new, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const float *q_weight,
+                                 const float *k_weight, void *k_cache, void *v_cache,
+                                 void *k_scale, void *v_scale, int64_t num_pages,
+                                 const int32_t *append_indptr, const int32_t *kv_indptr,
+                                 const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                                 const int32_t *append_indptr_host,
+                                 const int32_t *kv_indptr_host,
+                                 const int32_t *kv_last_page_len_host, int32_t batch,
+                                 void *q_out, void *k_out, int64_t q_out_stride,
+                                 int64_t k_out_stride, int32_t *status, void *stream);
+
 /* Tokens per q tile for GQA group size G = num_qo_heads / num_kv_heads:
  * 128 / G, the chunk grid on which chunked prefill is guaranteed to be
  * bit-identical ("sglang PR #43612", Summary).  0 if G does not divide 128. */
@@ -593,7 +688,7 @@ BIA_API const char *bia_last_error(void);
  * (bit 0: a page index was out of range; bit 1: the device index arrays
  * disagreed with the host-sized launch, broke a rule of the call or exceeded
  * the bounds of a bounded call, and nothing was computed; bit 2: a device wait
- * timed out) into *status_out.  Synchronises `stream`.
+ * timed out; bit 3: a rotary position was outside its table) into *status_out.  Synchronises `stream`.
  */
 BIA_API int bia_read_status(const void *workspace, int32_t *status_out, void *stream);
 

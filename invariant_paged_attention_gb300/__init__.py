@@ -46,7 +46,8 @@ EXPORTS = ("bia_prefill_paged", "bia_prefill_workspace_size", "bia_decode_paged"
            "bia_decode_bounded_workspace_size", "bia_append_paged_kv_fp8",
            "bia_gather_paged_kv_fp8", "bia_decode_paged_fp8", "bia_decode_fp8_workspace_size",
            "bia_decode_paged_fp8_bounded", "bia_decode_fp8_bounded_workspace_size",
-           "bia_prefill_ragged", "bia_prefill_ragged_workspace_size")
+           "bia_prefill_ragged", "bia_prefill_ragged_workspace_size", "bia_norm_rope",
+           "bia_append_paged_kv_rope", "bia_append_paged_kv_fp8_rope")
 
 
 class BiaError(RuntimeError):
@@ -78,6 +79,12 @@ MLA_CKV_DIM, MLA_KPE_DIM = 512, 64
 class Bounds(ctypes.Structure):
     _fields_ = [("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32),
                 ("max_total_q", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("num_positions", ctypes.c_int32),
+                ("norm_eps", ctypes.c_float), ("freq_axis", ctypes.c_uint8 * 128)]
 
 
 def load(path: str = LIB_PATH):
@@ -167,6 +174,17 @@ def load(path: str = LIB_PATH):
     lib.bia_prefill_ragged.restype = ctypes.c_int
     lib.bia_prefill_ragged_workspace_size.argtypes = [dp, vp, vp, i32, i32, i32]
     lib.bia_prefill_ragged_workspace_size.restype = sz
+    rp = ctypes.POINTER(Rope)
+    lib.bia_norm_rope.argtypes = [dp, rp, vp, vp, vp, vp, i64, i64, vp, vp, i64, vp, vp, i64, i64,
+                                  vp, vp]
+    lib.bia_norm_rope.restype = ctypes.c_int
+    rows = [dp, rp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp]
+    table = [i64, vp, vp, vp, vp, vp, vp, vp, i32]
+    lib.bia_append_paged_kv_rope.argtypes = rows + [vp, vp] + table + [vp, i64, vp, vp]
+    lib.bia_append_paged_kv_rope.restype = ctypes.c_int
+    lib.bia_append_paged_kv_fp8_rope.argtypes = (rows + [vp, vp, vp, vp] + table +
+                                                 [vp, vp, i64, i64, vp, vp])
+    lib.bia_append_paged_kv_fp8_rope.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -899,3 +917,169 @@ def bia_prefill_ragged(desc, q, k, v, qo_indptr, kv_indptr, qo_indptr_host, kv_i
         workspace.element_size(), out.data_ptr(), _at(lse), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_prefill_ragged")
+
+
+# ---------------------------------------------------------------- rotary positions
+
+
+def make_rope(rot_dim, num_positions, num_axes=1, freq_axis=None, interleaved=False,
+              norm_eps=1e-6) -> Rope:
+    """The rotation of a model's heads (include/bia.h states the rule):
+    freq_axis names the axis of each of the rot_dim / 2 frequencies where there
+    are several axes, for example [16 * 0, 24 * 1, 24 * 2] or 0, 1, 2 in turn."""
+    r = Rope(int(rot_dim), int(bool(interleaved)), int(num_axes), int(num_positions),
+             float(norm_eps))
+    axes = [] if freq_axis is None or num_axes == 1 else list(freq_axis)
+    if num_axes > 1 and len(axes) != rot_dim // 2:
+        raise ValueError(f"freq_axis must name an axis for each of {rot_dim // 2} frequencies, "
+                         f"got {len(axes)}")
+    if any(not 0 <= x < num_axes for x in axes):
+        raise ValueError(f"freq_axis names axes 0 to {num_axes - 1}")
+    if len(axes) <= 128:
+        r.freq_axis[:len(axes)] = axes
+    return r
+
+
+def _check_rope(desc, rope, table, positions, q_weight, k_weight, total):
+    if table.shape != (rope.num_positions, rope.rot_dim):
+        raise ValueError(f"table must be ({rope.num_positions}, {rope.rot_dim}), got "
+                         f"{tuple(table.shape)}")
+    if positions is not None and positions.numel() != rope.num_axes * total:
+        raise ValueError(f"positions must hold {rope.num_axes} x {total} entries, got "
+                         f"{positions.numel()}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w.shape != (desc.head_dim,):
+            raise ValueError(f"{name} must be ({desc.head_dim},), got {tuple(w.shape)}")
+
+
+def _rope_types(table, positions, q_weight, k_weight, status):
+    return _check_types(("table", table, F32), ("positions", positions, I32, True),
+                        ("q_weight", q_weight, F32, True), ("k_weight", k_weight, F32, True),
+                        ("status", status, I32, True))
+
+
+def _rope_dense(at, table, positions, q_weight, k_weight, status) -> bool:
+    return (_dense(at, F32, table) and (positions is None or _dense(at, I32, positions)) and
+            (q_weight is None or _dense(at, F32, q_weight)) and
+            (k_weight is None or _dense(at, F32, k_weight)) and
+            (status is None or _dense(at, I32, status)))
+
+
+def _pair(name, t, t_out, heads, head_dim, total):
+    """Token strides of rows and of their outputs (both may be None)."""
+    if t is None and t_out is None:
+        return 0, 0
+    return (_packed(name, t, heads, head_dim, total),
+            _packed(name + "_out", t_out, heads, head_dim, total))
+
+
+def bia_norm_rope(desc, rope, table, positions, q, k, q_out, k_out, q_weight=None, k_weight=None,
+                  status=None, stream=None):
+    """Norms and rotates q [total, Hq, D] and k [total, Hkv, D] into q_out and
+    k_out, each dense or a slice of a fused projection's rows, also in place;
+    q and q_out, or k and k_out, may be None.  positions [num_axes, total]."""
+    some = q if q is not None else k
+    if some is None:
+        raise TypeError("q or k is required")
+    total = some.shape[0]
+    hq, hkv, d = desc.num_qo_heads, desc.num_kv_heads, desc.head_dim
+    q_step, qo_step = _pair("q", q, q_out, hq, d, total)
+    k_step, ko_step = _pair("k", k, k_out, hkv, d, total)
+    at, ts = _index(some), None
+    if not (stream is None and at >= 0 and at == _current_device() and positions is not None and
+            _rope_dense(at, table, positions, q_weight, k_weight, status)):
+        if positions is None:
+            raise TypeError("positions is required")
+        ts = _rope_types(table, positions, q_weight, k_weight, status)
+    _check_rope(desc, rope, table, positions, q_weight, k_weight, total)
+    rows = [(n, t) for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
+            if t is not None]
+    if ts is not None or any(t.get_device() != at for _, t in rows):
+        _check_cuda(rows + (ts or []), stream)
+    rc = load().bia_norm_rope(
+        ctypes.byref(desc), ctypes.byref(rope), table.data_ptr(), positions.data_ptr(), _at(q),
+        _at(k), q_step, k_step, _at(q_weight), _at(k_weight), total, _at(q_out), _at(k_out),
+        qo_step, ko_step, _at(status), _handle(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_norm_rope")
+
+
+def _append_rope(fp8, desc, rope, table, q, k_new, v_new, caches, append_indptr, kv_indptr,
+                 kv_indices, kv_last_page_len, append_indptr_host, kv_indptr_host,
+                 kv_last_page_len_host, q_out, k_out, positions, q_weight, k_weight, status,
+                 stream):
+    """The checks of the two appends; the arguments from the strides' rows on."""
+    ap, kvp, last = (_host(append_indptr_host), _host(kv_indptr_host),
+                     _host(kv_last_page_len_host))
+    batch = ap.numel() - 1
+    total, hq, hkv, d = _last(ap), desc.num_qo_heads, desc.num_kv_heads, desc.head_dim
+    q_step, qo_step = _pair("q", q, q_out, hq, d, total)
+    k_step = _packed("k_new", k_new, hkv, d, total)
+    v_step = _packed("v_new", v_new, hkv, d, total)
+    ko_step = 0 if k_out is None else _packed("k_out", k_out, hkv, d, total)
+    k_cache = caches[0]
+    at, ts = _index(k_cache), None
+    if not (stream is None and at >= 0 and at == _current_device() and
+            _dense(at, E4M3 if fp8 else BF16, *caches[:2]) and _dense(at, E8M0, *caches[2:]) and
+            _dense(at, I32, append_indptr, kv_indptr, kv_indices, kv_last_page_len) and
+            _rope_dense(at, table, positions, q_weight, k_weight, status)):
+        kinds = (E4M3, E4M3, E8M0, E8M0) if fp8 else (BF16, BF16)
+        ts = _check_types(*zip(("k_cache", "v_cache", "k_scale", "v_scale"), caches, kinds),
+                          ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
+                          ("kv_indices", kv_indices, I32),
+                          ("kv_last_page_len", kv_last_page_len, I32))
+        ts += _rope_types(table, positions, q_weight, k_weight, status)
+    if fp8:
+        _check_caches_fp8(desc, *caches)
+    else:
+        want = (k_cache.shape[0], desc.page_size, hkv, d)
+        if k_cache.shape != want or caches[1].shape != want:
+            raise ValueError(f"k_cache and v_cache must be {want} (num_pages, page_size, "
+                             f"num_kv_heads, head_dim) for this descriptor, got "
+                             f"{tuple(k_cache.shape)} and {tuple(caches[1].shape)}")
+    _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
+    if append_indptr.numel() != batch + 1:
+        raise ValueError(f"append_indptr must hold {batch + 1} entries, got "
+                         f"{append_indptr.numel()}")
+    _check_rope(desc, rope, table, positions, q_weight, k_weight, total)
+    rows = [(n, t) for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("q_out", q_out),
+                                ("k_out", k_out)) if t is not None]
+    if ts is not None or any(t.get_device() != at for _, t in rows):
+        _check_cuda((ts or [("k_cache", k_cache)]) + rows, stream)
+    head = (ctypes.byref(desc), ctypes.byref(rope), table.data_ptr(), _at(positions), _at(q),
+            k_new.data_ptr(), v_new.data_ptr(), q_step, k_step, v_step, _at(q_weight),
+            _at(k_weight), *(c.data_ptr() for c in caches), k_cache.shape[0],
+            append_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
+            kv_last_page_len.data_ptr(), ap.data_ptr(), kvp.data_ptr(), last.data_ptr(), batch)
+    if fp8:
+        name, tail = "bia_append_paged_kv_fp8_rope", (_at(q_out), _at(k_out), qo_step, ko_step)
+    else:
+        name, tail = "bia_append_paged_kv_rope", (_at(q_out), qo_step)
+    rc = getattr(load(), name)(*head, *tail, _at(status), _handle(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, name)
+
+
+def bia_append_paged_kv_rope(desc, rope, table, q, k_new, v_new, k_cache, v_cache, append_indptr,
+                             kv_indptr, kv_indices, kv_last_page_len, append_indptr_host,
+                             kv_indptr_host, kv_last_page_len_host, q_out, positions=None,
+                             q_weight=None, k_weight=None, status=None, stream=None):
+    """bia_append_paged_kv with the keys normed and rotated on the way, and the
+    queries of the same tokens to q_out (q and q_out may be None).  Without
+    positions a token's position is its key's."""
+    _append_rope(False, desc, rope, table, q, k_new, v_new, (k_cache, v_cache), append_indptr,
+                 kv_indptr, kv_indices, kv_last_page_len, append_indptr_host, kv_indptr_host,
+                 kv_last_page_len_host, q_out, None, positions, q_weight, k_weight, status, stream)
+
+
+def bia_append_paged_kv_fp8_rope(desc, rope, table, q, k_new, v_new, k_cache, v_cache, k_scale,
+                                 v_scale, append_indptr, kv_indptr, kv_indices, kv_last_page_len,
+                                 append_indptr_host, kv_indptr_host, kv_last_page_len_host, q_out,
+                                 k_out=None, positions=None, q_weight=None, k_weight=None,
+                                 status=None, stream=None):
+    """The same into the 8-bit cache; k_out, when given, takes the rotated keys
+    as bf16 rows too."""
+    _append_rope(True, desc, rope, table, q, k_new, v_new, (k_cache, v_cache, k_scale, v_scale),
+                 append_indptr, kv_indptr, kv_indices, kv_last_page_len, append_indptr_host,
+                 kv_indptr_host, kv_last_page_len_host, q_out, k_out, positions, q_weight,
+                 k_weight, status, stream)

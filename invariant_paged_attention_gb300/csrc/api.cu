@@ -1359,6 +1359,226 @@ size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc, const int32_
 extern "C" {
 
 namespace {
+// The rotation of a call: its table, and which axis each frequency follows.
+int rope_args(const bia_attn_desc *desc, const bia_rope *rope, bia::RopeArgs *a) {
+  if (!rope) return BIA_ERR_INVALID_ARG;
+  if (rope->rot_dim < 16 || rope->rot_dim > desc->head_dim || rope->rot_dim % 16 != 0 ||
+      rope->num_axes < 1 || rope->num_axes > 4)
+    return BIA_ERR_UNSUPPORTED;
+  if (rope->num_positions < 1 || !(rope->norm_eps >= 0.f) || !std::isfinite(rope->norm_eps))
+    return BIA_ERR_INVALID_ARG;
+  a->rot = rope->rot_dim;
+  a->interleaved = rope->interleaved ? 1 : 0;
+  a->axes = rope->num_axes;
+  a->num_positions = rope->num_positions;
+  a->eps = rope->norm_eps;
+  a->D = desc->head_dim;
+  a->inv_D = 1.0f / static_cast<float>(desc->head_dim);
+  for (int i = 0; a->axes > 1 && i < a->rot / 2; ++i) {
+    if (rope->freq_axis[i] >= rope->num_axes) return BIA_ERR_INVALID_ARG;
+    a->freq_axis[i / 16] |= static_cast<uint32_t>(rope->freq_axis[i]) << (2 * (i % 16));
+  }
+  return BIA_OK;
+}
+
+// Sources, strides and outputs common to the three calls; the pointers, once
+// their checks on the host are done, must be device memory.
+int rope_rows(bia::RopeArgs *a, const bia_attn_desc *desc, const float *table,
+              const int32_t *positions, const void *q, const void *k, const void *v,
+              int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *q_weight,
+              const float *k_weight, int64_t total, void *q_out, void *k_out,
+              int64_t q_out_stride, int64_t k_out_stride, int32_t *status) {
+  const int64_t q_row = static_cast<int64_t>(desc->num_qo_heads) * desc->head_dim;
+  const int64_t k_row = static_cast<int64_t>(desc->num_kv_heads) * desc->head_dim;
+  if (misaligned(table, 16) || misaligned(positions, 4) || misaligned(q, 16) ||
+      misaligned(k, 16) || misaligned(v, 16) || misaligned(q_weight, 16) ||
+      misaligned(k_weight, 16) || misaligned(q_out, 16) || misaligned(k_out, 16) ||
+      misaligned(status, 4))
+    return BIA_ERR_INVALID_ARG;
+  if (total > 0 && (!table || (q == nullptr) != (q_out == nullptr))) return BIA_ERR_INVALID_ARG;
+  if (total > INT32_MAX / (desc->num_qo_heads + 2 * static_cast<int64_t>(desc->num_kv_heads)))
+    return BIA_ERR_UNSUPPORTED;
+  int rc = token_stride(q_stride, q_row, &a->q_stride);
+  if (rc == BIA_OK) rc = token_stride(k_stride, k_row, &a->k_stride);
+  if (rc == BIA_OK) rc = token_stride(v_stride, k_row, &a->v_stride);
+  if (rc == BIA_OK) rc = token_stride(q_out_stride, q_row, &a->q_out_stride);
+  if (rc == BIA_OK) rc = token_stride(k_out_stride, k_row, &a->k_out_stride);
+  if (rc != BIA_OK) return rc;
+  a->table = table;
+  a->positions = positions;
+  a->q = static_cast<const uint16_t *>(q);
+  a->k = static_cast<const uint16_t *>(k);
+  a->v = static_cast<const uint16_t *>(v);
+  a->q_out = static_cast<uint16_t *>(q_out);
+  a->k_out = static_cast<uint16_t *>(k_out);
+  a->q_weight = q ? q_weight : nullptr;
+  a->k_weight = k ? k_weight : nullptr;
+  a->total = total;
+  a->Hq = q ? desc->num_qo_heads : 0;
+  a->Hk = k ? desc->num_kv_heads : 0;
+  a->status = status;
+  return BIA_OK;
+}
+
+int rope_resident(const bia::RopeArgs &a) {
+  if (a.total == 0) return a.status ? check_resident({{"status", a.status}}) : BIA_OK;
+  return check_resident({{"table", a.table},
+                         {"positions", a.positions},
+                         {"q", a.q},
+                         {"k", a.k},
+                         {"v", a.v},
+                         {"q_weight", a.q_weight},
+                         {"k_weight", a.k_weight},
+                         {"q_out", a.q_out},
+                         {"k_out", a.k_out},
+                         {"k_cache", a.k_codes ? static_cast<const void *>(a.k_codes) : a.k_cache},
+                         {"v_cache", a.v_codes ? static_cast<const void *>(a.v_codes) : a.v_cache},
+                         {"k_scale", a.k_scale},
+                         {"v_scale", a.v_scale},
+                         {"append_indptr", a.row_indptr},
+                         {"kv_indptr", a.kv_indptr},
+                         {"kv_indices", a.kv_indices},
+                         {"kv_last_page_len", a.kv_last_page_len},
+                         {"status", a.status}});
+}
+
+int run_rope(const bia::RopeArgs &a, cudaStream_t st) {
+  if (a.status) {
+    const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), st);
+    if (e != cudaSuccess) return cuda_fail("status reset", e);
+  }
+  if (a.total == 0) return BIA_OK;
+  const cudaError_t e = bia::launch_rope(a, st);
+  if (e != cudaSuccess) return cuda_fail("rotation kernel launch", e);
+  __atomic_add_fetch(&g_launches, 1ull, __ATOMIC_RELAXED);
+  return BIA_OK;
+}
+
+// The two appends; scales NULL: bf16 pages.
+int append_rope(bool fp8, const bia_attn_desc *desc, const bia_rope *rope, const float *table,
+                const int32_t *positions, const void *q, const void *k_new, const void *v_new,
+                int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *q_weight,
+                const float *k_weight, void *k_cache, void *v_cache, void *k_scale,
+                void *v_scale, int64_t num_pages, const int32_t *append_indptr,
+                const int32_t *kv_indptr, const int32_t *kv_indices,
+                const int32_t *kv_last_page_len, const int32_t *append_host,
+                const int32_t *kvp_host, const int32_t *last_host, int32_t batch, void *q_out,
+                void *k_out, int64_t q_out_stride, int64_t k_out_stride, int32_t *status,
+                void *stream) {
+  int rc = check_desc(desc);
+  if (rc != BIA_OK) return rc;
+  if (batch <= 0 || !append_host || !kvp_host || !last_host) return BIA_ERR_INVALID_ARG;
+  if (append_host[0] != 0 || kvp_host[0] < 0) return BIA_ERR_INVALID_ARG;
+  for (int b = 0; b < batch; ++b) {
+    const int64_t n_new = static_cast<int64_t>(append_host[b + 1]) - append_host[b];
+    const int64_t pages = static_cast<int64_t>(kvp_host[b + 1]) - kvp_host[b];
+    if (n_new < 0 || pages < 0) return BIA_ERR_INVALID_ARG;
+    const int32_t last = last_host[b];
+    if (pages > 0 && (last < 1 || last > desc->page_size)) return BIA_ERR_INVALID_ARG;
+    const int64_t kv_len = pages > 0 ? (pages - 1) * desc->page_size + last : 0;
+    if (kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
+    if (n_new > kv_len) return BIA_ERR_INVALID_ARG;
+  }
+  const int64_t total = append_host[batch];
+  bia::RopeArgs a{};
+  rc = rope_args(desc, rope, &a);
+  if (rc != BIA_OK) return rc;
+  if (total > 0 && (!k_new || !v_new || !k_cache || !v_cache || !append_indptr || !kv_indptr ||
+                    !kv_indices || !kv_last_page_len || num_pages <= 0 ||
+                    (fp8 && (!k_scale || !v_scale))))
+    return BIA_ERR_INVALID_ARG;
+  if (misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(k_scale, 2) ||
+      misaligned(v_scale, 2) || misaligned(append_indptr, 4) || misaligned(kv_indptr, 4) ||
+      misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
+    return BIA_ERR_INVALID_ARG;
+  rc = rope_rows(&a, desc, table, positions, q, k_new, v_new, q_stride, k_stride, v_stride,
+                 q_weight, k_weight, total, q_out, k_out, q_out_stride, k_out_stride, status);
+  if (rc != BIA_OK) return rc;
+  if (fp8) {
+    a.k_codes = static_cast<uint8_t *>(k_cache);
+    a.v_codes = static_cast<uint8_t *>(v_cache);
+    a.k_scale = static_cast<uint8_t *>(k_scale);
+    a.v_scale = static_cast<uint8_t *>(v_scale);
+  } else {
+    a.k_cache = static_cast<uint16_t *>(k_cache);
+    a.v_cache = static_cast<uint16_t *>(v_cache);
+  }
+  a.row_indptr = append_indptr;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.kv_last_page_len = kv_last_page_len;
+  a.num_pages = num_pages;
+  a.batch = batch;
+  a.page_shift = log2i(desc->page_size);
+  rc = rope_resident(a);
+  return rc == BIA_OK ? run_rope(a, static_cast<cudaStream_t>(stream)) : rc;
+}
+} // namespace
+
+int bia_norm_rope(const bia_attn_desc *desc, const bia_rope *rope, const float *table,
+                  const int32_t *positions, const void *q, const void *k, int64_t q_stride,
+                  int64_t k_stride, const float *q_weight, const float *k_weight, int64_t total,
+                  void *q_out, void *k_out, int64_t q_out_stride, int64_t k_out_stride,
+                  int32_t *status, void *stream) {
+  if (!desc) return BIA_ERR_INVALID_ARG;
+  bia_attn_desc d = *desc;
+  d.page_size = 1; // not used
+  int rc = check_desc(&d);
+  if (rc != BIA_OK) return rc;
+  bia::RopeArgs a{};
+  rc = rope_args(&d, rope, &a);
+  if (rc != BIA_OK) return rc;
+  if (total < 0 || (total > 0 && (!positions || (!q && !k) || (k == nullptr) != (k_out == nullptr))))
+    return BIA_ERR_INVALID_ARG;
+  rc = rope_rows(&a, &d, table, positions, q, k, nullptr, q_stride, k_stride, 0, q_weight,
+                 k_weight, total, q_out, k_out, q_out_stride, k_out_stride, status);
+  if (rc == BIA_OK) rc = rope_resident(a);
+  return rc == BIA_OK ? run_rope(a, static_cast<cudaStream_t>(stream)) : rc;
+}
+
+int bia_append_paged_kv_rope(const bia_attn_desc *desc, const bia_rope *rope,
+                             const float *table, const int32_t *positions, const void *q,
+                             const void *k_new, const void *v_new, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float *q_weight,
+                             const float *k_weight, void *k_cache, void *v_cache,
+                             int64_t num_pages, const int32_t *append_indptr,
+                             const int32_t *kv_indptr, const int32_t *kv_indices,
+                             const int32_t *kv_last_page_len, const int32_t *append_indptr_host,
+                             const int32_t *kv_indptr_host, const int32_t *kv_last_page_len_host,
+                             int32_t batch, void *q_out, int64_t q_out_stride, int32_t *status,
+                             void *stream) {
+  return append_rope(false, desc, rope, table, positions, q, k_new, v_new, q_stride, k_stride,
+                     v_stride, q_weight, k_weight, k_cache, v_cache, nullptr, nullptr, num_pages,
+                     append_indptr, kv_indptr, kv_indices, kv_last_page_len, append_indptr_host,
+                     kv_indptr_host, kv_last_page_len_host, batch, q_out, nullptr, q_out_stride, 0,
+                     status, stream);
+}
+
+int bia_append_paged_kv_fp8_rope(const bia_attn_desc *desc, const bia_rope *rope,
+                                 const float *table, const int32_t *positions, const void *q,
+                                 const void *k_new, const void *v_new, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const float *q_weight,
+                                 const float *k_weight, void *k_cache, void *v_cache,
+                                 void *k_scale, void *v_scale, int64_t num_pages,
+                                 const int32_t *append_indptr, const int32_t *kv_indptr,
+                                 const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                                 const int32_t *append_indptr_host,
+                                 const int32_t *kv_indptr_host,
+                                 const int32_t *kv_last_page_len_host, int32_t batch,
+                                 void *q_out, void *k_out, int64_t q_out_stride,
+                                 int64_t k_out_stride, int32_t *status, void *stream) {
+  return append_rope(true, desc, rope, table, positions, q, k_new, v_new, q_stride, k_stride,
+                     v_stride, q_weight, k_weight, k_cache, v_cache, k_scale, v_scale, num_pages,
+                     append_indptr, kv_indptr, kv_indices, kv_last_page_len, append_indptr_host,
+                     kv_indptr_host, kv_last_page_len_host, batch, q_out, k_out, q_out_stride,
+                     k_out_stride, status, stream);
+}
+
+} // extern "C"
+
+extern "C" {
+
+namespace {
 // Multi-head latent attention: validation and plan sizes as for the GQA
 // decode (qo_host == nullptr, one query per request) or a causal extend of
 // one-token q tiles (qo_host given), with one shared 512 + 64 wide latent

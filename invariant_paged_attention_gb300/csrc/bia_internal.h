@@ -18,6 +18,7 @@ namespace bia {
 constexpr int32_t kStatusBadPage = 1;     // a page index outside [0, num_pages)
 constexpr int32_t kStatusPlanMismatch = 2; // device plan disagreed with the host-sized launch
 constexpr int32_t kStatusTimeout = 4;      // a bounded device wait gave up
+constexpr int32_t kStatusBadPosition = 8;  // a rotary position outside the table
 
 constexpr int kTileRows = 128; // q tile rows (GQA-packed)
 constexpr int kKvBlock = 128;  // keys per block of the prefill inner loop
@@ -271,6 +272,28 @@ struct CacheFp8Args {
   int32_t *status; // may be NULL
 };
 
+// Norm and rotation of q and k heads, to rows or into pages (rope.cu).
+struct RopeArgs {
+  const uint16_t *q, *k, *v; // bf16 [total, heads, D], token strides below
+  int64_t q_stride, k_stride, v_stride;
+  uint16_t *q_out, *k_out; // rows; k_out may be NULL when the keys go to pages
+  int64_t q_out_stride, k_out_stride;
+  const float *q_weight, *k_weight; // [D] of the norms, or NULL
+  const float *table;               // [num_positions, rot]: cos, then sin
+  const int32_t *positions;         // [axes, total], or NULL: the key positions
+  int64_t total;
+  int32_t Hq, Hk, D, rot, interleaved, axes, num_positions; // Hq or Hk may be 0 (rows)
+  float eps, inv_D;
+  uint32_t freq_axis[8]; // two bits a frequency
+  // pages: bf16 caches, or codes and scales; all NULL for rows
+  uint16_t *k_cache, *v_cache;
+  uint8_t *k_codes, *v_codes, *k_scale, *v_scale;
+  const int32_t *row_indptr, *kv_indptr, *kv_indices, *kv_last_page_len;
+  int64_t num_pages;
+  int32_t batch, page_shift;
+  int32_t *status; // may be NULL
+};
+
 // One split-KV tile of one request of an 8-bit decode.
 struct UnitFp8 {
   int32_t b; // request; -1: retired
@@ -349,6 +372,7 @@ cudaError_t launch_decode_tc(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s); // head_dim 256
 cudaError_t launch_cache_fp8(const CacheFp8Args &a, bool append, cudaStream_t s);
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s);
 cudaError_t launch_plan_decode_fp8(const PlanArgs &p, UnitFp8 *units, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g1(const DecodeFp8Args &f, cudaStream_t s); // by group size
