@@ -99,6 +99,8 @@ extern "C" {
 /* Default fixed split-KV sizes ("sglang PR #10417", Modifications). */
 #define BIA_PREFILL_SPLIT 4096
 #define BIA_DECODE_SPLIT 2048
+/* Default split-KV size of the windowed decode. */
+#define BIA_WINDOW_DECODE_SPLIT 512
 /* Largest split-KV size of bia_prefill_ragged. */
 #define BIA_RAGGED_MAX_SPLIT 16777216
 /* Largest (and default) split-KV size of the 8-bit decode. */
@@ -574,6 +576,60 @@ BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
                                          const int32_t *qo_indptr_host,
                                          const int32_t *kv_indptr_host, int32_t batch,
                                          int32_t causal, int32_t split_size);
+
+/*
+ * Attention with a window and sinks: a query at position p of its sequence
+ * sees key j <= p if j > p - window or j < sinks, that is the last `window`
+ * keys up to its own and the first `sinks` keys of the sequence.  window >= 1,
+ * sinks >= 0 (else BIA_ERR_INVALID_ARG).  Page table, layouts, workspace,
+ * ownership and errors are those of the calls without a window; kv_len counts
+ * every key, and a page none of whose keys a query of the call sees is not
+ * read: its entry in kv_indices may hold anything (the page was given up).
+ *
+ * A request whose device index arrays break a rule of the call (or its
+ * bounds) gets NaN rows and sets bit 1 of the status word; the others are
+ * computed.  A request's bits depend on the request alone.
+ */
+
+/*
+ * bia_decode_paged with a window and sinks.  The keys that a query sees are
+ * taken as one list, the sinks first, cut into tiles of split_size keys (a
+ * multiple of 128; 0 = BIA_WINDOW_DECODE_SPLIT) whose states are merged in
+ * order; with a window of at least kv_len the bits are those of
+ * bia_decode_paged at the same split size.
+ */
+BIA_API int bia_decode_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
+                            const void *q, const void *k_cache, const void *v_cache,
+                            int64_t num_pages, const int32_t *kv_indptr,
+                            const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                            const int32_t *kv_indptr_host, const int32_t *kv_last_page_len_host,
+                            int32_t batch, int32_t split_size, void *workspace,
+                            size_t workspace_bytes, void *out, float *lse, void *stream);
+
+/* Workspace bytes bia_decode_paged_window needs for this call (0 on invalid input). */
+BIA_API size_t bia_decode_window_workspace_size(const bia_attn_desc *desc, int32_t window,
+                                        int32_t sinks, const int32_t *kv_indptr_host,
+                                        const int32_t *kv_last_page_len_host, int32_t batch,
+                                        int32_t split_size);
+
+/* bia_decode_paged_window sized from `bounds` (max_kv_len), as
+ * bia_decode_paged_bounded is: one captured graph replays while the device
+ * arrays change, with the bits of the exact call.  Workspace and launch follow
+ * min(max_kv_len, window + sinks), not max_kv_len. */
+BIA_API int bia_decode_paged_window_bounded(const bia_attn_desc *desc, const bia_bounds *bounds,
+                                    int32_t window, int32_t sinks, const void *q,
+                                    const void *k_cache, const void *v_cache, int64_t num_pages,
+                                    const int32_t *kv_indptr, const int32_t *kv_indices,
+                                    const int32_t *kv_last_page_len, int32_t batch,
+                                    int32_t split_size, void *workspace, size_t workspace_bytes,
+                                    void *out, float *lse, void *stream);
+
+/* Workspace bytes of every bounded windowed decode of `batch` requests within
+ * `bounds` (0 on invalid input). */
+BIA_API size_t bia_decode_window_bounded_workspace_size(const bia_attn_desc *desc,
+                                                const bia_bounds *bounds, int32_t window,
+                                                int32_t sinks, int32_t batch,
+                                                int32_t split_size);
 
 /*
  * Rotary positions, with the norm of each query and key head in the same pass:

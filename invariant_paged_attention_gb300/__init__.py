@@ -33,6 +33,7 @@ BIA_PREFILL_SPLIT = 4096
 BIA_RAGGED_MAX_SPLIT = 1 << 24
 BIA_DECODE_SPLIT = 2048
 BIA_DECODE_FP8_SPLIT = 1024
+BIA_WINDOW_DECODE_SPLIT = 512
 
 # every symbol include/bia.h exports
 EXPORTS = ("bia_prefill_paged", "bia_prefill_workspace_size", "bia_decode_paged",
@@ -47,7 +48,9 @@ EXPORTS = ("bia_prefill_paged", "bia_prefill_workspace_size", "bia_decode_paged"
            "bia_gather_paged_kv_fp8", "bia_decode_paged_fp8", "bia_decode_fp8_workspace_size",
            "bia_decode_paged_fp8_bounded", "bia_decode_fp8_bounded_workspace_size",
            "bia_prefill_ragged", "bia_prefill_ragged_workspace_size", "bia_norm_rope",
-           "bia_append_paged_kv_rope", "bia_append_paged_kv_fp8_rope")
+           "bia_append_paged_kv_rope", "bia_append_paged_kv_fp8_rope", "bia_decode_paged_window",
+           "bia_decode_window_workspace_size", "bia_decode_paged_window_bounded",
+           "bia_decode_window_bounded_workspace_size")
 
 
 class BiaError(RuntimeError):
@@ -174,6 +177,16 @@ def load(path: str = LIB_PATH):
     lib.bia_prefill_ragged.restype = ctypes.c_int
     lib.bia_prefill_ragged_workspace_size.argtypes = [dp, vp, vp, i32, i32, i32]
     lib.bia_prefill_ragged_workspace_size.restype = sz
+    lib.bia_decode_paged_window.argtypes = [dp, i32, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, i32,
+                                            i32, vp, sz, vp, vp, vp]
+    lib.bia_decode_paged_window.restype = ctypes.c_int
+    lib.bia_decode_window_workspace_size.argtypes = [dp, i32, i32, vp, vp, i32, i32]
+    lib.bia_decode_window_workspace_size.restype = sz
+    lib.bia_decode_paged_window_bounded.argtypes = [dp, bp, i32, i32, vp, vp, vp, i64, vp, vp, vp,
+                                                    i32, i32, vp, sz, vp, vp, vp]
+    lib.bia_decode_paged_window_bounded.restype = ctypes.c_int
+    lib.bia_decode_window_bounded_workspace_size.argtypes = [dp, bp, i32, i32, i32, i32]
+    lib.bia_decode_window_bounded_workspace_size.restype = sz
     rp = ctypes.POINTER(Rope)
     lib.bia_norm_rope.argtypes = [dp, rp, vp, vp, vp, vp, i64, i64, vp, vp, i64, vp, vp, i64, i64,
                                   vp, vp]
@@ -1083,3 +1096,87 @@ def bia_append_paged_kv_fp8_rope(desc, rope, table, q, k_new, v_new, k_cache, v_
                  append_indptr, kv_indptr, kv_indices, kv_last_page_len, append_indptr_host,
                  kv_indptr_host, kv_last_page_len_host, q_out, k_out, positions, q_weight,
                  k_weight, status, stream)
+
+
+# ---------------------------------------------------------------- window and sinks
+
+
+def _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
+                  out, lse, stream, batch, kvp=None, last=None, qo_indptr=None):
+    """The tensors of a windowed call of `batch` requests over the bf16 cache."""
+    at, ts = _index(q), None
+    more = () if qo_indptr is None else (qo_indptr,)
+    if not (stream is None and _dense(at, BF16, q, out, k_cache, v_cache) and
+            _dense(at, I32, kv_indptr, kv_indices, kv_last_page_len, *more) and
+            (lse is None or _dense(at, F32, lse)) and at >= 0 and
+            _index(workspace) == at == _current_device() and workspace.is_contiguous()):
+        ts = _check_types(("q", q, BF16), ("k_cache", k_cache, BF16), ("v_cache", v_cache, BF16),
+                          ("kv_indptr", kv_indptr, I32), ("kv_indices", kv_indices, I32),
+                          ("kv_last_page_len", kv_last_page_len, I32),
+                          ("workspace", workspace, None), ("out", out, BF16),
+                          ("lse", lse, F32, True), *(("qo_indptr", t, I32) for t in more))
+    rows = (k_cache.shape[0], desc.page_size, desc.num_kv_heads, desc.head_dim)
+    if k_cache.shape != rows or v_cache.shape != rows:
+        raise ValueError(f"k_cache and v_cache must be {rows} (num_pages, page_size, "
+                         f"num_kv_heads, head_dim) for this descriptor, got "
+                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    want = (q.shape[0], desc.num_qo_heads, desc.head_dim)
+    if q.shape != want or out.shape != want:
+        raise ValueError(f"q and out must be {want}, got {tuple(q.shape)} and {tuple(out.shape)}")
+    if lse is not None and lse.numel() != want[0] * want[1]:
+        raise ValueError(f"lse must hold {want[0]} x {want[1]} floats")
+    _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
+    if ts is not None:
+        _check_cuda(ts, stream)
+
+
+def bia_decode_window_workspace_size(desc, window, sinks, kv_indptr_host, kv_last_page_len_host,
+                                     split_size=0) -> int:
+    kvp, last = _host_i32(kv_indptr_host), _host_i32(kv_last_page_len_host)
+    return int(load().bia_decode_window_workspace_size(
+        ctypes.byref(desc), int(window), int(sinks), _ptr(kvp), _ptr(last), len(kvp) - 1,
+        int(split_size)))
+
+
+def bia_decode_paged_window(desc, window, sinks, q, k_cache, v_cache, kv_indptr, kv_indices,
+                            kv_last_page_len, kv_indptr_host, kv_last_page_len_host, workspace,
+                            out, lse=None, split_size=0, stream=None):
+    """bia_decode_paged where a query sees the last `window` keys and the first
+    `sinks` keys of its request (include/bia.h states the rule)."""
+    kvp, last = _host(kv_indptr_host), _host(kv_last_page_len_host)
+    batch = q.shape[0]
+    _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
+                  out, lse, stream, batch, kvp, last)
+    rc = load().bia_decode_paged_window(
+        ctypes.byref(desc), int(window), int(sinks), q.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), k_cache.shape[0], kv_indptr.data_ptr(), kv_indices.data_ptr(),
+        kv_last_page_len.data_ptr(), kvp.data_ptr(), last.data_ptr(), batch, int(split_size),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
+        _at(lse), _handle(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_decode_paged_window")
+
+
+def bia_decode_window_bounded_workspace_size(desc, bounds, window, sinks, batch,
+                                             split_size=0) -> int:
+    return int(load().bia_decode_window_bounded_workspace_size(
+        ctypes.byref(desc), ctypes.byref(bounds), int(window), int(sinks), int(batch),
+        int(split_size)))
+
+
+def bia_decode_paged_window_bounded(desc, bounds, window, sinks, q, k_cache, v_cache, kv_indptr,
+                                    kv_indices, kv_last_page_len, workspace, out, lse=None,
+                                    split_size=0, stream=None):
+    """bia_decode_paged_window sized from `bounds` (max_kv_len): the index arrays
+    are read on the device only, so a captured decode replays step after step."""
+    batch = q.shape[0]
+    _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
+                  out, lse, stream, batch)
+    rc = load().bia_decode_paged_window_bounded(
+        ctypes.byref(desc), ctypes.byref(bounds), int(window), int(sinks), q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_last_page_len.data_ptr(), batch, int(split_size),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
+        _at(lse), _handle(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_decode_paged_window_bounded")

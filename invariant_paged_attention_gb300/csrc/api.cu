@@ -1359,6 +1359,190 @@ size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc, const int32_
 extern "C" {
 
 namespace {
+// Attention with a window and sinks.  Keys of the longest list that a query of
+// a sequence of up to kv_len keys sees.
+int64_t window_len(int64_t kv_len, int32_t window, int32_t sinks) {
+  const int64_t behind = std::max<int64_t>(0, kv_len - window);
+  return kv_len - behind + std::min<int64_t>(sinks, behind);
+}
+
+// A windowed decode: the longest request, the split tiles a request may have,
+// and where its states and status words lie.
+struct WindowDecodePlan {
+  int64_t max_kv_len = 0;
+  int32_t parts = 0, split = 0;
+  WsLayout w; // group_off: the status words of the CTAs
+};
+
+int window_decode_plan(const bia_attn_desc *desc, const bia_bounds *bounds, int32_t window,
+                       int32_t sinks, const int32_t *kvp_host, const int32_t *last_host,
+                       int32_t batch, int32_t split, WindowDecodePlan *p) {
+  int rc = check_desc(desc);
+  if (rc != BIA_OK) return rc;
+  if (window < 1 || sinks < 0 || batch <= 0) return BIA_ERR_INVALID_ARG;
+  if (split == 0) split = BIA_WINDOW_DECODE_SPLIT;
+  if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
+  if (bounds) {
+    if (bounds->max_kv_len < 1) return BIA_ERR_INVALID_ARG;
+    p->max_kv_len = bounds->max_kv_len;
+  } else {
+    if (!kvp_host || !last_host || kvp_host[0] < 0) return BIA_ERR_INVALID_ARG;
+    for (int b = 0; b < batch; ++b) {
+      const int64_t pages = static_cast<int64_t>(kvp_host[b + 1]) - kvp_host[b];
+      const int32_t last = last_host[b];
+      if (pages <= 0 || last < 1 || last > desc->page_size) return BIA_ERR_INVALID_ARG;
+      p->max_kv_len = std::max(p->max_kv_len, (pages - 1) * desc->page_size + last);
+    }
+  }
+  if (p->max_kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
+  p->split = split;
+  p->parts = static_cast<int32_t>((window_len(p->max_kv_len, window, sinks) + split - 1) / split);
+  const int64_t units = static_cast<int64_t>(batch) * p->parts;
+  const int64_t items = units * desc->num_kv_heads;
+  if (items > INT32_MAX) return BIA_ERR_UNSUPPORTED;
+  // the tensor-core kernel has a CTA per SM at most, the others one per item
+  const int64_t ctas = desc->head_dim == 128 ? std::min<int64_t>(items, 1024) : items;
+  p->w = bia::make_layout(0, 0, 0, 0, 0, desc->num_qo_heads, desc->head_dim);
+  p->w.part_o = bia::align_up(p->w.group_off + sizeof(int32_t) * static_cast<size_t>(ctas), 256);
+  const size_t rows = p->parts > 1 ? static_cast<size_t>(units) * desc->num_qo_heads : 0;
+  p->w.part_lse = bia::align_up(p->w.part_o + rows * desc->head_dim * sizeof(float), 256);
+  p->w.total = bia::align_up(p->w.part_lse + rows * sizeof(float), 256);
+  return BIA_OK;
+}
+
+int run_window_decode(const bia_attn_desc *desc, const bia_bounds *bounds, int32_t window,
+                      int32_t sinks, const void *q, const void *k_cache, const void *v_cache,
+                      int64_t num_pages, const int32_t *kv_indptr, const int32_t *kv_indices,
+                      const int32_t *kv_last_page_len, const int32_t *kvp_host,
+                      const int32_t *last_host, int32_t batch, int32_t split, void *workspace,
+                      size_t workspace_bytes, void *out, float *lse, void *stream) {
+  WindowDecodePlan p;
+  int rc = window_decode_plan(desc, bounds, window, sinks, kvp_host, last_host, batch, split, &p);
+  if (rc != BIA_OK) return rc;
+  if (!q || !k_cache || !v_cache || !kv_indptr || !kv_indices || !kv_last_page_len || !out ||
+      !workspace || num_pages <= 0)
+    return BIA_ERR_INVALID_ARG;
+  if (misaligned(workspace, 256) || misaligned(q, 16) || misaligned(k_cache, 16) ||
+      misaligned(v_cache, 16) || misaligned(out, 16) || misaligned(lse, 4) ||
+      misaligned(kv_indptr, 4) || misaligned(kv_indices, 4) || misaligned(kv_last_page_len, 4))
+    return BIA_ERR_INVALID_ARG;
+  if (workspace_bytes < p.w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
+  rc = check_resident({{"q", q},
+                       {"k_cache", k_cache},
+                       {"v_cache", v_cache},
+                       {"out", out},
+                       {"lse", lse},
+                       {"kv_indptr", kv_indptr},
+                       {"kv_indices", kv_indices},
+                       {"kv_last_page_len", kv_last_page_len},
+                       {"workspace", workspace}});
+  if (rc != BIA_OK) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  AttnArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k_cache = static_cast<const uint16_t *>(k_cache);
+  a.v_cache = static_cast<const uint16_t *>(v_cache);
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.kv_last_page_len = kv_last_page_len;
+  a.num_pages = num_pages;
+  a.Hq = desc->num_qo_heads;
+  a.Hkv = desc->num_kv_heads;
+  a.D = desc->head_dim;
+  a.G = a.Hq / a.Hkv;
+  a.page_shift = log2i(desc->page_size);
+  a.causal = 1;
+  a.split = p.split;
+  a.tile_tokens = 1;
+  a.scale_log2 = effective_scale(desc);
+  a.batch = batch;
+  a.parts = p.parts;
+  a.n_units = static_cast<int64_t>(batch) * p.parts;
+  a.window = window;
+  a.sinks = sinks;
+  a.max_kv_len = static_cast<int32_t>(p.max_kv_len);
+  a.status = reinterpret_cast<int32_t *>(ws + p.w.status);
+  a.slots = reinterpret_cast<int32_t *>(ws + p.w.group_off);
+  a.part_o = reinterpret_cast<float *>(ws + p.w.part_o);
+  a.part_lse = reinterpret_cast<float *>(ws + p.w.part_lse);
+  a.total_rows = batch;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  int64_t ctas = 0;
+  cudaError_t e = bia::window_decode_ctas(a, &ctas);
+  if (e != cudaSuccess) return cuda_fail("device size", e);
+  const bool profile = g_attn_begin != nullptr && g_attn_end != nullptr;
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_begin, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  e = bia::launch_decode(a, st);
+  if (e != cudaSuccess) return cuda_fail("decode kernel launch", e);
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_end, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  e = bia::launch_merge_window_decode(a, static_cast<int>(ctas), st);
+  if (e != cudaSuccess) return cuda_fail("merge kernel launch", e);
+  __atomic_add_fetch(&g_launches, 2ull, __ATOMIC_RELAXED);
+  return BIA_OK;
+}
+} // namespace
+
+int bia_decode_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
+                            const void *q, const void *k_cache, const void *v_cache,
+                            int64_t num_pages, const int32_t *kv_indptr,
+                            const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                            const int32_t *kv_indptr_host, const int32_t *kv_last_page_len_host,
+                            int32_t batch, int32_t split_size, void *workspace,
+                            size_t workspace_bytes, void *out, float *lse, void *stream) {
+  return run_window_decode(desc, nullptr, window, sinks, q, k_cache, v_cache, num_pages,
+                           kv_indptr, kv_indices, kv_last_page_len, kv_indptr_host,
+                           kv_last_page_len_host, batch, split_size, workspace, workspace_bytes,
+                           out, lse, stream);
+}
+
+size_t bia_decode_window_workspace_size(const bia_attn_desc *desc, int32_t window, int32_t sinks,
+                                        const int32_t *kv_indptr_host,
+                                        const int32_t *kv_last_page_len_host, int32_t batch,
+                                        int32_t split_size) {
+  WindowDecodePlan p;
+  return window_decode_plan(desc, nullptr, window, sinks, kv_indptr_host, kv_last_page_len_host,
+                            batch, split_size, &p) == BIA_OK
+             ? p.w.total
+             : 0;
+}
+
+int bia_decode_paged_window_bounded(const bia_attn_desc *desc, const bia_bounds *bounds,
+                                    int32_t window, int32_t sinks, const void *q,
+                                    const void *k_cache, const void *v_cache, int64_t num_pages,
+                                    const int32_t *kv_indptr, const int32_t *kv_indices,
+                                    const int32_t *kv_last_page_len, int32_t batch,
+                                    int32_t split_size, void *workspace, size_t workspace_bytes,
+                                    void *out, float *lse, void *stream) {
+  if (!bounds) return BIA_ERR_INVALID_ARG;
+  return run_window_decode(desc, bounds, window, sinks, q, k_cache, v_cache, num_pages, kv_indptr,
+                           kv_indices, kv_last_page_len, nullptr, nullptr, batch, split_size,
+                           workspace, workspace_bytes, out, lse, stream);
+}
+
+size_t bia_decode_window_bounded_workspace_size(const bia_attn_desc *desc,
+                                                const bia_bounds *bounds, int32_t window,
+                                                int32_t sinks, int32_t batch,
+                                                int32_t split_size) {
+  WindowDecodePlan p;
+  return bounds && window_decode_plan(desc, bounds, window, sinks, nullptr, nullptr, batch,
+                                      split_size, &p) == BIA_OK
+             ? p.w.total
+             : 0;
+}
+
+} // extern "C"
+
+extern "C" {
+
+namespace {
 // The rotation of a call: its table, and which axis each frequency follows.
 int rope_args(const bia_attn_desc *desc, const bia_rope *rope, bia::RopeArgs *a) {
   if (!rope) return BIA_ERR_INVALID_ARG;

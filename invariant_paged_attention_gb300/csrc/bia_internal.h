@@ -245,7 +245,36 @@ struct AttnArgs {
   const uint32_t *mask;
   const int64_t *mask_indptr;
   int64_t mask_words;
+  // attention with a window and sinks (window > 0): no plan; the kernels find
+  // a request's keys in these arrays
+  int32_t window, sinks, parts; // parts: split tiles a request may have
+  const int32_t *kv_indptr, *kv_last_page_len;
+  int32_t max_kv_len; // of any request
+  int32_t *slots;     // decode: a status word per CTA, joined by the merge
 };
+
+// The keys that the one query of a windowed decode sees, as a list of its own:
+// entry i is key i below `sunk` and key i + skip from there on (the sinks that
+// the window has left behind, then the window).
+struct WindowKeys {
+  int32_t page_base, len, sunk, skip;
+  bool ok; // the request's arrays keep the rules of the call
+};
+#ifdef __CUDACC__
+__device__ __forceinline__ WindowKeys window_keys(const AttnArgs &a, int b) {
+  WindowKeys k;
+  const int32_t p0 = __ldg(a.kv_indptr + b), p1 = __ldg(a.kv_indptr + b + 1);
+  const int32_t last = __ldg(a.kv_last_page_len + b);
+  const int64_t n = ((static_cast<int64_t>(p1) - p0 - 1) << a.page_shift) + last;
+  k.ok = p0 >= 0 && p1 > p0 && last >= 1 && last <= (1 << a.page_shift) && n <= a.max_kv_len;
+  const int32_t lo = k.ok ? max(0, static_cast<int32_t>(n) - a.window) : 0;
+  k.page_base = p0;
+  k.sunk = min(a.sinks, lo);
+  k.skip = lo - k.sunk;
+  k.len = k.ok ? static_cast<int32_t>(n) - k.skip : 0;
+  return k;
+}
+#endif
 
 // Paged-KV append: new token t of request b goes to position
 // kv_len(b) - n_new(b) + (t - append_indptr[b]).
@@ -365,6 +394,8 @@ inline cudaLaunchAttribute chained_launch_attr() {
 cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s);
 cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s);
+// CTAs of a windowed decode (its status words).
+cudaError_t window_decode_ctas(const AttnArgs &a, int64_t *ctas);
 // The tensor-core decode (head_dim 128, G in {1, 2, 4, 8}); launch_decode
 // takes it whenever it applies.
 bool decode_tc_supported(const AttnArgs &a);
@@ -373,6 +404,8 @@ cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s); // head_dim 256
 cudaError_t launch_cache_fp8(const CacheFp8Args &a, bool append, cudaStream_t s);
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s);
+// Joins the states of a windowed decode's split tiles and its status words.
+cudaError_t launch_merge_window_decode(const AttnArgs &a, int n_slots, cudaStream_t s);
 cudaError_t launch_plan_decode_fp8(const PlanArgs &p, UnitFp8 *units, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeFp8Args &f, cudaStream_t s);
 cudaError_t launch_decode_fp8_g1(const DecodeFp8Args &f, cudaStream_t s); // by group size

@@ -27,6 +27,9 @@
 // also needs its mask bit (a masked key is skipped exactly like a key past
 // the end, so a mask that hides nothing visible gives the unmasked bits).
 //
+// With a window and sinks (WIN) the keys are the list that the query sees
+// (window_keys), cut into split tiles; such a call has no plan.
+//
 // The fixed split of 2048 keys per tile and the merge of the tiles' partials
 // follow "sglang PR #10417 [POC] Support deterministic inference",
 // Modifications (split-KV fixed to 2048 for decode).
@@ -111,7 +114,7 @@ __device__ __forceinline__ float reduce_scatter4(const float (&s)[4]) {
   return c;
 }
 
-template <int D, int G, bool MASK>
+template <int D, int G, bool MASK, bool WIN>
 __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
     decode_kernel(const AttnArgs a) {
   using L = DecSmem<D>;
@@ -139,9 +142,30 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   const int64_t unit = blockIdx.x / a.Hkv;
   const int kvh = static_cast<int>(blockIdx.x - unit * a.Hkv);
   if (unit >= a.n_units) return;
-  const Unit u = a.units[unit];
-  if (u.b < 0) return;
-  const ReqInfo r = a.reqs[u.b];
+  int32_t *const status = WIN ? a.slots + blockIdx.x : a.status;
+  WindowKeys wk{};
+  Unit u;
+  ReqInfo r;
+  if constexpr (WIN) {
+    const int32_t b = static_cast<int32_t>(unit / a.parts);
+    wk = window_keys(a, b);
+    u = Unit{b, 0, static_cast<int32_t>(unit - static_cast<int64_t>(b) * a.parts), 1};
+    r = ReqInfo{b, 1, wk.len, a.parts, static_cast<int64_t>(b) * a.parts, wk.page_base, 0};
+    if (threadIdx.x == 0) *status = wk.ok ? 0 : kStatusPlanMismatch;
+    if (!wk.ok && u.split == 0) { // a request that breaks a rule: NaN, once
+      const int64_t head0 = static_cast<int64_t>(b) * a.Hq + kvh * G;
+      for (int e = threadIdx.x; e < G * a.D; e += kThreadsDec) a.out[head0 * a.D + e] = 0x7fc0u;
+      if (a.lse && threadIdx.x < G) a.lse[head0 + threadIdx.x] = __int_as_float(0x7fc00000);
+    }
+    if (u.split * static_cast<int64_t>(a.split) >= wk.len) return;
+    __syncthreads(); // the status word is clear
+  } else {
+    u = a.units[unit];
+    if (u.b < 0) return;
+    r = a.reqs[u.b];
+  }
+  // the key of entry `i` of the request's list
+  auto key_of = [&](int32_t i) { return WIN && i >= wk.sunk ? i + wk.skip : i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane / LPK, sub = lane % LPK;
   // the query: token t of the request (0 for decode); it sees keys < q_end
@@ -181,7 +205,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   auto page_of = [&](int i) -> int32_t { // page index of this lane's key in chunk i
     const int32_t key = key_begin + (warp + kWarps * i) * kChunk + kl_ld;
     if (lane >= 16 || i >= my_chunks || key >= key_end) return -1;
-    return __ldg(a.kv_indices + r.page_base + (key >> a.page_shift));
+    return __ldg(a.kv_indices + r.page_base + (key_of(key) >> a.page_shift));
   };
   int32_t pg_next = page_of(0);
   auto issue = [&](int i) {
@@ -191,7 +215,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
     const int32_t key = key_begin + (warp + kWarps * i) * kChunk + kl_ld;
     bool ok = lane < 16 && key < key_end;
     if (ok && (pg < 0 || pg >= a.num_pages)) {
-      atomicOr(a.status, kStatusBadPage);
+      atomicOr(status, kStatusBadPage);
       ok = false;
     }
     const uint32_t dst = (lane < 8 ? sK(st) : sV(st)) + kl_ld * L::kRow;
@@ -206,7 +230,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
     __syncwarp();
     if (ok) {
       const int64_t off =
-          (((static_cast<int64_t>(pg) << a.page_shift) + (key & page_mask)) * a.Hkv + kvh) * Dr;
+          (((static_cast<int64_t>(pg) << a.page_shift) + (key_of(key) & page_mask)) * a.Hkv + kvh) * Dr;
       bulk_g2s(dst, (lane < 8 ? a.k_cache : a.v_cache) + off, row_copy, bar(st));
     }
   };
@@ -240,7 +264,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   bool failed = false;
   for (int i = 0; i < my_chunks; ++i) {
     const int st = i % NS;
-    if (!mbar_wait(bar(st), (i / NS) & 1, a.status)) {
+    if (!mbar_wait(bar(st), (i / NS) & 1, status)) {
       failed = true;
       break;
     }
@@ -469,11 +493,11 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   }
 }
 
-template <int D, int G, bool MASK>
+template <int D, int G, bool MASK, bool WIN = false>
 cudaError_t launch_decode_dgm(const AttnArgs &a, cudaStream_t s) {
   using L = DecSmem<D>;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(decode_kernel<D, G, MASK>),
+  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(decode_kernel<D, G, MASK, WIN>),
                                        L::kAlloc, ready);
   if (e != cudaSuccess) return e;
   const int64_t blocks = a.n_units * a.Hkv;
@@ -486,11 +510,12 @@ cudaError_t launch_decode_dgm(const AttnArgs &a, cudaStream_t s) {
   cudaLaunchAttribute attr[1] = {chained_launch_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<D, G, MASK>, a);
+  return cudaLaunchKernelEx(&cfg, decode_kernel<D, G, MASK, WIN>, a);
 }
 
 template <int D, int G>
 cudaError_t launch_decode_dg(const AttnArgs &a, cudaStream_t s) {
+  if (a.window) return launch_decode_dgm<D, G, false, true>(a, s);
   return a.mask ? launch_decode_dgm<D, G, true>(a, s) : launch_decode_dgm<D, G, false>(a, s);
 }
 
@@ -506,6 +531,14 @@ cudaError_t launch_decode_d(const AttnArgs &a, cudaStream_t s) {
 }
 
 } // namespace
+
+cudaError_t window_decode_ctas(const AttnArgs &a, int64_t *ctas) {
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  const int64_t items = a.n_units * a.Hkv;
+  *ctas = decode_tc_supported(a) && items > sms ? sms : items;
+  return e;
+}
 
 cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
   if (a.n_units == 0) return cudaSuccess;

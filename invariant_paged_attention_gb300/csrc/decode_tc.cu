@@ -39,6 +39,11 @@
 // (keys past the split, masked-off tails and bad pages are zero-filled; each
 // copy group ends with an arrival that fires when the thread's copies land).
 //
+// With a window and sinks (WIN) a request's keys are the list that it sees
+// (window_keys): the first sinks, then the window; the split tiles cut that
+// list, so nothing outside it is read.  Such a call has no plan: every role
+// finds an item's keys in the index arrays, and the items go round the CTAs.
+//
 // Also runs the single-token q tiles a prefill call streams (with the
 // prefill split size), with or without a custom mask: a masked key is left
 // out of the softmax like a key past the end.
@@ -128,12 +133,35 @@ struct TcItem {
   int32_t q_end;      // keys < q_end are visible
   int32_t key_begin, key_end;
   int nb;             // 128-key blocks
+  int32_t sunk, skip; // WIN: entry i is key i, from sunk on i + skip
+  bool bad;           // WIN: the request breaks a rule of the call
 };
 
+template <bool WIN>
 __device__ __forceinline__ TcItem tc_item(const AttnArgs &a, int64_t w) {
   TcItem it;
   const int64_t unit = w / a.Hkv;
   it.kvh = static_cast<int>(w - unit * a.Hkv);
+  if constexpr (WIN) {
+    const int32_t b = static_cast<int32_t>(unit / a.parts);
+    const WindowKeys k = window_keys(a, b);
+    it.u = Unit{b, 0, static_cast<int32_t>(unit - static_cast<int64_t>(b) * a.parts), 1};
+    it.bad = !k.ok;
+    it.sunk = k.sunk;
+    it.skip = k.skip;
+    it.t = 0;
+    it.r.q_start = b;
+    it.r.q_len = 1;
+    it.r.kv_len = it.q_end = k.len;
+    it.r.nsp = a.parts;
+    it.r.rowbase = static_cast<int64_t>(b) * a.parts;
+    it.r.page_base = k.page_base;
+    it.key_begin = it.u.split * a.split;
+    it.key_end = min(it.key_begin + a.split, k.len);
+    it.live = it.key_begin < k.len;
+    it.nb = it.live ? (it.key_end - it.key_begin + kKeysT - 1) / kKeysT : 0;
+    return it;
+  }
   it.u = a.units[unit];
   it.live = it.u.b >= 0;
   it.nb = 0;
@@ -147,7 +175,7 @@ __device__ __forceinline__ TcItem tc_item(const AttnArgs &a, int64_t w) {
   return it;
 }
 
-template <int G, bool MASK>
+template <int G, bool MASK, bool WIN>
 __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
     decode_tc_kernel(const __grid_constant__ AttnArgs a) {
   using L = DecTcSmem;
@@ -175,9 +203,11 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
   grid_dep_launch(); // the next kernel of the call may start launching
   const int64_t n_work = a.n_units * a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t *const status = WIN ? a.slots + blockIdx.x : a.status;
 
   if (warp == kMmaWarpTc) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   if (tid == 0) {
+    if constexpr (WIN) *status = 0; // before the barrier below
     for (int s = 0; s < kKStagesT; ++s) {
       mbar_init(bar(L::bKFull + s), kProdThreadsT); // one arrival per copy thread
       mbar_init(bar(L::bKEmpty + s), 1);
@@ -214,7 +244,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
   auto read_item = [&](uint32_t k, bool single) -> int64_t {
     const int s = static_cast<int>(k & 3u);
     int64_t w = -1;
-    if (mbar_wait(bar(L::bItemFull + s), (k >> 2) & 1u, a.status)) w = items[s];
+    if (mbar_wait(bar(L::bItemFull + s), (k >> 2) & 1u, status)) w = items[s];
     if (!single) __syncwarp();
     if (single || lane == 0) mbar_arrive(bar(L::bItemEmpty + s));
     return w;
@@ -246,9 +276,10 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       if (!fetcher || posted) return;
       posted = true;
       int64_t nw = static_cast<int64_t>(gridDim.x) + taken;
+      if constexpr (WIN) nw = static_cast<int64_t>(blockIdx.x) + (k + 1) * static_cast<int64_t>(gridDim.x);
       if (nw >= n_work) nw = -1;
       const uint32_t kn = k + 1;
-      if (kn >= 4 && !mbar_wait(bar(L::bItemEmpty + (kn & 3u)), ((kn >> 2) - 1) & 1u, a.status))
+      if (kn >= 4 && !mbar_wait(bar(L::bItemEmpty + (kn & 3u)), ((kn >> 2) - 1) & 1u, status))
         nw = -1;
       items[kn & 3u] = nw;
       mbar_arrive(bar(L::bItemFull + (kn & 3u)));
@@ -256,15 +287,20 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
     for (uint32_t k = 0; ok; ++k) {
       const int64_t w = read_item(k, false);
       if (w < 0) break;
-      if (fetcher) taken = atomicAdd(a.status + kStatusWorkCounter, 1);
+      if constexpr (!WIN)
+        if (fetcher) taken = atomicAdd(a.status + kStatusWorkCounter, 1);
       posted = false;
-      const TcItem it = tc_item(a, w);
+      const TcItem it = tc_item<WIN>(a, w);
       if (!it.live) {
+        if constexpr (WIN)
+          if (fetcher && it.bad) atomicOr(status, kStatusPlanMismatch);
         post_next(k);
         continue;
       }
+      // the key of entry `i` of the request's list
+      auto key_of = [&](int32_t i) { return WIN && i >= it.sunk ? i + it.skip : i; };
       // q rows of the item's G heads (rows G..15 zero) into q buffer ig % 2
-      if (ig >= 2 && !mbar_wait(bar(L::bQEmpty + (ig & 1)), ((ig >> 1) - 1) & 1, a.status)) {
+      if (ig >= 2 && !mbar_wait(bar(L::bQEmpty + (ig & 1)), ((ig >> 1) - 1) & 1, status)) {
         ok = false;
         break;
       }
@@ -295,7 +331,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
               valid = (__ldg(a.mask + (bit >> 5)) >> (bit & 31)) & 1u;
             }
           }
-          pg[n] = valid ? __ldg(a.kv_indices + it.r.page_base + (key >> a.page_shift)) : -1;
+          pg[n] = valid ? __ldg(a.kv_indices + it.r.page_base + (key_of(key) >> a.page_shift)) : -1;
           vis |= static_cast<uint32_t>(valid) << n;
         }
       };
@@ -315,10 +351,10 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
           const int32_t key = it.key_begin + j * kKeysT + kb + kKeyStepT * n;
           bool valid = (vis >> n) & 1u;
           if (valid && (pg[n] < 0 || pg[n] >= a.num_pages)) {
-            atomicOr(a.status, kStatusBadPage);
+            atomicOr(status, kStatusBadPage);
             valid = false;
           }
-          row[n] = valid ? ((static_cast<int64_t>(pg[n]) << a.page_shift) + (key & page_mask)) *
+          row[n] = valid ? ((static_cast<int64_t>(pg[n]) << a.page_shift) + (key_of(key) & page_mask)) *
                                    a.Hkv + it.kvh
                          : 0;
           okeys |= static_cast<uint32_t>(valid) << n;
@@ -330,7 +366,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
           const int s = static_cast<int>(jg % ns);
           const int eb = (kv == 0 ? L::bKEmpty : L::bVEmpty) + s;
           if (jg >= static_cast<uint32_t>(ns) &&
-              !mbar_wait(bar(eb), ((jg / ns) - 1) & 1, a.status)) {
+              !mbar_wait(bar(eb), ((jg / ns) - 1) & 1, status)) {
             ok = false;
             break;
           }
@@ -359,7 +395,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       bool ok = true;
       auto issue_s = [&](uint32_t j_glob, uint32_t qb) {
         const int s = static_cast<int>(j_glob % kKStagesT);
-        ok = mbar_wait(bar(L::bKFull + s), (j_glob / kKStagesT) & 1, a.status);
+        ok = mbar_wait(bar(L::bKFull + s), (j_glob / kKStagesT) & 1, status);
         if (!ok) return;
         fence_proxy_async(); // the rows were written by cp.async (generic proxy)
         tc_fence_after();
@@ -376,15 +412,15 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       for (uint32_t k = 0; ok; ++k) {
         const int64_t w = read_item(k, true);
         if (w < 0) break;
-        const TcItem it = tc_item(a, w);
+        const TcItem it = tc_item<WIN>(a, w);
         if (!it.live) continue;
         const uint32_t qb = qbuf(ig & 1);
-        ok = mbar_wait(bar(L::bQFull + (ig & 1)), (ig >> 1) & 1, a.status);
+        ok = mbar_wait(bar(L::bQFull + (ig & 1)), (ig >> 1) & 1, status);
         if (!ok) break;
         fence_proxy_async();
         // the item's O buffer is free once the epilogue of item ig-2 read it
         if (ig >= 2) {
-          ok = mbar_wait(bar(L::bOFree + (ig & 1)), ((ig >> 1) - 1) & 1, a.status);
+          ok = mbar_wait(bar(L::bOFree + (ig & 1)), ((ig >> 1) - 1) & 1, status);
           if (!ok) break;
         }
         const uint32_t j0 = jg;
@@ -392,8 +428,8 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
         for (int j = 0; j < it.nb && ok; ++j) {
           const uint32_t jj = j0 + j;
           const int s = static_cast<int>(jj % kVStagesT);
-          ok = mbar_wait(bar(L::bVFull + s), (jj / kVStagesT) & 1, a.status);
-          if (ok) ok = mbar_wait(bar(L::bPFull + (jj & 1)), (jj >> 1) & 1, a.status);
+          ok = mbar_wait(bar(L::bVFull + s), (jj / kVStagesT) & 1, status);
+          if (ok) ok = mbar_wait(bar(L::bPFull + (jj & 1)), (jj >> 1) & 1, status);
           if (!ok) break;
           fence_proxy_async();
           tc_fence_after();
@@ -431,8 +467,17 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       const int64_t w = read_item(k, false);
       // the four warps share named barriers: they stop together
       if (bar_any_named(1, 128, w < 0)) break;
-      const TcItem it = tc_item(a, w);
-      if (!it.live) continue;
+      const TcItem it = tc_item<WIN>(a, w);
+      if (!it.live) {
+        if constexpr (WIN) { // a request that breaks a rule: NaN, once
+          if (it.bad && it.u.split == 0) {
+            const int64_t head0 = static_cast<int64_t>(it.u.b) * a.Hq + it.kvh * G;
+            for (int e = t; e < G * kDT; e += 128) a.out[head0 * kDT + e] = 0x7fc0u;
+            if (a.lse && t < G) a.lse[head0 + t] = __int_as_float(0x7fc00000);
+          }
+        }
+        continue;
+      }
       float m[G], l[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -443,7 +488,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
           MASK ? a.mask_indptr[it.u.b] + static_cast<int64_t>(it.t) * it.r.kv_len : 0;
       bool bad = false; // this thread's wait ran out
       for (int j = 0; j < it.nb; ++j, ++jg) {
-        bad = bad || !mbar_wait(bar(L::bSFull + (jg & 1)), (jg >> 1) & 1, a.status);
+        bad = bad || !mbar_wait(bar(L::bSFull + (jg & 1)), (jg >> 1) & 1, status);
         tc_fence_after();
         uint32_t v[NL];
         if (!bad) {
@@ -506,10 +551,10 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
         // P buffer jg % 2 is free once P.V(jg-2) is done; O may be rescaled
         // once P.V(jg-1) is done
         if (jg >= 2)
-          bad = bad || !mbar_wait(bar(L::bPVDone + (jg & 1)), ((jg >> 1) - 1) & 1, a.status);
+          bad = bad || !mbar_wait(bar(L::bPVDone + (jg & 1)), ((jg >> 1) - 1) & 1, status);
         if (j > 0 && up != 0) {
           bad = bad ||
-                !mbar_wait(bar(L::bPVDone + ((jg - 1) & 1)), ((jg - 1) >> 1) & 1, a.status);
+                !mbar_wait(bar(L::bPVDone + ((jg - 1) & 1)), ((jg - 1) >> 1) & 1, status);
           tc_fence_after();
           if (!bad) {
             uint32_t o[NL];
@@ -544,7 +589,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       // then the 4 warps in order); o = O^T / l; lse = (m + log2 l) ln 2
       if (it.nb > 0) {
         const uint32_t jl = jg - 1; // the item's last block
-        bad = bad || !mbar_wait(bar(L::bPVDone + (jl & 1)), (jl >> 1) & 1, a.status);
+        bad = bad || !mbar_wait(bar(L::bPVDone + (jl & 1)), (jl >> 1) & 1, status);
       }
       tc_fence_after();
 #pragma unroll
@@ -616,11 +661,11 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
   }
 }
 
-template <int G, bool MASK>
+template <int G, bool MASK, bool WIN = false>
 cudaError_t launch_tc(const AttnArgs &a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   int sms = 0;
-  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(decode_tc_kernel<G, MASK>),
+  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(decode_tc_kernel<G, MASK, WIN>),
                                        DecTcSmem::kAlloc, ready, &sms);
   if (e != cudaSuccess) return e;
   const int64_t work = a.n_units * a.Hkv;
@@ -632,11 +677,12 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t s) {
   cudaLaunchAttribute attr[1] = {chained_launch_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<G, MASK>, a);
+  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<G, MASK, WIN>, a);
 }
 
 template <int G>
 cudaError_t launch_tc_g(const AttnArgs &a, cudaStream_t s) {
+  if (a.window) return launch_tc<G, false, true>(a, s);
   return a.mask ? launch_tc<G, true>(a, s) : launch_tc<G, false>(a, s);
 }
 
