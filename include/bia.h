@@ -585,18 +585,46 @@ BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
  * ownership and errors are those of the calls without a window; kv_len counts
  * every key, and a page none of whose keys a query of the call sees is not
  * read: its entry in kv_indices may hold anything (the page was given up).
- *
- * A request whose device index arrays break a rule of the call (or its
- * bounds) gets NaN rows and sets bit 1 of the status word; the others are
- * computed.  A request's bits depend on the request alone.
  */
+
+/*
+ * bia_prefill_paged, causal, with a window and sinks: q tiles, split tiles
+ * (anchored at key 0; the sinks count to a q tile's first) and merge are the
+ * same, and a request's bits depend on the request alone, also when it is cut
+ * into chunks that start on the 128-row q-tile grid.  A non-finite key or value
+ * may reach every row of a q tile that sees its block of 128 keys; keys before
+ * the window of the first row of a pair of q tiles, and past the request's
+ * last key, are not read.  split_size: a multiple of 128, 0 =
+ * BIA_PREFILL_SPLIT; with few q tiles a smaller one spreads a long window over
+ * more of the GPU.  Weights lag the running maximum by up to 2^16 before they
+ * are divided by their sum, in fp32: values above 2^80 may overflow.
+ */
+BIA_API int bia_prefill_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
+                             const void *q, const void *k_cache, const void *v_cache,
+                             int64_t num_pages, const int32_t *qo_indptr,
+                             const int32_t *kv_indptr, const int32_t *kv_indices,
+                             const int32_t *kv_last_page_len, const int32_t *qo_indptr_host,
+                             const int32_t *kv_indptr_host, const int32_t *kv_last_page_len_host,
+                             int32_t batch, int32_t split_size, void *workspace,
+                             size_t workspace_bytes, void *out, float *lse, void *stream);
+
+/* Workspace bytes bia_prefill_paged_window needs for this call (0 on invalid
+ * input).  Of these lengths: a call with many q tiles keeps a state per CTA
+ * instead of one per row and split, so a longer call may need less. */
+BIA_API size_t bia_prefill_window_workspace_size(const bia_attn_desc *desc, int32_t window,
+                                         int32_t sinks, const int32_t *qo_indptr_host,
+                                         const int32_t *kv_indptr_host,
+                                         const int32_t *kv_last_page_len_host, int32_t batch,
+                                         int32_t split_size);
 
 /*
  * bia_decode_paged with a window and sinks.  The keys that a query sees are
  * taken as one list, the sinks first, cut into tiles of split_size keys (a
  * multiple of 128; 0 = BIA_WINDOW_DECODE_SPLIT) whose states are merged in
  * order; with a window of at least kv_len the bits are those of
- * bia_decode_paged at the same split size.
+ * bia_decode_paged at the same split size.  The device index arrays are checked
+ * request by request: one that breaks a rule of the call (or its bounds) gets
+ * NaN rows and sets bit 1 of the status word, the others are computed.
  */
 BIA_API int bia_decode_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
                             const void *q, const void *k_cache, const void *v_cache,

@@ -50,7 +50,8 @@ EXPORTS = ("bia_prefill_paged", "bia_prefill_workspace_size", "bia_decode_paged"
            "bia_prefill_ragged", "bia_prefill_ragged_workspace_size", "bia_norm_rope",
            "bia_append_paged_kv_rope", "bia_append_paged_kv_fp8_rope", "bia_decode_paged_window",
            "bia_decode_window_workspace_size", "bia_decode_paged_window_bounded",
-           "bia_decode_window_bounded_workspace_size")
+           "bia_decode_window_bounded_workspace_size", "bia_prefill_paged_window",
+           "bia_prefill_window_workspace_size")
 
 
 class BiaError(RuntimeError):
@@ -187,6 +188,11 @@ def load(path: str = LIB_PATH):
     lib.bia_decode_paged_window_bounded.restype = ctypes.c_int
     lib.bia_decode_window_bounded_workspace_size.argtypes = [dp, bp, i32, i32, i32, i32]
     lib.bia_decode_window_bounded_workspace_size.restype = sz
+    lib.bia_prefill_paged_window.argtypes = [dp, i32, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp,
+                                             vp, i32, i32, vp, sz, vp, vp, vp]
+    lib.bia_prefill_paged_window.restype = ctypes.c_int
+    lib.bia_prefill_window_workspace_size.argtypes = [dp, i32, i32, vp, vp, vp, i32, i32]
+    lib.bia_prefill_window_workspace_size.restype = sz
     rp = ctypes.POINTER(Rope)
     lib.bia_norm_rope.argtypes = [dp, rp, vp, vp, vp, vp, i64, i64, vp, vp, i64, vp, vp, i64, i64,
                                   vp, vp]
@@ -1180,3 +1186,37 @@ def bia_decode_paged_window_bounded(desc, bounds, window, sinks, q, k_cache, v_c
         _at(lse), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, "bia_decode_paged_window_bounded")
+
+
+def bia_prefill_window_workspace_size(desc, window, sinks, qo_indptr_host, kv_indptr_host,
+                                      kv_last_page_len_host, split_size=0) -> int:
+    qo, kvp, last = (_host_i32(qo_indptr_host), _host_i32(kv_indptr_host),
+                     _host_i32(kv_last_page_len_host))
+    return int(load().bia_prefill_window_workspace_size(
+        ctypes.byref(desc), int(window), int(sinks), _ptr(qo), _ptr(kvp), _ptr(last), len(qo) - 1,
+        int(split_size)))
+
+
+def bia_prefill_paged_window(desc, window, sinks, q, k_cache, v_cache, qo_indptr, kv_indptr,
+                             kv_indices, kv_last_page_len, qo_indptr_host, kv_indptr_host,
+                             kv_last_page_len_host, workspace, out, lse=None, split_size=0,
+                             stream=None):
+    """bia_prefill_paged (causal) where a query sees the last `window` keys up to
+    its own and the first `sinks` keys (include/bia.h states the rule)."""
+    qo, kvp, last = (_host(qo_indptr_host), _host(kv_indptr_host),
+                     _host(kv_last_page_len_host))
+    batch = qo.numel() - 1
+    _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
+                  out, lse, stream, batch, kvp, last, qo_indptr)
+    if qo_indptr.numel() != batch + 1:
+        raise ValueError(f"qo_indptr must hold {batch + 1} entries, got {qo_indptr.numel()}")
+    if q.shape[0] != _last(qo):
+        raise ValueError(f"q holds {q.shape[0]} tokens, qo_indptr_host ends at {_last(qo)}")
+    rc = load().bia_prefill_paged_window(
+        ctypes.byref(desc), int(window), int(sinks), q.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), k_cache.shape[0], qo_indptr.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_last_page_len.data_ptr(), qo.data_ptr(), kvp.data_ptr(),
+        last.data_ptr(), batch, int(split_size), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr(), _at(lse), _handle(stream))
+    if rc != BIA_OK:
+        raise BiaError(rc, "bia_prefill_paged_window")

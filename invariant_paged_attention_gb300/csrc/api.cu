@@ -1366,6 +1366,66 @@ int64_t window_len(int64_t kv_len, int32_t window, int32_t sinks) {
   return kv_len - behind + std::min<int64_t>(sinks, behind);
 }
 
+// No request has more keys: a window or sinks above stand for all of them.
+constexpr int32_t kAllKeys = INT32_MAX / 2;
+
+// A windowed extend: its q tile pairs, the split tiles a pair may have, and
+// whether the CTAs fold them.
+struct WindowPrefillPlan {
+  int64_t pairs = 0, total_q = 0, max_kv_len = 0;
+  int32_t parts = 1, split = 0, folds = 0;
+  bool states = false; // fp32 states in the workspace, merged
+  WsLayout w;
+};
+
+int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks,
+                        const int32_t *qo_host, const int32_t *kvp_host, const int32_t *last_host,
+                        int32_t batch, int32_t split, WindowPrefillPlan *p) {
+  int rc = check_desc(desc);
+  if (rc != BIA_OK) return rc;
+  if (window < 1 || sinks < 0 || batch <= 0 || !qo_host || !kvp_host || !last_host)
+    return BIA_ERR_INVALID_ARG;
+  if (split == 0) split = BIA_PREFILL_SPLIT;
+  if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
+  if (split > BIA_RAGGED_MAX_SPLIT) return BIA_ERR_UNSUPPORTED;
+  if (qo_host[0] != 0 || kvp_host[0] < 0) return BIA_ERR_INVALID_ARG;
+  const int D = desc->head_dim, Hq = desc->num_qo_heads, Hkv = desc->num_kv_heads;
+  const int64_t T = bia::kTileRows / (Hq / Hkv), nt = bia::window_tiles_per_unit(D);
+  for (int b = 0; b < batch; ++b) {
+    const int64_t q_len = static_cast<int64_t>(qo_host[b + 1]) - qo_host[b];
+    const int64_t pages = static_cast<int64_t>(kvp_host[b + 1]) - kvp_host[b];
+    if (q_len < 0 || pages < 0) return BIA_ERR_INVALID_ARG;
+    const int32_t last = last_host[b];
+    if (pages > 0 && (last < 1 || last > desc->page_size)) return BIA_ERR_INVALID_ARG;
+    const int64_t kv_len = pages > 0 ? (pages - 1) * desc->page_size + last : 0;
+    if (kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
+    if (q_len > kv_len) return BIA_ERR_INVALID_ARG;
+    p->pairs += ((q_len + T - 1) / T + nt - 1) / nt;
+    p->total_q += q_len;
+    p->max_kv_len = std::max(p->max_kv_len, kv_len);
+  }
+  p->split = split;
+  // a pair's keys: up to window + (the pair's tokens - 1), or all of them where
+  // the sinks meet the window, which then ends within sinks + a block of it
+  const int64_t span = std::min<int64_t>(
+      p->max_kv_len, static_cast<int64_t>(std::min(window, kAllKeys)) + nt * T +
+                         (sinks > 0 ? std::min(sinks, kAllKeys) + 2 * bia::kKvBlock : 0));
+  p->parts = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min<int64_t>((p->max_kv_len + split - 1) / split, (span + split - 1) / split + 1)));
+  const int64_t items = p->pairs * Hkv;
+  if (items * p->parts > INT32_MAX) return BIA_ERR_UNSUPPORTED;
+  p->folds = p->parts > 1 && items >= bia::kFoldItems ? 1 : 0;
+  p->states = p->parts > 1 && !p->folds;
+  const int64_t row = static_cast<int64_t>(Hq) * D;
+  int64_t rows = p->states ? p->total_q * p->parts : 0;
+  if (p->folds) {
+    const int64_t states = bia::kFoldCtas * nt * bia::kTileRows * (D == 256 ? 256 : D > 64 ? 128 : 64);
+    rows = (states + row - 1) / row;
+  }
+  p->w = bia::make_layout(batch, 0, 0, 0, rows, Hq, D);
+  return BIA_OK;
+}
+
 // A windowed decode: the longest request, the split tiles a request may have,
 // and where its states and status words lie.
 struct WindowDecodePlan {
@@ -1489,6 +1549,132 @@ int run_window_decode(const bia_attn_desc *desc, const bia_bounds *bounds, int32
   return BIA_OK;
 }
 } // namespace
+
+int bia_prefill_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
+                             const void *q, const void *k_cache, const void *v_cache,
+                             int64_t num_pages, const int32_t *qo_indptr,
+                             const int32_t *kv_indptr, const int32_t *kv_indices,
+                             const int32_t *kv_last_page_len, const int32_t *qo_indptr_host,
+                             const int32_t *kv_indptr_host, const int32_t *kv_last_page_len_host,
+                             int32_t batch, int32_t split_size, void *workspace,
+                             size_t workspace_bytes, void *out, float *lse, void *stream) {
+  WindowPrefillPlan p;
+  int rc = window_prefill_plan(desc, window, sinks, qo_indptr_host, kv_indptr_host,
+                               kv_last_page_len_host, batch, split_size, &p);
+  if (rc != BIA_OK) return rc;
+  if (misaligned(workspace, 256) || misaligned(q, 16) || misaligned(k_cache, 16) ||
+      misaligned(v_cache, 16) || misaligned(out, 16) || misaligned(lse, 4) ||
+      misaligned(qo_indptr, 4) || misaligned(kv_indptr, 4) || misaligned(kv_indices, 4) ||
+      misaligned(kv_last_page_len, 4))
+    return BIA_ERR_INVALID_ARG;
+  if (!workspace) return BIA_ERR_INVALID_ARG;
+  if (workspace_bytes < p.w.total) return BIA_ERR_WORKSPACE_TOO_SMALL;
+  if (p.total_q == 0) return BIA_OK;
+  if (!q || !k_cache || !v_cache || !qo_indptr || !kv_indptr || !kv_indices ||
+      !kv_last_page_len || !out || num_pages <= 0)
+    return BIA_ERR_INVALID_ARG;
+  const int D = desc->head_dim, Hq = desc->num_qo_heads, Hkv = desc->num_kv_heads, G = Hq / Hkv;
+  const int64_t slots = num_pages * desc->page_size;
+  if (num_pages > INT32_MAX || slots * Hkv >= INT32_MAX || p.total_q * Hq >= INT32_MAX)
+    return BIA_ERR_UNSUPPORTED;
+  rc = check_resident({{"q", q},
+                       {"k_cache", k_cache},
+                       {"v_cache", v_cache},
+                       {"out", out},
+                       {"lse", lse},
+                       {"qo_indptr", qo_indptr},
+                       {"kv_indptr", kv_indptr},
+                       {"kv_indices", kv_indices},
+                       {"kv_last_page_len", kv_last_page_len},
+                       {"workspace", workspace}});
+  if (rc != BIA_OK) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  PlanArgs pa{};
+  pa.qo_indptr = qo_indptr;
+  pa.kv_indptr = kv_indptr;
+  pa.kv_last_page_len = kv_last_page_len;
+  pa.batch = batch;
+  pa.page_size = desc->page_size;
+  pa.tile_tokens = bia::kTileRows / G;
+  pa.tiles_per_unit = bia::window_tiles_per_unit(D);
+  pa.max_total_q = p.total_q;
+  pa.max_kv_len = static_cast<int32_t>(p.max_kv_len);
+  pa.n_groups_expected = p.pairs;
+  pa.out = static_cast<uint16_t *>(out);
+  pa.out_elems = p.total_q * Hq * D;
+  pa.lse = lse;
+  pa.lse_elems = p.total_q * Hq;
+  pa.status = reinterpret_cast<int32_t *>(ws + p.w.status);
+  pa.reqs = reinterpret_cast<bia::ReqInfo *>(ws + p.w.reqs);
+  pa.group_off = reinterpret_cast<int32_t *>(ws + p.w.group_off);
+  cudaError_t e = bia::launch_plan_window(pa, st);
+  if (e != cudaSuccess) return cuda_fail("plan kernel launch", e);
+
+  AttnArgs a{};
+  a.kv_indices = kv_indices;
+  a.num_pages = num_pages;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.G = G;
+  a.page_shift = log2i(desc->page_size);
+  a.causal = 1;
+  a.split = p.split;
+  a.tile_tokens = pa.tile_tokens;
+  a.scale_log2 = effective_scale(desc);
+  a.batch = batch;
+  a.n_units = p.pairs * (p.folds ? 1 : p.parts);
+  a.reqs = pa.reqs;
+  a.part_o = reinterpret_cast<float *>(ws + p.w.part_o);
+  a.part_lse = reinterpret_cast<float *>(ws + p.w.part_lse);
+  a.total_rows = p.total_q;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.status = pa.status;
+  a.window = std::min(window, kAllKeys);
+  a.sinks = std::min(sinks, kAllKeys);
+  a.parts = p.parts;
+  a.kv_rows = static_cast<int32_t>(slots * Hkv);
+  int ce = encode_q_map(&a.tm_q, q, p.total_q, Hq, D, G, pa.tile_tokens);
+  if (ce == 0) ce = encode_rows_map(&a.tm_k, k_cache, a.kv_rows, D);
+  if (ce == 0) ce = encode_rows_map(&a.tm_v, v_cache, a.kv_rows, D);
+  if (desc->page_size >= 16) {
+    if (ce == 0) ce = encode_slots_map(&a.tm_k3, k_cache, slots, Hkv, D);
+    if (ce == 0) ce = encode_slots_map(&a.tm_v3, v_cache, slots, Hkv, D);
+  }
+  if (ce != 0) return fail(BIA_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable", ce);
+  const bool profile = g_attn_begin != nullptr && g_attn_end != nullptr;
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_begin, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  e = bia::launch_prefill_window(a, pa.group_off, p.folds, st);
+  if (e != cudaSuccess) return cuda_fail("prefill kernel launch", e);
+  if (profile) {
+    const cudaError_t re = cudaEventRecord(g_attn_end, st);
+    if (re != cudaSuccess) return cuda_fail("profile event record", re);
+  }
+  if (p.states) {
+    e = bia::launch_merge_window(a, st);
+    if (e != cudaSuccess) return cuda_fail("merge kernel launch", e);
+  }
+  __atomic_add_fetch(&g_launches, p.states ? 3ull : 2ull, __ATOMIC_RELAXED);
+  return BIA_OK;
+}
+
+size_t bia_prefill_window_workspace_size(const bia_attn_desc *desc, int32_t window, int32_t sinks,
+                                         const int32_t *qo_indptr_host,
+                                         const int32_t *kv_indptr_host,
+                                         const int32_t *kv_last_page_len_host, int32_t batch,
+                                         int32_t split_size) {
+  WindowPrefillPlan p;
+  return window_prefill_plan(desc, window, sinks, qo_indptr_host, kv_indptr_host,
+                             kv_last_page_len_host, batch, split_size, &p) == BIA_OK
+             ? p.w.total
+             : 0;
+}
 
 int bia_decode_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
                             const void *q, const void *k_cache, const void *v_cache,

@@ -253,6 +253,29 @@ struct AttnArgs {
   int32_t *slots;     // decode: a status word per CTA, joined by the merge
 };
 
+// The key blocks (of KB keys, anchored at key 0) that the rows of a q tile see
+// under a window and sinks: n_sink blocks from 0 on, then first .. last, cut
+// into the split tiles s0 .. s1 (the sinks' blocks go with s0).
+struct TileKeys {
+  int32_t n_sink, first, last, s0, s1;
+};
+__host__ __device__ inline TileKeys tile_keys(int32_t q_len, int32_t kv_len, int32_t tile,
+                                              int32_t tile_tokens, int32_t window, int32_t sinks,
+                                              int32_t split, int32_t KB) {
+  const int32_t p0 = kv_len - q_len + tile * tile_tokens; // of the first row
+  const int32_t end = (tile + 1) * tile_tokens < q_len ? (tile + 1) * tile_tokens : q_len;
+  const int32_t p1 = kv_len - q_len + end - 1; // of the last row
+  const int32_t lo = p0 - window + 1 > 0 ? p0 - window + 1 : 0;
+  TileKeys k;
+  k.first = lo / KB;
+  k.last = p1 / KB;
+  k.n_sink = ((sinks < p1 + 1 ? sinks : p1 + 1) + KB - 1) / KB;
+  if (k.n_sink >= k.first) k.first = k.n_sink = 0; // one range
+  k.s0 = k.first * KB / split;
+  k.s1 = p1 / split;
+  return k;
+}
+
 // The keys that the one query of a windowed decode sees, as a list of its own:
 // entry i is key i below `sunk` and key i + skip from there on (the sinks that
 // the window has left behind, then the window).
@@ -404,6 +427,14 @@ cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_wide(const AttnArgs &a, cudaStream_t s); // head_dim 256
 cudaError_t launch_cache_fp8(const CacheFp8Args &a, bool append, cudaStream_t s);
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s);
+// An extend with a window and sinks: its plan (records and first pairs of the
+// requests), its kernel, and the join of the states of split pairs.
+cudaError_t launch_plan_window(const PlanArgs &p, cudaStream_t s);
+cudaError_t launch_prefill_window(const AttnArgs &a, const int32_t *group_off, int folds,
+                                  cudaStream_t s);
+cudaError_t launch_merge_window(const AttnArgs &a, cudaStream_t s);
+inline int window_tiles_per_unit(int head_dim) { return head_dim == 256 ? 1 : 2; }
+__host__ __device__ inline int window_key_block(int head_dim) { return head_dim == 256 ? 64 : kKvBlock; }
 // Joins the states of a windowed decode's split tiles and its status words.
 cudaError_t launch_merge_window_decode(const AttnArgs &a, int n_slots, cudaStream_t s);
 cudaError_t launch_plan_decode_fp8(const PlanArgs &p, UnitFp8 *units, cudaStream_t s);

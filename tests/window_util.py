@@ -96,3 +96,16 @@ class Batch:
             seen = seen_of(n, self.keys[b], self.window, self.sinks)[t].cuda()
             t = t.cuda() + a
             fu.check(self.out[t], self.lse[t], *bounds(self.q[t], self.rows_k[b], self.rows_v[b], seen, sm_scale))
+
+
+def extend(self, split=0, ws=None, out=None, lse=True, **kw):
+    need = bia.bia_prefill_window_workspace_size(self.desc, self.window, self.sinks, self.qo, self.kvp, self.last, split)
+    assert need > 0
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda") if ws is None else ws
+    bia.bia_prefill_paged_window(self.desc, self.window, self.sinks, self.q, self.k_cache, self.v_cache, self.qo.cuda(),
+                                 *self.dev, self.qo, self.kvp, self.last, ws, self.out if out is None else out,
+                                 self.lse if lse is True else lse, split, **kw)
+    return ws
+
+
+Batch.extend = extend
