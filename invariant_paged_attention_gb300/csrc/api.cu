@@ -1640,10 +1640,8 @@ int bia_prefill_paged_window(const bia_attn_desc *desc, int32_t window, int32_t 
   int ce = encode_q_map(&a.tm_q, q, p.total_q, Hq, D, G, pa.tile_tokens);
   if (ce == 0) ce = encode_rows_map(&a.tm_k, k_cache, a.kv_rows, D);
   if (ce == 0) ce = encode_rows_map(&a.tm_v, v_cache, a.kv_rows, D);
-  if (desc->page_size >= 16) {
-    if (ce == 0) ce = encode_slots_map(&a.tm_k3, k_cache, slots, Hkv, D);
-    if (ce == 0) ce = encode_slots_map(&a.tm_v3, v_cache, slots, Hkv, D);
-  }
+  if (ce == 0) ce = encode_slots_map(&a.tm_k3, k_cache, slots, Hkv, D);
+  if (ce == 0) ce = encode_slots_map(&a.tm_v3, v_cache, slots, Hkv, D);
   if (ce != 0) return fail(BIA_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable", ce);
   const bool profile = g_attn_begin != nullptr && g_attn_end != nullptr;
   if (profile) {

@@ -258,6 +258,7 @@ struct AttnArgs {
 // into the split tiles s0 .. s1 (the sinks' blocks go with s0).
 struct TileKeys {
   int32_t n_sink, first, last, s0, s1;
+  int32_t k0, k1; // the keys of the range first .. last: k0 .. k1 - 1
 };
 __host__ __device__ inline TileKeys tile_keys(int32_t q_len, int32_t kv_len, int32_t tile,
                                               int32_t tile_tokens, int32_t window, int32_t sinks,
@@ -270,7 +271,9 @@ __host__ __device__ inline TileKeys tile_keys(int32_t q_len, int32_t kv_len, int
   k.first = lo / KB;
   k.last = p1 / KB;
   k.n_sink = ((sinks < p1 + 1 ? sinks : p1 + 1) + KB - 1) / KB;
-  if (k.n_sink >= k.first) k.first = k.n_sink = 0; // one range
+  k.k0 = lo;
+  k.k1 = p1 + 1;
+  if (k.n_sink >= k.first) k.first = k.n_sink = k.k0 = 0; // one range
   k.s0 = k.first * KB / split;
   k.s1 = p1 / split;
   return k;

@@ -11,9 +11,10 @@
 // (one at head_dim 256, whose O fills half of TMEM) against one kv head.  Its
 // roles walk the same items through a ring of records and each runs ahead as
 // far as its buffers allow: warps 0-3 and 4-7 softmax + epilogue of the two
-// tiles, 8 issues the MMAs and owns TMEM, 9 loads, 10 makes the items.  The two
-// tiles share every block that either needs; a tile leaves out the blocks that
-// only the other one sees.
+// tiles, 8 issues the MMAs and owns TMEM, 9 loads q and K, 11 V, 10 makes the
+// items.  The two tiles share every block that either needs; a tile leaves out
+// the blocks that only the other one sees, and the copies the 16-key steps of the
+// blocks at the window's and the sinks' ends that no row sees.
 //
 // A block of K or V comes as runs of 16 keys of one page (3-D TMA boxes) where
 // pages hold 16 keys and more, else, and where a run is not wholly needed, as
@@ -38,18 +39,18 @@ namespace {
 
 constexpr int kSoftWarpsW = 8;
 constexpr int kMmaWarpW = 8;
-constexpr int kProdWarpW = 9;
+constexpr int kKeyWarpW = 9; // loads q and K
 constexpr int kItemWarpW = 10;
+constexpr int kValueWarpW = 11; // loads V
 constexpr int kThreadsW = 384;
-constexpr int kSoftRegsW = 216, kOtherRegsW = 72; // as in prefill_ragged.cu
-static_assert(8 * kSoftRegsW + 4 * kOtherRegsW <= 12 * 168, "registers of the launch");
 constexpr int kItemsW = 3;               // items in flight
 constexpr int kAtomQW = kTileRows * 128; // one SW128 column block of a q tile
 constexpr float kRescaleW = 16.0f;       // log2 units the running max may lag a block's
+constexpr int kFewSteps = 2;             // of 16 keys: sinks that fit them are not a whole block
 
 struct WindowPrefillArgs {
   int32_t Hq, Hkv, D, G, split, tile_tokens, batch, page_shift, window, sinks, parts, folds;
-  int32_t kv_rows; // row extent of the gather maps
+  int32_t kv_rows, slots; // row extent of the gather maps, slot extent of the run maps
   float scale_log2;
   int64_t num_pages;
   const ReqInfo *reqs;
@@ -69,7 +70,23 @@ struct alignas(16) ItemW {
   int32_t n_sink, w0;                // the first n_sink blocks are 0 ..; then w0 ..
   int32_t sink[2];                   // whether the tile uses the sinks' blocks
   int32_t j0[2], j1[2];              // window blocks of the tile, counted in the item
+  int32_t steps;                     // of the blocks that are not whole
+  int32_t w_begin[2], w_end[2];      // blocks that every row of the tile sees in full
   int32_t part[2], n_parts[2];       // which of the tile's states; n_parts 0: not here
+};
+
+// The 16-key steps u .. v - 1 of block j of an item that a tile's rows see,
+// which are copied.  Only the sinks' last block and the ends of the window are
+// not whole.
+// An item holds four bits for each: the first step of the tile's block j0 and
+// the end of its block j1 - 1 (8 bits a tile), the end of block n_sink - 1.
+template <int KB>
+struct Steps {
+  int n_sink, j0, j1, bits;
+  __device__ __forceinline__ int u(int j) const { return j == j0 ? bits & 15 : 0; }
+  __device__ __forceinline__ int v(int j) const {
+    return j == j1 - 1 ? (bits >> 4) & 15 : j == n_sink - 1 ? (bits >> 16) & 15 : KB / 16;
+  }
 };
 
 template <int D>
@@ -85,6 +102,11 @@ struct SmemW {
   static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kVFull = 4, kKEmpty = 6, kVEmpty = 8,
                        kSFull = 10, kPFull = 12, kODone = 14, kIAsk = 16, kIFull = 17,
                        kIEmpty = kIFull + kItemsW, kNumBars = kIEmpty + kItemsW;
+  // registers: the softmax warps hold a whole S row, the MMA issuer its items'
+  // limits; no role spills with these (of 12 warps x 168)
+  static constexpr int kSoftRegs = D == 256 ? 200 : 208;
+  static constexpr int kOtherRegs = 504 - 2 * kSoftRegs;
+  static_assert(8 * kSoftRegs + 4 * kOtherRegs <= 12 * 168, "registers of the launch");
   static constexpr int kSlot = kBar + kNumBars * 8;
   static constexpr int kAlloc = kSlot + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory per CTA");
@@ -127,6 +149,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   using L = SmemW<D>;
   constexpr int NT = L::NT, KB = L::KB;
   constexpr uint32_t kIdescS = idesc_bf16(128, KB, false);
+  constexpr uint32_t kIdescFew = idesc_bf16(128, 16 * kFewSteps, false);
   constexpr uint32_t kIdescPV = idesc_bf16(128, D, true);
   constexpr uint32_t kTmemCols = 512;
 
@@ -158,7 +181,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     mbar_init(bar(L::kIAsk), 1);
     for (int s = 0; s < kItemsW; ++s) {
       mbar_init(bar(L::kIFull + s), 1);
-      mbar_init(bar(L::kIEmpty + s), kSoftWarpsW + 2);
+      mbar_init(bar(L::kIEmpty + s), kSoftWarpsW + 3);
     }
     fence_mbar_init();
   }
@@ -190,7 +213,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   };
 
   if (warp >= kSoftWarpsW) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegsW));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
     if (warp == kItemWarpW) {
       // ------------------------------------------------------------ items
       const int32_t n_pairs = a.status[kStatusMergeRows]; // 0: the plan failed its checks
@@ -270,10 +293,20 @@ __global__ void __launch_bounds__(kThreadsW, 1)
             w1 = max(w1, e[t]);
           }
           x.nb = x.n_sink + w1 - x.w0;
+          x.steps = x.n_sink > 0 ? (a.sinks - (x.n_sink - 1) * KB + 15) / 16 << 16 : 0;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             x.j0[t] = x.n_parts[t] ? x.n_sink + f[t] - x.w0 : 0;
             x.j1[t] = x.n_parts[t] ? x.n_sink + e[t] - x.w0 : 0;
+            // a split's first block starts it, or holds the window's first key
+            const int first = tk[t].first >= b0 ? (tk[t].k0 % KB) / 16 : 0;
+            const int end = tk[t].last < b1 ? (tk[t].k1 - tk[t].last * KB + 15) / 16 : KB / 16;
+            if (x.n_parts[t]) x.steps |= (first | end << 4) << (8 * t);
+            // from the last row's window on, up to the first row's position
+            const int32_t p0 = x.kv_len - x.q_len + (x.tile + t) * T;
+            const int32_t from = max(0, tk[t].k1 - a.window);
+            x.w_begin[t] = max(x.j0[t], x.n_sink + (from + KB - 1) / KB - x.w0);
+            x.w_end[t] = min(x.j1[t], x.n_sink + (p0 + 1) / KB - x.w0);
           }
         }
         more = x.kvh >= 0 && a.folds && s + 1 < s_end;
@@ -291,18 +324,35 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kIAsk), i & 1, a.status))) break;
         if (!more) take();
       }
-    } else if (warp == kProdWarpW) {
+    } else if (warp == kKeyWarpW || warp == kValueWarpW) {
       // ------------------------------------------------------------ loads
       // lane: the four rows 4*grp .. of a block, column blocks hh, hh + LPG ..
       constexpr int kGroups = KB / 4, LPG = 32 / kGroups;
       const int grp = lane % kGroups, hh = lane / kGroups;
       const int page_mask = (1 << a.page_shift) - 1;
       const bool runs = a.page_shift >= 4; // a run of 16 keys lies in one page
+      const bool keys = warp == kKeyWarpW;
+      const void *rows_map = keys ? &a.tm_k : &a.tm_v, *runs_map = keys ? &a.tm_k3 : &a.tm_v3;
+      const uint32_t full0 = bar(keys ? L::kKFull : L::kVFull);
+      const uint32_t empty0 = bar(keys ? L::kKEmpty : L::kVEmpty);
       bool ok = true;
-      int g = 0, nk = 0, nq = 0; // blocks, K blocks and q tile pairs loaded
+      int g = 0, n = 0, nq = 0; // blocks, those whose copies were issued, q tile pairs
       while (const ItemW *xp = next(false)) {
         const int nb = xp->nb, n_sink = xp->n_sink, w0 = xp->w0, kvh = xp->kvh;
         const int kv_len = xp->kv_len, lo = xp->lo;
+        // steps of block j that either tile needs
+        auto steps = [&](int j, int &u, int &v) {
+          u = KB / 16;
+          v = 0;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (uses(j, n_sink, xp->sink[t] != 0, xp->j0[t], xp->j1[t])) {
+              const Steps<KB> s{n_sink, xp->j0[t], xp->j1[t],
+                                (xp->steps >> (8 * t) & 255) | (xp->steps & 15 << 16)};
+              u = min(u, s.u(j));
+              v = max(v, s.v(j));
+            }
+        };
         const int32_t *pages = a.kv_indices + xp->page_base;
         auto wanted = [&](int32_t key) { return key < kv_len && (key >= lo || key < a.sinks); };
         auto key_of = [&](int j) { // the lane's first key of block j
@@ -314,7 +364,12 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           for (int i = 0; i < 4; ++i) pg[i] = -1;
           if (j >= nb) return;
           const int32_t key = key_of(j);
-          if (a.page_shift >= 2) { // one page
+          if (runs) { // of the run, if any key of it is wanted
+            const int32_t r0 = key - 4 * (grp & 3);
+            if ((r0 + 15 >= lo || r0 < a.sinks) && r0 < kv_len)
+              pg[0] = __ldg(pages + (r0 >> a.page_shift));
+            pg[1] = pg[2] = pg[3] = pg[0];
+          } else if (a.page_shift >= 2) { // one page
             if (wanted(key) || wanted(key + 1) || wanted(key + 2) || wanted(key + 3))
               pg[0] = __ldg(pages + (key >> a.page_shift));
             pg[1] = pg[2] = pg[3] = pg[0];
@@ -327,7 +382,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         int32_t pg[4];
         fetch(0, pg);
         for (int j = 0; j < nb; ++j, ++g) {
-          if (lane == 0 && j == max(0, nb - 3)) mbar_arrive(bar(L::kIAsk));
+          if (keys && lane == 0 && j == max(0, nb - 3)) mbar_arrive(bar(L::kIAsk));
           const int st = g & 1;
           const int32_t key = key_of(j), run0 = key - 4 * (grp & 3);
           int32_t rows[4];
@@ -344,30 +399,41 @@ __global__ void __launch_bounds__(kThreadsW, 1)
               good = good && there;
             }
           }
-          const bool run =
-              runs && good && run0 + 15 < kv_len && (run0 >= lo || run0 + 15 < a.sinks);
-          const int32_t slot = run ? (pg[0] << a.page_shift) + (run0 & page_mask) : 0;
+          // A run of 16 keys of one page is one copy a column block.  Keys of it
+          // that are not wanted only cost their column of S, which no row
+          // sees; as values they must be zeros (0 * NaN), so such a run of V
+          // is gathered row by row.
+          const int32_t page = pg[0];
+          const bool whole = run0 + 15 < kv_len && (run0 >= lo || run0 + 15 < a.sinks);
+          const bool run = runs && page >= 0 && page < a.num_pages && (keys || whole);
+          const int32_t slot = run ? (page << a.page_shift) + (run0 & page_mask) : 0;
+          int u, v;
+          steps(j, u, v);
+          const bool needed = (grp >> 2) >= u && (grp >> 2) < v;
+          // The MMAs take a whole block: K columns that no row sees may hold
+          // anything, V rows must be zeros.
+          const bool few = j < n_sink && a.sinks <= 16 * kFewSteps;
+          const bool zeros = !keys && !needed && (!few || (grp >> 2) < kFewSteps);
+          const int copied = keys ? v - u : few ? kFewSteps : KB / 16;
           fetch(j + 1, pg); // in flight while this block's copies are issued
-          auto issue = [&](uint32_t dst, const void *rows_map, const void *runs_map, uint32_t b) {
-            if (run) {
-              if (hh == 0 && (grp & 3) < D / 64)
-                tma_load_3d(dst + (grp & 3) * L::kAtom + (grp & ~3) * 512, runs_map,
-                            64 * (grp & 3), kvh, slot, b);
-            } else {
-#pragma unroll
-              for (int h = 0; h < D / 64; h += LPG)
-                if (h + hh < D / 64)
-                  gather4(dst + (h + hh) * L::kAtom + grp * 512, rows_map, 64 * (h + hh), rows, b);
-            }
-          };
-          ok = __all_sync(0xffffffffu, g < 2 || mbar_wait(bar(L::kKEmpty + st),
-                                                          ((g >> 1) - 1) & 1, a.status));
+          ok = __all_sync(0xffffffffu,
+                          g < 2 || mbar_wait(empty0 + 8 * st, ((g >> 1) - 1) & 1, a.status));
           if (!ok) break;
-          if (lane == 0) mbar_expect_tx(bar(L::kKFull + st), L::kKV);
+          const uint32_t b = full0 + 8 * st, dst = keys ? sK(st) : sV(st);
+          if (lane == 0) mbar_expect_tx(b, static_cast<uint32_t>(copied) * (16 * D * 2));
           __syncwarp();
-          issue(sK(st), &a.tm_k, &a.tm_k3, bar(L::kKFull + st));
-          nk = g + 1;
-          if (j == 0) {
+          if ((needed && run) || zeros) {
+            if (hh == 0 && (grp & 3) < D / 64)
+              tma_load_3d(dst + (grp & 3) * L::kAtom + (grp & ~3) * 512, runs_map, 64 * (grp & 3),
+                          kvh, zeros ? a.slots : slot, b);
+          } else if (needed) {
+#pragma unroll
+            for (int h = 0; h < D / 64; h += LPG)
+              if (h + hh < D / 64)
+                gather4(dst + (h + hh) * L::kAtom + grp * 512, rows_map, 64 * (h + hh), rows, b);
+          }
+          n = g + 1;
+          if (keys && j == 0) {
             // q of this item while the previous one is still in its last P.V
             ok = __all_sync(0xffffffffu,
                             nq == 0 || mbar_wait(bar(L::kQEmpty), (nq - 1) & 1, a.status));
@@ -385,28 +451,19 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                                 xp->q_start + (xp->tile + t) * T, bar(L::kQFull));
             }
           }
-          ok = __all_sync(0xffffffffu, g < 2 || mbar_wait(bar(L::kVEmpty + st),
-                                                          ((g >> 1) - 1) & 1, a.status));
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(bar(L::kVFull + st), L::kKV);
-          __syncwarp();
-          issue(sV(st), &a.tm_v, &a.tm_v3, bar(L::kVFull + st));
         }
         if (!ok) break;
         __syncwarp();
         if (lane == 0) release();
       }
-      // no copy and no commit outlives the CTA, also when a wait ran out
+      // no copy and no commit outlives the CTA, also when a wait ran out (the
+      // block that was begun then is copied in full all the same)
       __syncwarp();
       if (nq > 0) mbar_wait(bar(L::kQFull), (nq - 1) & 1, a.status);
       if (nq > 0 && ok) mbar_wait(bar(L::kQEmpty), (nq - 1) & 1, a.status);
-      for (int b = max(0, nk - 2); b < nk; ++b) {
-        mbar_wait(bar(L::kKFull + (b & 1)), (b >> 1) & 1, a.status);
-        if (ok) mbar_wait(bar(L::kKEmpty + (b & 1)), (b >> 1) & 1, a.status);
-      }
-      for (int b = max(0, g - 2); b < g; ++b) {
-        mbar_wait(bar(L::kVFull + (b & 1)), (b >> 1) & 1, a.status);
-        if (ok) mbar_wait(bar(L::kVEmpty + (b & 1)), (b >> 1) & 1, a.status);
+      for (int b = max(0, n - 2); b < n; ++b) {
+        mbar_wait(full0 + 8 * (b & 1), (b >> 1) & 1, a.status);
+        if (ok) mbar_wait(empty0 + 8 * (b & 1), (b >> 1) & 1, a.status);
       }
     } else if (warp == kMmaWarpW) {
       // ------------------------------------------------------------ MMA issuer
@@ -420,27 +477,31 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         int ns = 0;           // S blocks so far (one tile)
         int np0 = 0, np1 = 0; // P blocks of each tile so far
         bool ok = true;
-        auto issue_s = [&](int t, int buf, int st) {
+        // S and P.V of a block, or of its first kFewSteps steps of 16 keys
+        // (the counts are known here: operands that follow data would go
+        // through vector registers, 250 us of 950 for W = 1024 below)
+        auto issue_s = [&](int t, int buf, int st, bool few) {
           uint64_t dq = t ? dQ1 : dQ0, dk = st ? dK1 : dK0;
           asm volatile("" : "+l"(dq), "+l"(dk)); // kept from hoisting: 32 registers
-          const uint32_t ts = tS(buf);
+          const uint32_t ts = tS(buf), idesc = few ? kIdescFew : kIdescS;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t qoff = ((kk >> 2) * kAtomQW + (kk & 3) * 32) >> 4;
             const uint32_t koff = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(ts, dq + qoff, dk + koff, kIdescS, kk > 0);
+            mma_bf16_ss(ts, dq + qoff, dk + koff, idesc, kk > 0);
           }
           mma_commit(bar(L::kSFull + buf));
         };
-        auto issue_pv = [&](int t, int buf, int st, bool first) {
+        auto issue_pv = [&](int t, int buf, int st, bool first, bool few) {
           tc_fence_after();
           uint64_t dv = st ? dV1 : dV0;
           asm volatile("" : "+l"(dv));
           const uint32_t to = tO(t), ts = tS(buf);
 #pragma unroll
           for (int kk = 0; kk < KB / 16; ++kk)
-            mma_bf16_ts(to, ts + kk * 8, dv + ((kk * 2048) >> 4), kIdescPV,
-                        (!first || kk > 0) ? 1u : 0u);
+            if (kk < kFewSteps || !few)
+              mma_bf16_ts(to, ts + kk * 8, dv + ((kk * 2048) >> 4), kIdescPV,
+                          (!first || kk > 0) ? 1u : 0u);
         };
         while (ok) {
           const ItemW *xp = next(true);
@@ -449,6 +510,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           const bool sk0 = xp->sink[0] != 0, sk1 = xp->sink[1] != 0;
           const int j00 = xp->j0[0], j01 = xp->j1[0], j10 = xp->j0[1], j11 = xp->j1[1];
           release();
+          const int n_few = a.sinks <= 16 * kFewSteps ? nsk : 0; // blocks < n_few have few keys
           ok = mbar_wait(bar(L::kQFull), nq & 1, a.status);
           ++nq;
           ok = ok && mbar_wait(bar(L::kKFull + (g & 1)), (g >> 1) & 1, a.status);
@@ -458,8 +520,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
             // S of this item follows the last P.V of the one before in the pipe;
             // its first P.V waits for P, and so for the epilogue that reads O
             const int first0 = sk0 ? 0 : j00, first1 = sk1 ? 0 : j10;
-            if (uses(0, nsk, sk0, j00, j01)) issue_s(0, 0, g & 1);
-            if (uses(0, nsk, sk1, j10, j11)) issue_s(1, 1, g & 1);
+            if (uses(0, nsk, sk0, j00, j01)) issue_s(0, 0, g & 1, 0 < n_few);
+            if (uses(0, nsk, sk1, j10, j11)) issue_s(1, 1, g & 1, 0 < n_few);
             mma_commit(bar(L::kKEmpty + (g & 1)));
             if (nb == 1) mma_commit(bar(L::kQEmpty));
             for (int j = 0; j < nb && ok; ++j, ++g) {
@@ -476,23 +538,23 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 ok = pa_rdy || mbar_wait(bar(L::kPFull + 0), np0 & 1, a.status);
                 ++np0;
                 if (!ok) break;
-                issue_pv(0, 0, st, j == first0);
+                issue_pv(0, 0, st, j == first0, j < n_few);
                 if (j1 == j01) mma_commit(bar(L::kODone + 0));
               }
               if (j1 < nb) {
                 ok = k_rdy || mbar_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1, a.status);
                 if (!ok) break;
                 tc_fence_after();
-                if (uses(j1, nsk, sk0, j00, j01)) issue_s(0, 0, s1);
+                if (uses(j1, nsk, sk0, j00, j01)) issue_s(0, 0, s1, j1 < n_few);
               }
               if (u1) {
                 ok = mbar_wait(bar(L::kPFull + 1), np1 & 1, a.status);
                 ++np1;
                 if (!ok) break;
-                issue_pv(1, 1, st, j == first1);
+                issue_pv(1, 1, st, j == first1, j < n_few);
                 if (j1 == j11) mma_commit(bar(L::kODone + 1));
               }
-              if (j1 < nb && uses(j1, nsk, sk1, j10, j11)) issue_s(1, 1, s1);
+              if (j1 < nb && uses(j1, nsk, sk1, j10, j11)) issue_s(1, 1, s1, j1 < n_few);
               mma_commit(bar(L::kVEmpty + st));
               if (j1 < nb) mma_commit(bar(L::kKEmpty + s1));
               if (j1 == nb - 1) mma_commit(bar(L::kQEmpty));
@@ -500,7 +562,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           } else {
             // one tile, two S buffers: the next block's S runs while this one's
             // softmax does
-            issue_s(0, ns & 1, g & 1);
+            issue_s(0, ns & 1, g & 1, 0 < n_few);
             ++ns;
             mma_commit(bar(L::kKEmpty + (g & 1)));
             if (nb == 1) mma_commit(bar(L::kQEmpty));
@@ -510,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 ok = mbar_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1, a.status);
                 if (!ok) break;
                 tc_fence_after();
-                issue_s(0, ns & 1, s1);
+                issue_s(0, ns & 1, s1, j + 1 < n_few);
                 ++ns;
                 mma_commit(bar(L::kKEmpty + s1));
                 if (j + 2 == nb) mma_commit(bar(L::kQEmpty));
@@ -518,7 +580,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
               ok = mbar_wait(bar(L::kVFull + st), (g >> 1) & 1, a.status) &&
                    mbar_wait(bar(L::kPFull + (np0 & 1)), (np0 >> 1) & 1, a.status);
               if (!ok) break;
-              issue_pv(0, np0 & 1, st, j == 0);
+              issue_pv(0, np0 & 1, st, j == 0, j < n_few);
               mma_commit(bar(L::kODone + (np0 & 1)));
               ++np0;
               mma_commit(bar(L::kVEmpty + st));
@@ -529,7 +591,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegsW));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftRegs));
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -538,83 +600,116 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     int ns = 0, no = 0;        // S blocks and O tiles of this q tile so far
     float run_lse = -INFINITY; // of the splits folded so far
     while (const ItemW *xp = next(false)) {
-      const int n_parts = xp->n_parts[t];
-      const int n_sink = xp->n_sink, j0 = xp->j0[t], j1 = xp->j1[t], w0 = xp->w0;
-      const bool sink = xp->sink[t] != 0;
-      // the row sees keys < p1, of them those >= p0 or < sinks
-      const int32_t t_row = (xp->tile + t) * T + (row >> gs);
-      const int32_t p1 = xp->kv_len - xp->q_len + t_row + 1, p0 = p1 - a.window;
+      // read again where they are used: the scores need the registers
+      const volatile ItemW *vx = xp;
       float m = -INFINITY, l = 0.f; // running max (log2 units) and sum
       bool failed = false;
       bool begun = false; // O holds an earlier block's
-      for (int j = sink ? 0 : j0; j < j1; ++j) {
-        if (sink && j == n_sink) j = j0; // past what only the other tile sees
-        const int32_t key0 = (j < n_sink ? j : w0 + j - n_sink) * KB;
-        const int n_vis = p1 - key0, n_lo = p0 - key0, n_snk = a.sinks - key0;
+      for (int j = vx->sink[t] ? 0 : vx->j0[t]; j < vx->j1[t]; ++j) {
+        if (j == vx->n_sink && vx->sink[t]) j = vx->j0[t]; // past what only the other tile sees
+        const bool whole = j >= vx->w_begin[t] && j < vx->w_end[t];
         const int buf = NT == 2 ? t : ns & 1;
         failed = __any_sync(
             0xffffffffu, !mbar_wait(bar(L::kSFull + buf), (NT == 2 ? ns : ns >> 1) & 1, a.status));
         if (failed) break;
         tc_fence_after();
-        // blocks every row of the warp sees in full skip the per-column test
-        const bool full = __all_sync(0xffffffffu, n_vis >= KB && (n_lo <= 0 || n_snk >= KB));
         const uint32_t srow = tS(buf) + lane_base;
-        uint32_t v[KB / 32][32]; // the row's scores, in registers from here on
-        float bm;
-        if (full) { // the loads give the maximum of their 32 columns
-          float b4[KB / 32];
-#pragma unroll
-          for (int c = 0; c < KB / 32; ++c) tmem_ld32_max(srow + c * 32, v[c], b4[c]);
-          tmem_wait_ld();
-          bm = b4[0];
-#pragma unroll
-          for (int c = 1; c < KB / 32; ++c) bm = fmaxf(bm, b4[c]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < KB / 32; ++c) tmem_ld32(srow + c * 32, v[c]);
-          tmem_wait_ld();
-          bm = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < KB / 32; ++c) {
-            const uint32_t vis = first_bits(n_vis - 32 * c) &
-                                 (~first_bits(n_lo - 32 * c) | first_bits(n_snk - 32 * c));
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!((vis >> i) & 1u)) v[c][i] = 0xff800000u; // -inf: a weight of zero
-              bm = fmaxf(bm, __uint_as_float(v[c][i]));
-            }
+        float alpha = 1.f, m_sub = 0.f;
+        auto move_max = [&](float bm) { // bm: the block's largest score
+          bm = bm == -INFINITY ? -INFINITY : bm * a.scale_log2;
+          if (bm > m + kRescaleW || (m == -INFINITY && bm != -INFINITY)) {
+            alpha = ex2(m - bm); // 0 when m == -inf
+            m = bm;
           }
-        }
-        bm = bm == -INFINITY ? -INFINITY : bm * a.scale_log2;
-        float m_use = m, alpha = 1.f;
-        if (bm > m + kRescaleW || (m == -INFINITY && bm != -INFINITY)) {
-          m_use = bm;
-          alpha = ex2(m - bm); // 0 when m == -inf
-        }
-        const float m_sub = m_use == -INFINITY ? 0.f : m_use;
-        // P = 2^(s * scale - m) as bf16 pairs over the row's first KB/2 columns
-        const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
-        const uint64_t neg2 = f32x2(-m_sub, -m_sub);
+          m_sub = m == -INFINITY ? 0.f : m;
+        };
+        // P = 2^(s * scale - m) of 32 columns as bf16 pairs over 16 of S's
         uint64_t psum2 = 0;
-#pragma unroll
-        for (int c = 0; c < KB / 32; ++c) {
+        auto weights = [&](int c, const uint32_t (&v)[32]) {
+          const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+          const uint64_t neg2 = f32x2(-m_sub, -m_sub);
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float x0, x1;
-            f32x2_split(ffma2r(f32x2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])),
-                               scale2, neg2),
-                        x0, x1);
+            f32x2_split(
+                ffma2r(f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, neg2), x0,
+                x1);
             const float q0 = ex2(x0), q1 = ex2(x1);
             psum2 = fadd2(psum2, f32x2(q0, q1));
             pk[i / 2] = pack_bf16(q0, q1);
           }
           tmem_st16(srow + c * 16, pk);
+        };
+        if (whole) {
+          uint32_t v[KB / 32][32]; // the row's scores, in registers from here on
+          float b4[KB / 32];       // the loads give the maximum of their 32 columns
+#pragma unroll
+          for (int c = 0; c < KB / 32; ++c) tmem_ld32_max(srow + c * 32, v[c], b4[c]);
+          tmem_wait_ld();
+          float bm = b4[0];
+#pragma unroll
+          for (int c = 1; c < KB / 32; ++c) bm = fmaxf(bm, b4[c]);
+          move_max(bm);
+#pragma unroll
+          for (int c = 0; c < KB / 32; ++c) weights(c, v[c]);
+        } else {
+          // 32 columns at a time, read twice.  The row sees keys < p1, of them
+          // those >= p1 - window or < sinks; what the warp's rows see of 32
+          // columns may be all of them, none (no load, no exponentials), or not
+          // the same (a test a column): the first row's limits are `span` below
+          // the last one's.
+          const int key0 = (j < vx->n_sink ? j : vx->w0 + j - vx->n_sink) * KB;
+          const int32_t p1_w = vx->kv_len - vx->q_len + (vx->tile + t) * T +
+                               (((warp & 3) * 32) >> gs) + 1;
+          const int32_t p1 = p1_w + (lane >> gs);
+          uint32_t cls = 0; // bit c: all of columns 32c ..; bit 8 + c: none of them
+          {
+            const int span = 31 >> gs, snk = a.sinks - key0;
+            const int vis_0 = p1_w - key0, vis_31 = vis_0 + span;
+            const int lo_0 = vis_0 - a.window, lo_31 = lo_0 + span;
+#pragma unroll
+            for (int c = 0; c < KB / 32; ++c) {
+              if (vis_0 >= 32 * c + 32 && (lo_31 <= 32 * c || snk >= 32 * c + 32)) cls |= 1u << c;
+              if (vis_31 <= 32 * c || (lo_0 >= 32 * c + 32 && snk <= 32 * c)) cls |= 256u << c;
+            }
+          }
+          uint32_t v[32];
+          auto load = [&](int c) {
+            tmem_ld32(srow + c * 32, v);
+            tmem_wait_ld();
+            if (cls >> c & 1u) return;
+            const int at = key0 + 32 * c;
+            const uint32_t vis = first_bits(p1 - at) &
+                                 (~first_bits(p1 - a.window - at) | first_bits(a.sinks - at));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((vis >> i) & 1u)) v[i] = 0xff800000u; // -inf: a weight of zero
+          };
+          float bm = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < KB / 32; ++c) {
+            if (cls >> (8 + c) & 1u) continue;
+            load(c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              bm = fmax3(bm, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          }
+          move_max(bm);
+#pragma unroll 1
+          for (int c = 0; c < KB / 32; ++c) { // (its P lies over columns read before)
+            if (cls >> (8 + c) & 1u) {
+              const uint32_t zero[16] = {};
+              tmem_st16(srow + c * 16, zero);
+            } else {
+              load(c);
+              weights(c, v);
+            }
+          }
         }
         float ps0, ps1;
         f32x2_split(psum2, ps0, ps1);
         l = fmaf(l, alpha, ps0 + ps1);
-        m = m_use;
         // rescale the running O row when the max moved, once the previous P.V
         // has completed (two tiles: S of this block was issued after it)
         if (begun && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -644,6 +739,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       // epilogue: o_s = O / l; bf16 when the tile has one state or this is the
       // last of the folded ones, else the fp32 state; a thread stores its own row
       const ItemW &x = *xp;
+      const int n_parts = x.n_parts[t];
       int ln = lane; // opaque: what follows from it is not kept over the blocks
       asm volatile("" : "+r"(ln));
       if (n_parts > 0) {
@@ -784,6 +880,7 @@ cudaError_t launch_prefill_window(const AttnArgs &a, const int32_t *group_off, i
   w.parts = a.parts;
   w.folds = folds;
   w.kv_rows = a.kv_rows;
+  w.slots = a.kv_rows / a.Hkv;
   w.scale_log2 = a.scale_log2;
   w.num_pages = a.num_pages;
   w.reqs = a.reqs;
