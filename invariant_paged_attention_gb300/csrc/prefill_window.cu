@@ -46,7 +46,6 @@ constexpr int kThreadsW = 384;
 constexpr int kItemsW = 3;               // items in flight
 constexpr int kAtomQW = kTileRows * 128; // one SW128 column block of a q tile
 constexpr float kRescaleW = 16.0f;       // log2 units the running max may lag a block's
-constexpr int kFewSteps = 2;             // of 16 keys: sinks that fit them are not a whole block
 
 struct WindowPrefillArgs {
   int32_t Hq, Hkv, D, G, split, tile_tokens, batch, page_shift, window, sinks, parts, folds;
@@ -120,6 +119,35 @@ __device__ __forceinline__ void gather4(uint32_t dst, const void *tmap, int32_t 
                : "memory");
 }
 
+// The MMAs of ptx.cuh for a warp that runs together, issued by the lane whose
+// `lead` is set: operands that are the same on every lane stay in uniform
+// registers, where the instruction wants them.
+__device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d, uint64_t da, uint64_t db,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p, q;\n\t"
+               "setp.ne.b32 p, %4, 0;\n\t"
+               "setp.ne.b32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+               "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "r"(lead)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ts_lead(uint32_t lead, uint32_t d, uint32_t ta, uint64_t db,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p, q;\n\t"
+               "setp.ne.b32 p, %4, 0;\n\t"
+               "setp.ne.b32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+               "r"(ta), "l"(db), "r"(idesc), "r"(accumulate), "r"(lead)
+               : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint32_t lead, uint32_t bar) {
+  asm volatile("{\n\t.reg .pred q;\n\t"
+               "setp.ne.b32 q, %1, 0;\n\t"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               "\n\t}" ::"r"(bar), "r"(lead)
+               : "memory");
+}
+
 // N words of a thread's row, 32 bytes a store where out allows it
 template <int N>
 __device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[N]) {
@@ -149,7 +177,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   using L = SmemW<D>;
   constexpr int NT = L::NT, KB = L::KB;
   constexpr uint32_t kIdescS = idesc_bf16(128, KB, false);
-  constexpr uint32_t kIdescFew = idesc_bf16(128, 16 * kFewSteps, false);
   constexpr uint32_t kIdescPV = idesc_bf16(128, D, true);
   constexpr uint32_t kTmemCols = 512;
 
@@ -163,7 +190,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   auto sV = [&](int st) { return sbase + L::kRing + (2 * st + 1) * L::kKV; };
   ItemW *items = reinterpret_cast<ItemW *>(smem + L::kItem);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kSlot);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (warp == kMmaWarpW) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   if (tid == 0) {
@@ -188,7 +216,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // TMEM columns: S buffers (one a tile; two of the one tile) from 0, O from 256
   auto tS = [&](int i) { return tmem + static_cast<uint32_t>(KB) * i; };
   auto tO = [&](int t) { return tmem + 256u + static_cast<uint32_t>(D) * t; };
@@ -412,9 +440,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           const bool needed = (grp >> 2) >= u && (grp >> 2) < v;
           // The MMAs take a whole block: K columns that no row sees may hold
           // anything, V rows must be zeros.
-          const bool few = j < n_sink && a.sinks <= 16 * kFewSteps;
-          const bool zeros = !keys && !needed && (!few || (grp >> 2) < kFewSteps);
-          const int copied = keys ? v - u : few ? kFewSteps : KB / 16;
+          const bool zeros = !keys && !needed;
+          const int copied = keys ? v - u : KB / 16;
           fetch(j + 1, pg); // in flight while this block's copies are issued
           ok = __all_sync(0xffffffffu,
                           g < 2 || mbar_wait(empty0 + 8 * st, ((g >> 1) - 1) & 1, a.status));
@@ -467,124 +494,129 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       }
     } else if (warp == kMmaWarpW) {
       // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        // descriptors built once: a K step only advances the address field
-        const uint64_t dQ0 = desc_sw128(sQ(0), 16, 1024), dQ1 = desc_sw128(sQ(NT - 1), 16, 1024);
-        const uint64_t dK0 = desc_sw128(sK(0), 16, 1024), dK1 = desc_sw128(sK(1), 16, 1024);
-        const uint64_t dV0 = desc_sw128(sV(0), L::kAtom, 1024);
-        const uint64_t dV1 = desc_sw128(sV(1), L::kAtom, 1024);
-        int g = 0, nq = 0;    // blocks and q tile pairs so far
-        int ns = 0;           // S blocks so far (one tile)
-        int np0 = 0, np1 = 0; // P blocks of each tile so far
-        bool ok = true;
-        // S and P.V of a block, or of its first kFewSteps steps of 16 keys
-        // (the counts are known here: operands that follow data would go
-        // through vector registers, 250 us of 950 for W = 1024 below)
-        auto issue_s = [&](int t, int buf, int st, bool few) {
-          uint64_t dq = t ? dQ1 : dQ0, dk = st ? dK1 : dK0;
-          asm volatile("" : "+l"(dq), "+l"(dk)); // kept from hoisting: 32 registers
-          const uint32_t ts = tS(buf), idesc = few ? kIdescFew : kIdescS;
+      // The warp runs together, one lane issues: what the MMAs take is uniform.
+      // Every block is taken whole: with N and the steps of P.V held to what a
+      // block's rows see, their operands followed data and went through vector
+      // registers (W = 1024: 795 -> 950 us).
+      const uint32_t lead = lane == 0;
+      auto all_wait = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(b, parity, a.status)) != 0;
+      };
+      auto all_try = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try(b, parity)) != 0;
+      };
+      auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      // a K step only advances the address field of a descriptor
+      const uint64_t dQ0 = desc_sw128(sQ(0), 16, 1024), dQ1 = desc_sw128(sQ(NT - 1), 16, 1024);
+      const uint64_t dK0 = desc_sw128(sK(0), 16, 1024), dK1 = desc_sw128(sK(1), 16, 1024);
+      const uint64_t dV0 = desc_sw128(sV(0), L::kAtom, 1024);
+      const uint64_t dV1 = desc_sw128(sV(1), L::kAtom, 1024);
+      int g = 0, nq = 0;    // blocks and q tile pairs so far
+      int ns = 0;           // S blocks so far (one tile)
+      int np0 = 0, np1 = 0; // P blocks of each tile so far
+      bool ok = true;
+      auto issue_s = [&](int t, int buf, int st) {
+        const uint64_t dq = t ? dQ1 : dQ0, dk = st ? dK1 : dK0;
+        const uint32_t ts = tS(buf);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t qoff = ((kk >> 2) * kAtomQW + (kk & 3) * 32) >> 4;
-            const uint32_t koff = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(ts, dq + qoff, dk + koff, idesc, kk > 0);
-          }
-          mma_commit(bar(L::kSFull + buf));
-        };
-        auto issue_pv = [&](int t, int buf, int st, bool first, bool few) {
-          tc_fence_after();
-          uint64_t dv = st ? dV1 : dV0;
-          asm volatile("" : "+l"(dv));
-          const uint32_t to = tO(t), ts = tS(buf);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t qoff = ((kk >> 2) * kAtomQW + (kk & 3) * 32) >> 4;
+          const uint32_t koff = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
+          mma_ss_lead(lead, ts, dq + qoff, dk + koff, kIdescS, kk > 0);
+        }
+        commit_lead(lead, bar(L::kSFull + buf));
+      };
+      auto issue_pv = [&](int t, int buf, int st, bool first) {
+        tc_fence_after();
+        const uint64_t dv = st ? dV1 : dV0;
+        const uint32_t to = tO(t), ts = tS(buf);
 #pragma unroll
-          for (int kk = 0; kk < KB / 16; ++kk)
-            if (kk < kFewSteps || !few)
-              mma_bf16_ts(to, ts + kk * 8, dv + ((kk * 2048) >> 4), kIdescPV,
-                          (!first || kk > 0) ? 1u : 0u);
-        };
-        while (ok) {
-          const ItemW *xp = next(true);
-          if (!xp) break;
-          const int nb = xp->nb, nsk = xp->n_sink;
-          const bool sk0 = xp->sink[0] != 0, sk1 = xp->sink[1] != 0;
-          const int j00 = xp->j0[0], j01 = xp->j1[0], j10 = xp->j0[1], j11 = xp->j1[1];
-          release();
-          const int n_few = a.sinks <= 16 * kFewSteps ? nsk : 0; // blocks < n_few have few keys
-          ok = mbar_wait(bar(L::kQFull), nq & 1, a.status);
-          ++nq;
-          ok = ok && mbar_wait(bar(L::kKFull + (g & 1)), (g >> 1) & 1, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          if constexpr (NT == 2) {
-            // S of this item follows the last P.V of the one before in the pipe;
-            // its first P.V waits for P, and so for the epilogue that reads O
-            const int first0 = sk0 ? 0 : j00, first1 = sk1 ? 0 : j10;
-            if (uses(0, nsk, sk0, j00, j01)) issue_s(0, 0, g & 1, 0 < n_few);
-            if (uses(0, nsk, sk1, j10, j11)) issue_s(1, 1, g & 1, 0 < n_few);
-            mma_commit(bar(L::kKEmpty + (g & 1)));
-            if (nb == 1) mma_commit(bar(L::kQEmpty));
-            for (int j = 0; j < nb && ok; ++j, ++g) {
-              const int st = g & 1, s1 = st ^ 1, j1 = j + 1;
-              const bool u0 = uses(j, nsk, sk0, j00, j01), u1 = uses(j, nsk, sk1, j10, j11);
-              // a barrier's answer takes ~170 cycles even when its phase is
-              // complete: ask for the three at once
-              const bool v_rdy = mbar_try(bar(L::kVFull + st), (g >> 1) & 1);
-              const bool pa_rdy = u0 && mbar_try(bar(L::kPFull + 0), np0 & 1);
-              const bool k_rdy = j1 < nb && mbar_try(bar(L::kKFull + s1), ((g + 1) >> 1) & 1);
-              ok = v_rdy || mbar_wait(bar(L::kVFull + st), (g >> 1) & 1, a.status);
-              if (!ok) break;
-              if (u0) {
-                ok = pa_rdy || mbar_wait(bar(L::kPFull + 0), np0 & 1, a.status);
-                ++np0;
-                if (!ok) break;
-                issue_pv(0, 0, st, j == first0, j < n_few);
-                if (j1 == j01) mma_commit(bar(L::kODone + 0));
-              }
-              if (j1 < nb) {
-                ok = k_rdy || mbar_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1, a.status);
-                if (!ok) break;
-                tc_fence_after();
-                if (uses(j1, nsk, sk0, j00, j01)) issue_s(0, 0, s1, j1 < n_few);
-              }
-              if (u1) {
-                ok = mbar_wait(bar(L::kPFull + 1), np1 & 1, a.status);
-                ++np1;
-                if (!ok) break;
-                issue_pv(1, 1, st, j == first1, j < n_few);
-                if (j1 == j11) mma_commit(bar(L::kODone + 1));
-              }
-              if (j1 < nb && uses(j1, nsk, sk1, j10, j11)) issue_s(1, 1, s1, j1 < n_few);
-              mma_commit(bar(L::kVEmpty + st));
-              if (j1 < nb) mma_commit(bar(L::kKEmpty + s1));
-              if (j1 == nb - 1) mma_commit(bar(L::kQEmpty));
-            }
-          } else {
-            // one tile, two S buffers: the next block's S runs while this one's
-            // softmax does
-            issue_s(0, ns & 1, g & 1, 0 < n_few);
-            ++ns;
-            mma_commit(bar(L::kKEmpty + (g & 1)));
-            if (nb == 1) mma_commit(bar(L::kQEmpty));
-            for (int j = 0; j < nb && ok; ++j, ++g) {
-              const int st = g & 1, s1 = st ^ 1;
-              if (j + 1 < nb) {
-                ok = mbar_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1, a.status);
-                if (!ok) break;
-                tc_fence_after();
-                issue_s(0, ns & 1, s1, j + 1 < n_few);
-                ++ns;
-                mma_commit(bar(L::kKEmpty + s1));
-                if (j + 2 == nb) mma_commit(bar(L::kQEmpty));
-              }
-              ok = mbar_wait(bar(L::kVFull + st), (g >> 1) & 1, a.status) &&
-                   mbar_wait(bar(L::kPFull + (np0 & 1)), (np0 >> 1) & 1, a.status);
-              if (!ok) break;
-              issue_pv(0, np0 & 1, st, j == 0, j < n_few);
-              mma_commit(bar(L::kODone + (np0 & 1)));
+        for (int kk = 0; kk < KB / 16; ++kk)
+          mma_ts_lead(lead, to, ts + kk * 8, dv + ((kk * 2048) >> 4), kIdescPV,
+                      (!first || kk > 0) ? 1u : 0u);
+      };
+      while (ok) {
+        const ItemW *xp = next(false);
+        if (!xp) break;
+        const int nb = same(xp->nb), nsk = same(xp->n_sink);
+        const bool sk0 = same(xp->sink[0]) != 0, sk1 = same(xp->sink[1]) != 0;
+        const int j00 = same(xp->j0[0]), j01 = same(xp->j1[0]);
+        const int j10 = same(xp->j0[1]), j11 = same(xp->j1[1]);
+        __syncwarp();
+        if (lane == 0) release();
+        ok = all_wait(bar(L::kQFull), nq & 1);
+        ++nq;
+        ok = ok && all_wait(bar(L::kKFull + (g & 1)), (g >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if constexpr (NT == 2) {
+          // S of this item follows the last P.V of the one before in the pipe;
+          // its first P.V waits for P, and so for the epilogue that reads O
+          const int first0 = sk0 ? 0 : j00, first1 = sk1 ? 0 : j10;
+          if (uses(0, nsk, sk0, j00, j01)) issue_s(0, 0, g & 1);
+          if (uses(0, nsk, sk1, j10, j11)) issue_s(1, 1, g & 1);
+          commit_lead(lead, bar(L::kKEmpty + (g & 1)));
+          if (nb == 1) commit_lead(lead, bar(L::kQEmpty));
+          for (int j = 0; j < nb && ok; ++j, ++g) {
+            const int st = g & 1, s1 = st ^ 1, j1 = j + 1;
+            const bool u0 = uses(j, nsk, sk0, j00, j01), u1 = uses(j, nsk, sk1, j10, j11);
+            // a barrier's answer takes ~170 cycles even when its phase is
+            // complete: ask for the three at once
+            const bool v_rdy = all_try(bar(L::kVFull + st), (g >> 1) & 1);
+            const bool pa_rdy = u0 && all_try(bar(L::kPFull + 0), np0 & 1);
+            const bool k_rdy = j1 < nb && all_try(bar(L::kKFull + s1), ((g + 1) >> 1) & 1);
+            ok = v_rdy || all_wait(bar(L::kVFull + st), (g >> 1) & 1);
+            if (!ok) break;
+            if (u0) {
+              ok = pa_rdy || all_wait(bar(L::kPFull + 0), np0 & 1);
               ++np0;
-              mma_commit(bar(L::kVEmpty + st));
+              if (!ok) break;
+              issue_pv(0, 0, st, j == first0);
+              if (j1 == j01) commit_lead(lead, bar(L::kODone + 0));
             }
+            if (j1 < nb) {
+              ok = k_rdy || all_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              if (uses(j1, nsk, sk0, j00, j01)) issue_s(0, 0, s1);
+            }
+            if (u1) {
+              ok = all_wait(bar(L::kPFull + 1), np1 & 1);
+              ++np1;
+              if (!ok) break;
+              issue_pv(1, 1, st, j == first1);
+              if (j1 == j11) commit_lead(lead, bar(L::kODone + 1));
+            }
+            if (j1 < nb && uses(j1, nsk, sk1, j10, j11)) issue_s(1, 1, s1);
+            commit_lead(lead, bar(L::kVEmpty + st));
+            if (j1 < nb) commit_lead(lead, bar(L::kKEmpty + s1));
+            if (j1 == nb - 1) commit_lead(lead, bar(L::kQEmpty));
+          }
+        } else {
+          // one tile, two S buffers: the next block's S runs while this one's
+          // softmax does
+          issue_s(0, ns & 1, g & 1);
+          ++ns;
+          commit_lead(lead, bar(L::kKEmpty + (g & 1)));
+          if (nb == 1) commit_lead(lead, bar(L::kQEmpty));
+          for (int j = 0; j < nb && ok; ++j, ++g) {
+            const int st = g & 1, s1 = st ^ 1;
+            if (j + 1 < nb) {
+              ok = all_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(0, ns & 1, s1);
+              ++ns;
+              commit_lead(lead, bar(L::kKEmpty + s1));
+              if (j + 2 == nb) commit_lead(lead, bar(L::kQEmpty));
+            }
+            ok = all_wait(bar(L::kVFull + st), (g >> 1) & 1) &&
+                 all_wait(bar(L::kPFull + (np0 & 1)), (np0 >> 1) & 1);
+            if (!ok) break;
+            issue_pv(0, np0 & 1, st, j == 0);
+            commit_lead(lead, bar(L::kODone + (np0 & 1)));
+            ++np0;
+            commit_lead(lead, bar(L::kVEmpty + st));
           }
         }
       }
