@@ -11,14 +11,15 @@
 // rounding, so nothing is rounded twice).
 //
 // A head is a row of D/16 lanes, 16 columns a lane as two 16-byte pieces that
-// hold both columns of each of its pairs: lane c has frequencies 8c .. 8c+7,
-// columns 8c .. and rot/2 + 8c .. (halves) or 16c .. 16c+15 (interleaved); the
-// lanes behind the rotating columns, and values, just 16 columns.  So a pair
-// never crosses lanes, the norm is one shuffle sum, and a lane's eight (cos,
-// sin) serve every head of its token.  A warp runs through the heads of one
-// token (queries, keys, values) with kInFlight steps' loads under way; the
-// token's slot and position are found meanwhile.  A call with few tokens
-// splits a token's heads over several warps, down to a step a warp.
+// hold both columns of each of its eight pairs: lane c has frequencies 8c ..
+// 8c+7, columns 8c .. and rot/2 + 8c .. (halves) or 16c .. 16c+15
+// (interleaved); the lanes behind the rotating columns, and values, just 16
+// columns.  So a pair never crosses lanes, the norm is one shuffle sum, and a
+// lane's factors (cos and sin times the weights of their columns) serve every
+// head of its token; the arithmetic runs on fp32 pairs.  A warp runs through
+// the heads of one token (queries, keys, values) with kRing steps' loads
+// under way; the token's slot and position are found meanwhile.  A call with
+// few tokens splits a token's heads over several warps, down to a step a warp.
 #include <algorithm>
 
 #include "bia_internal.h"
@@ -31,47 +32,56 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kInFlight = 4; // steps whose loads are issued together
+constexpr int kRing = 2; // steps of a warp whose loads are under way (1 KB of shared memory each)
 enum RopeDest { kToRows, kToPages, kToPagesFp8 };
 
-// 16 bytes that nobody else reads (also through q_out == q: a row is loaded
-// and stored by the same lanes, so no .nc).
-__device__ __forceinline__ uint4 ld_once(const uint16_t *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// The lane's sixteen columns as a[8], b[8]: pair f is (a[f], b[f]).
+template <bool INTER>
+__device__ __forceinline__ void unpack(const uint4 (&x)[2], float (&a)[8], float (&b)[8]) {
+  const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+  if constexpr (INTER) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int f = 0; f < 8; ++f) {
+      a[f] = __uint_as_float(u[f] << 16);
+      b[f] = __uint_as_float(u[f] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[2 * i] = __uint_as_float(u[i] << 16);
+      a[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      b[2 * i] = __uint_as_float(u[4 + i] << 16);
+      b[2 * i + 1] = __uint_as_float(u[4 + i] & 0xffff0000u);
+    }
   }
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                    pack_bf16(x[6], x[7]));
+template <bool INTER>
+__device__ __forceinline__ void pack(const float (&a)[8], const float (&b)[8], uint4 (&x)[2]) {
+  if constexpr (INTER) {
+    x[0] = make_uint4(pack_bf16(a[0], b[0]), pack_bf16(a[1], b[1]), pack_bf16(a[2], b[2]),
+                      pack_bf16(a[3], b[3]));
+    x[1] = make_uint4(pack_bf16(a[4], b[4]), pack_bf16(a[5], b[5]), pack_bf16(a[6], b[6]),
+                      pack_bf16(a[7], b[7]));
+  } else {
+    x[0] = make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]),
+                      pack_bf16(a[6], a[7]));
+    x[1] = make_uint4(pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3]), pack_bf16(b[4], b[5]),
+                      pack_bf16(b[6], b[7]));
+  }
 }
-// (a, b) turned; explicit roundings, so that every destination has the same bits.
-__device__ __forceinline__ void turn(float a, float b, float c, float s, float &x, float &y) {
-  x = __fmaf_rn(a, c, -__fmul_rn(b, s));
-  y = __fmaf_rn(b, c, __fmul_rn(a, s));
+// max(m, |x|, |y|); a NaN among them is kept.
+__device__ __forceinline__ float max_abs(float m, float x, float y) {
+  float r;
+  asm("{\n\t.reg .f32 p, q;\n\tabs.f32 p, %2;\n\tabs.f32 q, %3;\n\t"
+      "max.NaN.f32 %0, %1, p, q;\n\t}"
+      : "=f"(r) : "f"(m), "f"(x), "f"(y));
+  return r;
 }
-// Eight fp32 as codes under the scale 2^-e = inv; non-finite ones as NaN.
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if ((__float_as_uint(x[i]) & 0x7fffffffu) >= 0x7f800000u) c[i >> 1] |= 0x7fu << (8 * (i & 1));
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+// Four fp32 times inv as four codes.
+__device__ __forceinline__ uint32_t codes4(float x0, float x1, float x2, float x3, float inv) {
+  return e4m3x2(x0 * inv, x1 * inv) | e4m3x2(x2 * inv, x3 * inv) << 16;
 }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 // The request of a token: the largest b with indptr[b] <= token, by the whole
 // warp, 32 probes a round.
@@ -89,8 +99,8 @@ __device__ __forceinline__ int find_request(const int32_t *indptr, int batch, in
   return lo;
 }
 
-template <int LPH, int DEST>
-__global__ void __launch_bounds__(kRopeThreads)
+template <int LPH, int DEST, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 6)
     rope_kernel(const __grid_constant__ RopeArgs a, const int parts) {
   constexpr int HPS = 32 / LPH; // heads a step
   constexpr bool kPaged = DEST != kToRows;
@@ -102,208 +112,270 @@ __global__ void __launch_bounds__(kRopeThreads)
   if (token >= a.total) return;
   const int part = static_cast<int>(w - token * parts);
   const int D = a.D, half = a.rot >> 1;
-  const bool in_row = c * 16 < D;
-  const bool turns = c * 16 < a.rot;
-  const int n_turned = a.Hq + a.Hk;               // q heads (0: none), then k heads
-  const int heads = n_turned + (kPaged ? a.Hk : 0); // then v heads
-  // the lane's two pieces of a head that rotates (or not), and of a value
-  const int col0 = turns && !a.interleaved ? 8 * c : 16 * c;
-  const int col1 = turns && !a.interleaved ? half + 8 * c : 16 * c + 8;
-
-  auto source = [&](int h, int &at0, int &at1) -> const uint16_t * {
-    at0 = h < n_turned ? col0 : 16 * c;
-    at1 = h < n_turned ? col1 : 16 * c + 8;
-    if (h < a.Hq) return a.q + token * a.q_stride + h * D;
-    if (h < n_turned) return a.k + token * a.k_stride + (h - a.Hq) * D;
-    return a.v + token * a.v_stride + (h - n_turned) * D;
+  const bool in_row = c * 16 < D, turns = c * 16 < a.rot;
+  // the lane's two pieces of a head that rotates (or not); of a value 16c, 16c + 8
+  const bool apart = turns && !INTER;
+  const int col0 = apart ? 8 * c : 16 * c, col1 = apart ? half + 8 * c : 16 * c + 8;
+  // steps: of queries, then of keys, then of values; a step is of one kind
+  const int steps_q = (a.Hq + HPS - 1) / HPS, steps_k = (a.Hk + HPS - 1) / HPS;
+  const int steps = steps_q + (kPaged ? 2 : 1) * steps_k;
+  auto kind_of = [&](int s) { return s < steps_q ? 0 : s < steps_q + steps_k ? 1 : 2; };
+  auto head_of = [&](int s, int kind) {
+    return (s - (kind == 0 ? 0 : kind == 1 ? steps_q : steps_q + steps_k)) * HPS + hl;
   };
 
-  int64_t slot = -1; // of the token in the cache
-  float cs[8], sn[8];
-  float wt[16];
-  int wt_of = -1; // whose weights wt holds: 0 q, 1 k
+  // the token's rows at the lane's first head of a step
+  const uint16_t *src[3] = {a.q + token * a.q_stride, a.k + token * a.k_stride,
+                            kPaged ? a.v + token * a.v_stride : nullptr};
+  uint16_t *q_dst = a.q_out + token * a.q_out_stride;
+  uint16_t *k_dst = !a.k_out || DEST == kToPages ? nullptr : a.k_out + token * a.k_out_stride;
+
+  // The lane copies its pieces of a step (and reads only those: no warp meets)
+  // into a ring, so that what is under way holds no registers (four steps in
+  // registers: 16 warps an SM, 76 us for 17868 tokens of 32/8 heads x 128).
+  // Also with q_out == q: a row is loaded and stored by the same lanes.
+  extern __shared__ uint4 ring[];
+  uint4 *mine = ring + (threadIdx.x >> 5) * (kRing * 64) + lane; // step: 64 pieces
+  int n_issued = 0;
+  auto issue = [&](int s) {
+    const int kind = kind_of(s), h = head_of(s, kind);
+    const bool live = s < steps && h < (kind == 0 ? a.Hq : a.Hk) && in_row;
+    const uint16_t *row = (kind == 0 ? src[0] : kind == 1 ? src[1] : src[2]) + (live ? h * D : 0);
+    const uint32_t dst = smem_u32(mine + (n_issued % kRing) * 64);
+    if (live) {
+      cp_async16(dst, row + (kPaged && kind == 2 ? 16 * c : col0), true);
+      cp_async16(dst + 512, row + (kPaged && kind == 2 ? 16 * c + 8 : col1), true);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++n_issued;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kRing; ++i) issue(part + i * parts);
+
+  // while the first heads are on their way: the token's place
+  int64_t slot = -1; // in the cache
+  int32_t pos = 0;
+  if constexpr (kPaged) {
+    const int b = find_request(a.row_indptr, a.batch, token, lane);
+    const int32_t first = __ldg(a.row_indptr + b), next = __ldg(a.row_indptr + b + 1);
+    const int32_t p0 = __ldg(a.kv_indptr + b), p1 = __ldg(a.kv_indptr + b + 1);
+    const int32_t kv_len =
+        p1 > p0 ? ((p1 - p0 - 1) << a.page_shift) + __ldg(a.kv_last_page_len + b) : 0;
+    pos = kv_len - (next - first) + static_cast<int32_t>(token - first);
+    bool ok = pos >= 0 && pos < kv_len; // the host checks the row counts
+    if (ok) {
+      const int32_t page = __ldg(a.kv_indices + p0 + (pos >> a.page_shift));
+      ok = page >= 0 && page < a.num_pages;
+      if (ok)
+        slot = (static_cast<int64_t>(page) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    }
+    if (!ok && lane == 0 && a.status) atomicOr(a.status, kStatusBadPage);
+    if (DEST == kToPages && ok) k_dst = a.k_cache + slot * a.Hk * D;
+  }
+  // factors of a and b: cos and sin, times the weights of the kind they hold;
+  // from a position outside the table: NaN
+  float ac[8], as[8], bc[8], bs[8];
+  const float *have = nullptr; // whose weights
   bool found = false;
-  for (int s0 = part; s0 * HPS < heads; s0 += kInFlight * parts) {
-    uint4 x[kInFlight][2];
+  auto factors = [&](const float *weight) {
+    float cs[8], sn[8];
 #pragma unroll
-    for (int i = 0; i < kInFlight; ++i) {
-      const int h = (s0 + i * parts) * HPS + hl;
-      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-      if (h < heads && in_row) {
-        int at0, at1;
-        const uint16_t *src = source(h, at0, at1);
-        x[i][0] = ld_once(src + at0);
-        x[i][1] = ld_once(src + at1);
+    for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fc00000);
+    for (int ax = 0; ax < a.axes; ++ax) {
+      const int32_t p = a.positions ? __ldg(a.positions + ax * a.total + token) : pos;
+      if (p < 0 || p >= a.num_positions) {
+        if (lane == 0 && a.status) atomicOr(a.status, kStatusBadPosition);
+        continue;
       }
+      if (!turns) continue;
+      // which of the lane's frequencies follow this axis (two bits each)
+      const uint32_t who = a.freq_axis[c >> 1] >> (16 * (c & 1)) & 0xffffu;
+      const uint32_t off = who ^ (0x5555u * ax); // zero pairs follow it
+      const float4 *row =
+          reinterpret_cast<const float4 *>(a.table + static_cast<int64_t>(p) * a.rot + 8 * c);
+      const float4 *row_s = reinterpret_cast<const float4 *>(
+          a.table + static_cast<int64_t>(p) * a.rot + half + 8 * c);
+      const float4 t[4] = {__ldg(row), __ldg(row + 1), __ldg(row_s), __ldg(row_s + 1)};
+      const float tc[8] = {t[0].x, t[0].y, t[0].z, t[0].w, t[1].x, t[1].y, t[1].z, t[1].w};
+      const float ts[8] = {t[2].x, t[2].y, t[2].z, t[2].w, t[3].x, t[3].y, t[3].z, t[3].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((off >> (2 * i) & 3u) == 0) {
+          cs[i] = tc[i];
+          sn[i] = ts[i];
+        }
     }
-    if (!found) { // while the first heads are on their way
-      found = true;
-      int32_t pos = 0;
-      if constexpr (kPaged) {
-        const int b = find_request(a.row_indptr, a.batch, token, lane);
-        const int32_t first = __ldg(a.row_indptr + b), next = __ldg(a.row_indptr + b + 1);
-        const int32_t p0 = __ldg(a.kv_indptr + b), p1 = __ldg(a.kv_indptr + b + 1);
-        const int32_t kv_len =
-            p1 > p0 ? ((p1 - p0 - 1) << a.page_shift) + __ldg(a.kv_last_page_len + b) : 0;
-        pos = kv_len - (next - first) + static_cast<int32_t>(token - first);
-        bool ok = pos >= 0 && pos < kv_len; // the host checks the row counts
-        if (ok) {
-          const int32_t page = __ldg(a.kv_indices + p0 + (pos >> a.page_shift));
-          ok = page >= 0 && page < a.num_pages;
-          if (ok)
-            slot = (static_cast<int64_t>(page) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-        }
-        if (!ok && lane == 0 && a.status) atomicOr(a.status, kStatusBadPage);
+    float wa[8], wb[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.f;
+    if (weight && in_row) {
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float4 u0 = __ldg(reinterpret_cast<const float4 *>(weight + col0 + e));
+        const float4 u1 = __ldg(reinterpret_cast<const float4 *>(weight + col1 + e));
+        v[e] = u0.x, v[e + 1] = u0.y, v[e + 2] = u0.z, v[e + 3] = u0.w;
+        v[8 + e] = u1.x, v[9 + e] = u1.y, v[10 + e] = u1.z, v[11 + e] = u1.w;
       }
-      // the lane's (cos, sin); a position outside the table: NaN
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fc00000);
-      for (int ax = 0; ax < a.axes; ++ax) {
-        const int32_t p = a.positions ? __ldg(a.positions + ax * a.total + token) : pos;
-        const bool ok = p >= 0 && p < a.num_positions;
-        if (!ok) {
-          if (lane == 0 && a.status) atomicOr(a.status, kStatusBadPosition);
-          continue;
-        }
-        if (!turns) continue;
-        // which of the lane's frequencies follow this axis (two bits each)
-        uint32_t mine = 0;
-        const uint32_t who = a.freq_axis[c >> 1] >> (16 * (c & 1));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine |= static_cast<uint32_t>(((who >> (2 * i)) & 3u) == ax) << i;
-        if (mine == 0) continue;
-        const float4 *row =
-            reinterpret_cast<const float4 *>(a.table + static_cast<int64_t>(p) * a.rot + 8 * c);
-        const float4 *row_s = reinterpret_cast<const float4 *>(
-            a.table + static_cast<int64_t>(p) * a.rot + half + 8 * c);
-        const float4 t[4] = {__ldg(row), __ldg(row + 1), __ldg(row_s), __ldg(row_s + 1)};
-        const float tc[8] = {t[0].x, t[0].y, t[0].z, t[0].w, t[1].x, t[1].y, t[1].z, t[1].w};
-        const float ts[8] = {t[2].x, t[2].y, t[2].z, t[2].w, t[3].x, t[3].y, t[3].z, t[3].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((mine >> i) & 1u) {
-            cs[i] = tc[i];
-            sn[i] = ts[i];
-          }
+      for (int e = 0; e < 8; ++e) {
+        wa[e] = INTER ? v[2 * e] : v[e];
+        wb[e] = INTER ? v[2 * e + 1] : v[8 + e];
       }
     }
 #pragma unroll
-    for (int i = 0; i < kInFlight; ++i) {
-      const int h = (s0 + i * parts) * HPS + hl;
-      const bool is_q = h < a.Hq, is_v = kPaged && h >= n_turned;
-      if (is_v && DEST == kToPages) { // as they are
-        if (h < heads && in_row && slot >= 0) {
-          uint16_t *dst = a.v_cache + (slot * a.Hk + (h - n_turned)) * D + 16 * c;
-          *reinterpret_cast<uint4 *>(dst) = x[i][0];
-          *reinterpret_cast<uint4 *>(dst + 8) = x[i][1];
-        }
+    for (int e = 0; e < 8; ++e) {
+      ac[e] = turns ? wa[e] * cs[e] : wa[e];
+      as[e] = wa[e] * sn[e];
+      bc[e] = turns ? wb[e] * cs[e] : wb[e];
+      bs[e] = -(wb[e] * sn[e]);
+    }
+  };
+#pragma unroll 1
+  for (int s = part, i = 0; s < steps; s += parts, ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    uint4 x[2] = {mine[(i % kRing) * 64], mine[(i % kRing) * 64 + 32]};
+    const int kind = kind_of(s), h = head_of(s, kind); // the same kind on the warp
+    const bool live = h < (kind == 0 ? a.Hq : a.Hk) && in_row;
+    if (!live) x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    issue(s + kRing * parts);
+    if (kind == 2 && DEST == kToPages) { // as they are
+      if (live && slot >= 0) {
+        uint16_t *dst = a.v_cache + slot * a.Hk * D + h * D + 16 * c;
+        *reinterpret_cast<uint4 *>(dst) = x[0];
+        *reinterpret_cast<uint4 *>(dst + 8) = x[1];
       }
-      float y0[8], y1[8];
-      unpack8(x[i][0], y0);
-      unpack8(x[i][1], y1);
-      const float *weight = is_q ? a.q_weight : a.k_weight;
-      if (a.q_weight || a.k_weight) { // uniform; the lanes of a head meet
-        float ss = 0.f;
+      continue;
+    }
+    float ya[8], yb[8];
+    if (INTER && kind == 2) unpack<false>(x, ya, yb);
+    else unpack<INTER>(x, ya, yb);
+    if (kind != 2) {
+      const float *weight = kind == 0 ? a.q_weight : a.k_weight;
+      if (!found || have != weight) { // once, and again where the keys begin
+        found = true;
+        have = weight;
+        factors(weight);
+      }
+      float r = 1.f;
+      if (weight) { // the lanes of a head meet
+        uint64_t ss2 = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y0[e], y0[e], fmaf(y1[e], y1[e], ss));
+        for (int e = 0; e < 8; e += 2) {
+          ffma2(ss2, f32x2(ya[e], ya[e + 1]), f32x2(ya[e], ya[e + 1]));
+          ffma2(ss2, f32x2(yb[e], yb[e + 1]), f32x2(yb[e], yb[e + 1]));
+        }
+        float s_lo, s_hi;
+        f32x2_split(ss2, s_lo, s_hi);
+        float ss = s_lo + s_hi;
 #pragma unroll
         for (int off = LPH / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        if (!is_v && weight && in_row) {
-          const int want = is_q ? 0 : 1;
-          if (wt_of != want) { // once, and again where the keys begin
-            wt_of = want;
+        r = rsqrtf(__fmaf_rn(ss, a.inv_D, a.eps));
+      }
+      // explicit roundings: every destination has the same bits
+      const uint64_t r2 = f32x2(r, r);
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const float4 u = __ldg(reinterpret_cast<const float4 *>(weight + col0 + e));
-              const float4 v = __ldg(reinterpret_cast<const float4 *>(weight + col1 + e));
-              wt[e] = u.x, wt[e + 1] = u.y, wt[e + 2] = u.z, wt[e + 3] = u.w;
-              wt[8 + e] = v.x, wt[9 + e] = v.y, wt[10 + e] = v.z, wt[11 + e] = v.w;
-            }
-          }
-          const float r = rsqrtf(__fmaf_rn(ss, a.inv_D, a.eps));
+      for (int e = 0; e < 8; e += 2) {
+        const uint64_t a2 = f32x2(ya[e], ya[e + 1]), b2 = f32x2(yb[e], yb[e + 1]);
+        uint64_t na = fmul2(a2, f32x2(ac[e], ac[e + 1]));
+        uint64_t nb = fmul2(b2, f32x2(bc[e], bc[e + 1]));
+        if (turns) {
+          ffma2(na, b2, f32x2(bs[e], bs[e + 1]));
+          ffma2(nb, a2, f32x2(as[e], as[e + 1]));
+        }
+        if (weight) {
+          na = fmul2(na, r2);
+          nb = fmul2(nb, r2);
+        }
+        f32x2_split(na, ya[e], ya[e + 1]);
+        f32x2_split(nb, yb[e], yb[e + 1]);
+      }
+    }
+    if (kind != 2 && live) { // a bf16 row of q, or of k (rows, or the cache's)
+      uint16_t *dst = kind == 0 ? q_dst : k_dst;
+      if (dst) {
+        uint4 o[2];
+        pack<INTER>(ya, yb, o);
+        *reinterpret_cast<uint4 *>(dst + h * D + col0) = o[0];
+        *reinterpret_cast<uint4 *>(dst + h * D + col1) = o[1];
+      }
+    }
+    if (DEST == kToPagesFp8 && kind != 0) {
+      // the row's largest finite magnitude gives its scale
+      float big = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) big = max_abs(big, ya[e], yb[e]);
+      const bool odd = !finite(big); // an infinity or NaN among them: rare
+      if (odd) {
+        big = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          big = fmaxf(big, fmaxf(finite(ya[e]) ? fabsf(ya[e]) : 0.f,
+                                 finite(yb[e]) ? fabsf(yb[e]) : 0.f));
+      }
+#pragma unroll
+      for (int off = LPH / 2; off >= 1; off >>= 1)
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+      if (live && slot >= 0) {
+        const int ex = row_exponent(big);
+        const float inv = exp2_int(-ex);
+        if (odd) { // stored as NaN (the conversion keeps NaN, but not infinities)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            y0[e] = __fmul_rn(__fmul_rn(y0[e], r), wt[e]);
-            y1[e] = __fmul_rn(__fmul_rn(y1[e], r), wt[8 + e]);
+            if (!finite(ya[e])) ya[e] = __int_as_float(0x7fc00000);
+            if (!finite(yb[e])) yb[e] = __int_as_float(0x7fc00000);
           }
         }
-      }
-      if (turns && !is_v) {
-        if (a.interleaved) { // pairs inside each piece
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p0 = y0[2 * e], p1 = y0[2 * e + 1], q0 = y1[2 * e], q1 = y1[2 * e + 1];
-            turn(p0, p1, cs[e], sn[e], y0[2 * e], y0[2 * e + 1]);
-            turn(q0, q1, cs[4 + e], sn[4 + e], y1[2 * e], y1[2 * e + 1]);
-          }
+        const int64_t row = slot * a.Hk + h;
+        uint8_t *dst = (kind == 2 ? a.v_codes : a.k_codes) + row * D;
+        if (INTER && kind != 2) {
+          *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(
+              codes4(ya[0], yb[0], ya[1], yb[1], inv), codes4(ya[2], yb[2], ya[3], yb[3], inv),
+              codes4(ya[4], yb[4], ya[5], yb[5], inv), codes4(ya[6], yb[6], ya[7], yb[7], inv));
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float p0 = y0[e], p1 = y1[e];
-            turn(p0, p1, cs[e], sn[e], y0[e], y1[e]);
-          }
-        }
-      }
-      if constexpr (DEST == kToPagesFp8) {
-        // the row's largest finite magnitude gives its scale
-        uint32_t big = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t b0 = __float_as_uint(y0[e]) & 0x7fffffffu;
-          const uint32_t b1 = __float_as_uint(y1[e]) & 0x7fffffffu;
-          big = max(big, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
-        }
-#pragma unroll
-        for (int off = LPH / 2; off >= 1; off >>= 1)
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, off));
-        if (!is_q && h < heads && in_row && slot >= 0) {
-          const int e = row_exponent(__uint_as_float(big));
-          const float inv = exp2_int(-e);
-          const int64_t row = slot * a.Hk + (is_v ? h - n_turned : h - a.Hq);
-          uint8_t *dst = (is_v ? a.v_codes : a.k_codes) + row * D;
-          const uint2 r0 = codes8(y0, inv), r1 = codes8(y1, inv);
-          if (is_v) {
+          const uint2 r0 = make_uint2(codes4(ya[0], ya[1], ya[2], ya[3], inv),
+                                      codes4(ya[4], ya[5], ya[6], ya[7], inv));
+          const uint2 r1 = make_uint2(codes4(yb[0], yb[1], yb[2], yb[3], inv),
+                                      codes4(yb[4], yb[5], yb[6], yb[7], inv));
+          if (kind == 2) {
             *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(r0.x, r0.y, r1.x, r1.y);
           } else {
             *reinterpret_cast<uint2 *>(dst + col0) = r0;
             *reinterpret_cast<uint2 *>(dst + col1) = r1;
           }
-          if (c == 0) (is_v ? a.v_scale : a.k_scale)[row] = static_cast<uint8_t>(e + 127);
         }
-      }
-      if (h < n_turned && in_row) { // a bf16 row of q, or of k (rows, or the cache's)
-        uint16_t *dst = nullptr;
-        if (is_q) dst = a.q_out + token * a.q_out_stride + h * D;
-        else if (DEST != kToPages)
-          dst = a.k_out ? a.k_out + token * a.k_out_stride + (h - a.Hq) * D : nullptr;
-        else if (slot >= 0)
-          dst = a.k_cache + (slot * a.Hk + (h - a.Hq)) * D;
-        if (dst) {
-          *reinterpret_cast<uint4 *>(dst + col0) = pack8(y0);
-          *reinterpret_cast<uint4 *>(dst + col1) = pack8(y1);
-        }
+        if (c == 0) (kind == 2 ? a.v_scale : a.k_scale)[row] = static_cast<uint8_t>(ex + 127);
       }
     }
   }
+  cp_async_wait_all(); // no copy outlives the CTA
 }
 
-template <int LPH, int DEST>
-cudaError_t launch_rope_ld(const RopeArgs &a, cudaStream_t s) {
+template <int LPH, int DEST, bool INTER>
+cudaError_t launch_rope_ldi(const RopeArgs &a, cudaStream_t s) {
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  const int heads = a.Hq + a.Hk + (DEST != kToRows ? a.Hk : 0);
-  const int64_t steps = (heads + 32 / LPH - 1) / (32 / LPH);
+  const int hps = 32 / LPH;
+  const int64_t steps =
+      (a.Hq + hps - 1) / hps + (DEST != kToRows ? 2 : 1) * ((a.Hk + hps - 1) / hps);
   // warps a token: while the call has fewer than 8 warps an SM
   const int parts = static_cast<int>(std::clamp<int64_t>(8 * sms / a.total, 1, steps));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.total * parts + kRopeWarps - 1) / kRopeWarps));
   cfg.blockDim = dim3(kRopeThreads);
+  cfg.dynamicSmemBytes = kRopeWarps * kRing * 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {chained_launch_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_kernel<LPH, DEST>, a, parts);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<LPH, DEST, INTER>, a, parts);
+}
+
+template <int LPH, int DEST>
+cudaError_t launch_rope_ld(const RopeArgs &a, cudaStream_t s) {
+  return a.interleaved ? launch_rope_ldi<LPH, DEST, true>(a, s)
+                       : launch_rope_ldi<LPH, DEST, false>(a, s);
 }
 
 template <int DEST>
