@@ -977,19 +977,34 @@ def _rope_types(table, positions, q_weight, k_weight, status):
                         ("status", status, I32, True))
 
 
-def _rope_dense(at, table, positions, q_weight, k_weight, status) -> bool:
-    return (_dense(at, F32, table) and (positions is None or _dense(at, I32, positions)) and
-            (q_weight is None or _dense(at, F32, q_weight)) and
-            (k_weight is None or _dense(at, F32, k_weight)) and
-            (status is None or _dense(at, I32, status)))
+_Tensor = torch.Tensor
 
 
-def _pair(name, t, t_out, heads, head_dim, total):
-    """Token strides of rows and of their outputs (both may be None)."""
-    if t is None and t_out is None:
-        return 0, 0
-    return (_packed(name, t, heads, head_dim, total),
-            _packed(name + "_out", t_out, heads, head_dim, total))
+def _all_dense(device, *pairs) -> bool:
+    """Whether every tensor that is not None of the (tensor, dtype) pairs is
+    contiguous, of its dtype, on CUDA device `device`, the current one."""
+    if device < 0 or device != _current_device():
+        return False
+    for t, dtype in pairs:
+        if t is not None and (type(t) is not _Tensor or t.dtype is not dtype or
+                              t.get_device() != device or not t.is_contiguous()):
+            return False
+    return True
+
+
+def _step(name, t, heads, head_dim, tokens, device) -> int:
+    """_packed for rows on CUDA device `device`; what is not plain goes there."""
+    if (type(t) is _Tensor and t.dtype is BF16 and t.get_device() == device and tokens > 1 and
+            t.shape == (tokens, heads, head_dim)):
+        step, head, col = t.stride()
+        if col == 1 and (head == head_dim or heads == 1) and step % 8 == 0 and \
+                step >= heads * head_dim:
+            return step
+    step = _packed(name, t, heads, head_dim, tokens)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on CUDA device {device}"
+                         if device >= 0 else f"{name} must be on the device of the others")
+    return step
 
 
 def bia_norm_rope(desc, rope, table, positions, q, k, q_out, k_out, q_weight=None, k_weight=None,
@@ -1000,21 +1015,25 @@ def bia_norm_rope(desc, rope, table, positions, q, k, q_out, k_out, q_weight=Non
     some = q if q is not None else k
     if some is None:
         raise TypeError("q or k is required")
-    total = some.shape[0]
+    if not isinstance(some, torch.Tensor):
+        raise TypeError(f"q and k must be torch.Tensor, got {type(some).__name__}")
+    if positions is None:
+        raise TypeError("positions is required")
+    total, at = some.shape[0], some.get_device()
     hq, hkv, d = desc.num_qo_heads, desc.num_kv_heads, desc.head_dim
-    q_step, qo_step = _pair("q", q, q_out, hq, d, total)
-    k_step, ko_step = _pair("k", k, k_out, hkv, d, total)
-    at, ts = _index(some), None
-    if not (stream is None and at >= 0 and at == _current_device() and positions is not None and
-            _rope_dense(at, table, positions, q_weight, k_weight, status)):
-        if positions is None:
-            raise TypeError("positions is required")
-        ts = _rope_types(table, positions, q_weight, k_weight, status)
+    q_step = qo_step = k_step = ko_step = 0
+    if q is not None or q_out is not None:
+        q_step = _step("q", q, hq, d, total, at)
+        qo_step = _step("q_out", q_out, hq, d, total, at)
+    if k is not None or k_out is not None:
+        k_step = _step("k", k, hkv, d, total, at)
+        ko_step = _step("k_out", k_out, hkv, d, total, at)
+    if not (stream is None and
+            _all_dense(at, (table, F32), (positions, I32), (q_weight, F32), (k_weight, F32),
+                       (status, I32))):
+        _check_cuda([("q" if q is not None else "k", some)] +
+                    _rope_types(table, positions, q_weight, k_weight, status), stream)
     _check_rope(desc, rope, table, positions, q_weight, k_weight, total)
-    rows = [(n, t) for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
-            if t is not None]
-    if ts is not None or any(t.get_device() != at for _, t in rows):
-        _check_cuda(rows + (ts or []), stream)
     rc = load().bia_norm_rope(
         ctypes.byref(desc), ctypes.byref(rope), table.data_ptr(), positions.data_ptr(), _at(q),
         _at(k), q_step, k_step, _at(q_weight), _at(k_weight), total, _at(q_out), _at(k_out),
@@ -1027,54 +1046,56 @@ def _append_rope(fp8, desc, rope, table, q, k_new, v_new, caches, append_indptr,
                  kv_indices, kv_last_page_len, append_indptr_host, kv_indptr_host,
                  kv_last_page_len_host, q_out, k_out, positions, q_weight, k_weight, status,
                  stream):
-    """The checks of the two appends; the arguments from the strides' rows on."""
+    """The checks of the two appends, and the call."""
     ap, kvp, last = (_host(append_indptr_host), _host(kv_indptr_host),
                      _host(kv_last_page_len_host))
     batch = ap.numel() - 1
     total, hq, hkv, d = _last(ap), desc.num_qo_heads, desc.num_kv_heads, desc.head_dim
-    q_step, qo_step = _pair("q", q, q_out, hq, d, total)
-    k_step = _packed("k_new", k_new, hkv, d, total)
-    v_step = _packed("v_new", v_new, hkv, d, total)
-    ko_step = 0 if k_out is None else _packed("k_out", k_out, hkv, d, total)
-    k_cache = caches[0]
-    at, ts = _index(k_cache), None
-    if not (stream is None and at >= 0 and at == _current_device() and
-            _dense(at, E4M3 if fp8 else BF16, *caches[:2]) and _dense(at, E8M0, *caches[2:]) and
-            _dense(at, I32, append_indptr, kv_indptr, kv_indices, kv_last_page_len) and
-            _rope_dense(at, table, positions, q_weight, k_weight, status)):
-        kinds = (E4M3, E4M3, E8M0, E8M0) if fp8 else (BF16, BF16)
+    k_cache, v_cache = caches[0], caches[1]
+    at = _index(k_cache)
+    q_step = qo_step = ko_step = 0
+    if q is not None or q_out is not None:
+        q_step = _step("q", q, hq, d, total, at)
+        qo_step = _step("q_out", q_out, hq, d, total, at)
+    k_step = _step("k_new", k_new, hkv, d, total, at)
+    v_step = _step("v_new", v_new, hkv, d, total, at)
+    if k_out is not None:
+        ko_step = _step("k_out", k_out, hkv, d, total, at)
+    kinds = (E4M3, E4M3, E8M0, E8M0) if fp8 else (BF16, BF16)
+    if not (stream is None and
+            _all_dense(at, *zip(caches, kinds), (append_indptr, I32), (kv_indptr, I32),
+                       (kv_indices, I32), (kv_last_page_len, I32), (table, F32),
+                       (positions, I32), (q_weight, F32), (k_weight, F32), (status, I32))):
         ts = _check_types(*zip(("k_cache", "v_cache", "k_scale", "v_scale"), caches, kinds),
                           ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
                           ("kv_indices", kv_indices, I32),
                           ("kv_last_page_len", kv_last_page_len, I32))
-        ts += _rope_types(table, positions, q_weight, k_weight, status)
+        _check_cuda(ts + _rope_types(table, positions, q_weight, k_weight, status), stream)
     if fp8:
         _check_caches_fp8(desc, *caches)
     else:
         want = (k_cache.shape[0], desc.page_size, hkv, d)
-        if k_cache.shape != want or caches[1].shape != want:
+        if k_cache.shape != want or v_cache.shape != want:
             raise ValueError(f"k_cache and v_cache must be {want} (num_pages, page_size, "
                              f"num_kv_heads, head_dim) for this descriptor, got "
-                             f"{tuple(k_cache.shape)} and {tuple(caches[1].shape)}")
+                             f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
     _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
     if append_indptr.numel() != batch + 1:
         raise ValueError(f"append_indptr must hold {batch + 1} entries, got "
                          f"{append_indptr.numel()}")
     _check_rope(desc, rope, table, positions, q_weight, k_weight, total)
-    rows = [(n, t) for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("q_out", q_out),
-                                ("k_out", k_out)) if t is not None]
-    if ts is not None or any(t.get_device() != at for _, t in rows):
-        _check_cuda((ts or [("k_cache", k_cache)]) + rows, stream)
-    head = (ctypes.byref(desc), ctypes.byref(rope), table.data_ptr(), _at(positions), _at(q),
-            k_new.data_ptr(), v_new.data_ptr(), q_step, k_step, v_step, _at(q_weight),
-            _at(k_weight), *(c.data_ptr() for c in caches), k_cache.shape[0],
-            append_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
-            kv_last_page_len.data_ptr(), ap.data_ptr(), kvp.data_ptr(), last.data_ptr(), batch)
     if fp8:
-        name, tail = "bia_append_paged_kv_fp8_rope", (_at(q_out), _at(k_out), qo_step, ko_step)
+        name, pages = "bia_append_paged_kv_fp8_rope", [c.data_ptr() for c in caches]
+        tail = (_at(q_out), _at(k_out), qo_step, ko_step)
     else:
-        name, tail = "bia_append_paged_kv_rope", (_at(q_out), qo_step)
-    rc = getattr(load(), name)(*head, *tail, _at(status), _handle(stream))
+        name, pages = "bia_append_paged_kv_rope", (k_cache.data_ptr(), v_cache.data_ptr())
+        tail = (_at(q_out), qo_step)
+    rc = getattr(load(), name)(
+        ctypes.byref(desc), ctypes.byref(rope), table.data_ptr(), _at(positions), _at(q),
+        k_new.data_ptr(), v_new.data_ptr(), q_step, k_step, v_step, _at(q_weight), _at(k_weight),
+        *pages, k_cache.shape[0], append_indptr.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_last_page_len.data_ptr(), ap.data_ptr(), kvp.data_ptr(),
+        last.data_ptr(), batch, *tail, _at(status), _handle(stream))
     if rc != BIA_OK:
         raise BiaError(rc, name)
 
@@ -1110,30 +1131,31 @@ def bia_append_paged_kv_fp8_rope(desc, rope, table, q, k_new, v_new, k_cache, v_
 def _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
                   out, lse, stream, batch, kvp=None, last=None, qo_indptr=None):
     """The tensors of a windowed call of `batch` requests over the bf16 cache."""
-    at, ts = _index(q), None
-    more = () if qo_indptr is None else (qo_indptr,)
-    if not (stream is None and _dense(at, BF16, q, out, k_cache, v_cache) and
-            _dense(at, I32, kv_indptr, kv_indices, kv_last_page_len, *more) and
-            (lse is None or _dense(at, F32, lse)) and at >= 0 and
-            _index(workspace) == at == _current_device() and workspace.is_contiguous()):
-        ts = _check_types(("q", q, BF16), ("k_cache", k_cache, BF16), ("v_cache", v_cache, BF16),
-                          ("kv_indptr", kv_indptr, I32), ("kv_indices", kv_indices, I32),
-                          ("kv_last_page_len", kv_last_page_len, I32),
-                          ("workspace", workspace, None), ("out", out, BF16),
-                          ("lse", lse, F32, True), *(("qo_indptr", t, I32) for t in more))
-    rows = (k_cache.shape[0], desc.page_size, desc.num_kv_heads, desc.head_dim)
+    at = _index(q)
+    if not (stream is None and
+            _all_dense(at, (q, BF16), (out, BF16), (k_cache, BF16), (v_cache, BF16),
+                       (kv_indptr, I32), (kv_indices, I32), (kv_last_page_len, I32), (lse, F32),
+                       (qo_indptr, I32)) and
+            _index(workspace) == at and workspace.is_contiguous()):
+        more = () if qo_indptr is None else (("qo_indptr", qo_indptr, I32),)
+        _check_cuda(_check_types(("q", q, BF16), ("k_cache", k_cache, BF16),
+                                 ("v_cache", v_cache, BF16), ("kv_indptr", kv_indptr, I32),
+                                 ("kv_indices", kv_indices, I32),
+                                 ("kv_last_page_len", kv_last_page_len, I32),
+                                 ("workspace", workspace, None), ("out", out, BF16),
+                                 ("lse", lse, F32, True), *more), stream)
+    hq, d = desc.num_qo_heads, desc.head_dim
+    rows = (k_cache.shape[0], desc.page_size, desc.num_kv_heads, d)
     if k_cache.shape != rows or v_cache.shape != rows:
         raise ValueError(f"k_cache and v_cache must be {rows} (num_pages, page_size, "
                          f"num_kv_heads, head_dim) for this descriptor, got "
                          f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
-    want = (q.shape[0], desc.num_qo_heads, desc.head_dim)
+    want = (q.shape[0], hq, d)
     if q.shape != want or out.shape != want:
         raise ValueError(f"q and out must be {want}, got {tuple(q.shape)} and {tuple(out.shape)}")
-    if lse is not None and lse.numel() != want[0] * want[1]:
-        raise ValueError(f"lse must hold {want[0]} x {want[1]} floats")
+    if lse is not None and lse.numel() != want[0] * hq:
+        raise ValueError(f"lse must hold {want[0]} x {hq} floats")
     _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
-    if ts is not None:
-        _check_cuda(ts, stream)
 
 
 def bia_decode_window_workspace_size(desc, window, sinks, kv_indptr_host, kv_last_page_len_host,
