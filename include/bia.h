@@ -620,7 +620,8 @@ BIA_API size_t bia_prefill_window_workspace_size(const bia_attn_desc *desc, int3
 /*
  * bia_decode_paged with a window and sinks.  The keys that a query sees are
  * taken as one list, the sinks first, cut into tiles of split_size keys (a
- * multiple of 128; 0 = BIA_WINDOW_DECODE_SPLIT) whose states are merged in
+ * multiple of 128; 0 = BIA_WINDOW_DECODE_SPLIT; fewer than 128 sinks before the
+ * window make the first tile longer) whose states are merged in
  * order; with a window of at least kv_len the bits are those of
  * bia_decode_paged at the same split size.  The device index arrays are checked
  * request by request: one that breaks a rule of the call (or its bounds) gets

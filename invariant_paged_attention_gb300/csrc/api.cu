@@ -1359,11 +1359,12 @@ size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc, const int32_
 extern "C" {
 
 namespace {
-// Attention with a window and sinks.  Keys of the longest list that a query of
-// a sequence of up to kv_len keys sees.
+// Attention with a window and sinks.  Entries that the split tiles of a query of
+// a sequence of up to kv_len keys share out (it grows with kv_len).
 int64_t window_len(int64_t kv_len, int32_t window, int32_t sinks) {
   const int64_t behind = std::max<int64_t>(0, kv_len - window);
-  return kv_len - behind + std::min<int64_t>(sinks, behind);
+  const int64_t sunk = std::min<int64_t>(sinks, behind);
+  return kv_len - behind + sunk - bia::window_lead(static_cast<int32_t>(sunk));
 }
 
 // No request has more keys: a window or sinks above stand for all of them.

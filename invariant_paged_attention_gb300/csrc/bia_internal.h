@@ -281,24 +281,38 @@ __host__ __device__ inline TileKeys tile_keys(int32_t q_len, int32_t kv_len, int
 
 // The keys that the one query of a windowed decode sees, as a list of its own:
 // entry i is key i below `sunk` and key i + skip from there on (the sinks that
-// the window has left behind, then the window).
+// the window has left behind, then the window).  Sinks of less than a key block
+// ride with the first split tile, which is `lead` entries longer: windows are
+// mostly whole tiles, and the sinks would be one more of a few keys.
+__host__ __device__ inline int32_t window_lead(int32_t sunk) { return sunk < kKvBlock ? sunk : 0; }
 struct WindowKeys {
-  int32_t page_base, len, sunk, skip;
+  int32_t page_base, len, sunk, skip, lead;
   bool ok; // the request's arrays keep the rules of the call
 };
 #ifdef __CUDACC__
-__device__ __forceinline__ WindowKeys window_keys(const AttnArgs &a, int b) {
+__device__ __forceinline__ WindowKeys window_keys(const AttnArgs &a, int32_t p0, int32_t p1,
+                                                  int32_t last) {
   WindowKeys k;
-  const int32_t p0 = __ldg(a.kv_indptr + b), p1 = __ldg(a.kv_indptr + b + 1);
-  const int32_t last = __ldg(a.kv_last_page_len + b);
   const int64_t n = ((static_cast<int64_t>(p1) - p0 - 1) << a.page_shift) + last;
   k.ok = p0 >= 0 && p1 > p0 && last >= 1 && last <= (1 << a.page_shift) && n <= a.max_kv_len;
   const int32_t lo = k.ok ? max(0, static_cast<int32_t>(n) - a.window) : 0;
   k.page_base = p0;
   k.sunk = min(a.sinks, lo);
   k.skip = lo - k.sunk;
+  k.lead = window_lead(k.sunk);
   k.len = k.ok ? static_cast<int32_t>(n) - k.skip : 0;
   return k;
+}
+// First entry of split tile s, and how many tiles there are.
+__device__ __forceinline__ int32_t window_tile(const WindowKeys &k, int32_t s, int32_t split) {
+  return s == 0 ? 0 : k.lead + s * split;
+}
+__device__ __forceinline__ int32_t window_tiles(const WindowKeys &k, int32_t split) {
+  return (k.len - k.lead + split - 1) / split;
+}
+__device__ __forceinline__ WindowKeys window_keys(const AttnArgs &a, int b) {
+  return window_keys(a, __ldg(a.kv_indptr + b), __ldg(a.kv_indptr + b + 1),
+                     __ldg(a.kv_last_page_len + b));
 }
 #endif
 

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
       for (int e = threadIdx.x; e < G * a.D; e += kThreadsDec) a.out[head0 * a.D + e] = 0x7fc0u;
       if (a.lse && threadIdx.x < G) a.lse[head0 + threadIdx.x] = __int_as_float(0x7fc00000);
     }
-    if (u.split * static_cast<int64_t>(a.split) >= wk.len) return;
+    if (u.split >= window_tiles(wk, a.split)) return;
     __syncthreads(); // the status word is clear
   } else {
     u = a.units[unit];
@@ -172,8 +172,9 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   const int32_t t = u.tile;
   const int32_t q_end = a.causal ? r.kv_len - r.q_len + t + 1 : r.kv_len;
   const int64_t q_row = static_cast<int64_t>(r.q_start) + t;
-  const int32_t key_begin = u.split * a.split;
-  const int32_t key_end = min(key_begin + a.split, q_end);
+  const int32_t key_begin = WIN ? window_tile(wk, u.split, a.split) : u.split * a.split;
+  const int32_t key_end =
+      WIN ? min(window_tile(wk, u.split + 1, a.split), wk.len) : min(key_begin + a.split, q_end);
   // custom mask: bit (t, key) of the request's [q_len, kv_len] mask
   const int64_t mask_row = MASK ? a.mask_indptr[u.b] + static_cast<int64_t>(t) * r.kv_len : 0;
   const int n_chunks = (key_end - key_begin + kChunk - 1) / kChunk;
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   }
   __syncthreads();
 
-  const bool single = (q_end - 1) / a.split == 0; // one split: the final row
+  const bool single = WIN ? window_tiles(wk, a.split) == 1 : (q_end - 1) / a.split == 0;
   for (int e = threadIdx.x; e < G * D; e += kThreadsDec) {
     const int g = e / D, d = e % D;
     if (d >= Dr) continue;

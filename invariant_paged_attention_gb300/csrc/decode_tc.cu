@@ -41,8 +41,11 @@
 //
 // With a window and sinks (WIN) a request's keys are the list that it sees
 // (window_keys): the first sinks, then the window; the split tiles cut that
-// list, so nothing outside it is read.  Such a call has no plan: every role
-// finds an item's keys in the index arrays, and the items go round the CTAs.
+// list, so nothing outside it is read.  Such a call has no plan: the items go
+// round the CTAs, and one copy thread finds each in the index arrays, two items
+// ahead, and posts what the roles need of it; the copy warps look up the next
+// item's first pages while the last block's copies are issued (with each role
+// looking its items up when it came to them, a 4-block item cost 1.5 us more).
 //
 // Also runs the single-token q tiles a prefill call streams (with the
 // prefill split size), with or without a custom mask: a masked key is left
@@ -90,7 +93,8 @@ struct DecTcSmem {
   static constexpr int kLred = kRed + 2 * 4 * kNT * 4; // float [4 warps][16 heads]
   static constexpr int kSlot = kLred + 4 * kNT * 4;
   static constexpr int kItems = kSlot + 16;            // int64 [4]: the item mailbox
-  static constexpr int kBytes = kItems + 4 * 8;
+  static constexpr int kWinItems = kItems + 4 * 8;     // WinItem [4]: with a window
+  static constexpr int kBytes = kWinItems + 4 * 48;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kKRing % 1024 == 0, "rings on the 128-byte swizzle period");
   static_assert(kP % 512 == 0 && kPBuf % 512 == 0, "P on the 64-byte swizzle period");
@@ -137,31 +141,37 @@ struct TcItem {
   bool bad;           // WIN: the request breaks a rule of the call
 };
 
-template <bool WIN>
+// What the roles need of an item of a windowed decode (parts 0: the request
+// breaks a rule of the call).
+struct alignas(16) WinItem {
+  int32_t b, split, kvh, page_base, sunk, skip, key_begin, key_end;
+  int32_t parts, pad[3];
+};
+
+__device__ __forceinline__ TcItem win_item(const AttnArgs &a, const WinItem &x) {
+  TcItem it;
+  it.kvh = x.kvh;
+  it.u = Unit{x.b, 0, x.split, 1};
+  it.bad = x.parts == 0;
+  it.sunk = x.sunk;
+  it.skip = x.skip;
+  it.t = 0;
+  it.r.q_start = x.b;
+  it.r.q_len = 1;
+  it.r.nsp = x.parts;
+  it.r.rowbase = static_cast<int64_t>(x.b) * a.parts;
+  it.r.page_base = x.page_base;
+  it.key_begin = x.key_begin;
+  it.key_end = it.q_end = x.key_end;
+  it.live = x.split < x.parts;
+  it.nb = it.live ? (it.key_end - it.key_begin + kKeysT - 1) / kKeysT : 0;
+  return it;
+}
+
 __device__ __forceinline__ TcItem tc_item(const AttnArgs &a, int64_t w) {
   TcItem it;
   const int64_t unit = w / a.Hkv;
   it.kvh = static_cast<int>(w - unit * a.Hkv);
-  if constexpr (WIN) {
-    const int32_t b = static_cast<int32_t>(unit / a.parts);
-    const WindowKeys k = window_keys(a, b);
-    it.u = Unit{b, 0, static_cast<int32_t>(unit - static_cast<int64_t>(b) * a.parts), 1};
-    it.bad = !k.ok;
-    it.sunk = k.sunk;
-    it.skip = k.skip;
-    it.t = 0;
-    it.r.q_start = b;
-    it.r.q_len = 1;
-    it.r.kv_len = it.q_end = k.len;
-    it.r.nsp = a.parts;
-    it.r.rowbase = static_cast<int64_t>(b) * a.parts;
-    it.r.page_base = k.page_base;
-    it.key_begin = it.u.split * a.split;
-    it.key_end = min(it.key_begin + a.split, k.len);
-    it.live = it.key_begin < k.len;
-    it.nb = it.live ? (it.key_end - it.key_begin + kKeysT - 1) / kKeysT : 0;
-    return it;
-  }
   it.u = a.units[unit];
   it.live = it.u.b >= 0;
   it.nb = 0;
@@ -245,9 +255,19 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
     const int s = static_cast<int>(k & 3u);
     int64_t w = -1;
     if (mbar_wait(bar(L::bItemFull + s), (k >> 2) & 1u, status)) w = items[s];
+    if constexpr (WIN) {
+      if (w >= 0) return w; // its record is read first, then `done` hands the slot back
+    }
     if (!single) __syncwarp();
     if (single || lane == 0) mbar_arrive(bar(L::bItemEmpty + s));
     return w;
+  };
+  WinItem *win_items = reinterpret_cast<WinItem *>(smem + L::kWinItems);
+  auto done = [&](uint32_t k, bool single) {
+    if constexpr (WIN) {
+      if (!single) __syncwarp();
+      if (single || lane == 0) mbar_arrive(bar(L::bItemEmpty + (k & 3u)));
+    }
   };
 
   if (warp >= kProdWarpTc) {
@@ -261,130 +281,249 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
     const uint32_t piece_off = static_cast<uint32_t>(cc >> 3) * kPieceT;
     uint32_t jg = 0, ig = 0;
     bool ok = true;
-    // copy thread 0 fetches the items: the first is the CTA's own index, each
-    // next one is taken from the counter when the current item starts and
-    // posted once the item's first block of copies is issued, so that the
-    // copy warps find it waiting when they reach it (one item ahead)
     const bool fetcher = pt == 0;
-    if (fetcher) {
-      items[0] = blockIdx.x < n_work ? static_cast<int64_t>(blockIdx.x) : -1;
-      mbar_arrive(bar(L::bItemFull + 0));
-    }
-    int32_t taken = 0;   // the counter's answer for the next item
-    bool posted = false; // the next item is posted
-    auto post_next = [&](uint32_t k) { // item k + 1
-      if (!fetcher || posted) return;
-      posted = true;
-      int64_t nw = static_cast<int64_t>(gridDim.x) + taken;
-      if constexpr (WIN) nw = static_cast<int64_t>(blockIdx.x) + (k + 1) * static_cast<int64_t>(gridDim.x);
-      if (nw >= n_work) nw = -1;
-      const uint32_t kn = k + 1;
-      if (kn >= 4 && !mbar_wait(bar(L::bItemEmpty + (kn & 3u)), ((kn >> 2) - 1) & 1u, status))
-        nw = -1;
-      items[kn & 3u] = nw;
-      mbar_arrive(bar(L::bItemFull + (kn & 3u)));
-    };
-    for (uint32_t k = 0; ok; ++k) {
-      const int64_t w = read_item(k, false);
-      if (w < 0) break;
-      if constexpr (!WIN)
-        if (fetcher) taken = atomicAdd(a.status + kStatusWorkCounter, 1);
-      posted = false;
-      const TcItem it = tc_item<WIN>(a, w);
-      if (!it.live) {
-        if constexpr (WIN)
-          if (fetcher && it.bad) atomicOr(status, kStatusPlanMismatch);
-        post_next(k);
-        continue;
+    if constexpr (WIN) {
+      // item k of the CTA is blockIdx.x + k * gridDim.x; the fetcher's arrays'
+      // entries of item k + 1 are on their way while item k begins
+      int32_t f_p0 = 0, f_p1 = 0, f_last = 0, f_b = 0, f_split = 0, f_kvh = 0;
+      int64_t f_w = blockIdx.x;
+      auto look = [&]() { // loads for item f_w
+        if (f_w >= n_work) return;
+        const int64_t unit = f_w / a.Hkv;
+        f_kvh = static_cast<int32_t>(f_w - unit * a.Hkv);
+        f_b = static_cast<int32_t>(unit / a.parts);
+        f_split = static_cast<int32_t>(unit - static_cast<int64_t>(f_b) * a.parts);
+        f_p0 = __ldg(a.kv_indptr + f_b);
+        f_p1 = __ldg(a.kv_indptr + f_b + 1);
+        f_last = __ldg(a.kv_last_page_len + f_b);
+      };
+      auto post = [&](uint32_t k) { // item k, then the loads of the next one
+        int64_t w = f_w < n_work ? f_w : -1;
+        if (k >= 4 && !mbar_wait(bar(L::bItemEmpty + (k & 3u)), ((k >> 2) - 1) & 1u, status))
+          w = -1;
+        if (w >= 0) {
+          const WindowKeys x = window_keys(a, f_p0, f_p1, f_last);
+          if (!x.ok) atomicOr(status, kStatusPlanMismatch);
+          const int32_t end = min(window_tile(x, f_split + 1, a.split), x.len);
+          win_items[k & 3u] =
+              WinItem{f_b, f_split, f_kvh, x.page_base, x.sunk, x.skip,
+                      window_tile(x, f_split, a.split), end, window_tiles(x, a.split), {}};
+        }
+        items[k & 3u] = w;
+        mbar_arrive(bar(L::bItemFull + (k & 3u)));
+        f_w += gridDim.x;
+        look();
+      };
+      if (fetcher) {
+        look();
+        post(0);
       }
-      // the key of entry `i` of the request's list
-      auto key_of = [&](int32_t i) { return WIN && i >= it.sunk ? i + it.skip : i; };
-      // q rows of the item's G heads (rows G..15 zero) into q buffer ig % 2
-      if (ig >= 2 && !mbar_wait(bar(L::bQEmpty + (ig & 1)), ((ig >> 1) - 1) & 1, status)) {
-        ok = false;
-        break;
-      }
-      const int64_t q_row = static_cast<int64_t>(it.r.q_start) + it.t;
-      for (int idx = pt; idx < kNT * 16; idx += kProdThreadsT) { // 16 rows x 16 chunks
-        const int h = idx >> 4, c = idx & 15;
-        const bool valid = h < G;
-        const uint16_t *src = a.q + ((q_row * a.Hq + it.kvh * G + (valid ? h : 0)) * kDT + c * 8);
-        cp_async16(qbuf(ig & 1) + (c >> 3) * (kNT * 128) + h * 128 +
-                       ((static_cast<uint32_t>(c & 7) ^ static_cast<uint32_t>(h & 7)) << 4),
-                   src, valid);
-      }
-      cp_async_arrive(bar(L::bQFull + (ig & 1)));
-      ++ig;
-      const int64_t mask_row =
-          MASK ? a.mask_indptr[it.u.b] + static_cast<int64_t>(it.t) * it.r.kv_len : 0;
-      // page of each of this thread's keys of block j (-1: not copied) and
-      // which of them are visible; fetched a block ahead
-      auto fetch = [&](int j, int32_t (&pg)[kNkT], uint32_t &vis) {
-        vis = 0;
+      // the k-th item, and the pages of its first block
+      TcItem it{};
+      int32_t pg_next[kNkT];
+      auto key_of = [&](int32_t i) { return i >= it.sunk ? i + it.skip : i; };
+      auto fetch = [&](int j) {
 #pragma unroll
         for (int n = 0; n < kNkT; ++n) {
           const int32_t key = it.key_begin + j * kKeysT + kb + kKeyStepT * n;
-          bool valid = j < it.nb && key < it.key_end;
-          if constexpr (MASK) {
-            if (valid) {
-              const int64_t bit = mask_row + key;
-              valid = (__ldg(a.mask + (bit >> 5)) >> (bit & 31)) & 1u;
-            }
-          }
-          pg[n] = valid ? __ldg(a.kv_indices + it.r.page_base + (key_of(key) >> a.page_shift)) : -1;
-          vis |= static_cast<uint32_t>(valid) << n;
+          pg_next[n] = j < it.nb && key < it.key_end
+                           ? __ldg(a.kv_indices + it.r.page_base + (key_of(key) >> a.page_shift))
+                           : -1;
         }
       };
-      int32_t pg_next[kNkT];
-      uint32_t vis_next;
-      fetch(0, pg_next, vis_next);
-      for (int j = 0; j < it.nb; ++j, ++jg) {
-        int32_t pg[kNkT];
-#pragma unroll
-        for (int n = 0; n < kNkT; ++n) pg[n] = pg_next[n];
-        const uint32_t vis = vis_next;
-        fetch(j + 1, pg_next, vis_next); // in flight while this block's copies are issued
-        int64_t row[kNkT];
-        uint32_t okeys = 0;
-#pragma unroll
-        for (int n = 0; n < kNkT; ++n) {
-          const int32_t key = it.key_begin + j * kKeysT + kb + kKeyStepT * n;
-          bool valid = (vis >> n) & 1u;
-          if (valid && (pg[n] < 0 || pg[n] >= a.num_pages)) {
-            atomicOr(status, kStatusBadPage);
-            valid = false;
-          }
-          row[n] = valid ? ((static_cast<int64_t>(pg[n]) << a.page_shift) + (key_of(key) & page_mask)) *
-                                   a.Hkv + it.kvh
-                         : 0;
-          okeys |= static_cast<uint32_t>(valid) << n;
+      auto take = [&](uint32_t k) { // false: no more items
+        if (read_item(k, false) < 0) return false;
+        it = win_item(a, win_items[k & 3u]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bItemEmpty + (k & 3u)));
+        fetch(0);
+        return true;
+      };
+      bool more = take(0);
+      for (uint32_t k = 0; more && ok; ++k) {
+        if (fetcher) post(k + 1);
+        if (it.nb == 0) {
+          more = take(k + 1);
+          continue;
         }
-        // key rows (their slot frees when the block's S is done), then value
-        // rows (free when its P.V is done)
-        for (int kv = 0; kv < 2; ++kv) {
-          const int ns = kv == 0 ? kKStagesT : kVStagesT;
-          const int s = static_cast<int>(jg % ns);
-          const int eb = (kv == 0 ? L::bKEmpty : L::bVEmpty) + s;
-          if (jg >= static_cast<uint32_t>(ns) &&
-              !mbar_wait(bar(eb), ((jg / ns) - 1) & 1, status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t base = (kv == 0 ? kstage(s) : vstage(s)) + piece_off;
-          const uint16_t *src = (kv == 0 ? a.k_cache : a.v_cache) + cc * 8;
+        // q rows of the item's G heads (rows G..15 zero) into q buffer ig % 2
+        if (ig >= 2 && !mbar_wait(bar(L::bQEmpty + (ig & 1)), ((ig >> 1) - 1) & 1, status)) break;
+        const int64_t q_row = it.r.q_start;
+        for (int idx = pt; idx < kNT * 16; idx += kProdThreadsT) { // 16 rows x 16 chunks
+          const int h = idx >> 4, c = idx & 15;
+          const bool valid = h < G;
+          const uint16_t *src = a.q + ((q_row * a.Hq + it.kvh * G + (valid ? h : 0)) * kDT + c * 8);
+          cp_async16(qbuf(ig & 1) + (c >> 3) * (kNT * 128) + h * 128 +
+                         ((static_cast<uint32_t>(c & 7) ^ static_cast<uint32_t>(h & 7)) << 4),
+                     src, valid);
+        }
+        cp_async_arrive(bar(L::bQFull + (ig & 1)));
+        ++ig;
+        const int nb = it.nb;
+        for (int j = 0; j < nb; ++j, ++jg) {
+          const int kvh = it.kvh;
+          int64_t row[kNkT];
+          uint32_t okeys = 0;
 #pragma unroll
           for (int n = 0; n < kNkT; ++n) {
-            const int k = kb + kKeyStepT * n;
-            cp_async16(base + static_cast<uint32_t>(k) * 128 +
-                           ((static_cast<uint32_t>(cc & 7) ^ static_cast<uint32_t>(k & 7)) << 4),
-                       src + row[n] * kDT, (okeys >> n) & 1u);
+            const int32_t key = it.key_begin + j * kKeysT + kb + kKeyStepT * n;
+            bool valid = key < it.key_end;
+            const int32_t pg = pg_next[n];
+            if (valid && (pg < 0 || pg >= a.num_pages)) {
+              atomicOr(status, kStatusBadPage);
+              valid = false;
+            }
+            row[n] = valid ? ((static_cast<int64_t>(pg) << a.page_shift) +
+                              (key_of(key) & page_mask)) * a.Hkv + kvh
+                           : 0;
+            okeys |= static_cast<uint32_t>(valid) << n;
           }
-          cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
+          // in flight while this block's copies are issued: the next one's
+          // pages, after the last block the next item's
+          if (j + 1 < nb) fetch(j + 1);
+          else more = take(k + 1);
+          for (int kv = 0; kv < 2; ++kv) {
+            const int ns = kv == 0 ? kKStagesT : kVStagesT;
+            const int s = static_cast<int>(jg % ns);
+            const int eb = (kv == 0 ? L::bKEmpty : L::bVEmpty) + s;
+            if (jg >= static_cast<uint32_t>(ns) &&
+                !mbar_wait(bar(eb), ((jg / ns) - 1) & 1, status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t base = (kv == 0 ? kstage(s) : vstage(s)) + piece_off;
+            const uint16_t *src = (kv == 0 ? a.k_cache : a.v_cache) + cc * 8;
+#pragma unroll
+            for (int n = 0; n < kNkT; ++n) {
+              const int x = kb + kKeyStepT * n;
+              cp_async16(base + static_cast<uint32_t>(x) * 128 +
+                             ((static_cast<uint32_t>(cc & 7) ^ static_cast<uint32_t>(x & 7)) << 4),
+                         src + row[n] * kDT, (okeys >> n) & 1u);
+            }
+            cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
+          }
+          if (!ok) break;
         }
-        if (!ok) break;
-        post_next(k); // after the first block
       }
-      post_next(k);
+    } else {
+      // copy thread 0 fetches the items: the first is the CTA's own index, each
+      // next one is taken from the counter when the current item starts and
+      // posted once the item's first block of copies is issued, so that the
+      // copy warps find it waiting when they reach it (one item ahead)
+      if (fetcher) {
+        items[0] = blockIdx.x < n_work ? static_cast<int64_t>(blockIdx.x) : -1;
+        mbar_arrive(bar(L::bItemFull + 0));
+      }
+      int32_t taken = 0;   // the counter's answer for the next item
+      bool posted = false; // the next item is posted
+      auto post_next = [&](uint32_t k) { // item k + 1
+        if (!fetcher || posted) return;
+        posted = true;
+        int64_t nw = static_cast<int64_t>(gridDim.x) + taken;
+        if (nw >= n_work) nw = -1;
+        const uint32_t kn = k + 1;
+        if (kn >= 4 && !mbar_wait(bar(L::bItemEmpty + (kn & 3u)), ((kn >> 2) - 1) & 1u, status))
+          nw = -1;
+        items[kn & 3u] = nw;
+        mbar_arrive(bar(L::bItemFull + (kn & 3u)));
+      };
+      for (uint32_t k = 0; ok; ++k) {
+        const int64_t w = read_item(k, false);
+        if (w < 0) break;
+        if (fetcher) taken = atomicAdd(a.status + kStatusWorkCounter, 1);
+        posted = false;
+        const TcItem it = tc_item(a, w);
+        if (!it.live) {
+          post_next(k);
+          continue;
+        }
+        // q rows of the item's G heads (rows G..15 zero) into q buffer ig % 2
+        if (ig >= 2 && !mbar_wait(bar(L::bQEmpty + (ig & 1)), ((ig >> 1) - 1) & 1, status)) {
+          ok = false;
+          break;
+        }
+        const int64_t q_row = static_cast<int64_t>(it.r.q_start) + it.t;
+        for (int idx = pt; idx < kNT * 16; idx += kProdThreadsT) { // 16 rows x 16 chunks
+          const int h = idx >> 4, c = idx & 15;
+          const bool valid = h < G;
+          const uint16_t *src = a.q + ((q_row * a.Hq + it.kvh * G + (valid ? h : 0)) * kDT + c * 8);
+          cp_async16(qbuf(ig & 1) + (c >> 3) * (kNT * 128) + h * 128 +
+                         ((static_cast<uint32_t>(c & 7) ^ static_cast<uint32_t>(h & 7)) << 4),
+                     src, valid);
+        }
+        cp_async_arrive(bar(L::bQFull + (ig & 1)));
+        ++ig;
+        const int64_t mask_row =
+            MASK ? a.mask_indptr[it.u.b] + static_cast<int64_t>(it.t) * it.r.kv_len : 0;
+        // page of each of this thread's keys of block j (-1: not copied) and
+        // which of them are visible; fetched a block ahead
+        auto fetch = [&](int j, int32_t (&pg)[kNkT], uint32_t &vis) {
+          vis = 0;
+  #pragma unroll
+          for (int n = 0; n < kNkT; ++n) {
+            const int32_t key = it.key_begin + j * kKeysT + kb + kKeyStepT * n;
+            bool valid = j < it.nb && key < it.key_end;
+            if constexpr (MASK) {
+              if (valid) {
+                const int64_t bit = mask_row + key;
+                valid = (__ldg(a.mask + (bit >> 5)) >> (bit & 31)) & 1u;
+              }
+            }
+            pg[n] = valid ? __ldg(a.kv_indices + it.r.page_base + (key >> a.page_shift)) : -1;
+            vis |= static_cast<uint32_t>(valid) << n;
+          }
+        };
+        int32_t pg_next[kNkT];
+        uint32_t vis_next;
+        fetch(0, pg_next, vis_next);
+        for (int j = 0; j < it.nb; ++j, ++jg) {
+          int32_t pg[kNkT];
+  #pragma unroll
+          for (int n = 0; n < kNkT; ++n) pg[n] = pg_next[n];
+          const uint32_t vis = vis_next;
+          fetch(j + 1, pg_next, vis_next); // in flight while this block's copies are issued
+          int64_t row[kNkT];
+          uint32_t okeys = 0;
+  #pragma unroll
+          for (int n = 0; n < kNkT; ++n) {
+            const int32_t key = it.key_begin + j * kKeysT + kb + kKeyStepT * n;
+            bool valid = (vis >> n) & 1u;
+            if (valid && (pg[n] < 0 || pg[n] >= a.num_pages)) {
+              atomicOr(status, kStatusBadPage);
+              valid = false;
+            }
+            row[n] = valid ? ((static_cast<int64_t>(pg[n]) << a.page_shift) + (key & page_mask)) *
+                                     a.Hkv + it.kvh
+                           : 0;
+            okeys |= static_cast<uint32_t>(valid) << n;
+          }
+          // key rows (their slot frees when the block's S is done), then value
+          // rows (free when its P.V is done)
+          for (int kv = 0; kv < 2; ++kv) {
+            const int ns = kv == 0 ? kKStagesT : kVStagesT;
+            const int s = static_cast<int>(jg % ns);
+            const int eb = (kv == 0 ? L::bKEmpty : L::bVEmpty) + s;
+            if (jg >= static_cast<uint32_t>(ns) &&
+                !mbar_wait(bar(eb), ((jg / ns) - 1) & 1, status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t base = (kv == 0 ? kstage(s) : vstage(s)) + piece_off;
+            const uint16_t *src = (kv == 0 ? a.k_cache : a.v_cache) + cc * 8;
+  #pragma unroll
+            for (int n = 0; n < kNkT; ++n) {
+              const int k = kb + kKeyStepT * n;
+              cp_async16(base + static_cast<uint32_t>(k) * 128 +
+                             ((static_cast<uint32_t>(cc & 7) ^ static_cast<uint32_t>(k & 7)) << 4),
+                         src + row[n] * kDT, (okeys >> n) & 1u);
+            }
+            cp_async_arrive(bar((kv == 0 ? L::bKFull : L::bVFull) + s));
+          }
+          if (!ok) break;
+          post_next(k); // after the first block
+        }
+        post_next(k);
+      }
     }
     cp_async_wait_all(); // no copy outlives the CTA
   } else if (warp == kMmaWarpTc) {
@@ -412,7 +551,8 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       for (uint32_t k = 0; ok; ++k) {
         const int64_t w = read_item(k, true);
         if (w < 0) break;
-        const TcItem it = tc_item<WIN>(a, w);
+        const TcItem it = WIN ? win_item(a, win_items[k & 3u]) : tc_item(a, w);
+        done(k, true);
         if (!it.live) continue;
         const uint32_t qb = qbuf(ig & 1);
         ok = mbar_wait(bar(L::bQFull + (ig & 1)), (ig >> 1) & 1, status);
@@ -467,7 +607,8 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       const int64_t w = read_item(k, false);
       // the four warps share named barriers: they stop together
       if (bar_any_named(1, 128, w < 0)) break;
-      const TcItem it = tc_item<WIN>(a, w);
+      const TcItem it = WIN ? win_item(a, win_items[k & 3u]) : tc_item(a, w);
+      done(k, false);
       if (!it.live) {
         if constexpr (WIN) { // a request that breaks a rule: NaN, once
           if (it.bad && it.u.split == 0) {
@@ -629,7 +770,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::bOFree + (ig & 1))); // O read: the buffer is free
-      const bool single = (it.q_end - 1) / a.split == 0; // one split: the final row
+      const bool single = WIN ? it.r.nsp == 1 : (it.q_end - 1) / a.split == 0; // the final row
       const int64_t q_row = static_cast<int64_t>(it.r.q_start) + it.t;
       const int64_t head0 = q_row * a.Hq + it.kvh * G;
       const int64_t prow0 =

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (row >= static_cast<int64_t>(a.batch) * a.Hq) return;
   const int b = static_cast<int>(row / a.Hq), h = static_cast<int>(row - static_cast<int64_t>(b) * a.Hq);
   const WindowKeys k = window_keys(a, b);
-  const int n = (k.len + a.split - 1) / a.split;
+  const int n = window_tiles(k, a.split);
   if (n <= 1) return; // stored by its only tile, or NaN
   const int64_t first = static_cast<int64_t>(b) * a.parts * a.Hq + h;
   const float *po = a.part_o + first * a.D, *pl = a.part_lse + first;
