@@ -42,7 +42,7 @@ constexpr int kMmaWarpW = 8;
 constexpr int kKeyWarpW = 9; // loads q and K
 constexpr int kItemWarpW = 10;
 constexpr int kValueWarpW = 11; // loads V
-constexpr int kThreadsW = 384;
+constexpr int kLoad2W = 12; // with row gathers 12 and 13 are second warps of K and of V
 constexpr int kItemsW = 3;               // items in flight
 constexpr int kAtomQW = kTileRows * 128; // one SW128 column block of a q tile
 constexpr float kRescaleW = 16.0f;       // log2 units the running max may lag a block's
@@ -88,8 +88,13 @@ struct Steps {
   }
 };
 
-template <int D>
+// ROWS: pages of fewer than 16 keys, whose rows are gathered four at a time.  A
+// warp issues its lanes' gathers one after the other, so K and V have two warps
+// each (window 1024, page 1: 1010 -> 887 us); runs of 16 keys need one, and the
+// warps more would cost 4 %.
+template <int D, bool ROWS>
 struct SmemW {
+  static constexpr int kThreads = ROWS ? 512 : 384, kLoaders = ROWS ? 4 : 2;
   static constexpr int NT = D == 256 ? 1 : 2;    // q tiles an item
   static constexpr int KB = D == 256 ? 64 : 128; // keys a block
   static constexpr int kQTile = kTileRows * D * 2;
@@ -101,11 +106,11 @@ struct SmemW {
   static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kVFull = 4, kKEmpty = 6, kVEmpty = 8,
                        kSFull = 10, kPFull = 12, kODone = 14, kIAsk = 16, kIFull = 17,
                        kIEmpty = kIFull + kItemsW, kNumBars = kIEmpty + kItemsW;
-  // registers: the softmax warps hold a whole S row, the MMA issuer its items'
-  // limits; no role spills with these (of 12 warps x 168)
-  static constexpr int kSoftRegs = D == 256 ? 200 : 208;
-  static constexpr int kOtherRegs = 504 - 2 * kSoftRegs;
-  static_assert(8 * kSoftRegs + 4 * kOtherRegs <= 12 * 168, "registers of the launch");
+  // registers: the softmax warps hold a whole S row
+  static constexpr int kSoftRegs = D == 256 && !ROWS ? 200 : 208;
+  static constexpr int kOtherRegs = ROWS ? 48 : 504 - 2 * kSoftRegs;
+  static_assert(8 * kSoftRegs + (kThreads / 32 - 8) * kOtherRegs <=
+                    kThreads / 32 * (ROWS ? 128 : 168), "registers of the launch");
   static constexpr int kSlot = kBar + kNumBars * 8;
   static constexpr int kAlloc = kSlot + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory per CTA");
@@ -171,10 +176,10 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
   return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsW, 1)
+template <int D, bool ROWS>
+__global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
     prefill_window_kernel(const __grid_constant__ WindowPrefillArgs a) {
-  using L = SmemW<D>;
+  using L = SmemW<D, ROWS>;
   constexpr int NT = L::NT, KB = L::KB;
   constexpr uint32_t kIdescS = idesc_bf16(128, KB, false);
   constexpr uint32_t kIdescPV = idesc_bf16(128, D, true);
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     mbar_init(bar(L::kIAsk), 1);
     for (int s = 0; s < kItemsW; ++s) {
       mbar_init(bar(L::kIFull + s), 1);
-      mbar_init(bar(L::kIEmpty + s), kSoftWarpsW + 3);
+      mbar_init(bar(L::kIEmpty + s), kSoftWarpsW + 1 + L::kLoaders);
     }
     fence_mbar_init();
   }
@@ -352,14 +357,16 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kIAsk), i & 1, a.status))) break;
         if (!more) take();
       }
-    } else if (warp == kKeyWarpW || warp == kValueWarpW) {
+    } else if (warp == kKeyWarpW || warp == kValueWarpW ||
+               (ROWS && (warp == kLoad2W || warp == kLoad2W + 1))) {
       // ------------------------------------------------------------ loads
       // lane: the four rows 4*grp .. of a block, column blocks hh, hh + LPG ..
       constexpr int kGroups = KB / 4, LPG = 32 / kGroups;
       const int grp = lane % kGroups, hh = lane / kGroups;
       const int page_mask = (1 << a.page_shift) - 1;
-      const bool runs = a.page_shift >= 4; // a run of 16 keys lies in one page
-      const bool keys = warp == kKeyWarpW;
+      constexpr bool runs = !ROWS; // a run of 16 keys lies in one page
+      const bool second = ROWS && warp >= kLoad2W;
+      const bool keys = warp == kKeyWarpW || warp == kLoad2W;
       const void *rows_map = keys ? &a.tm_k : &a.tm_v, *runs_map = keys ? &a.tm_k3 : &a.tm_v3;
       const uint32_t full0 = bar(keys ? L::kKFull : L::kVFull);
       const uint32_t empty0 = bar(keys ? L::kKEmpty : L::kVEmpty);
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         int32_t pg[4];
         fetch(0, pg);
         for (int j = 0; j < nb; ++j, ++g) {
-          if (keys && lane == 0 && j == max(0, nb - 3)) mbar_arrive(bar(L::kIAsk));
+          if (keys && !second && lane == 0 && j == max(0, nb - 3)) mbar_arrive(bar(L::kIAsk));
           const int st = g & 1;
           const int32_t key = key_of(j), run0 = key - 4 * (grp & 3);
           int32_t rows[4];
@@ -447,20 +454,20 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                           g < 2 || mbar_wait(empty0 + 8 * st, ((g >> 1) - 1) & 1, a.status));
           if (!ok) break;
           const uint32_t b = full0 + 8 * st, dst = keys ? sK(st) : sV(st);
-          if (lane == 0) mbar_expect_tx(b, static_cast<uint32_t>(copied) * (16 * D * 2));
+          if (lane == 0 && !second) mbar_expect_tx(b, static_cast<uint32_t>(copied) * (16 * D * 2));
           __syncwarp();
           if ((needed && run) || zeros) {
-            if (hh == 0 && (grp & 3) < D / 64)
+            if (hh == 0 && !second && (grp & 3) < D / 64)
               tma_load_3d(dst + (grp & 3) * L::kAtom + (grp & ~3) * 512, runs_map, 64 * (grp & 3),
                           kvh, zeros ? a.slots : slot, b);
           } else if (needed) {
 #pragma unroll
             for (int h = 0; h < D / 64; h += LPG)
-              if (h + hh < D / 64)
+              if (h + hh < D / 64 && (!ROWS || (D == 64 ? !second : second == (h / LPG & 1))))
                 gather4(dst + (h + hh) * L::kAtom + grp * 512, rows_map, 64 * (h + hh), rows, b);
           }
           n = g + 1;
-          if (keys && j == 0) {
+          if (keys && !second && j == 0) {
             // q of this item while the previous one is still in its last P.V
             ok = __all_sync(0xffffffffu,
                             nq == 0 || mbar_wait(bar(L::kQEmpty), (nq - 1) & 1, a.status));
@@ -874,24 +881,30 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   }
 }
 
-template <int D>
-cudaError_t launch_window_d(const WindowPrefillArgs &a, int64_t items, cudaStream_t s) {
-  using L = SmemW<D>;
+template <int D, bool ROWS>
+cudaError_t launch_window_dr(const WindowPrefillArgs &a, int64_t items, cudaStream_t s) {
+  using L = SmemW<D, ROWS>;
   static std::atomic<uint64_t> ready{0};
   int sms = 0;
-  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(prefill_window_kernel<D>),
+  const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(prefill_window_kernel<D, ROWS>),
                                        L::kAlloc, ready, &sms);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   // (the running states of folded pairs are kept for kFoldCtas CTAs)
   cfg.gridDim = dim3(static_cast<unsigned>(std::min({static_cast<int64_t>(sms), kFoldCtas, items})));
-  cfg.blockDim = dim3(kThreadsW);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {chained_launch_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_window_kernel<D>, a);
+  return cudaLaunchKernelEx(&cfg, prefill_window_kernel<D, ROWS>, a);
+}
+
+template <int D>
+cudaError_t launch_window_d(const WindowPrefillArgs &a, int64_t items, cudaStream_t s) {
+  return a.page_shift >= 4 ? launch_window_dr<D, false>(a, items, s)
+                           : launch_window_dr<D, true>(a, items, s);
 }
 
 } // namespace
