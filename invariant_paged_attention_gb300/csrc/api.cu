@@ -1415,7 +1415,11 @@ int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks
       1, std::min<int64_t>((p->max_kv_len + split - 1) / split, (span + split - 1) / split + 1)));
   const int64_t items = p->pairs * Hkv;
   if (items * p->parts > INT32_MAX) return BIA_ERR_UNSUPPORTED;
-  p->folds = p->parts > 1 && items >= bia::kFoldItems ? 1 : 0;
+  // Whole pairs take full rounds of the CTAs, split ones share them out and pay
+  // for their states: folding is taken while its last round is mostly full.  240
+  // pairs of 34 blocks (two rounds) 146 us folded, 171 split; 8 of them 64 and 25.
+  const int64_t rounds = (items + bia::kFoldCtas - 1) / bia::kFoldCtas;
+  p->folds = p->parts > 1 && 10 * rounds * bia::kFoldCtas <= 13 * items ? 1 : 0;
   p->states = p->parts > 1 && !p->folds;
   const int64_t row = static_cast<int64_t>(Hq) * D;
   int64_t rows = p->states ? p->total_q * p->parts : 0;
