@@ -101,8 +101,10 @@ extern "C" {
 #define BIA_DECODE_SPLIT 2048
 /* Default split-KV size of the windowed decode. */
 #define BIA_WINDOW_DECODE_SPLIT 512
-/* Largest split-KV size of bia_prefill_ragged. */
+/* Largest split-KV size of bia_prefill_ragged and bia_prefill_paged_window. */
 #define BIA_RAGGED_MAX_SPLIT 16777216
+/* Most sinks (that a sequence has) of bia_prefill_paged_window. */
+#define BIA_WINDOW_MAX_SINKS 4194304
 /* Largest (and default) split-KV size of the 8-bit decode. */
 #define BIA_DECODE_FP8_SPLIT 1024
 
@@ -594,9 +596,11 @@ BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
  * into chunks that start on the 128-row q-tile grid.  A non-finite key or value
  * may reach every row of a q tile that sees its block of 128 keys; keys before
  * the window of the first row of a pair of q tiles, and past the request's
- * last key, are not read.  split_size: a multiple of 128, 0 =
- * BIA_PREFILL_SPLIT; with few q tiles a smaller one spreads a long window over
- * more of the GPU.  Weights lag the running maximum by up to 2^16 before they
+ * last key, never do.  split_size: a multiple of 128 up to
+ * BIA_RAGGED_MAX_SPLIT, 0 = BIA_PREFILL_SPLIT (a larger one:
+ * BIA_ERR_UNSUPPORTED, as are min(sinks, kv_len) above BIA_WINDOW_MAX_SINKS and
+ * caches of 2^31 - 1 (key, kv head) rows and more); with few q tiles a smaller
+ * one spreads a long window over more of the GPU.  Weights lag the running maximum by up to 2^16 before they
  * are divided by their sum, in fp32: values above 2^80 may overflow.
  */
 BIA_API int bia_prefill_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,

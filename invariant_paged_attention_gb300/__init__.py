@@ -34,6 +34,7 @@ BIA_RAGGED_MAX_SPLIT = 1 << 24
 BIA_DECODE_SPLIT = 2048
 BIA_DECODE_FP8_SPLIT = 1024
 BIA_WINDOW_DECODE_SPLIT = 512
+BIA_WINDOW_MAX_SINKS = 1 << 22
 
 # every symbol include/bia.h exports
 EXPORTS = ("bia_prefill_paged", "bia_prefill_workspace_size", "bia_decode_paged",

@@ -1405,6 +1405,9 @@ int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks
     p->total_q += q_len;
     p->max_kv_len = std::max(p->max_kv_len, kv_len);
   }
+  // the sinks go with a tile's first split: its time stays far below the limit
+  // of the kernel's waits
+  if (std::min<int64_t>(sinks, p->max_kv_len) > BIA_WINDOW_MAX_SINKS) return BIA_ERR_UNSUPPORTED;
   p->split = split;
   // a pair's keys: up to window + (the pair's tokens - 1), or all of them where
   // the sinks meet the window, which then ends within sinks + a block of it

@@ -477,9 +477,12 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
         Ls = fmaf(s_l[k * G + g], w, Ls);
         O = fmaf(s_o[(k * G + g) * D + d], w, O);
       }
+    } else if constexpr (WIN) { // no maximum: nothing was seen, or only NaN
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) Ls = fmaf(s_l[k * G + g], 0.f, Ls);
     }
     const int h = kvh * G + g;
-    const bool empty_row = !(Ls > 0.f);
+    const bool empty_row = WIN ? Ls == 0.f : !(Ls > 0.f); // a window's NaN sum stays NaN
     const float val = empty_row ? 0.f : __fdiv_rn(O, Ls);
     const float lse = empty_row ? -INFINITY : __fmul_rn(__fadd_rn(M, lg2(Ls)), kLn2);
     const int64_t row = q_row * a.Hq + h;

@@ -755,7 +755,7 @@ __global__ void __launch_bounds__((kProdWarpTc + tc_copy_warps(G)) * 32, 1)
       for (int h = 0; h < G; ++h) {
         const float ls = __fadd_rn(__fadd_rn(__fadd_rn(lr[h], lr[kNT + h]), lr[2 * kNT + h]),
                                    lr[3 * kNT + h]);
-        nz[h] = have && ls > 0.f;
+        nz[h] = have && (WIN ? !(ls == 0.f) : ls > 0.f); // a window's NaN sum stays NaN
         inv[h] = nz[h] ? __frcp_rn(ls) : 0.f;
         const float lse = nz[h] ? __fmul_rn(__fadd_rn(m[h], lg2(ls)), kLn2) : -INFINITY;
         lse_mine = t == h ? lse : lse_mine;

@@ -133,6 +133,9 @@ def test_extend(bia):
     assert extend(bia, d, [0, 5], [0, 4], [17]) == inv
     assert extend(bia, d, [0, 5], [3, 2], [7]) == inv
     assert extend(bia, d, [0, 5], [0, 1 << 27], [1]) == uns
+    long = ([0, 5], [0, 1 << 19], [16])  # 2^23 keys
+    assert extend(bia, d, *long, sinks=bia.BIA_WINDOW_MAX_SINKS + 1) == uns
+    assert extend(bia, d, *one, sinks=2**31 - 1, ws_bytes=511) == bia.BIA_ERR_WORKSPACE_TOO_SMALL
     assert extend(bia, d, [0, 0], [0, 0], [0]) == bia.BIA_OK  # no token
 
 
