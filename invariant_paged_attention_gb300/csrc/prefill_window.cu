@@ -124,33 +124,15 @@ __device__ __forceinline__ void gather4(uint32_t dst, const void *tmap, int32_t 
                : "memory");
 }
 
-// The MMAs of ptx.cuh for a warp that runs together, issued by the lane whose
-// `lead` is set: operands that are the same on every lane stay in uniform
-// registers, where the instruction wants them.
-__device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d, uint64_t da, uint64_t db,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile("{\n\t.reg .pred p, q;\n\t"
-               "setp.ne.b32 p, %4, 0;\n\t"
-               "setp.ne.b32 q, %5, 0;\n\t"
-               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-               "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "r"(lead)
-               : "memory");
-}
-__device__ __forceinline__ void mma_ts_lead(uint32_t lead, uint32_t d, uint32_t ta, uint64_t db,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile("{\n\t.reg .pred p, q;\n\t"
-               "setp.ne.b32 p, %4, 0;\n\t"
-               "setp.ne.b32 q, %5, 0;\n\t"
-               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-               "r"(ta), "l"(db), "r"(idesc), "r"(accumulate), "r"(lead)
-               : "memory");
-}
-__device__ __forceinline__ void commit_lead(uint32_t lead, uint32_t bar) {
-  asm volatile("{\n\t.reg .pred q;\n\t"
-               "setp.ne.b32 q, %1, 0;\n\t"
-               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               "\n\t}" ::"r"(bar), "r"(lead)
-               : "memory");
+// One lane of a warp that runs together.  The MMAs behind a branch on it take
+// their operands from uniform registers without a step more: 64 cycles an MMA
+// of 128 x 128 x 16, where a predicate on a lane's own flag took 79 whatever N
+// (window 8192: 1870 -> 1700 us), and a branch on the lane's number as long.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
 }
 
 // N words of a thread's row, 32 bytes a store where out allows it
@@ -505,12 +487,15 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
       // Every block is taken whole: with N and the steps of P.V held to what a
       // block's rows see, their operands followed data and went through vector
       // registers (W = 1024: 795 -> 950 us).
-      const uint32_t lead = lane == 0;
+      auto commit = [&](int b) {
+        if (elect_one()) mma_commit(bar(b));
+        __syncwarp();
+      };
       auto all_wait = [&](uint32_t b, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(b, parity, a.status)) != 0;
       };
-      auto all_try = [&](uint32_t b, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_try(b, parity)) != 0;
+      auto all_test = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_test(b, parity)) != 0;
       };
       auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
       // a K step only advances the address field of a descriptor
@@ -525,22 +510,28 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
       auto issue_s = [&](int t, int buf, int st) {
         const uint64_t dq = t ? dQ1 : dQ0, dk = st ? dK1 : dK0;
         const uint32_t ts = tS(buf);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t qoff = ((kk >> 2) * kAtomQW + (kk & 3) * 32) >> 4;
-          const uint32_t koff = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
-          mma_ss_lead(lead, ts, dq + qoff, dk + koff, kIdescS, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qoff = ((kk >> 2) * kAtomQW + (kk & 3) * 32) >> 4;
+            const uint32_t koff = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
+            mma_bf16_ss(ts, dq + qoff, dk + koff, kIdescS, kk > 0);
+          }
+          mma_commit(bar(L::kSFull + buf));
         }
-        commit_lead(lead, bar(L::kSFull + buf));
+        __syncwarp();
       };
       auto issue_pv = [&](int t, int buf, int st, bool first) {
         tc_fence_after();
         const uint64_t dv = st ? dV1 : dV0;
         const uint32_t to = tO(t), ts = tS(buf);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < KB / 16; ++kk)
-          mma_ts_lead(lead, to, ts + kk * 8, dv + ((kk * 2048) >> 4), kIdescPV,
-                      (!first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < KB / 16; ++kk)
+            mma_bf16_ts(to, ts + kk * 8, dv + ((kk * 2048) >> 4), kIdescPV,
+                        (!first || kk > 0) ? 1u : 0u);
+        }
+        __syncwarp();
       };
       while (ok) {
         const ItemW *xp = next(false);
@@ -562,24 +553,24 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
           const int first0 = sk0 ? 0 : j00, first1 = sk1 ? 0 : j10;
           if (uses(0, nsk, sk0, j00, j01)) issue_s(0, 0, g & 1);
           if (uses(0, nsk, sk1, j10, j11)) issue_s(1, 1, g & 1);
-          commit_lead(lead, bar(L::kKEmpty + (g & 1)));
-          if (nb == 1) commit_lead(lead, bar(L::kQEmpty));
+          commit(L::kKEmpty + (g & 1));
+          if (nb == 1) commit(L::kQEmpty);
+          // The pipe holds some 8 MMAs: what the next ones wait for is asked
+          // for while it has work (asked for at the head of a block, it ran dry
+          // for 600 cycles of 2990).  A test, as a wait for a phase that is not
+          // complete would hold the warp.
+          bool v_rdy = false, k_rdy = false;
           for (int j = 0; j < nb && ok; ++j, ++g) {
             const int st = g & 1, s1 = st ^ 1, j1 = j + 1;
             const bool u0 = uses(j, nsk, sk0, j00, j01), u1 = uses(j, nsk, sk1, j10, j11);
-            // a barrier's answer takes ~170 cycles even when its phase is
-            // complete: ask for the three at once
-            const bool v_rdy = all_try(bar(L::kVFull + st), (g >> 1) & 1);
-            const bool pa_rdy = u0 && all_try(bar(L::kPFull + 0), np0 & 1);
-            const bool k_rdy = j1 < nb && all_try(bar(L::kKFull + s1), ((g + 1) >> 1) & 1);
             ok = v_rdy || all_wait(bar(L::kVFull + st), (g >> 1) & 1);
             if (!ok) break;
             if (u0) {
-              ok = pa_rdy || all_wait(bar(L::kPFull + 0), np0 & 1);
+              ok = all_wait(bar(L::kPFull + 0), np0 & 1);
               ++np0;
               if (!ok) break;
               issue_pv(0, 0, st, j == first0);
-              if (j1 == j01) commit_lead(lead, bar(L::kODone + 0));
+              if (j1 == j01) commit(L::kODone + 0);
             }
             if (j1 < nb) {
               ok = k_rdy || all_wait(bar(L::kKFull + s1), ((g + 1) >> 1) & 1);
@@ -592,20 +583,25 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
               ++np1;
               if (!ok) break;
               issue_pv(1, 1, st, j == first1);
-              if (j1 == j11) commit_lead(lead, bar(L::kODone + 1));
+              if (j1 == j11) commit(L::kODone + 1);
             }
+            v_rdy = j1 < nb && all_test(bar(L::kVFull + s1), ((g + 1) >> 1) & 1);
+            k_rdy = j1 + 1 < nb && all_test(bar(L::kKFull + st), ((g + 2) >> 1) & 1);
             if (j1 < nb && uses(j1, nsk, sk1, j10, j11)) issue_s(1, 1, s1);
-            commit_lead(lead, bar(L::kVEmpty + st));
-            if (j1 < nb) commit_lead(lead, bar(L::kKEmpty + s1));
-            if (j1 == nb - 1) commit_lead(lead, bar(L::kQEmpty));
+            if (elect_one()) {
+              mma_commit(bar(L::kVEmpty + st));
+              if (j1 < nb) mma_commit(bar(L::kKEmpty + s1));
+              if (j1 == nb - 1) mma_commit(bar(L::kQEmpty));
+            }
+            __syncwarp();
           }
         } else {
           // one tile, two S buffers: the next block's S runs while this one's
           // softmax does
           issue_s(0, ns & 1, g & 1);
           ++ns;
-          commit_lead(lead, bar(L::kKEmpty + (g & 1)));
-          if (nb == 1) commit_lead(lead, bar(L::kQEmpty));
+          commit(L::kKEmpty + (g & 1));
+          if (nb == 1) commit(L::kQEmpty);
           for (int j = 0; j < nb && ok; ++j, ++g) {
             const int st = g & 1, s1 = st ^ 1;
             if (j + 1 < nb) {
@@ -614,16 +610,16 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
               tc_fence_after();
               issue_s(0, ns & 1, s1);
               ++ns;
-              commit_lead(lead, bar(L::kKEmpty + s1));
-              if (j + 2 == nb) commit_lead(lead, bar(L::kQEmpty));
+              commit(L::kKEmpty + s1);
+              if (j + 2 == nb) commit(L::kQEmpty);
             }
             ok = all_wait(bar(L::kVFull + st), (g >> 1) & 1) &&
                  all_wait(bar(L::kPFull + (np0 & 1)), (np0 >> 1) & 1);
             if (!ok) break;
             issue_pv(0, np0 & 1, st, j == 0);
-            commit_lead(lead, bar(L::kODone + (np0 & 1)));
+            commit(L::kODone + (np0 & 1));
             ++np0;
-            commit_lead(lead, bar(L::kVEmpty + st));
+            commit(L::kVEmpty + st);
           }
         }
       }

@@ -130,6 +130,17 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
                : "memory");
   return ok != 0;
 }
+// The same without waiting: mbar_try may hold the warp for a while.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
 // Waits for the phase with the given parity to complete.  Gives up after
 // kWaitLimitNs, sets kStatusTimeout and returns false.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t *status) {
