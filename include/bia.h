@@ -597,10 +597,11 @@ BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
  * may reach every row of a q tile that sees its block of 128 keys; keys before
  * the window of the first row of a pair of q tiles, and past the request's
  * last key, never do.  split_size: a multiple of 128 up to
- * BIA_RAGGED_MAX_SPLIT, 0 = BIA_PREFILL_SPLIT (a larger one:
- * BIA_ERR_UNSUPPORTED, as are min(sinks, kv_len) above BIA_WINDOW_MAX_SINKS and
- * caches of 2^31 - 1 (key, kv head) rows and more); with few q tiles a smaller
- * one spreads a long window over more of the GPU.  Weights lag the running maximum by up to 2^16 before they
+ * BIA_RAGGED_MAX_SPLIT (a larger one: BIA_ERR_UNSUPPORTED, as are min(sinks,
+ * kv_len) above BIA_WINDOW_MAX_SINKS and caches of 2^31 - 1 (key, kv head) rows
+ * and more); 0 = BIA_RAGGED_MAX_SPLIT for windows up to BIA_PREFILL_SPLIT, else
+ * BIA_PREFILL_SPLIT; with few q tiles a smaller one spreads a long window over
+ * more of the GPU.  Weights lag the running maximum by up to 2^16 before they
  * are divided by their sum, in fp32: values above 2^80 may overflow.
  */
 BIA_API int bia_prefill_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,

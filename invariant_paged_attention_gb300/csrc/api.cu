@@ -1386,7 +1386,13 @@ int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks
   if (rc != BIA_OK) return rc;
   if (window < 1 || sinks < 0 || batch <= 0 || !qo_host || !kvp_host || !last_host)
     return BIA_ERR_INVALID_ARG;
-  if (split == 0) split = BIA_PREFILL_SPLIT;
+  // A window within one split is not split: its tiles would only be cut where a
+  // split's end falls into them, and pay for their states (prompts of 512 to
+  // 8192 tokens at window 1024: 690 us split at 4096, 660 whole; 6 chunks at
+  // window 4096: 133 and 120, one of them 71 and 62).  A longer one is split for
+  // calls of few q tiles (one chunk at window 15000: 86 us, 200 split at 16384;
+  // six 432 and 393).
+  if (split == 0) split = window <= BIA_PREFILL_SPLIT ? BIA_RAGGED_MAX_SPLIT : BIA_PREFILL_SPLIT;
   if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
   if (split > BIA_RAGGED_MAX_SPLIT) return BIA_ERR_UNSUPPORTED;
   if (qo_host[0] != 0 || kvp_host[0] < 0) return BIA_ERR_INVALID_ARG;
@@ -1420,7 +1426,7 @@ int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks
   if (items * p->parts > INT32_MAX) return BIA_ERR_UNSUPPORTED;
   // Whole pairs take full rounds of the CTAs, split ones share them out and pay
   // for their states: folding is taken while its last round is mostly full.  240
-  // pairs of 34 blocks (two rounds) 146 us folded, 171 split; 8 of them 64 and 25.
+  // pairs of 34 blocks (two rounds) took 152 us folded and 172 split.
   const int64_t rounds = (items + bia::kFoldCtas - 1) / bia::kFoldCtas;
   p->folds = p->parts > 1 && 10 * rounds * bia::kFoldCtas <= 13 * items ? 1 : 0;
   p->states = p->parts > 1 && !p->folds;
