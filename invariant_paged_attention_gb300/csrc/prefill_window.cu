@@ -689,56 +689,49 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
 #pragma unroll
           for (int c = 0; c < KB / 32; ++c) weights(c, v[c]);
         } else {
-          // 32 columns at a time, read twice.  The row sees keys < p1, of them
-          // those >= p1 - window or < sinks; what the warp's rows see of 32
-          // columns may be all of them, none (no load, no exponentials), or not
-          // the same (a test a column): the first row's limits are `span` below
-          // the last one's.
+          // The row sees keys < p1, of them those >= p1 - window or < sinks; what
+          // the warp's rows see of 32 columns may be all of them, none (no
+          // exponentials), or not the same (a test a column): the first row's
+          // limits are `span` below the last one's.
+          uint32_t v[KB / 32][32];
+          float b4[KB / 32];
+          uint32_t none = 0; // bit c: none of columns 32c ..
+#pragma unroll
+          for (int c = 0; c < KB / 32; ++c) tmem_ld32_max(srow + c * 32, v[c], b4[c]);
           const int key0 = (j < vx->n_sink ? j : vx->w0 + j - vx->n_sink) * KB;
-          const int32_t p1_w = vx->kv_len - vx->q_len + (vx->tile + t) * T +
-                               (((warp & 3) * 32) >> gs) + 1;
-          const int32_t p1 = p1_w + (lane >> gs);
-          uint32_t cls = 0; // bit c: all of columns 32c ..; bit 8 + c: none of them
-          {
-            const int span = 31 >> gs, snk = a.sinks - key0;
-            const int vis_0 = p1_w - key0, vis_31 = vis_0 + span;
-            const int lo_0 = vis_0 - a.window, lo_31 = lo_0 + span;
-#pragma unroll
-            for (int c = 0; c < KB / 32; ++c) {
-              if (vis_0 >= 32 * c + 32 && (lo_31 <= 32 * c || snk >= 32 * c + 32)) cls |= 1u << c;
-              if (vis_31 <= 32 * c || (lo_0 >= 32 * c + 32 && snk <= 32 * c)) cls |= 256u << c;
-            }
-          }
-          uint32_t v[32];
-          auto load = [&](int c) {
-            tmem_ld32(srow + c * 32, v);
-            tmem_wait_ld();
-            if (cls >> c & 1u) return;
-            const int at = key0 + 32 * c;
-            const uint32_t vis = first_bits(p1 - at) &
-                                 (~first_bits(p1 - a.window - at) | first_bits(a.sinks - at));
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((vis >> i) & 1u)) v[i] = 0xff800000u; // -inf: a weight of zero
-          };
+          const int span = 31 >> gs, snk = a.sinks - key0;
+          const int vis_0 = vx->kv_len - vx->q_len + (vx->tile + t) * T +
+                            (((warp & 3) * 32) >> gs) + 1 - key0;
+          const int lo_0 = vis_0 - a.window, n_vis = vis_0 + (lane >> gs);
+          tmem_wait_ld();
           float bm = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < KB / 32; ++c) {
-            if (cls >> (8 + c) & 1u) continue;
-            load(c);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              bm = fmax3(bm, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          for (int c = 0; c < KB / 32; ++c) {
+            if (vis_0 + span <= 32 * c || (lo_0 >= 32 * c + 32 && snk <= 32 * c)) {
+              none |= 1u << c;
+              continue;
+            }
+            if (vis_0 < 32 * c + 32 || (lo_0 + span > 32 * c && snk < 32 * c + 32)) {
+              const uint32_t vis = first_bits(n_vis - 32 * c) &
+                                   (~first_bits(n_vis - a.window - 32 * c) | first_bits(snk - 32 * c));
+              b4[c] = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                if (!((vis >> i) & 1u)) v[c][i] = 0xff800000u; // -inf: a weight of zero
+                if (!((vis >> i) & 2u)) v[c][i + 1] = 0xff800000u;
+                b4[c] = fmax3(b4[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+              }
+            }
+            bm = fmaxf(bm, b4[c]);
           }
           move_max(bm);
-#pragma unroll 1
-          for (int c = 0; c < KB / 32; ++c) { // (its P lies over columns read before)
-            if (cls >> (8 + c) & 1u) {
+#pragma unroll
+          for (int c = 0; c < KB / 32; ++c) {
+            if (none >> c & 1u) {
               const uint32_t zero[16] = {};
               tmem_st16(srow + c * 16, zero);
             } else {
-              load(c);
-              weights(c, v);
+              weights(c, v[c]);
             }
           }
         }
