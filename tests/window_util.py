@@ -81,6 +81,8 @@ class Batch:
         need = bia.bia_decode_window_workspace_size(self.desc, self.window, self.sinks, self.kvp, self.last, split)
         assert need > 0
         ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda") if ws is None else ws
+        if kw.get("stream"):  # the workspace is filled on the current one
+            kw["stream"].wait_stream(torch.cuda.current_stream())
         bia.bia_decode_paged_window(self.desc, self.window, self.sinks, self.q, self.k_cache, self.v_cache, *self.dev,
                                     self.kvp, self.last, ws, self.out if out is None else out,
                                     self.lse if lse is True else lse, split, **kw)
@@ -102,6 +104,8 @@ def extend(self, split=0, ws=None, out=None, lse=True, **kw):
     need = bia.bia_prefill_window_workspace_size(self.desc, self.window, self.sinks, self.qo, self.kvp, self.last, split)
     assert need > 0
     ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda") if ws is None else ws
+    if kw.get("stream"):
+        kw["stream"].wait_stream(torch.cuda.current_stream())
     bia.bia_prefill_paged_window(self.desc, self.window, self.sinks, self.q, self.k_cache, self.v_cache, self.qo.cuda(),
                                  *self.dev, self.qo, self.kvp, self.last, ws, self.out if out is None else out,
                                  self.lse if lse is True else lse, split, **kw)
