@@ -209,7 +209,35 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
     return __ldg(a.kv_indices + r.page_base + (key_of(key) >> a.page_shift));
   };
   int32_t pg_next = page_of(0);
+  // With a window every lane copies 16-byte pieces, a row LPK lanes: the split
+  // tiles are short, and a bulk copy a row costs the same whatever its length
+  // (64 requests, window 4096, 32/8 heads x 64: 236 us with bulk copies, 196
+  // with pieces; 16/8 x 256: 425 and 398; one request x 64: 16.6 and 13.3).
+  constexpr bool kPieces = WIN;
+  auto pieces = [&](int i) {
+    if (i < my_chunks) {
+      const int32_t key = key_begin + (warp + kWarps * i) * kChunk + kl_ld;
+      const bool good = pg_next >= 0 && pg_next < a.num_pages;
+      if (lane < 8 && key < key_end && !good) atomicOr(status, kStatusBadPage);
+      const int32_t slot = good ? (key_of(key) & page_mask) : -1;
+      const int32_t pg = pg_next;
+      pg_next = page_of(i + 1);
+      const int st = i % NS;
+#pragma unroll
+      for (int n = 0; n < kChunk / KPW; ++n) {
+        const int kl = n * KPW + grp;
+        const int32_t in_page = __shfl_sync(0xffffffffu, slot, kl);
+        const int64_t at = (static_cast<int64_t>(__shfl_sync(0xffffffffu, pg, kl)) << a.page_shift) + in_page;
+        const bool some = in_page >= 0 && 8 * sub < Dr;
+        const int64_t off = some ? (at * a.Hkv + kvh) * Dr + 8 * sub : 0;
+        cp_async16(sK(st) + kl * L::kRow + sub * 16, a.k_cache + off, some);
+        cp_async16(sV(st) + kl * L::kRow + sub * 16, a.v_cache + off, some);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   auto issue = [&](int i) {
+    if constexpr (kPieces) return pieces(i);
     const int st = i % NS;
     const int32_t pg = pg_next;
     pg_next = page_of(i + 1);
@@ -235,7 +263,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
       bulk_g2s(dst, (lane < 8 ? a.k_cache : a.v_cache) + off, row_copy, bar(st));
     }
   };
-  for (int i = 0; i < NS && i < my_chunks; ++i) issue(i);
+  for (int i = 0; i < NS && (kPieces || i < my_chunks); ++i) issue(i);
 
   // ---- queries of the group as fp32 pairs, pre-scaled by sm_scale * log2(e)
   // (G == 4 with 16 lanes a key: slot g holds head own_head_order(g, sub))
@@ -265,7 +293,10 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   bool failed = false;
   for (int i = 0; i < my_chunks; ++i) {
     const int st = i % NS;
-    if (!mbar_wait(bar(st), (i / NS) & 1, status)) {
+    if constexpr (kPieces) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+      __syncwarp(); // every lane's pieces
+    } else if (!mbar_wait(bar(st), (i / NS) & 1, status)) {
       failed = true;
       break;
     }
@@ -407,7 +438,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
     }
     __syncwarp();
     fence_proxy_async(); // this warp's reads of the stage precede the refill
-    if (i + NS < my_chunks) issue(i + NS);
+    if (kPieces || i + NS < my_chunks) issue(i + NS);
   }
 
   if constexpr (kOwnHead) {
@@ -444,6 +475,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
       m[g] = M;
     }
   }
+  if constexpr (kPieces) cp_async_wait_all(); // (what is left are empty groups)
   // every ring has drained: reuse the shared memory for the warp states
   __syncthreads();
   float *s_m = reinterpret_cast<float *>(smem);
