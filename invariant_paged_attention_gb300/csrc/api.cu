@@ -1454,6 +1454,9 @@ int window_decode_plan(const bia_attn_desc *desc, const bia_bounds *bounds, int3
   int rc = check_desc(desc);
   if (rc != BIA_OK) return rc;
   if (window < 1 || sinks < 0 || batch <= 0) return BIA_ERR_INVALID_ARG;
+  // 512 by default: short tiles spread few requests over the SMs (one at window
+  // 1024: 11.5 us in tiles of 256 keys, 13.7 of 512, 18.4 of 1024), long ones have
+  // fewer starts and states (64 requests: 239, 200 and 189 us).
   if (split == 0) split = BIA_WINDOW_DECODE_SPLIT;
   if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
   if (bounds) {

@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   // With a window every lane copies 16-byte pieces, a row LPK lanes: the split
   // tiles are short, and a bulk copy a row costs the same whatever its length
   // (64 requests, window 4096, 32/8 heads x 64: 236 us with bulk copies, 196
-  // with pieces; 16/8 x 256: 425 and 398; one request x 64: 16.6 and 13.3).
+  // with pieces; 16/8 x 256: 425 and 398; one request at window 1024 x 64: 16.6 and
+  // 13.3).
   constexpr bool kPieces = WIN;
   auto pieces = [&](int i) {
     if (i < my_chunks) {

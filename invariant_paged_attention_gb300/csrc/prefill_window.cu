@@ -27,6 +27,18 @@
 // pair and the CTA folds each state into the running one as the merge would
 // (fold.cuh).  The sinks go with a q tile's first split.  The bits are the same
 // either way, whatever the batch.
+//
+// Measured with 32/8 heads x 128 on prompts of 512 to 8192 tokens: window 1024
+// 655 us (1030 TFLOP/s of the scores seen), 8192 1675 us (1370), 16/8 heads x
+// 256 750 us (880); pages of one key 760 and 1220 us.  A pair of tiles takes a
+// 128-key block in ~2950 cycles, 2050 of them MMAs back to back; the rest is the
+// chain P -> P.V -> S -> P (a wait answered in 100 to 150 cycles, commits of 60)
+// and, at the power that this draws, a clock of 1.6 to 1.75 GHz.  Exponentials
+// left out, it took as long.  A short window adds its two ends (a block that is
+// not whole costs up to twice its time) and an epilogue of ~4500 cycles every
+// ten blocks; 256-wide heads, one tile an item, read twice the bytes a flop and
+// wait for values; pages of fewer than 16 keys for the gathers (four rows of
+// 128 bytes about every 29 cycles an SM).
 #include "bia_internal.h"
 #include "fold.cuh"
 #include "ptx.cuh"
@@ -90,8 +102,8 @@ struct Steps {
 
 // ROWS: pages of fewer than 16 keys, whose rows are gathered four at a time.  A
 // warp issues its lanes' gathers one after the other, so K and V have two warps
-// each (window 1024, page 1: 1010 -> 887 us); runs of 16 keys need one, and the
-// warps more would cost 4 %.
+// each (window 1024, page 1: 962 us with one, 760 with two; 256-wide heads 1602
+// and 1220); runs of 16 keys need one.
 template <int D, bool ROWS>
 struct SmemW {
   static constexpr int kThreads = ROWS ? 512 : 384, kLoaders = ROWS ? 4 : 2;
@@ -484,9 +496,9 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
     } else if (warp == kMmaWarpW) {
       // ------------------------------------------------------------ MMA issuer
       // The warp runs together, one lane issues: what the MMAs take is uniform.
-      // Every block is taken whole: with N and the steps of P.V held to what a
-      // block's rows see, their operands followed data and went through vector
-      // registers (W = 1024: 795 -> 950 us).
+      // Every block is taken whole: N and the steps of P.V held to what a
+      // block's rows see would be operands that follow data, each MMA's from
+      // vector registers.
       auto commit = [&](int b) {
         if (elect_one()) mma_commit(bar(b));
         __syncwarp();

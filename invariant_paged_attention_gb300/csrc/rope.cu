@@ -13,13 +13,20 @@
 // A head is a row of D/16 lanes, 16 columns a lane as two 16-byte pieces that
 // hold both columns of each of its eight pairs: lane c has frequencies 8c ..
 // 8c+7, columns 8c .. and rot/2 + 8c .. (halves) or 16c .. 16c+15
-// (interleaved); the lanes behind the rotating columns, and values, just 16
+// (interleaved; with rot = D columns 8c .. and D/2 + 8c ..); the lanes behind the rotating columns, and values, just 16
 // columns.  So a pair never crosses lanes, the norm is one shuffle sum, and a
 // lane's factors (cos and sin times the weights of their columns) serve every
 // head of its token; the arithmetic runs on fp32 pairs.  A warp runs through
 // the heads of one token (queries, keys, values) with kRing steps' loads
 // under way; the token's slot and position are found meanwhile.  A call with
 // few tokens splits a token's heads over several warps, down to a step a warp.
+//
+// Bound by the copy rate and, close behind, by its instructions (three in four
+// cycles issue one): 17868 tokens of 32/8 heads x 128 66 us (5.6 TB/s, 81 % of a
+// plain copy), 44213 tokens into bf16 pages 190 us (5.75 TB/s, 85 %), into 8-bit
+// pages 216 us (5.05 TB/s, 74 %; the scales' maxima and the codes come on top),
+// 10693 tokens of 16/2 heads, half of the columns turning on three axes, 25 us (4.0
+// TB/s).
 #include <algorithm>
 
 #include "bia_internal.h"
@@ -32,7 +39,10 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRing = 2; // steps of a warp whose loads are under way (1 KB of shared memory each)
+// Steps of a warp whose loads are under way (1 KB of shared memory each): with 4
+// the four calls above took 68, 190, 220 and 27 us, with 8 (fewer CTAs an SM)
+// 72, 192, 239 and 33.
+constexpr int kRing = 2;
 enum RopeDest { kToRows, kToPages, kToPagesFp8 };
 
 // The lane's sixteen columns as a[8], b[8]: pair f is (a[f], b[f]).
@@ -113,9 +123,13 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
   const int part = static_cast<int>(w - token * parts);
   const int D = a.D, half = a.rot >> 1;
   const bool in_row = c * 16 < D, turns = c * 16 < a.rot;
-  // the lane's two pieces of a head that rotates (or not); of a value 16c, 16c + 8
-  const bool apart = turns && !INTER;
+  // the lane's two pieces of a head that rotates (or not); of a value 16c, 16c +
+  // 8.  Interleaved pairs of a whole row lie half a row apart too, four a piece
+  // (44213 tokens into bf16 pages 199 us, with one run of eight pairs 229: two
+  // copies touched each sector).
+  const bool apart = turns && (!INTER || a.rot == D), split = INTER && apart;
   const int col0 = apart ? 8 * c : 16 * c, col1 = apart ? half + 8 * c : 16 * c + 8;
+  const int freq0 = split ? 4 * c : 8 * c, freq1 = split ? half / 2 + 4 * c : 8 * c + 4;
   // steps: of queries, then of keys, then of values; a step is of one kind
   const int steps_q = (a.Hq + HPS - 1) / HPS, steps_k = (a.Hk + HPS - 1) / HPS;
   const int steps = steps_q + (kPaged ? 2 : 1) * steps_k;
@@ -189,13 +203,12 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
       }
       if (!turns) continue;
       // which of the lane's frequencies follow this axis (two bits each)
-      const uint32_t who = a.freq_axis[c >> 1] >> (16 * (c & 1)) & 0xffffu;
+      const uint32_t who = (a.freq_axis[freq0 >> 4] >> (2 * (freq0 & 15)) & 0xffu) |
+                           (a.freq_axis[freq1 >> 4] >> (2 * (freq1 & 15)) & 0xffu) << 8;
       const uint32_t off = who ^ (0x5555u * ax); // zero pairs follow it
-      const float4 *row =
-          reinterpret_cast<const float4 *>(a.table + static_cast<int64_t>(p) * a.rot + 8 * c);
-      const float4 *row_s = reinterpret_cast<const float4 *>(
-          a.table + static_cast<int64_t>(p) * a.rot + half + 8 * c);
-      const float4 t[4] = {__ldg(row), __ldg(row + 1), __ldg(row_s), __ldg(row_s + 1)};
+      const float *row = a.table + static_cast<int64_t>(p) * a.rot;
+      auto four = [&](int f) { return __ldg(reinterpret_cast<const float4 *>(row + f)); };
+      const float4 t[4] = {four(freq0), four(freq1), four(half + freq0), four(half + freq1)};
       const float tc[8] = {t[0].x, t[0].y, t[0].z, t[0].w, t[1].x, t[1].y, t[1].z, t[1].w};
       const float ts[8] = {t[2].x, t[2].y, t[2].z, t[2].w, t[3].x, t[3].y, t[3].z, t[3].w};
 #pragma unroll
@@ -328,21 +341,23 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
         }
         const int64_t row = slot * a.Hk + h;
         uint8_t *dst = (kind == 2 ? a.v_codes : a.k_codes) + row * D;
+        uint2 r0, r1;
         if (INTER && kind != 2) {
-          *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(
-              codes4(ya[0], yb[0], ya[1], yb[1], inv), codes4(ya[2], yb[2], ya[3], yb[3], inv),
-              codes4(ya[4], yb[4], ya[5], yb[5], inv), codes4(ya[6], yb[6], ya[7], yb[7], inv));
+          r0 = make_uint2(codes4(ya[0], yb[0], ya[1], yb[1], inv),
+                          codes4(ya[2], yb[2], ya[3], yb[3], inv));
+          r1 = make_uint2(codes4(ya[4], yb[4], ya[5], yb[5], inv),
+                          codes4(ya[6], yb[6], ya[7], yb[7], inv));
         } else {
-          const uint2 r0 = make_uint2(codes4(ya[0], ya[1], ya[2], ya[3], inv),
-                                      codes4(ya[4], ya[5], ya[6], ya[7], inv));
-          const uint2 r1 = make_uint2(codes4(yb[0], yb[1], yb[2], yb[3], inv),
-                                      codes4(yb[4], yb[5], yb[6], yb[7], inv));
-          if (kind == 2) {
-            *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(r0.x, r0.y, r1.x, r1.y);
-          } else {
-            *reinterpret_cast<uint2 *>(dst + col0) = r0;
-            *reinterpret_cast<uint2 *>(dst + col1) = r1;
-          }
+          r0 = make_uint2(codes4(ya[0], ya[1], ya[2], ya[3], inv),
+                          codes4(ya[4], ya[5], ya[6], ya[7], inv));
+          r1 = make_uint2(codes4(yb[0], yb[1], yb[2], yb[3], inv),
+                          codes4(yb[4], yb[5], yb[6], yb[7], inv));
+        }
+        if (kind == 2) {
+          *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(r0.x, r0.y, r1.x, r1.y);
+        } else {
+          *reinterpret_cast<uint2 *>(dst + col0) = r0;
+          *reinterpret_cast<uint2 *>(dst + col1) = r1;
         }
         if (c == 0) (kind == 2 ? a.v_scale : a.k_scale)[row] = static_cast<uint8_t>(ex + 127);
       }
