@@ -1472,6 +1472,9 @@ int window_decode_plan(const bia_attn_desc *desc, const bia_bounds *bounds, int3
     }
   }
   if (p->max_kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
+  // (a tile longer than every request is the same as one of 2^30 keys, and its
+  // ends stay in 32 bits)
+  split = std::min(split, 1 << 30);
   p->split = split;
   p->parts = static_cast<int32_t>((window_len(p->max_kv_len, window, sinks) + split - 1) / split);
   const int64_t units = static_cast<int64_t>(batch) * p->parts;

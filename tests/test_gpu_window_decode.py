@@ -162,3 +162,22 @@ def test_offsets_past_32_bits_and_another_stream():
     assert bia.bia_read_status(ws, s) == 0
     s.synchronize()
     assert torch.equal(bits(want), bits(c.out))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_split_tile_longer_than_every_request(d):
+    """Whatever its size: 32-bit arithmetic on it must not wrap."""
+    c = Batch([900, 3], [1, 1], 8, 4, d, 16, 500, 4, seed=12)
+    c.decode(1024)
+    want = c.out.clone(), c.lse.clone()
+    c.check()
+    for split in (1 << 30, 2**31 - 128):
+        c.out.fill_(7), c.lse.fill_(7)
+        c.decode(split)
+        assert torch.equal(bits(want[0]), bits(c.out)) and torch.equal(bits(want[1]), bits(c.lse))
+    e = Batch([900, 300], [40, 300], 8, 4, d, 16, 500, 4, seed=13)
+    e.extend(1024)
+    want = e.out.clone()
+    e.extend(1 << 24)
+    e.check()
+    assert torch.equal(bits(want), bits(e.out))
