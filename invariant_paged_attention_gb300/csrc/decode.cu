@@ -45,9 +45,12 @@ constexpr int kThreadsDec = kWarps * 32;
 constexpr int kChunk = 8;              // keys per chunk
 constexpr float kLazyThreshold = 8.0f; // log2 units
 
-template <int D>
+// The short split tiles of a window (WIN) have a stage or two less and so more
+// CTAs an SM where registers allow (64 requests, window 4096, 64-wide heads: one a
+// group 146 -> 115 us, four 196 -> 192; 96 wide 233 -> 221).
+template <int D, bool WIN = false>
 struct DecSmem {
-  static constexpr int kStages = D == 256 ? 2 : (D == 128 ? 3 : 5);
+  static constexpr int kStages = D == 256 ? 2 : (D == 128 ? (WIN ? 2 : 3) : (WIN ? 3 : 5));
   static constexpr int kRow = D * 2;                  // bytes of one key row
   static constexpr int kStage = 2 * kChunk * kRow;    // K rows then V rows
   static constexpr int kRing = kStages * kStage;      // one warp's ring
@@ -117,7 +120,8 @@ __device__ __forceinline__ float reduce_scatter4(const float (&s)[4]) {
 template <int D, int G, bool MASK, bool WIN>
 __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
     decode_kernel(const AttnArgs a) {
-  using L = DecSmem<D>;
+  using L = DecSmem<D, WIN>;
+  static_assert(G * (D + 2) * 4 <= L::kRing, "the warps' states take the place of their rings");
   constexpr int LPK = D / 8;         // lanes per key row
   constexpr int KPW = 32 / LPK;      // key rows per warp step
   constexpr int STEPS = kChunk / KPW; // steps per chunk
@@ -532,7 +536,7 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
 
 template <int D, int G, bool MASK, bool WIN = false>
 cudaError_t launch_decode_dgm(const AttnArgs &a, cudaStream_t s) {
-  using L = DecSmem<D>;
+  using L = DecSmem<D, WIN>;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = prepare_launch(reinterpret_cast<const void *>(decode_kernel<D, G, MASK, WIN>),
                                        L::kAlloc, ready);
