@@ -978,34 +978,40 @@ def _rope_types(table, positions, q_weight, k_weight, status):
                         ("status", status, I32, True))
 
 
-_Tensor = torch.Tensor
+# The calls below look at a tensor's dtype, layout and shape in as few steps as
+# they can and leave its device to the library, which refuses what is not memory
+# of the current device before it enqueues anything.  What is not plain (another
+# stream, no tokens, a dtype or layout that is wrong), and what the library
+# refused, goes through the checks above, which name the argument.
 
 
-def _all_dense(device, *pairs) -> bool:
-    """Whether every tensor that is not None of the (tensor, dtype) pairs is
-    contiguous, of its dtype, on CUDA device `device`, the current one."""
-    if device < 0 or device != _current_device():
-        return False
-    for t, dtype in pairs:
-        if t is not None and (type(t) is not _Tensor or t.dtype is not dtype or
-                              t.get_device() != device or not t.is_contiguous()):
-            return False
-    return True
-
-
-def _step(name, t, heads, head_dim, tokens, device) -> int:
-    """_packed for rows on CUDA device `device`; what is not plain goes there."""
-    if (type(t) is _Tensor and t.dtype is BF16 and t.get_device() == device and tokens > 1 and
-            t.shape == (tokens, heads, head_dim)):
+def _step(name, t, heads, head_dim, tokens) -> int:
+    """_packed; what is not plain goes there."""
+    if isinstance(t, torch.Tensor) and t.dtype is BF16 and tokens > 1 and \
+            t.shape == (tokens, heads, head_dim):
         step, head, col = t.stride()
         if col == 1 and (head == head_dim or heads == 1) and step % 8 == 0 and \
                 step >= heads * head_dim:
             return step
-    step = _packed(name, t, heads, head_dim, tokens)
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, the other arguments on CUDA device {device}"
-                         if device >= 0 else f"{name} must be on the device of the others")
-    return step
+    return _packed(name, t, heads, head_dim, tokens)
+
+
+def _check_rope_tensors(given, rows, table, positions, q_weight, k_weight, status, stream):
+    """All on one device: `given`, the rotation's tensors, and the packed rows."""
+    given = given + _rope_types(table, positions, q_weight, k_weight, status)
+    _check_cuda(given, stream)
+    for name, t in rows:
+        if t is not None and t.device != given[0][1].device:
+            raise ValueError(f"{name} is on {t.device}, the other arguments on "
+                             f"{given[0][1].device}")
+
+
+def _plain_rope(table, positions, q_weight, k_weight, status) -> bool:
+    return (table.is_cuda and table.dtype is F32 and table.is_contiguous() and
+            (positions is None or (positions.dtype is I32 and positions.is_contiguous())) and
+            (q_weight is None or (q_weight.dtype is F32 and q_weight.is_contiguous())) and
+            (k_weight is None or (k_weight.dtype is F32 and k_weight.is_contiguous())) and
+            (status is None or (status.dtype is I32 and status.is_contiguous())))
 
 
 def bia_norm_rope(desc, rope, table, positions, q, k, q_out, k_out, q_weight=None, k_weight=None,
@@ -1020,26 +1026,35 @@ def bia_norm_rope(desc, rope, table, positions, q, k, q_out, k_out, q_weight=Non
         raise TypeError(f"q and k must be torch.Tensor, got {type(some).__name__}")
     if positions is None:
         raise TypeError("positions is required")
-    total, at = some.shape[0], some.get_device()
+    total = some.shape[0]
     hq, hkv, d = desc.num_qo_heads, desc.num_kv_heads, desc.head_dim
     q_step = qo_step = k_step = ko_step = 0
     if q is not None or q_out is not None:
-        q_step = _step("q", q, hq, d, total, at)
-        qo_step = _step("q_out", q_out, hq, d, total, at)
+        q_step = _step("q", q, hq, d, total)
+        qo_step = _step("q_out", q_out, hq, d, total)
     if k is not None or k_out is not None:
-        k_step = _step("k", k, hkv, d, total, at)
-        ko_step = _step("k_out", k_out, hkv, d, total, at)
-    if not (stream is None and
-            _all_dense(at, (table, F32), (positions, I32), (q_weight, F32), (k_weight, F32),
-                       (status, I32))):
-        _check_cuda([("q" if q is not None else "k", some)] +
-                    _rope_types(table, positions, q_weight, k_weight, status), stream)
+        k_step = _step("k", k, hkv, d, total)
+        ko_step = _step("k_out", k_out, hkv, d, total)
+
+    def check():
+        _check_rope_tensors([("q" if q is not None else "k", some)],
+                            (("q_out", q_out), ("k", k), ("k_out", k_out)), table, positions,
+                            q_weight, k_weight, status, stream)
+
+    try:
+        plain = stream is None and total > 0 and _plain_rope(table, positions, q_weight, k_weight,
+                                                             status)
+    except AttributeError:
+        plain = False
+    if not plain:
+        check()
     _check_rope(desc, rope, table, positions, q_weight, k_weight, total)
     rc = load().bia_norm_rope(
         ctypes.byref(desc), ctypes.byref(rope), table.data_ptr(), positions.data_ptr(), _at(q),
         _at(k), q_step, k_step, _at(q_weight), _at(k_weight), total, _at(q_out), _at(k_out),
         qo_step, ko_step, _at(status), _handle(stream))
     if rc != BIA_OK:
+        check()
         raise BiaError(rc, "bia_norm_rope")
 
 
@@ -1053,25 +1068,40 @@ def _append_rope(fp8, desc, rope, table, q, k_new, v_new, caches, append_indptr,
     batch = ap.numel() - 1
     total, hq, hkv, d = _last(ap), desc.num_qo_heads, desc.num_kv_heads, desc.head_dim
     k_cache, v_cache = caches[0], caches[1]
-    at = _index(k_cache)
     q_step = qo_step = ko_step = 0
     if q is not None or q_out is not None:
-        q_step = _step("q", q, hq, d, total, at)
-        qo_step = _step("q_out", q_out, hq, d, total, at)
-    k_step = _step("k_new", k_new, hkv, d, total, at)
-    v_step = _step("v_new", v_new, hkv, d, total, at)
+        q_step = _step("q", q, hq, d, total)
+        qo_step = _step("q_out", q_out, hq, d, total)
+    k_step = _step("k_new", k_new, hkv, d, total)
+    v_step = _step("v_new", v_new, hkv, d, total)
     if k_out is not None:
-        ko_step = _step("k_out", k_out, hkv, d, total, at)
+        ko_step = _step("k_out", k_out, hkv, d, total)
     kinds = (E4M3, E4M3, E8M0, E8M0) if fp8 else (BF16, BF16)
-    if not (stream is None and
-            _all_dense(at, *zip(caches, kinds), (append_indptr, I32), (kv_indptr, I32),
-                       (kv_indices, I32), (kv_last_page_len, I32), (table, F32),
-                       (positions, I32), (q_weight, F32), (k_weight, F32), (status, I32))):
+
+    def check():
         ts = _check_types(*zip(("k_cache", "v_cache", "k_scale", "v_scale"), caches, kinds),
                           ("append_indptr", append_indptr, I32), ("kv_indptr", kv_indptr, I32),
                           ("kv_indices", kv_indices, I32),
                           ("kv_last_page_len", kv_last_page_len, I32))
-        _check_cuda(ts + _rope_types(table, positions, q_weight, k_weight, status), stream)
+        _check_rope_tensors(ts, (("q", q), ("q_out", q_out), ("k_new", k_new), ("v_new", v_new),
+                                 ("k_out", k_out)), table, positions, q_weight, k_weight, status,
+                            stream)
+
+    try:
+        plain = (stream is None and total > 0 and
+                 k_cache.dtype is kinds[0] and k_cache.is_contiguous() and
+                 v_cache.dtype is kinds[0] and v_cache.is_contiguous() and
+                 (not fp8 or (caches[2].dtype is E8M0 and caches[2].is_contiguous() and
+                              caches[3].dtype is E8M0 and caches[3].is_contiguous())) and
+                 append_indptr.dtype is I32 and append_indptr.is_contiguous() and
+                 kv_indptr.dtype is I32 and kv_indptr.is_contiguous() and
+                 kv_indices.dtype is I32 and kv_indices.is_contiguous() and
+                 kv_last_page_len.dtype is I32 and kv_last_page_len.is_contiguous() and
+                 _plain_rope(table, positions, q_weight, k_weight, status))
+    except AttributeError:
+        plain = False
+    if not plain:
+        check()
     if fp8:
         _check_caches_fp8(desc, *caches)
     else:
@@ -1098,6 +1128,7 @@ def _append_rope(fp8, desc, rope, table, q, k_new, v_new, caches, append_indptr,
         kv_indices.data_ptr(), kv_last_page_len.data_ptr(), ap.data_ptr(), kvp.data_ptr(),
         last.data_ptr(), batch, *tail, _at(status), _handle(stream))
     if rc != BIA_OK:
+        check()
         raise BiaError(rc, name)
 
 
@@ -1129,33 +1160,50 @@ def bia_append_paged_kv_fp8_rope(desc, rope, table, q, k_new, v_new, k_cache, v_
 # ---------------------------------------------------------------- window and sinks
 
 
+def _check_window_tensors(q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
+                          out, lse, stream, qo_indptr=None):
+    more = () if qo_indptr is None else (("qo_indptr", qo_indptr, I32),)
+    _check_cuda(_check_types(("q", q, BF16), ("k_cache", k_cache, BF16),
+                             ("v_cache", v_cache, BF16), ("kv_indptr", kv_indptr, I32),
+                             ("kv_indices", kv_indices, I32),
+                             ("kv_last_page_len", kv_last_page_len, I32),
+                             ("workspace", workspace, None), ("out", out, BF16),
+                             ("lse", lse, F32, True), *more), stream)
+
+
 def _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
                   out, lse, stream, batch, kvp=None, last=None, qo_indptr=None):
     """The tensors of a windowed call of `batch` requests over the bf16 cache."""
-    at = _index(q)
-    if not (stream is None and
-            _all_dense(at, (q, BF16), (out, BF16), (k_cache, BF16), (v_cache, BF16),
-                       (kv_indptr, I32), (kv_indices, I32), (kv_last_page_len, I32), (lse, F32),
-                       (qo_indptr, I32)) and
-            _index(workspace) == at and workspace.is_contiguous()):
-        more = () if qo_indptr is None else (("qo_indptr", qo_indptr, I32),)
-        _check_cuda(_check_types(("q", q, BF16), ("k_cache", k_cache, BF16),
-                                 ("v_cache", v_cache, BF16), ("kv_indptr", kv_indptr, I32),
-                                 ("kv_indices", kv_indices, I32),
-                                 ("kv_last_page_len", kv_last_page_len, I32),
-                                 ("workspace", workspace, None), ("out", out, BF16),
-                                 ("lse", lse, F32, True), *more), stream)
+    try:
+        plain = (stream is None and q.is_cuda and q.dtype is BF16 and q.is_contiguous() and
+                 out.dtype is BF16 and out.is_contiguous() and
+                 k_cache.dtype is BF16 and k_cache.is_contiguous() and
+                 v_cache.dtype is BF16 and v_cache.is_contiguous() and
+                 kv_indptr.dtype is I32 and kv_indptr.is_contiguous() and
+                 kv_indices.dtype is I32 and kv_indices.is_contiguous() and
+                 kv_last_page_len.dtype is I32 and kv_last_page_len.is_contiguous() and
+                 (lse is None or (lse.dtype is F32 and lse.is_contiguous())) and
+                 (qo_indptr is None or (qo_indptr.dtype is I32 and qo_indptr.is_contiguous())) and
+                 workspace.is_contiguous())
+        shape, cache = q.shape, k_cache.shape
+        plain = plain and shape[0] > 0
+    except (AttributeError, IndexError):
+        plain = False
+    if not plain:
+        _check_window_tensors(q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len,
+                              workspace, out, lse, stream, qo_indptr)
+        shape, cache = q.shape, k_cache.shape
     hq, d = desc.num_qo_heads, desc.head_dim
-    rows = (k_cache.shape[0], desc.page_size, desc.num_kv_heads, d)
-    if k_cache.shape != rows or v_cache.shape != rows:
+    rows = (cache[0], desc.page_size, desc.num_kv_heads, d)
+    if cache != rows or v_cache.shape != rows:
         raise ValueError(f"k_cache and v_cache must be {rows} (num_pages, page_size, "
                          f"num_kv_heads, head_dim) for this descriptor, got "
-                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
-    want = (q.shape[0], hq, d)
-    if q.shape != want or out.shape != want:
-        raise ValueError(f"q and out must be {want}, got {tuple(q.shape)} and {tuple(out.shape)}")
-    if lse is not None and lse.numel() != want[0] * hq:
-        raise ValueError(f"lse must hold {want[0]} x {hq} floats")
+                         f"{tuple(cache)} and {tuple(v_cache.shape)}")
+    if shape != (shape[0], hq, d) or out.shape != shape:
+        raise ValueError(f"q and out must be {(shape[0], hq, d)}, got {tuple(shape)} and "
+                         f"{tuple(out.shape)}")
+    if lse is not None and lse.numel() != shape[0] * hq:
+        raise ValueError(f"lse must hold {shape[0]} x {hq} floats")
     _check_table(batch, kv_indptr, kv_indices, kv_last_page_len, kvp, last)
 
 
@@ -1183,6 +1231,8 @@ def bia_decode_paged_window(desc, window, sinks, q, k_cache, v_cache, kv_indptr,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
         _at(lse), _handle(stream))
     if rc != BIA_OK:
+        _check_window_tensors(q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len,
+                              workspace, out, lse, stream)
         raise BiaError(rc, "bia_decode_paged_window")
 
 
@@ -1208,6 +1258,8 @@ def bia_decode_paged_window_bounded(desc, bounds, window, sinks, q, k_cache, v_c
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
         _at(lse), _handle(stream))
     if rc != BIA_OK:
+        _check_window_tensors(q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len,
+                              workspace, out, lse, stream)
         raise BiaError(rc, "bia_decode_paged_window_bounded")
 
 
@@ -1242,4 +1294,6 @@ def bia_prefill_paged_window(desc, window, sinks, q, k_cache, v_cache, qo_indptr
         last.data_ptr(), batch, int(split_size), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), out.data_ptr(), _at(lse), _handle(stream))
     if rc != BIA_OK:
+        _check_window_tensors(q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len,
+                              workspace, out, lse, stream, qo_indptr)
         raise BiaError(rc, "bia_prefill_paged_window")
