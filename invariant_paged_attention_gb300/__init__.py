@@ -964,9 +964,13 @@ def _check_rope(desc, rope, table, positions, q_weight, k_weight, total):
     if table.shape != (rope.num_positions, rope.rot_dim):
         raise ValueError(f"table must be ({rope.num_positions}, {rope.rot_dim}), got "
                          f"{tuple(table.shape)}")
-    if positions is not None and positions.numel() != rope.num_axes * total:
-        raise ValueError(f"positions must hold {rope.num_axes} x {total} entries, got "
-                         f"{positions.numel()}")
+    if positions is not None:
+        # with one axis every shape has the same order; with more a transposed one would
+        # turn by other tokens' positions
+        axes = rope.num_axes
+        if positions.numel() != axes * total or (axes > 1 and positions.dim() != 1 and
+                                                 positions.shape != (axes, total)):
+            raise ValueError(f"positions must be ({axes}, {total}), got {tuple(positions.shape)}")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None and w.shape != (desc.head_dim,):
             raise ValueError(f"{name} must be ({desc.head_dim},), got {tuple(w.shape)}")
