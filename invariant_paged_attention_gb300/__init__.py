@@ -295,6 +295,14 @@ def _host_i32(t) -> torch.Tensor:
     return t.contiguous()
 
 
+def _int32(name, x) -> int:
+    """x as a 32-bit argument; ctypes would cut a wider one to its low bits."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -947,8 +955,8 @@ def make_rope(rot_dim, num_positions, num_axes=1, freq_axis=None, interleaved=Fa
     """The rotation of a model's heads (include/bia.h states the rule):
     freq_axis names the axis of each of the rot_dim / 2 frequencies where there
     are several axes, for example [16 * 0, 24 * 1, 24 * 2] or 0, 1, 2 in turn."""
-    r = Rope(int(rot_dim), int(bool(interleaved)), int(num_axes), int(num_positions),
-             float(norm_eps))
+    r = Rope(_int32("rot_dim", rot_dim), int(bool(interleaved)), _int32("num_axes", num_axes),
+             _int32("num_positions", num_positions), float(norm_eps))
     axes = [] if freq_axis is None or num_axes == 1 else list(freq_axis)
     if num_axes > 1 and len(axes) != rot_dim // 2:
         raise ValueError(f"freq_axis must name an axis for each of {rot_dim // 2} frequencies, "
@@ -1164,6 +1172,10 @@ def bia_append_paged_kv_fp8_rope(desc, rope, table, q, k_new, v_new, k_cache, v_
 # ---------------------------------------------------------------- window and sinks
 
 
+def _window_ints(window, sinks, split_size):
+    return _int32("window", window), _int32("sinks", sinks), _int32("split_size", split_size)
+
+
 def _check_window_tensors(q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
                           out, lse, stream, qo_indptr=None):
     more = () if qo_indptr is None else (("qo_indptr", qo_indptr, I32),)
@@ -1213,10 +1225,11 @@ def _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page
 
 def bia_decode_window_workspace_size(desc, window, sinks, kv_indptr_host, kv_last_page_len_host,
                                      split_size=0) -> int:
+    window, sinks, split_size = _window_ints(window, sinks, split_size)
     kvp, last = _host_i32(kv_indptr_host), _host_i32(kv_last_page_len_host)
     return int(load().bia_decode_window_workspace_size(
-        ctypes.byref(desc), int(window), int(sinks), _ptr(kvp), _ptr(last), len(kvp) - 1,
-        int(split_size)))
+        ctypes.byref(desc), window, sinks, _ptr(kvp), _ptr(last), len(kvp) - 1,
+        split_size))
 
 
 def bia_decode_paged_window(desc, window, sinks, q, k_cache, v_cache, kv_indptr, kv_indices,
@@ -1224,14 +1237,15 @@ def bia_decode_paged_window(desc, window, sinks, q, k_cache, v_cache, kv_indptr,
                             out, lse=None, split_size=0, stream=None):
     """bia_decode_paged where a query sees the last `window` keys and the first
     `sinks` keys of its request (include/bia.h states the rule)."""
+    window, sinks, split_size = _window_ints(window, sinks, split_size)
     kvp, last = _host(kv_indptr_host), _host(kv_last_page_len_host)
     batch = q.shape[0]
     _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
                   out, lse, stream, batch, kvp, last)
     rc = load().bia_decode_paged_window(
-        ctypes.byref(desc), int(window), int(sinks), q.data_ptr(), k_cache.data_ptr(),
+        ctypes.byref(desc), window, sinks, q.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), k_cache.shape[0], kv_indptr.data_ptr(), kv_indices.data_ptr(),
-        kv_last_page_len.data_ptr(), kvp.data_ptr(), last.data_ptr(), batch, int(split_size),
+        kv_last_page_len.data_ptr(), kvp.data_ptr(), last.data_ptr(), batch, split_size,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
         _at(lse), _handle(stream))
     if rc != BIA_OK:
@@ -1242,9 +1256,10 @@ def bia_decode_paged_window(desc, window, sinks, q, k_cache, v_cache, kv_indptr,
 
 def bia_decode_window_bounded_workspace_size(desc, bounds, window, sinks, batch,
                                              split_size=0) -> int:
+    window, sinks, split_size = _window_ints(window, sinks, split_size)
     return int(load().bia_decode_window_bounded_workspace_size(
-        ctypes.byref(desc), ctypes.byref(bounds), int(window), int(sinks), int(batch),
-        int(split_size)))
+        ctypes.byref(desc), ctypes.byref(bounds), window, sinks, int(batch),
+        split_size))
 
 
 def bia_decode_paged_window_bounded(desc, bounds, window, sinks, q, k_cache, v_cache, kv_indptr,
@@ -1252,13 +1267,14 @@ def bia_decode_paged_window_bounded(desc, bounds, window, sinks, q, k_cache, v_c
                                     split_size=0, stream=None):
     """bia_decode_paged_window sized from `bounds` (max_kv_len): the index arrays
     are read on the device only, so a captured decode replays step after step."""
+    window, sinks, split_size = _window_ints(window, sinks, split_size)
     batch = q.shape[0]
     _check_window(desc, q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len, workspace,
                   out, lse, stream, batch)
     rc = load().bia_decode_paged_window_bounded(
-        ctypes.byref(desc), ctypes.byref(bounds), int(window), int(sinks), q.data_ptr(),
+        ctypes.byref(desc), ctypes.byref(bounds), window, sinks, q.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], kv_indptr.data_ptr(),
-        kv_indices.data_ptr(), kv_last_page_len.data_ptr(), batch, int(split_size),
+        kv_indices.data_ptr(), kv_last_page_len.data_ptr(), batch, split_size,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
         _at(lse), _handle(stream))
     if rc != BIA_OK:
@@ -1269,11 +1285,12 @@ def bia_decode_paged_window_bounded(desc, bounds, window, sinks, q, k_cache, v_c
 
 def bia_prefill_window_workspace_size(desc, window, sinks, qo_indptr_host, kv_indptr_host,
                                       kv_last_page_len_host, split_size=0) -> int:
+    window, sinks, split_size = _window_ints(window, sinks, split_size)
     qo, kvp, last = (_host_i32(qo_indptr_host), _host_i32(kv_indptr_host),
                      _host_i32(kv_last_page_len_host))
     return int(load().bia_prefill_window_workspace_size(
-        ctypes.byref(desc), int(window), int(sinks), _ptr(qo), _ptr(kvp), _ptr(last), len(qo) - 1,
-        int(split_size)))
+        ctypes.byref(desc), window, sinks, _ptr(qo), _ptr(kvp), _ptr(last), len(qo) - 1,
+        split_size))
 
 
 def bia_prefill_paged_window(desc, window, sinks, q, k_cache, v_cache, qo_indptr, kv_indptr,
@@ -1282,6 +1299,7 @@ def bia_prefill_paged_window(desc, window, sinks, q, k_cache, v_cache, qo_indptr
                              stream=None):
     """bia_prefill_paged (causal) where a query sees the last `window` keys up to
     its own and the first `sinks` keys (include/bia.h states the rule)."""
+    window, sinks, split_size = _window_ints(window, sinks, split_size)
     qo, kvp, last = (_host(qo_indptr_host), _host(kv_indptr_host),
                      _host(kv_last_page_len_host))
     batch = qo.numel() - 1
@@ -1292,10 +1310,10 @@ def bia_prefill_paged_window(desc, window, sinks, q, k_cache, v_cache, qo_indptr
     if q.shape[0] != _last(qo):
         raise ValueError(f"q holds {q.shape[0]} tokens, qo_indptr_host ends at {_last(qo)}")
     rc = load().bia_prefill_paged_window(
-        ctypes.byref(desc), int(window), int(sinks), q.data_ptr(), k_cache.data_ptr(),
+        ctypes.byref(desc), window, sinks, q.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), k_cache.shape[0], qo_indptr.data_ptr(), kv_indptr.data_ptr(),
         kv_indices.data_ptr(), kv_last_page_len.data_ptr(), qo.data_ptr(), kvp.data_ptr(),
-        last.data_ptr(), batch, int(split_size), workspace.data_ptr(),
+        last.data_ptr(), batch, split_size, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), out.data_ptr(), _at(lse), _handle(stream))
     if rc != BIA_OK:
         _check_window_tensors(q, k_cache, v_cache, kv_indptr, kv_indices, kv_last_page_len,

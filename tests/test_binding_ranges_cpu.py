@@ -74,3 +74,42 @@ def test_positions_lie_an_axis_a_row(call):
             call(rope, good)
     with pytest.raises(ValueError, match="positions"):
         call(rope, torch.zeros(2, N, dtype=torch.int32))
+
+
+WIDE = [2**31, 2**32, 2**32 + 5, 2**32 + 128, 2**63 - 1, 2**80, -2**31 - 1, -2**32 + 128]
+
+
+def windowed(window=100, sinks=4, split=0):
+    """Each windowed call, of one request of 24 keys."""
+    q, c, ws = bf16(1, 4, 64), bf16(2, 16, 2, 64), torch.zeros(4096, dtype=torch.uint8)
+    qo, kvp, pages, last = i32(0, 1), i32(0, 2), i32(0, 1), i32(8)
+    b = bia.make_bounds(max_kv_len=64)
+    tail = (ws, torch.zeros_like(q), None, split)
+    return {
+        "decode": lambda: bia.bia_decode_paged_window(DESC, window, sinks, q, c, c, kvp, pages, last, kvp, last, *tail),
+        "bounded": lambda: bia.bia_decode_paged_window_bounded(DESC, b, window, sinks, q, c, c, kvp, pages, last, *tail),
+        "extend": lambda: bia.bia_prefill_paged_window(DESC, window, sinks, q, c, c, qo, kvp, pages, last, qo, kvp, last, *tail),
+        "decode size": lambda: bia.bia_decode_window_workspace_size(DESC, window, sinks, kvp, last, split),
+        "bounded size": lambda: bia.bia_decode_window_bounded_workspace_size(DESC, b, window, sinks, 1, split),
+        "extend size": lambda: bia.bia_prefill_window_workspace_size(DESC, window, sinks, qo, kvp, last, split),
+    }
+
+
+@pytest.mark.parametrize("name", list(windowed()))
+def test_window_sinks_and_split_of_32_bits(name):
+    """A number past 32 bits is refused, not cut to its low bits (2^32 sinks would be none)."""
+    for wide in WIDE:
+        for what in ("window", "sinks", "split"):
+            with pytest.raises(ValueError, match=what):
+                windowed(**{what: wide})[name]()
+    for good in (dict(), dict(window=2**31 - 1), dict(sinks=2**31 - 1), dict(split=128), dict(window=-2**31)):
+        with pytest.raises(Taken):  # the library refuses what it does not take
+            windowed(**good)[name]()
+
+
+def test_rotation_of_32_bits():
+    for wide in WIDE:
+        for args in ((wide, 10), (64, wide), (64, 10, wide, [0] * 32)):
+            with pytest.raises(ValueError):
+                bia.make_rope(*args)
+    assert bia.make_rope(64, 2**31 - 1).num_positions == 2**31 - 1
