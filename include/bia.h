@@ -595,14 +595,19 @@ BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
  * same, and a request's bits depend on the request alone, also when it is cut
  * into chunks that start on the 128-row q-tile grid.  A non-finite key or value
  * may reach every row of a q tile that sees its block of 128 keys; keys before
- * the window of the first row of a pair of q tiles, and past the request's
- * last key, never do.  split_size: a multiple of 128 up to
- * BIA_RAGGED_MAX_SPLIT (a larger one: BIA_ERR_UNSUPPORTED, as are min(sinks,
- * kv_len) above BIA_WINDOW_MAX_SINKS and caches of 2^31 - 1 (key, kv head) rows
- * and more); 0 = BIA_RAGGED_MAX_SPLIT for windows up to BIA_PREFILL_SPLIT, else
- * BIA_PREFILL_SPLIT; with few q tiles a smaller one spreads a long window over
- * more of the GPU.  Weights lag the running maximum by up to 2^16 before they
- * are divided by their sum, in fp32: values above 2^80 may overflow.
+ * the window of the first row of a pair of q tiles, and past the request's last
+ * key, never do.  split_size: a multiple of 128 up to BIA_RAGGED_MAX_SPLIT (a
+ * larger one: BIA_ERR_UNSUPPORTED, as are min(sinks, kv_len) above
+ * BIA_WINDOW_MAX_SINKS and caches of 2^31 - 1 (key, kv head) rows and more); 0 =
+ * BIA_RAGGED_MAX_SPLIT for windows up to BIA_PREFILL_SPLIT,
+ * else BIA_PREFILL_SPLIT; with few q tiles a smaller one spreads a long window
+ * over more of the GPU.  With a window or sinks above 65536 a larger split_size
+ * counts as 65536 (a longer fp32 sum loses what its keys add), and more sinks
+ * than that are visited with every key up to the window, those that no row sees
+ * unread; fewer sinks that the window has left behind are walked whole with a q
+ * tile's first split, whatever split_size.  Weights lag the running maximum by up
+ * to 2^16 before they are divided by their sum, in fp32: values above 2^80 may
+ * overflow.
  */
 BIA_API int bia_prefill_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
                              const void *q, const void *k_cache, const void *v_cache,
@@ -623,14 +628,14 @@ BIA_API size_t bia_prefill_window_workspace_size(const bia_attn_desc *desc, int3
                                          int32_t split_size);
 
 /*
- * bia_decode_paged with a window and sinks.  The keys that a query sees are
- * taken as one list, the sinks first, cut into tiles of split_size keys (a
- * multiple of 128; 0 = BIA_WINDOW_DECODE_SPLIT; fewer than 128 sinks before the
- * window make the first tile longer) whose states are merged in
- * order; with a window of at least kv_len the bits are those of
- * bia_decode_paged at the same split size.  The device index arrays are checked
- * request by request: one that breaks a rule of the call (or its bounds) gets
- * NaN rows and sets bit 1 of the status word, the others are computed.
+ * bia_decode_paged with a window and sinks.  The keys that a query sees are taken
+ * as one list, the sinks first, cut into tiles of split_size keys (a multiple of
+ * 128; 0 = BIA_WINDOW_DECODE_SPLIT; fewer than 128 sinks before the window make
+ * the first tile longer) whose states are merged in order; split_size above 65536
+ * counts as 65536, as above; with a window of at least kv_len the bits are those
+ * of bia_decode_paged at the same split size.  The device index arrays are
+ * checked request by request: one that breaks a rule of the call (or its bounds)
+ * gets NaN rows and sets bit 1 of the status word, the others are computed.
  */
 BIA_API int bia_decode_paged_window(const bia_attn_desc *desc, int32_t window, int32_t sinks,
                             const void *q, const void *k_cache, const void *v_cache,

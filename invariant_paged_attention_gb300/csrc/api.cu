@@ -1411,15 +1411,19 @@ int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks
     p->total_q += q_len;
     p->max_kv_len = std::max(p->max_kv_len, kv_len);
   }
-  // the sinks go with a tile's first split: its time stays far below the limit
-  // of the kernel's waits
   if (std::min<int64_t>(sinks, p->max_kv_len) > BIA_WINDOW_MAX_SINKS) return BIA_ERR_UNSUPPORTED;
+  // (of the call's arguments alone, so that a request's bits are)
+  if (window > bia::kWindowRun || sinks > bia::kWindowRun) split = std::min(split, bia::kWindowRun);
   p->split = split;
   // a pair's keys: up to window + (the pair's tokens - 1), or all of them where
-  // the sinks meet the window, which then ends within sinks + a block of it
-  const int64_t span = std::min<int64_t>(
-      p->max_kv_len, static_cast<int64_t>(std::min(window, kAllKeys)) + nt * T +
-                         (sinks > 0 ? std::min(sinks, kAllKeys) + 2 * bia::kKvBlock : 0));
+  // the sinks meet the window, which then ends within sinks + a block of it, and
+  // where tile_keys makes one range of them
+  const int64_t span =
+      sinks > bia::kWindowRun
+          ? p->max_kv_len
+          : std::min<int64_t>(p->max_kv_len,
+                              static_cast<int64_t>(std::min(window, kAllKeys)) + nt * T +
+                                  (sinks > 0 ? sinks + 2 * bia::kKvBlock : 0));
   p->parts = static_cast<int32_t>(std::max<int64_t>(
       1, std::min<int64_t>((p->max_kv_len + split - 1) / split, (span + split - 1) / split + 1)));
   const int64_t items = p->pairs * Hkv;
@@ -1472,9 +1476,7 @@ int window_decode_plan(const bia_attn_desc *desc, const bia_bounds *bounds, int3
     }
   }
   if (p->max_kv_len > INT32_MAX / 2) return BIA_ERR_UNSUPPORTED;
-  // (a tile longer than every request is the same as one of 2^30 keys, and its
-  // ends stay in 32 bits)
-  split = std::min(split, 1 << 30);
+  split = std::min(split, bia::kWindowRun); // (which also keeps a tile's ends in 32 bits)
   p->split = split;
   p->parts = static_cast<int32_t>((window_len(p->max_kv_len, window, sinks) + split - 1) / split);
   const int64_t units = static_cast<int64_t>(batch) * p->parts;
