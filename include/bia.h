@@ -599,7 +599,7 @@ BIA_API size_t bia_prefill_ragged_workspace_size(const bia_attn_desc *desc,
  * key, never do.  split_size: a multiple of 128 up to BIA_RAGGED_MAX_SPLIT (a
  * larger one: BIA_ERR_UNSUPPORTED, as are min(sinks, kv_len) above
  * BIA_WINDOW_MAX_SINKS and caches of 2^31 - 1 (key, kv head) rows and more); 0 =
- * BIA_RAGGED_MAX_SPLIT for windows up to BIA_PREFILL_SPLIT,
+ * BIA_RAGGED_MAX_SPLIT where window and sinks are at most BIA_PREFILL_SPLIT each,
  * else BIA_PREFILL_SPLIT; with few q tiles a smaller one spreads a long window
  * over more of the GPU.  With a window or sinks above 65536 a larger split_size
  * counts as 65536 (a longer fp32 sum loses what its keys add), and more sinks

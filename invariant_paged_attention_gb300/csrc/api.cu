@@ -1391,8 +1391,11 @@ int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks
   // 8192 tokens at window 1024: 690 us split at 4096, 660 whole; 6 chunks at
   // window 4096: 133 and 120, one of them 71 and 62).  A longer one is split for
   // calls of few q tiles (one chunk at window 15000: 86 us, 200 split at 16384;
-  // six 432 and 393).
-  if (split == 0) split = window <= BIA_PREFILL_SPLIT ? BIA_RAGGED_MAX_SPLIT : BIA_PREFILL_SPLIT;
+  // six 432 and 393), as is one of many sinks, which the window may meet (4 tokens that
+  // see 65536 keys took 902 us whole and 98 split).
+  if (split == 0)
+    split = window <= BIA_PREFILL_SPLIT && sinks <= BIA_PREFILL_SPLIT ? BIA_RAGGED_MAX_SPLIT
+                                                                      : BIA_PREFILL_SPLIT;
   if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
   if (split > BIA_RAGGED_MAX_SPLIT) return BIA_ERR_UNSUPPORTED;
   if (qo_host[0] != 0 || kvp_host[0] < 0) return BIA_ERR_INVALID_ARG;

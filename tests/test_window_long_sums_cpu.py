@@ -39,3 +39,14 @@ def test_decode(bia, d):  # noqa: F811
         assert size(65536, split) == size(65536, 65536) < 4096
         b = bia.make_bounds(max_kv_len=1 << 20)
         assert bia.bia_decode_window_bounded_workspace_size(desc, b, MOST, 0, 1, split) == size(1 << 20, 65536)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 4, 64), (32, 8, 128), (16, 8, 256)])
+def test_default_split_with_sinks(bia, hq, hkv, d):  # noqa: F811
+    """A short window is one state by default, but not with all the sinks that it may meet."""
+    desc = bia.make_desc(hq, hkv, d, 16)
+    states = lambda n, parts: n * parts * hq * (d + 1) * 4
+    keys = 1 << 20
+    assert extend(bia, desc, 4, keys, 1024, MOST) >= states(4, keys // 4096)
+    assert extend(bia, desc, 4, keys, 1024, MOST) == extend(bia, desc, 4, keys, MOST, 0)
+    assert extend(bia, desc, 4, keys, 1024, 5000) >= states(4, 2)
