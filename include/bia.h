@@ -688,8 +688,9 @@ BIA_API size_t bia_decode_window_bounded_workspace_size(const bia_attn_desc *des
  *   q_weight, k_weight: fp32 [head_dim], 16-byte aligned, of the norms of
  *              queries and of keys; NULL: no norm of theirs
  * Squares above the range of fp32 (elements above 1.8e19) make a normed head
- * zero or NaN.  A head's bits depend on that head, its position and the table
- * alone.
+ * zero or NaN, as 0 / sqrt(0) does a head of zeros where norm_eps is 0; squares
+ * below it count in full.  A head's bits depend on that head, its position and
+ * the table alone.
  */
 typedef struct bia_rope {
     int32_t rot_dim;       /* columns that turn: a multiple of 16 up to head_dim */

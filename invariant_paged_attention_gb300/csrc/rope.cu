@@ -43,6 +43,7 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 // the four calls above took 68, 190, 220 and 27 us, with 8 (fewer CTAs an SM)
 // 72, 192, 239 and 33.
 constexpr int kRing = 2;
+constexpr float kTinyVar = 0x1p-80f; // mean squares below it are taken again, scaled
 enum RopeDest { kToRows, kToPages, kToPagesFp8 };
 
 // The lane's sixteen columns as a[8], b[8]: pair f is (a[f], b[f]).
@@ -283,7 +284,24 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
         float ss = s_lo + s_hi;
 #pragma unroll
         for (int off = LPH / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        r = rsqrtf(__fmaf_rn(ss, a.inv_D, a.eps));
+        float var = __fmaf_rn(ss, a.inv_D, a.eps);
+        if (a.eps < kTinyVar) { // uniform over the call
+          // A head whose squares leave fp32 (with a larger eps they do not count) is
+          // taken 2^90 times as large, exactly: its elements of 2^-133 to 2^-36 are
+          // 2^-43 to 2^54 then.
+          const bool tiny = var < kTinyVar;
+          const float up = tiny ? 0x1p90f : 1.f;
+          ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            ya[e] *= up, yb[e] *= up;
+            ss = __fmaf_rn(ya[e], ya[e], __fmaf_rn(yb[e], yb[e], ss));
+          }
+#pragma unroll
+          for (int off = LPH / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          if (tiny) var = __fmaf_rn(ss, a.inv_D, a.eps * up * up);
+        }
+        r = rsqrtf(var);
       }
       // explicit roundings: every destination has the same bits
       const uint64_t r2 = f32x2(r, r);
