@@ -415,17 +415,14 @@ __global__ void __launch_bounds__((SmemW<D, ROWS>::kThreads), 1)
           const int st = g & 1;
           const int32_t key = key_of(j), run0 = key - 4 * (grp & 3);
           int32_t rows[4];
-          bool good = true;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             rows[i] = a.kv_rows; // outside the map: zeros
             if (wanted(key + i)) {
-              const bool there = pg[i] >= 0 && pg[i] < a.num_pages;
-              if (there)
+              if (pg[i] >= 0 && pg[i] < a.num_pages)
                 rows[i] = ((pg[i] << a.page_shift) + ((key + i) & page_mask)) * a.Hkv + kvh;
               else
                 atomicOr(a.status, kStatusBadPage);
-              good = good && there;
             }
           }
           // A run of 16 keys of one page is one copy a column block.  Keys of it
