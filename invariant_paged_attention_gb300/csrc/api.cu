@@ -1388,11 +1388,15 @@ int window_prefill_plan(const bia_attn_desc *desc, int32_t window, int32_t sinks
     return BIA_ERR_INVALID_ARG;
   // A window within one split is not split: its tiles would only be cut where a
   // split's end falls into them, and pay for their states (prompts of 512 to
-  // 8192 tokens at window 1024: 690 us split at 4096, 660 whole; 6 chunks at
-  // window 4096: 133 and 120, one of them 71 and 62).  A longer one is split for
-  // calls of few q tiles (one chunk at window 15000: 86 us, 200 split at 16384;
-  // six 432 and 393), as is one of many sinks, which the window may meet (4 tokens that
-  // see 65536 keys took 902 us whole and 98 split).
+  // 8192 tokens at window 1024: 689 us split at 4096, 656 whole; 6 chunks at
+  // window 4096: 132 and 119, one of them 70 and 61; 16 requests of 4 to 7 draft
+  // tokens 58 whole and 70 split at 2048).  What it costs are a few draft tokens
+  // alone, one CTA a kv head through the whole window (a request's at window 4096:
+  // 53 us, 39 split at 2048 and 36 at 1024; four requests' 55, 41 and 48): the
+  // caller's to split.  A longer window is split for calls of few q tiles (one
+  // chunk at window 15000: 86 us, 197 split at 16384; six 427 and 390), as is one
+  // of many sinks, which the window may meet (4 tokens that see 65536 keys took 902
+  // us whole and 98 split).
   if (split == 0)
     split = window <= BIA_PREFILL_SPLIT && sinks <= BIA_PREFILL_SPLIT ? BIA_RAGGED_MAX_SPLIT
                                                                       : BIA_PREFILL_SPLIT;
@@ -1462,8 +1466,8 @@ int window_decode_plan(const bia_attn_desc *desc, const bia_bounds *bounds, int3
   if (rc != BIA_OK) return rc;
   if (window < 1 || sinks < 0 || batch <= 0) return BIA_ERR_INVALID_ARG;
   // 512 by default: short tiles spread few requests over the SMs (one at window
-  // 1024: 11.5 us in tiles of 256 keys, 13.7 of 512, 18.4 of 1024), long ones have
-  // fewer starts and states (64 requests: 239, 200 and 189 us).
+  // 1024: 11.9 us in tiles of 256 keys, 14.0 of 512, 18.9 of 1024), long ones have
+  // fewer starts and states (64 requests: 237, 200 and 190 us).
   if (split == 0) split = BIA_WINDOW_DECODE_SPLIT;
   if (split <= 0 || split % bia::kKvBlock != 0) return BIA_ERR_UNSUPPORTED;
   if (bounds) {

@@ -47,7 +47,7 @@ constexpr float kLazyThreshold = 8.0f; // log2 units
 
 // The short split tiles of a window (WIN) have a stage or two less and so more
 // CTAs an SM where registers allow (64 requests, window 4096, 64-wide heads: one a
-// group 146 -> 115 us, four 196 -> 192; 96 wide 233 -> 221).
+// group 124 -> 104 us, four 182 -> 181, eight 400 -> 388; 96 wide 227 -> 221).
 template <int D, bool WIN = false>
 struct DecSmem {
   static constexpr int kStages = D == 256 ? 2 : (D == 128 ? (WIN ? 2 : 3) : (WIN ? 3 : 5));
@@ -215,9 +215,9 @@ __global__ void __launch_bounds__(kThreadsDec, (G <= 4 ? 2 : 1))
   int32_t pg_next = page_of(0);
   // With a window every lane copies 16-byte pieces, a row LPK lanes: the split
   // tiles are short, and a bulk copy a row costs the same whatever its length
-  // (64 requests, window 4096, 32/8 heads x 64: 236 us with bulk copies, 196
-  // with pieces; 16/8 x 256: 425 and 398; one request at window 1024 x 64: 16.6 and
-  // 13.3).
+  // (64 requests, window 4096, 32/8 heads x 64: 235 us with bulk copies, 181
+  // with pieces; 16/8 x 256: 427 and 397; one request at window 1024 x 64: 16.8 and
+  // 13.4).
   constexpr bool kPieces = WIN;
   auto pieces = [&](int i) {
     if (i < my_chunks) {

@@ -48,7 +48,7 @@
 // looking its items up when it came to them, a 4-block item cost 1.5 us more).
 // 64 requests of 32/8 heads at window 4096 + 64 sinks: 200 us (5.4 TB/s, 79 % of
 // a plain copy; split tiles of 2048 keys 183 us); what is left is the copy
-// warps' refill at each item's start.  One request at window 1024: 13.7 us, the
+// warps' refill at each item's start.  One request at window 1024: 14.0 us, the
 // latencies of this kernel and the merge.
 //
 // Also runs the single-token q tiles a prefill call streams (with the

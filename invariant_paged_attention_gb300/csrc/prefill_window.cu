@@ -29,8 +29,8 @@
 // either way, whatever the batch.
 //
 // Measured with 32/8 heads x 128 on prompts of 512 to 8192 tokens: window 1024
-// 655 us (1030 TFLOP/s of the scores seen), 8192 1675 us (1370), 16/8 heads x
-// 256 750 us (880); pages of one key 760 and 1220 us.  A pair of tiles takes a
+// 657 us (1028 TFLOP/s of the scores seen), 8192 1700 us (1343), 16/8 heads x
+// 256 750 us (880); pages of one key 765 and 1220 us.  A pair of tiles takes a
 // 128-key block in ~2950 cycles, 2050 of them MMAs back to back; the rest is the
 // chain P -> P.V -> S -> P (a wait answered in 100 to 150 cycles, commits of 60)
 // and, at the power that this draws, a clock of 1.6 to 1.75 GHz.  Exponentials
@@ -38,7 +38,9 @@
 // not whole costs up to twice its time) and an epilogue of ~4500 cycles every
 // ten blocks; 256-wide heads, one tile an item, read twice the bytes a flop and
 // wait for values; pages of fewer than 16 keys for the gathers (four rows of
-// 128 bytes about every 29 cycles an SM).
+// 128 bytes about every 29 cycles an SM; 256-wide heads spill 50 bytes there).
+//
+// P is rounded to bf16 for the tensor cores; scores, sums and states are fp32.
 #include "bia_internal.h"
 #include "fold.cuh"
 #include "ptx.cuh"
@@ -102,7 +104,7 @@ struct Steps {
 
 // ROWS: pages of fewer than 16 keys, whose rows are gathered four at a time.  A
 // warp issues its lanes' gathers one after the other, so K and V have two warps
-// each (window 1024, page 1: 962 us with one, 760 with two; 256-wide heads 1602
+// each (window 1024, page 1: 962 us with one, 765 with two; 256-wide heads 1602
 // and 1220); runs of 16 keys need one.
 template <int D, bool ROWS>
 struct SmemW {

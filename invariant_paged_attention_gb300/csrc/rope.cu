@@ -22,11 +22,12 @@
 // few tokens splits a token's heads over several warps, down to a step a warp.
 //
 // Bound by the copy rate and, close behind, by its instructions (three in four
-// cycles issue one): 17868 tokens of 32/8 heads x 128 66 us (5.6 TB/s, 81 % of a
-// plain copy), 44213 tokens into bf16 pages 190 us (5.75 TB/s, 85 %), into 8-bit
-// pages 216 us (5.05 TB/s, 74 %; the scales' maxima and the codes come on top),
-// 10693 tokens of 16/2 heads, half of the columns turning on three axes, 25 us (4.0
-// TB/s).
+// cycles issue one): 17868 tokens of 32/8 heads x 128 68 us (5.4 TB/s, 80 % of a
+// plain copy), 44213 tokens into bf16 pages 186 us (5.85 TB/s, 86 %), into 8-bit
+// pages 210 us (5.2 TB/s, 77 %; the scales' maxima and the codes come on top).
+// 10693 tokens of 16/2 heads, half of the columns turning on three axes, take 27.5
+// us (3.6 TB/s): a token waits for a position and then for its table row axis by
+// axis, and has five steps to pay for it.
 #include <algorithm>
 
 #include "bia_internal.h"
@@ -40,8 +41,8 @@ namespace {
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 // Steps of a warp whose loads are under way (1 KB of shared memory each): with 4
-// the four calls above took 68, 190, 220 and 27 us, with 8 (fewer CTAs an SM)
-// 72, 192, 239 and 33.
+// the four calls above take 70, 188, 214 and 30 us, with 8 (fewer CTAs an SM)
+// 76, 203, 229 and 31.
 constexpr int kRing = 2;
 constexpr float kTinyVar = 0x1p-80f; // mean squares below it are taken again, scaled
 enum RopeDest { kToRows, kToPages, kToPagesFp8 };
