@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
   const bool in_row = c * 16 < D, turns = c * 16 < a.rot;
   // the lane's two pieces of a head that rotates (or not); of a value 16c, 16c +
   // 8.  Interleaved pairs of a whole row lie half a row apart too, four a piece
-  // (44213 tokens into bf16 pages 199 us, with one run of eight pairs 229: two
+  // (44213 tokens into bf16 pages 191 us, with one run of eight pairs 224: two
   // copies touched each sector).
   const bool apart = turns && (!INTER || a.rot == D), split = INTER && apart;
   const int col0 = apart ? 8 * c : 16 * c, col1 = apart ? half + 8 * c : 16 * c + 8;
